@@ -9,6 +9,9 @@ it:
     gdp_prefill / gdp_decode_step   (Gated DeltaProduct: n_h transitions per token)
     prefill_bwd(...)                (the backward pass of prefill)
     conv_gates(...)                 (the front end: short conv + SiLU, gate activations)
+    linear / linear_bwd             (the projections: bias, activation, residual in the epilogue)
+    residual_norm / residual_norm_bwd (the norms around a block, its gate and residual scale)
+    gated_norm / gated_norm_bwd     (the output norm of the recurrence with its gate)
 
 There is no CPU or eager fallback: if the library is missing, calls raise.
 """
@@ -16,7 +19,9 @@ from .kda import (decode_step, get_device_error, make_params, prefill,  # noqa: 
                   prefill_no_alloc, no_alloc_form, set_stage_events, uses_tensor_cores,
                   workspace_size, verify_window, fold_accepted, ring_record_elems,
                   gdp_prefill, gdp_decode_step, prefill_bwd, conv_gates)
+from .layer import (linear, linear_bwd, residual_norm, residual_norm_bwd,  # noqa: F401
+                    gated_norm, gated_norm_bwd)
 from ._lib import KdaError, KdaParams, load  # noqa: F401
 
 __all__ = ["prefill", "decode_step", "workspace_size", "get_device_error", "make_params",
-           "set_stage_events", "prefill_no_alloc", "no_alloc_form", "uses_tensor_cores", "verify_window", "fold_accepted", "ring_record_elems", "gdp_prefill", "gdp_decode_step", "prefill_bwd", "conv_gates", "KdaError", "KdaParams", "load"]
+           "set_stage_events", "prefill_no_alloc", "no_alloc_form", "uses_tensor_cores", "verify_window", "fold_accepted", "ring_record_elems", "gdp_prefill", "gdp_decode_step", "prefill_bwd", "conv_gates", "linear", "linear_bwd", "residual_norm", "residual_norm_bwd", "gated_norm", "gated_norm_bwd", "KdaError", "KdaParams", "load"]

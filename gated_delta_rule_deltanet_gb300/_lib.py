@@ -38,7 +38,16 @@ EXPORTS = ("kda_abi_version", "kda_status_string", "kda_prefill_workspace_size",
            "kda_prefill_uses_tensor_cores", "kda_ring_record_elems", "kda_verify_window",
            "kda_fold_accepted", "kda_gdp_prefill_fwd", "kda_gdp_decode_step",
            "kda_gdp_workspace_size", "kda_prefill_bwd", "kda_prefill_bwd_workspace_size",
-           "kda_conv_gates_fwd", "kda_prefill_no_alloc_form")
+           "kda_conv_gates_fwd", "kda_prefill_no_alloc_form", "kda_linear_fwd",
+           "kda_linear_bwd", "kda_linear_workspace_size", "kda_residual_norm_fwd",
+           "kda_residual_norm_bwd", "kda_gated_norm_fwd", "kda_gated_norm_bwd",
+           "kda_norm_workspace_size")
+
+KDA_ACT_NONE = 0
+KDA_ACT_RELU = 1
+KDA_ACT_SILU = 2
+KDA_ACT_GELU = 3
+KDA_ACT_SIGMOID = 4
 
 KDA_NO_ALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -64,6 +73,46 @@ class KdaParams(ctypes.Structure):
         ("q_row_stride", ctypes.c_int64),
         ("k_row_stride", ctypes.c_int64),
         ("v_row_stride", ctypes.c_int64),
+    ]
+
+
+class KdaLinearParams(ctypes.Structure):
+    """Mirror of kda_linear_params_t."""
+
+    _fields_ = [
+        ("tokens", ctypes.c_int64),
+        ("in_features", ctypes.c_int32),
+        ("out_features", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("y_dtype", ctypes.c_int32),
+        ("residual_dtype", ctypes.c_int32),
+        ("dw_dtype", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("x_row_stride", ctypes.c_int64),
+        ("w_row_stride", ctypes.c_int64),
+        ("y_row_stride", ctypes.c_int64),
+        ("residual_row_stride", ctypes.c_int64),
+        ("flags", ctypes.c_uint32),
+    ]
+
+
+class KdaNormParams(ctypes.Structure):
+    """Mirror of kda_norm_params_t."""
+
+    _fields_ = [
+        ("tokens", ctypes.c_int64),
+        ("features", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32),
+        ("h_dtype", ctypes.c_int32),
+        ("gate_dtype", ctypes.c_int32),
+        ("y_dtype", ctypes.c_int32),
+        ("gate_per_token", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("scale", ctypes.c_float),
+        ("gate_row_stride", ctypes.c_int64),
     ]
 
 
@@ -135,6 +184,17 @@ def load():
         L.kda_prefill_bwd_workspace_size.restype = ctypes.c_int
         L.kda_conv_gates_fwd.argtypes = [pp, ctypes.c_int32] + [P] * 14
         L.kda_conv_gates_fwd.restype = ctypes.c_int
+        Z, lp, np_ = ctypes.c_size_t, ctypes.POINTER(KdaLinearParams), ctypes.POINTER(KdaNormParams)
+        for name, args in (("kda_linear_fwd", [lp] + [P] * 7 + [Z, P]),
+                           ("kda_linear_bwd", [lp] + [P] * 8 + [Z, P]),
+                           ("kda_linear_workspace_size", [lp, ctypes.c_int32, ctypes.POINTER(Z)]),
+                           ("kda_residual_norm_fwd", [np_] + [P] * 8),
+                           ("kda_residual_norm_bwd", [np_] + [P] * 13 + [Z, P]),
+                           ("kda_gated_norm_fwd", [np_] + [P] * 5),
+                           ("kda_gated_norm_bwd", [np_] + [P] * 8 + [Z, P]),
+                           ("kda_norm_workspace_size", [np_, ctypes.c_int32, ctypes.POINTER(Z)])):
+            getattr(L, name).argtypes = args
+            getattr(L, name).restype = ctypes.c_int
         L.kda_set_stage_events.argtypes = [P, ctypes.c_int32]
         L.kda_set_stage_events.restype = ctypes.c_int
         _lib = L

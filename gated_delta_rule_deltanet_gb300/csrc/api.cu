@@ -71,6 +71,14 @@ int32_t* device_error_word() {
   return g_err_ptr[dev];
 }
 
+}  // namespace
+
+namespace kda {
+int32_t* layer_error_word() { return device_error_word(); }
+}  // namespace kda
+
+namespace {
+
 std::mutex g_stage_mutex;
 kda::Stages g_stages = {};
 

@@ -1,0 +1,57 @@
+// gemm.cuh -- the matrix product behind the projections (linear.cu, linear_tc.cu):
+//
+//     out[j, i] = residual[j, i] + scale act(sum_c A(i, c) B(j, c) + bias[i])
+//
+// with i the contiguous dimension of every [J, I] array.  The forward takes A = w, B = x over
+// c = k; dx takes A = w^T, B = dz over c = n; dw takes A = x^T, B = dz^T over c = t.
+#pragma once
+
+#include "layer_common.cuh"
+
+namespace kda {
+
+struct GemmOperand {
+  const void* p;
+  int64_t ld;      // elements between rows of the stored matrix
+  bool mn;         // false: rows are i (or j) and c is contiguous; true: rows are c
+};
+
+struct GemmEpilogue {
+  const float* bias;   // [I] or null
+  const void* res;     // [J, I] or null
+  void* out;           // [J, I]
+  void* z;             // [J, I] or null: the sum before the activation
+  int64_t res_ld, out_ld, z_ld;
+  float scale;
+  int32_t act;
+  bool res_bf, out_bf, z_bf;
+};
+
+struct Gemm {
+  GemmOperand A, B;
+  int64_t I, J, C;
+  bool bf16;           // operand type: bf16 or fp32
+  GemmEpilogue epi;
+  int32_t* err;
+};
+
+__device__ __forceinline__ float ld_any(const void* p, bool bf, int64_t i) {
+  return bf ? bf16_bits_to_f32(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+__device__ __forceinline__ void st_any(void* p, bool bf, int64_t i, float v) {
+  if (bf) static_cast<uint16_t*>(p)[i] = f32_to_bf16_bits(v);
+  else static_cast<float*>(p)[i] = v;
+}
+
+// one element of the result; `acc` is the finished sum over c
+__device__ __forceinline__ void epilogue_store(const GemmEpilogue& E, int64_t j, int64_t i, float acc) {
+  if (E.bias) acc += __ldg(E.bias + i);
+  if (E.z) st_any(E.z, E.z_bf, j * E.z_ld + i, acc);
+  float y = E.scale * (E.out_bf ? act_f<true>(E.act, acc) : act_f<false>(E.act, acc));
+  if (E.res) y += ld_any(E.res, E.res_bf, j * E.res_ld + i);
+  st_any(E.out, E.out_bf, j * E.out_ld + i, y);
+}
+
+cudaError_t launch_gemm_simt(const Gemm& g, cudaStream_t st);
+
+}  // namespace kda

@@ -1,0 +1,172 @@
+// layer_common.cuh -- pieces shared by the kernels of the layer around the recurrence
+// (linear.cu, norms.cu): eight-element chunks of a row in either dtype, the activations and
+// their derivatives, and the fixed-order sum over partial rows.
+#pragma once
+
+#include "kda_common.cuh"
+
+namespace kda {
+
+// The device error word of the current device (null when CUDA reports an error).
+int32_t* layer_error_word();
+
+inline size_t dtype_bytes(int32_t dt) { return dt == KDA_DTYPE_BF16 ? 2 : 4; }
+
+// ---------------------------------------------------------------- eight elements of a row
+
+// VEC: elements [8 c, 8 c + 8) as 16-byte vectors (rows of a multiple of 8 elements, 16-byte
+// aligned).  Otherwise: elements c, c + step, c + 2 step, ... below n, each loaded by itself,
+// so that rows of any length and alignment are read with consecutive lanes on consecutive
+// elements.
+template <bool VEC>
+__device__ __forceinline__ int chunk_index(int c, int step, int e) {
+  return VEC ? 8 * c + e : c + e * step;
+}
+
+template <bool BF>
+struct Raw8 {               // the chunk as loaded: no arithmetic waits on it until f32() is called
+  uint32_t w[BF ? 4 : 8];
+  __device__ __forceinline__ float f32(int e) const {
+    if constexpr (BF)
+      return (e & 1) ? __uint_as_float(w[e >> 1] & 0xffff0000u) : __uint_as_float(w[e >> 1] << 16);
+    else
+      return __uint_as_float(w[e]);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (BF ? 4 : 8); ++i) w[i] = 0;
+  }
+};
+
+template <bool BF, bool VEC>
+__device__ __forceinline__ Raw8<BF> load_chunk(const void* row, int c, int step, int n) {
+  Raw8<BF> r;
+  if constexpr (VEC) {
+    if (8 * c < n) {
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(row) +
+                                                      static_cast<int64_t>(c) * (BF ? 16 : 32));
+      const uint4 a = p[0];
+      r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+      if constexpr (!BF) {
+        const uint4 b = p[1];
+        r.w[4] = b.x; r.w[5] = b.y; r.w[6] = b.z; r.w[7] = b.w;
+      }
+    } else {
+      r.zero();
+    }
+  } else {
+    r.zero();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int i = c + e * step;
+      if (i < n) {
+        if constexpr (BF)
+          r.w[e >> 1] |= static_cast<uint32_t>(static_cast<const uint16_t*>(row)[i]) << (16 * (e & 1));
+        else
+          r.w[e] = __float_as_uint(static_cast<const float*>(row)[i]);
+      }
+    }
+  }
+  return r;
+}
+
+// rounds to nearest even where the row is bf16
+template <bool BF, bool VEC>
+__device__ __forceinline__ void store_chunk(void* row, int c, int step, int n, const float (&x)[8]) {
+  if constexpr (VEC) {
+    if (8 * c >= n) return;
+    uint4* p = reinterpret_cast<uint4*>(static_cast<char*>(row) + static_cast<int64_t>(c) * (BF ? 16 : 32));
+    if constexpr (BF) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(x[2 * e + 1]), "f"(x[2 * e]));
+      p[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      p[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+      p[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int i = c + e * step;
+      if (i < n) {
+        if constexpr (BF) static_cast<uint16_t*>(row)[i] = f32_to_bf16_bits(x[e]);
+        else static_cast<float*>(row)[i] = x[e];
+      }
+    }
+  }
+}
+
+// eight fp32 parameters of a chunk's columns (cached: every row reads them)
+template <bool VEC>
+__device__ __forceinline__ void load_params(const float* p, int c, int step, int n, float (&x)[8]) {
+  if constexpr (VEC) {
+    if (8 * c < n) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(p) + 2 * c);
+      const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 2 * c + 1);
+      x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int i = c + e * step;
+      x[e] = i < n ? __ldg(p + i) : 0.f;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- activations
+
+// sigmoid(z).  FAST (bf16 results): __expf's error, 2 + 1.2 |z| ulp, stays far below the bf16
+// rounding; otherwise expf.  The quotient is 0 where exp(-z) overflows.
+template <bool FAST>
+__device__ __forceinline__ float sigmoid_f(float z) {
+  return __fdividef(1.f, 1.f + (FAST ? __expf(-z) : expf(-z)));
+}
+
+template <bool FAST>
+__device__ __forceinline__ float act_f(int act, float z) {
+  switch (act) {
+    case KDA_ACT_RELU: return z > 0.f ? z : (z == z ? 0.f : z);   // a NaN stays one
+    case KDA_ACT_SILU: return z == -INFINITY ? 0.f : z * sigmoid_f<FAST>(z);
+    case KDA_ACT_GELU: return z == -INFINITY ? 0.f : 0.5f * z * erfcf(-0.70710678f * z);   // 2 Phi(z) without cancellation
+    case KDA_ACT_SIGMOID: return sigmoid_f<FAST>(z);
+    default: return z;
+  }
+}
+
+template <bool FAST>
+__device__ __forceinline__ float act_grad_f(int act, float z) {
+  switch (act) {
+    case KDA_ACT_RELU: return z > 0.f ? 1.f : (z == z ? 0.f : z);
+    case KDA_ACT_SILU: {
+      // p (1 + z (1 - p)), 1 - p = sigmoid(-z): no cancellation, and 0 / 1 at the infinities
+      if (fabsf(z) > 3e38f) return z > 0.f ? 1.f : 0.f;
+      const float p = sigmoid_f<FAST>(z);
+      return p * (1.f + z * sigmoid_f<FAST>(-z));
+    }
+    case KDA_ACT_GELU: {
+      if (fabsf(z) > 20.f) return z > 0.f ? 1.f : 0.f;
+      return 0.5f * erfcf(-0.70710678f * z) + 0.39894228f * z * expf(-0.5f * z * z);
+    }
+    case KDA_ACT_SIGMOID: return sigmoid_f<FAST>(z) * sigmoid_f<FAST>(-z);
+    default: return 1.f;
+  }
+}
+
+// ---------------------------------------------------------------- partial rows
+
+// Partial rows of `segments` (at most 3) stretches of `cols` columns each: outs.p[s][c] =
+// alpha * sum_{p < parts} part[(p * segments + s) * cols + c], added in a fixed order; stretches
+// with a null output are skipped.
+struct SumOuts {
+  float* p[3];
+};
+cudaError_t launch_sum_parts(const float* part, int parts, int64_t cols, int segments, float alpha,
+                             const SumOuts& outs, cudaStream_t st);
+
+}  // namespace kda

@@ -1,0 +1,367 @@
+"""Torch-facing binding of the layer around the recurrence: the projections, the norms on both
+sides of a block and the output norm with its gate (kda_linear_*, kda_residual_norm_*,
+kda_gated_norm_*).  Argument marshalling only, as in `kda.py`.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+import inspect
+from typing import Optional
+
+import torch
+
+from . import _lib
+from ._lib import KdaError, KdaLinearParams, KdaNormParams
+from .kda import _QKV_DTYPES, _workspace
+
+_ACTIVATIONS = {"none": _lib.KDA_ACT_NONE, "relu": _lib.KDA_ACT_RELU, "silu": _lib.KDA_ACT_SILU,
+                "gelu": _lib.KDA_ACT_GELU, "sigmoid": _lib.KDA_ACT_SIGMOID}
+_NORM_GATES = ("sigmoid", "silu", "none")
+
+
+def _device(*ts):
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("all tensors must be CUDA tensors")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("all tensors must be on the same device")
+    return dev
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on_stream(fn):
+    """With `stream=`, the whole call runs with that stream current, so that the outputs and the
+    workspace it allocates belong to the stream that uses them."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    call.__signature__ = inspect.signature(fn).replace(parameters=[
+        *inspect.signature(fn).parameters.values(),
+        inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None,
+                          annotation=Optional[torch.cuda.Stream])])
+    return call
+
+
+def _call(name, dev, *args):
+    """Calls entry point `name` on the current stream of the tensors' device, `dev` current."""
+    fn = getattr(_lib.load(), name)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != _lib.KDA_OK:
+        raise KdaError(st, name)
+
+
+def _rows(t, shape, dtypes, name):
+    """Checks a [T, C] array with dense rows; returns the elements between rows (0: one row or
+    dense)."""
+    if t.dim() != 2 or t.shape != shape or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {list(shape)} {' / '.join(str(d) for d in dtypes)}")
+    if shape[0] > 1 and shape[1] > 0:
+        if shape[1] > 1 and t.stride(1) != 1 or t.stride(0) < shape[1]:
+            raise ValueError(f"{name} must have dense rows")
+        return t.stride(0)
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have dense rows")
+    return 0
+
+
+def _dense(t, shape, dtype, name):
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}")
+
+
+def _linear_params(x, weight, activation, scale, y_dtype, flags):
+    if x.dim() != 2 or x.dtype not in _QKV_DTYPES:
+        raise ValueError("x must be [T, K] float32 or bfloat16")
+    if weight.dim() != 2:
+        raise ValueError("weight must be [N, K]")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}")
+    if y_dtype not in _QKV_DTYPES:
+        raise ValueError("the output dtype must be float32 or bfloat16")
+    (T, K), N = x.shape, weight.shape[0]
+    dt = _QKV_DTYPES[x.dtype]
+    return KdaLinearParams(
+        tokens=T, in_features=K, out_features=N, dtype=dt, y_dtype=_QKV_DTYPES[y_dtype],
+        residual_dtype=dt, dw_dtype=dt, activation=_ACTIVATIONS[activation], scale=scale,
+        x_row_stride=_rows(x, (T, K), (x.dtype,), "x"),
+        w_row_stride=_rows(weight, (N, K), (x.dtype,), "weight"), flags=flags)
+
+
+def _linear_workspace(p, backward, workspace, dev):
+    n = ctypes.c_size_t(0)
+    st = _lib.load().kda_linear_workspace_size(ctypes.byref(p), backward, ctypes.byref(n))
+    if st != _lib.KDA_OK:
+        raise KdaError(st, "kda_linear_workspace_size")
+    if n.value == 0:
+        return None, 0
+    workspace = _workspace(n.value, workspace, dev)
+    _device(workspace)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+@_on_stream
+def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
+           activation: str = "none", residual: Optional[torch.Tensor] = None, scale: float = 1.0,
+           out_dtype: Optional[torch.dtype] = None, save_pre_activation: bool = False,
+           cuda_cores: bool = False, out: Optional[torch.Tensor] = None,
+           workspace: Optional[torch.Tensor] = None):
+    """Projection with its epilogue (kda_linear_fwd): residual + scale * act(x weight^T + bias).
+
+    x [T, K] and weight [N, K] in one dtype (bfloat16: tensor cores, fp32 sums; float32: CUDA
+    cores), rows dense with any stride; bias [N] float32; residual [T, N] float32 or bfloat16.
+    `activation`: none, relu, silu, gelu (erf form) or sigmoid.  Returns y [T, N] in `out_dtype`
+    (default x's), or (y, z) with `save_pre_activation`, z [T, N] in x's dtype being what
+    `linear_bwd` needs as `pre_activation`.  `out` may be `residual` itself.
+    """
+    dev = _device(x, weight, bias, residual, out)
+    y_dtype = out.dtype if out is not None else (out_dtype or x.dtype)
+    if out is not None and out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("out does not have out_dtype")
+    p = _linear_params(x, weight, activation, scale, y_dtype,
+                       _lib.KDA_FLAG_CUDA_CORES if cuda_cores else 0)
+    T, N = x.shape[0], weight.shape[0]
+    if bias is not None:
+        _dense(bias, (N,), torch.float32, "bias")
+    if residual is not None:
+        p.residual_row_stride = _rows(residual, (T, N), tuple(_QKV_DTYPES), "residual")
+        p.residual_dtype = _QKV_DTYPES[residual.dtype]
+    if out is None:
+        out = torch.empty((T, N), dtype=y_dtype, device=dev)
+    else:
+        p.y_row_stride = _rows(out, (T, N), (y_dtype,), "out")
+    z = torch.empty((T, N), dtype=x.dtype, device=dev) if save_pre_activation else None
+    workspace, nbytes = _linear_workspace(p, 0, workspace, dev)
+    _call("kda_linear_fwd", dev, ctypes.byref(p), _p(x), _p(weight), _p(bias),
+          _p(residual), _p(out), _p(z), _p(workspace), nbytes)
+    return (out, z) if save_pre_activation else out
+
+
+@_on_stream
+def linear_bwd(x: torch.Tensor, weight: torch.Tensor, d_y: torch.Tensor, *,
+               activation: str = "none", pre_activation: Optional[torch.Tensor] = None,
+               scale: float = 1.0, need_dx: bool = True, need_dw: bool = True,
+               need_bias: bool = False, dw_dtype: Optional[torch.dtype] = None,
+               cuda_cores: bool = False, workspace: Optional[torch.Tensor] = None):
+    """Backward of `linear` (kda_linear_bwd).  d_y [T, N] float32 or bfloat16; `pre_activation`
+    as `linear` returned it (needed with an activation).  Returns (dx [T, K] in x's dtype,
+    dw [N, K] in `dw_dtype` (default x's), dbias [N] float32), None for those not needed.
+    The residual's gradient is d_y itself."""
+    dev = _device(x, weight, d_y, pre_activation)
+    if d_y.dtype not in _QKV_DTYPES:
+        raise ValueError("d_y must be float32 or bfloat16")
+    p = _linear_params(x, weight, activation, scale, d_y.dtype,
+                       _lib.KDA_FLAG_CUDA_CORES if cuda_cores else 0)
+    (T, K), N = x.shape, weight.shape[0]
+    p.y_row_stride = _rows(d_y, (T, N), (d_y.dtype,), "d_y")
+    if activation != "none":
+        if pre_activation is None:
+            raise ValueError("an activation's gradient needs pre_activation")
+        _dense(pre_activation, (T, N), x.dtype, "pre_activation")
+    dw_dtype = dw_dtype or x.dtype
+    if dw_dtype not in _QKV_DTYPES:
+        raise ValueError("dw_dtype must be float32 or bfloat16")
+    p.dw_dtype = _QKV_DTYPES[dw_dtype]
+    dx = torch.empty((T, K), dtype=x.dtype, device=dev) if need_dx else None
+    dw = torch.empty((N, K), dtype=dw_dtype, device=dev) if need_dw else None
+    dbias = torch.empty((N,), dtype=torch.float32, device=dev) if need_bias else None
+    workspace, nbytes = _linear_workspace(p, 1, workspace, dev)
+    _call("kda_linear_bwd", dev, ctypes.byref(p), _p(x), _p(weight),
+          _p(pre_activation) if activation != "none" else None, _p(d_y), _p(dx), _p(dw), _p(dbias),
+          _p(workspace), nbytes)
+    return dx, dw, dbias
+
+
+# ----------------------------------------------------------------------------------------- norms
+
+def _norm_gate(gate, x, p, N):
+    if gate is None:
+        return
+    if gate.dim() == 1:
+        _dense(gate, (N,), torch.float32, "a per-channel gate")
+    else:
+        p.gate_per_token = 1
+        p.gate_row_stride = _rows(gate, tuple(x.shape), (x.dtype,), "a per-token gate")
+
+
+def _norm_workspace(p, gated, workspace, dev):
+    n = ctypes.c_size_t(0)
+    st = _lib.load().kda_norm_workspace_size(ctypes.byref(p), gated, ctypes.byref(n))
+    if st != _lib.KDA_OK:
+        raise KdaError(st, "kda_norm_workspace_size")
+    workspace = _workspace(n.value, workspace, dev)
+    _device(workspace)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _residual_params(x, h_dtype, scale, eps):
+    if x.dim() != 2 or x.dtype not in _QKV_DTYPES or not x.is_contiguous():
+        raise ValueError("x must be contiguous [T, N] float32 or bfloat16")
+    dt = _QKV_DTYPES[x.dtype]
+    return KdaNormParams(tokens=x.shape[0], features=x.shape[1], x_dtype=dt,
+                         h_dtype=_QKV_DTYPES[h_dtype], y_dtype=dt, eps=eps, scale=scale)
+
+
+@_on_stream
+def residual_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
+                  residual: Optional[torch.Tensor] = None,
+                  post_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                  scale: float = 1.0, eps: float = 1e-6, out: Optional[torch.Tensor] = None,
+                  h_out: Optional[torch.Tensor] = None):
+    """The norms around a block in one pass (kda_residual_norm_fwd).  With
+    rms(a) = a / sqrt(mean(a^2) + eps) over each row:
+
+        u = rms(x) * post_weight (x without one);  h = residual + scale * gate * u;
+        y = rms(h) * weight
+
+    x [T, N]; residual [T, N] (float32 or bfloat16: h's dtype); gate [N] float32 or [T, N] in x's
+    dtype (row stride free); weights [N] float32.  Returns (y in x's dtype, or None without
+    `weight`; h in the residual's dtype, x's without one).  `h_out` may be `residual`.
+    """
+    dev = _device(x, weight, residual, post_weight, gate, out, h_out)
+    h_dtype = residual.dtype if residual is not None else x.dtype
+    if h_dtype not in _QKV_DTYPES:
+        raise ValueError("residual must be float32 or bfloat16")
+    p = _residual_params(x, h_dtype, scale, eps)
+    shape, N = x.shape, x.shape[1]
+    if residual is not None:
+        _dense(residual, shape, h_dtype, "residual")
+    for name, t in (("weight", weight), ("post_weight", post_weight)):
+        if t is not None:
+            _dense(t, (N,), torch.float32, name)
+    _norm_gate(gate, x, p, N)
+    if h_out is None:
+        h_out = torch.empty(shape, dtype=h_dtype, device=dev)
+    else:
+        _dense(h_out, shape, h_dtype, "h_out")
+    if weight is None:
+        if out is not None:
+            raise ValueError("out needs a weight")
+    elif out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=dev)
+    else:
+        _dense(out, shape, x.dtype, "out")
+    _call("kda_residual_norm_fwd", dev, ctypes.byref(p), _p(x), _p(residual), _p(gate),
+          _p(post_weight), _p(weight), _p(h_out), _p(out))
+    return out, h_out
+
+
+@_on_stream
+def residual_norm_bwd(x: torch.Tensor, h: torch.Tensor, weight: Optional[torch.Tensor],
+                      d_y: Optional[torch.Tensor], d_h: Optional[torch.Tensor] = None, *,
+                      post_weight: Optional[torch.Tensor] = None,
+                      gate: Optional[torch.Tensor] = None, scale: float = 1.0, eps: float = 1e-6,
+                      workspace: Optional[torch.Tensor] = None):
+    """Backward of `residual_norm` (kda_residual_norm_bwd).  h as the forward returned it; d_y
+    [T, N] in x's dtype (None exactly without `weight`) and d_h [T, N] in h's dtype (None: zero)
+    are the gradients of y and h.  Returns (dx, d_residual in h's dtype, d_weight, d_post_weight,
+    d_gate), None where the forward had no such argument (d_residual is always formed)."""
+    dev = _device(x, h, weight, d_y, d_h, post_weight, gate)
+    if h.dtype not in _QKV_DTYPES:
+        raise ValueError("h must be float32 or bfloat16")
+    p = _residual_params(x, h.dtype, scale, eps)
+    shape, N = x.shape, x.shape[1]
+    _dense(h, shape, h.dtype, "h")
+    if (weight is None) != (d_y is None):
+        raise ValueError("d_y and weight come together")
+    if d_y is None and d_h is None:
+        raise ValueError("one of d_y and d_h is needed")
+    if d_y is not None:
+        _dense(d_y, shape, x.dtype, "d_y")
+    if d_h is not None:
+        _dense(d_h, shape, h.dtype, "d_h")
+    for name, t in (("weight", weight), ("post_weight", post_weight)):
+        if t is not None:
+            _dense(t, (N,), torch.float32, name)
+    _norm_gate(gate, x, p, N)
+    dx = torch.empty_like(x)
+    d_residual = torch.empty_like(h)
+    f32 = dict(dtype=torch.float32, device=dev)
+    d_weight = torch.empty((N,), **f32) if weight is not None else None
+    d_post = torch.empty((N,), **f32) if post_weight is not None else None
+    d_gate = None
+    if gate is not None:
+        d_gate = torch.empty(gate.shape, dtype=gate.dtype, device=dev)
+    workspace, nbytes = _norm_workspace(p, 0, workspace, dev)
+    _call("kda_residual_norm_bwd", dev, ctypes.byref(p), _p(x), _p(h), _p(gate),
+          _p(post_weight), _p(weight), _p(d_y), _p(d_h), _p(dx), _p(d_residual), _p(d_gate),
+          _p(d_post), _p(d_weight), _p(workspace), nbytes)
+    return dx, d_residual, d_weight, d_post, d_gate
+
+
+def _gated_params(o, gate, weight, y_dtype, activation, eps):
+    if o.dim() != 3 or o.dtype not in _QKV_DTYPES or not o.is_contiguous():
+        raise ValueError("o must be contiguous [T, H, D] float32 or bfloat16")
+    T, H, D = o.shape
+    if gate.shape != o.shape or gate.dtype not in _QKV_DTYPES:
+        raise ValueError("gate must be [T, H, D] float32 or bfloat16")
+    if activation not in _NORM_GATES:
+        raise ValueError(f"activation must be one of {', '.join(_NORM_GATES)}")
+    if y_dtype not in _QKV_DTYPES:
+        raise ValueError("y must be float32 or bfloat16")
+    _dense(weight, (D,), torch.float32, "weight")
+    stride = 0
+    if T > 0:
+        if not gate[0].is_contiguous():
+            raise ValueError("gate must have dense (H, D) rows")
+        if T > 1:
+            stride = gate.stride(0)
+            if stride < H * D:
+                raise ValueError("gate's rows must not overlap")
+    return KdaNormParams(tokens=T, features=D, num_heads=H, x_dtype=_QKV_DTYPES[o.dtype],
+                         gate_dtype=_QKV_DTYPES[gate.dtype], y_dtype=_QKV_DTYPES[y_dtype],
+                         activation=_ACTIVATIONS[activation], eps=eps, scale=1.0,
+                         gate_row_stride=stride)
+
+
+@_on_stream
+def gated_norm(o: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, *,
+               activation: str = "sigmoid", eps: float = 1e-6,
+               out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The output norm of the recurrence (kda_gated_norm_fwd): the RMS norm of each token's and
+    head's o row, times weight [D], times act(gate).  o [T, H, D] as `prefill` and `decode_step`
+    return it; gate [T, H, D] in either dtype, a column block of a packed projection if need be;
+    `activation` of the gate: sigmoid, silu or none.  Returns y [T, H, D] (default the gate's
+    dtype), ready as [T, H * D] for the output projection."""
+    dev = _device(o, gate, weight, out)
+    y_dtype = out.dtype if out is not None else (out_dtype or gate.dtype)
+    p = _gated_params(o, gate, weight, y_dtype, activation, eps)
+    if out is None:
+        out = torch.empty(o.shape, dtype=y_dtype, device=dev)
+    else:
+        _dense(out, o.shape, out_dtype or out.dtype, "out")
+    _call("kda_gated_norm_fwd", dev, ctypes.byref(p), _p(o), _p(gate), _p(weight), _p(out))
+    return out
+
+
+@_on_stream
+def gated_norm_bwd(o: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, d_y: torch.Tensor, *,
+                   activation: str = "sigmoid", eps: float = 1e-6,
+                   workspace: Optional[torch.Tensor] = None):
+    """Backward of `gated_norm` (kda_gated_norm_bwd).  Returns (d_o in o's dtype -- `prefill_bwd`'s
+    d_o for the fp32 o of `prefill` --, d_gate dense in the gate's dtype, d_weight [D] float32)."""
+    dev = _device(o, gate, weight, d_y)
+    p = _gated_params(o, gate, weight, d_y.dtype, activation, eps)
+    _dense(d_y, o.shape, d_y.dtype, "d_y")
+    d_o = torch.empty_like(o)
+    d_gate = torch.empty(gate.shape, dtype=gate.dtype, device=dev)
+    d_weight = torch.empty(weight.shape, dtype=torch.float32, device=dev)
+    workspace, nbytes = _norm_workspace(p, 1, workspace, dev)
+    _call("kda_gated_norm_bwd", dev, ctypes.byref(p), _p(o), _p(gate), _p(weight), _p(d_y),
+          _p(d_o), _p(d_gate), _p(d_weight), _p(workspace), nbytes)
+    return d_o, d_gate, d_weight

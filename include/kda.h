@@ -455,6 +455,157 @@ kda_status_t kda_prefill_fwd_no_alloc(const kda_params_t *p, const void *q, cons
 int kda_prefill_no_alloc_form(const kda_params_t *p);
 
 /*
+ * The layer around the recurrence: the projections into the front end and out of the
+ * recurrence, the norms on both sides of a block, and the output norm with its gate.  All
+ * three read and write token-major rows; sums, norms and accumulators are fp32.  Work is
+ * enqueued on `stream`; zero tokens is a valid call (sums over no tokens are zero).
+ */
+typedef enum kda_activation {
+  KDA_ACT_NONE = 0,
+  KDA_ACT_RELU = 1,
+  KDA_ACT_SILU = 2,   /* z sigmoid(z) */
+  KDA_ACT_GELU = 3,   /* z Phi(z), Phi the normal distribution function (the erf form) */
+  KDA_ACT_SIGMOID = 4
+} kda_activation_t;
+
+typedef struct kda_linear_params {
+  int64_t tokens;       /* T: rows of x and y */
+  int32_t in_features;  /* K >= 1 */
+  int32_t out_features; /* N >= 1 */
+  int32_t dtype;          /* kda_dtype_t of x, w and pre_act (and of dx) */
+  int32_t y_dtype;        /* kda_dtype_t of y (backward: of d_y) */
+  int32_t residual_dtype; /* kda_dtype_t of residual (forward) */
+  int32_t dw_dtype;       /* kda_dtype_t of dw (backward) */
+  int32_t activation;     /* kda_activation_t */
+  float scale;            /* s; any finite value */
+  /* elements between rows; 0 means dense.  y_row_stride is y's, or d_y's in the backward. */
+  int64_t x_row_stride, w_row_stride, y_row_stride, residual_row_stride;
+  uint32_t flags;         /* 0 or KDA_FLAG_CUDA_CORES (fp32 arithmetic on CUDA cores) */
+} kda_linear_params_t;
+
+/*
+ * Projection with its epilogue:
+ *
+ *     z[t, n] = sum_k x[t, k] w[n, k] + bias[n]
+ *     y[t, n] = residual[t, n] + scale act(z[t, n])
+ *
+ *   x         [T, K]   w [N, K]     one dtype, aligned to their elements; any row stride
+ *   bias      [N] fp32 or NULL      residual [T, N] or NULL (may be y itself: same pointer,
+ *                                   dtype and stride)
+ *   y         [T, N], y_dtype       pre_act [T, N] dense, dtype, or NULL: receives z
+ *   workspace >= kda_linear_workspace_size(p, 0) bytes, 256-byte aligned (NULL when 0)
+ * bf16 operands are multiplied on tensor cores with fp32 accumulation.  Operands whose base
+ * or rows are not 16-byte aligned are first copied into aligned rows of the workspace.
+ */
+kda_status_t kda_linear_fwd(const kda_linear_params_t *p, const void *x, const void *w,
+                            const float *bias, const void *residual, void *y, void *pre_act,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Backward of kda_linear_fwd.  With dz = scale act'(z) d_y (z as the forward wrote it):
+ *
+ *     dx = dz w        dw = dz^T x        dbias = sum_t dz
+ *
+ * and d_residual = d_y, which needs no work.
+ *   d_y       [T, N], y_dtype       pre_act [T, N] dense, dtype (NULL with KDA_ACT_NONE)
+ *   dx        [T, K] dense, dtype, or NULL      dw [N, K] dense, dw_dtype, or NULL
+ *   dbias     [N] fp32 or NULL
+ *   workspace >= kda_linear_workspace_size(p, 1) bytes, 256-byte aligned
+ * With bf16 operands dz is rounded to bf16 (to nearest) before the two products, as the
+ * tensor cores read it; with KDA_ACT_NONE and a bf16 d_y the products read d_y itself and scale
+ * multiplies their fp32 sums.  dbias is summed from the unrounded dz.
+ */
+kda_status_t kda_linear_bwd(const kda_linear_params_t *p, const void *x, const void *w,
+                            const void *pre_act, const void *d_y, void *dx, void *dw, float *dbias,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of kda_linear_fwd (backward = 0) or kda_linear_bwd (backward = 1). */
+kda_status_t kda_linear_workspace_size(const kda_linear_params_t *p, int32_t backward,
+                                       size_t *bytes);
+
+typedef struct kda_norm_params {
+  int64_t tokens;         /* T */
+  int32_t features;       /* N of residual_norm (1..16384); head size D of gated_norm (1..1024) */
+  int32_t num_heads;      /* gated_norm: H >= 1; residual_norm: ignored */
+  int32_t x_dtype;        /* x, y, d_y, dx, a per-token gate; gated_norm: of o and d_o */
+  int32_t h_dtype;        /* residual_norm: residual, h, d_h, d_residual */
+  int32_t gate_dtype;     /* gated_norm: gate, d_gate; residual_norm: ignored */
+  int32_t y_dtype;        /* y, d_y */
+  int32_t gate_per_token; /* residual_norm: gate is [T, N] (nonzero) or [N] fp32 (zero) */
+  int32_t activation;     /* gated_norm: KDA_ACT_SIGMOID, KDA_ACT_SILU or KDA_ACT_NONE */
+  float eps;              /* > 0: added to the mean square */
+  float scale;            /* residual_norm: the residual scale s */
+  int64_t gate_row_stride; /* elements between tokens of a per-token gate; 0 means dense */
+} kda_norm_params_t;
+
+/*
+ * The norms around a block in one pass: the (optional) norm of the block's output, its gate and
+ * residual scale, the residual add, and the norm before the next block.  Per token, with
+ * rms(a) = a / sqrt(mean(a^2) + eps):
+ *
+ *     u = post_weight ? rms(x) post_weight : x
+ *     h = residual + scale gate u
+ *     y = rms(h) weight                                (from the fp32 h, before its rounding)
+ *
+ *   x [T, N], x_dtype               residual [T, N], h_dtype, or NULL (zero)
+ *   gate [N] fp32 or [T, N] x_dtype, or NULL (one)
+ *   post_weight, weight [N] fp32; post_weight may be NULL; weight and y may be NULL together
+ *   h [T, N], h_dtype, or NULL      y [T, N], y_dtype
+ * Rows are dense but a per-token gate's, aligned to their elements.  h may be residual, and y
+ * or h may be x, when the dtypes agree.
+ */
+kda_status_t kda_residual_norm_fwd(const kda_norm_params_t *p, const void *x, const void *residual,
+                                   const void *gate, const float *post_weight,
+                                   const float *weight, void *h, void *y, void *stream);
+
+/*
+ * Backward of kda_residual_norm_fwd, given h as the forward wrote it (or, without anything to
+ * add, x itself as h):
+ *
+ *     dh = d_h + rms'(h)^T (d_y weight)     d_residual = dh      d_weight = sum_t d_y rms(h)
+ *     du = scale gate dh                    d_gate = scale u dh  (summed over t for [N])
+ *     dx = post_weight ? rms'(x)^T (du post_weight) : du         d_post_weight = sum_t du rms(x)
+ *
+ *   d_y [T, N], y_dtype, or NULL with weight = NULL; d_h [T, N], h_dtype, or NULL (zero)
+ *   dx [T, N], x_dtype        d_residual [T, N], h_dtype, or NULL (may be d_h)
+ *   d_gate like gate          d_weight, d_post_weight [N] fp32
+ *   (d_gate, d_weight, d_post_weight: needed when gate, weight, post_weight are given)
+ *   workspace >= kda_norm_workspace_size bytes, 256-byte aligned
+ * The sums over tokens are formed in a fixed order: repeated calls give the same bits.
+ */
+kda_status_t kda_residual_norm_bwd(const kda_norm_params_t *p, const void *x, const void *h,
+                                   const void *gate, const float *post_weight,
+                                   const float *weight, const void *d_y, const void *d_h, void *dx,
+                                   void *d_residual, void *d_gate, float *d_post_weight,
+                                   float *d_weight, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/*
+ * The output norm of the recurrence: per token and head
+ *
+ *     y[t, h] = rms(o[t, h]) weight act(gate[t, h])
+ *
+ *   o [T, H, D], x_dtype (fp32 as kda_prefill_fwd writes it)
+ *   gate [T, H, D], gate_dtype, rows of H * D elements gate_row_stride apart
+ *   weight [D] fp32      y [T, H, D], y_dtype
+ */
+kda_status_t kda_gated_norm_fwd(const kda_norm_params_t *p, const void *o, const void *gate,
+                                const float *weight, void *y, void *stream);
+
+/*
+ * Backward of kda_gated_norm_fwd: d_o [T, H, D] x_dtype (fp32: what kda_prefill_bwd takes as
+ * d_o), d_gate [T, H, D] dense, gate_dtype, d_weight [D] fp32 (in a fixed order).
+ * workspace >= kda_norm_workspace_size bytes, 256-byte aligned.
+ */
+kda_status_t kda_gated_norm_bwd(const kda_norm_params_t *p, const void *o, const void *gate,
+                                const float *weight, const void *d_y, void *d_o, void *d_gate,
+                                float *d_weight, void *workspace, size_t workspace_bytes,
+                                void *stream);
+
+/* Workspace bytes of kda_residual_norm_bwd (gated = 0) or kda_gated_norm_bwd (gated = 1). */
+kda_status_t kda_norm_workspace_size(const kda_norm_params_t *p, int32_t gated, size_t *bytes);
+
+/*
  * Measurement aid (no counterpart on the pages).  Registers up to 8 CUDA events
  * (cudaEvent_t handles passed as void*, created by the caller) that later
  * kda_prefill_fwd / kda_decode_step calls on this process record on their
