@@ -22,6 +22,9 @@ KDA_FLAG_CHECKED = 1
 KDA_FLAG_CUDA_CORES = 2
 KDA_FLAG_COMPACT = 4
 KDA_FLAG_NO_DELTA = 8
+KDA_FLAG_UNALIGNED_X = 16
+KDA_FLAG_UNALIGNED_W = 32
+KDA_FLAG_UNALIGNED_DY = 64
 
 KDA_DEVERR_NONE = 0
 KDA_DEVERR_OFFSETS = 1

@@ -50,13 +50,24 @@ bool stride_ok(int64_t stride, int64_t cols, int64_t rows) {
   return s >= cols && s <= (int64_t{1} << 40) && rows <= (int64_t{1} << 60) / s;
 }
 
+constexpr uint32_t kLinearFlags =
+    KDA_FLAG_CUDA_CORES | KDA_FLAG_UNALIGNED_X | KDA_FLAG_UNALIGNED_W | KDA_FLAG_UNALIGNED_DY;
+
+// A bf16 operand that the tensor cores read: 16-byte aligned unless its flag announces a copy
+// (rows that are not a multiple of 8 elements apart are copied anyway).
+bool operand_ok(const kda_linear_params_t* p, const void* base, int64_t stride, uint32_t flag) {
+  if (!elem_aligned(base, p->dtype)) return false;
+  if (p->dtype != KDA_DTYPE_BF16 || (p->flags & (KDA_FLAG_CUDA_CORES | flag)) || stride % 8) return true;
+  return reinterpret_cast<uintptr_t>(base) % 16 == 0;
+}
+
 kda_status_t check_linear(const kda_linear_params_t* p) {
   if (!p) return KDA_ERR_INVALID_ARG;
   if (p->tokens < 0 || p->in_features < 1 || p->out_features < 1) return KDA_ERR_INVALID_ARG;
   if (!is_dtype(p->dtype) || !is_dtype(p->y_dtype) || !is_dtype(p->residual_dtype) || !is_dtype(p->dw_dtype))
     return KDA_ERR_INVALID_ARG;
   if (p->activation < KDA_ACT_NONE || p->activation > KDA_ACT_SIGMOID) return KDA_ERR_INVALID_ARG;
-  if (!isfinite(p->scale) || (p->flags & ~KDA_FLAG_CUDA_CORES)) return KDA_ERR_INVALID_ARG;
+  if (!isfinite(p->scale) || (p->flags & ~kLinearFlags)) return KDA_ERR_INVALID_ARG;
   const int64_t T = p->tokens, K = p->in_features, N = p->out_features;
   if (!stride_ok(p->x_row_stride, K, T) || !stride_ok(p->w_row_stride, K, N) ||
       !stride_ok(p->y_row_stride, N, T) || !stride_ok(p->residual_row_stride, N, T))
@@ -111,8 +122,10 @@ kda_status_t kda_linear_fwd(const kda_linear_params_t* p, const void* x, const v
   if (s != KDA_OK) return s;
   if (p->tokens == 0) return KDA_OK;
   if (!x || !w || !y) return KDA_ERR_INVALID_ARG;
-  if (!elem_aligned(x, p->dtype) || !elem_aligned(w, p->dtype) || !elem_aligned(pre_act, p->dtype) ||
-      !elem_aligned(y, p->y_dtype) || !elem_aligned(residual, p->residual_dtype) || !f32_aligned(bias))
+  const int64_t K = p->in_features;
+  if (!operand_ok(p, x, p->x_row_stride ? p->x_row_stride : K, KDA_FLAG_UNALIGNED_X) ||
+      !operand_ok(p, w, p->w_row_stride ? p->w_row_stride : K, KDA_FLAG_UNALIGNED_W) ||
+      !elem_aligned(pre_act, p->dtype) || !elem_aligned(y, p->y_dtype) || !elem_aligned(residual, p->residual_dtype) || !f32_aligned(bias))
     return KDA_ERR_INVALID_ARG;
   if (!workspace_ok(workspace, workspace_bytes, kda::linear_workspace_bytes(*p, false))) return KDA_ERR_WORKSPACE;
   int32_t* err = kda::layer_error_word();
@@ -128,8 +141,12 @@ kda_status_t kda_linear_bwd(const kda_linear_params_t* p, const void* x, const v
   if (s != KDA_OK) return s;
   if (p->tokens > 0 && (!d_y || (dx && !w) || (dw && !x))) return KDA_ERR_INVALID_ARG;
   if (p->tokens > 0 && p->activation != KDA_ACT_NONE && !pre_act) return KDA_ERR_INVALID_ARG;
-  if (!elem_aligned(x, p->dtype) || !elem_aligned(w, p->dtype) || !elem_aligned(pre_act, p->dtype) ||
-      !elem_aligned(d_y, p->y_dtype) || !elem_aligned(dx, p->dtype) || !elem_aligned(dw, p->dw_dtype) ||
+  const int64_t K = p->in_features, N = p->out_features;
+  if (!operand_ok(p, x, p->x_row_stride ? p->x_row_stride : K, KDA_FLAG_UNALIGNED_X) ||
+      !operand_ok(p, w, p->w_row_stride ? p->w_row_stride : K, KDA_FLAG_UNALIGNED_W) ||
+      !elem_aligned(pre_act, p->dtype) || !elem_aligned(d_y, p->y_dtype) ||
+      (p->activation == KDA_ACT_NONE && p->y_dtype == p->dtype &&
+       !operand_ok(p, d_y, p->y_row_stride ? p->y_row_stride : N, KDA_FLAG_UNALIGNED_DY)) || !elem_aligned(dx, p->dtype) || !elem_aligned(dw, p->dw_dtype) ||
       !f32_aligned(dbias))
     return KDA_ERR_INVALID_ARG;
   if (!workspace_ok(workspace, workspace_bytes, kda::linear_workspace_bytes(*p, true))) return KDA_ERR_WORKSPACE;

@@ -201,24 +201,40 @@ static cudaError_t launch_dz(const DzArgs& A, bool dybf, bool zbf, cudaStream_t 
 static int64_t or_dense(int64_t stride, int64_t dense) { return stride ? stride : dense; }
 static size_t up256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 
-// The gradient of the epilogue has to be formed unless the products can read d_y itself.
-static bool needs_dz(const kda_linear_params_t& p) {
-  return p.activation != KDA_ACT_NONE || p.y_dtype != p.dtype;
-}
-
+// What a call keeps in the workspace (offsets; kNone: nothing).  The tensor cores read aligned
+// bf16 rows: bf16 operands as they are where their rows and base are 16-byte aligned, else a
+// copy; fp32 operands always as three planes of parts.
+constexpr size_t kNone = ~static_cast<size_t>(0);
 struct LinearLayout {
-  size_t part, dz, total;
+  bool tc;
+  size_t part, dz, x, w, dz_planes, total;
   int64_t dz_ld;
 };
 static LinearLayout linear_layout(const kda_linear_params_t& p, bool bwd) {
+  const int64_t T = p.tokens, K = p.in_features, N = p.out_features;
+  const bool bf = p.dtype == KDA_DTYPE_BF16;
   LinearLayout L{};
+  L.tc = !(p.flags & KDA_FLAG_CUDA_CORES);
   size_t at = 0;
+  auto take = [&](bool yes, size_t bytes) {
+    if (!yes) return kNone;
+    const size_t here = at;
+    at = up256(at + bytes);
+    return here;
+  };
+  L.x = take(L.tc && (!bf || (p.flags & KDA_FLAG_UNALIGNED_X) || or_dense(p.x_row_stride, K) % 8),
+             repacked_bytes(T, K, bf));
+  L.w = take(L.tc && (!bf || (p.flags & KDA_FLAG_UNALIGNED_W) || or_dense(p.w_row_stride, K) % 8),
+             repacked_bytes(N, K, bf));
+  L.dz = L.part = L.dz_planes = kNone;
   if (bwd) {
-    L.part = at;
-    at = up256(at + static_cast<size_t>(dz_rows(p.tokens, p.out_features)) * p.out_features * 4);
-    L.dz_ld = (p.out_features + 7) / 8 * 8;
-    L.dz = at;
-    if (needs_dz(p)) at = up256(at + static_cast<size_t>(p.tokens) * L.dz_ld * dtype_bytes(p.dtype));
+    L.part = take(true, static_cast<size_t>(dz_rows(T, p.out_features)) * N * 4);
+    // dz is formed unless the products can read d_y itself
+    const bool unaligned = L.tc && bf && ((p.flags & KDA_FLAG_UNALIGNED_DY) || or_dense(p.y_row_stride, N) % 8);
+    L.dz_ld = (N + 7) / 8 * 8;
+    L.dz = take(p.activation != KDA_ACT_NONE || p.y_dtype != p.dtype || unaligned,
+                static_cast<size_t>(T) * L.dz_ld * dtype_bytes(p.dtype));
+    L.dz_planes = take(L.tc && !bf, repacked_bytes(T, N, false));
   }
   L.total = at;
   return L;
@@ -226,35 +242,50 @@ static LinearLayout linear_layout(const kda_linear_params_t& p, bool bwd) {
 
 size_t linear_workspace_bytes(const kda_linear_params_t& p, bool bwd) { return linear_layout(p, bwd).total; }
 
-static cudaError_t run_gemm(const Gemm& g, cudaStream_t st) { return launch_gemm_simt(g, st); }
+// The operand as the product reads it: copied into the workspace where the layout says so.
+static cudaError_t stage(GemmOperand* X, size_t at, char* ws, int64_t rows, int64_t cols, bool bf16, cudaStream_t st) {
+  if (at == kNone) return cudaSuccess;
+  const cudaError_t e = launch_repack(X->p, X->ld, rows, cols, bf16, ws + at, st);
+  X->p = ws + at;
+  X->ld = (cols + 7) / 8 * 8;
+  return e;
+}
+
+static cudaError_t run_gemm(const Gemm& g, bool tc, cudaStream_t st) {
+  return tc && g.C > 0 ? launch_gemm_tc(g, g.bf16 ? 1 : 3, st) : launch_gemm_simt(g, st);
+}
 
 cudaError_t launch_linear_fwd(const kda_linear_params_t& p, const void* x, const void* w, const float* bias,
                               const void* res, void* y, void* z, void* workspace, int32_t* err,
                               cudaStream_t st) {
-  (void)workspace;
   const int64_t T = p.tokens, K = p.in_features, N = p.out_features;
   if (T == 0) return cudaSuccess;
+  const LinearLayout L = linear_layout(p, false);
+  char* ws = static_cast<char*>(workspace);
+  cudaError_t e;
   Gemm g{};
+  g.bf16 = p.dtype == KDA_DTYPE_BF16;
   g.A = {w, or_dense(p.w_row_stride, K), false};
   g.B = {x, or_dense(p.x_row_stride, K), false};
+  if ((e = stage(&g.A, L.w, ws, N, K, g.bf16, st)) != cudaSuccess) return e;
+  if ((e = stage(&g.B, L.x, ws, T, K, g.bf16, st)) != cudaSuccess) return e;
   g.I = N; g.J = T; g.C = K;
-  g.bf16 = p.dtype == KDA_DTYPE_BF16;
   g.epi = {bias, res, y, z, or_dense(p.residual_row_stride, N), or_dense(p.y_row_stride, N), N, p.scale,
            p.activation, p.residual_dtype == KDA_DTYPE_BF16, p.y_dtype == KDA_DTYPE_BF16, g.bf16};
   g.err = err;
-  return run_gemm(g, st);
+  return run_gemm(g, L.tc, st);
 }
 
 cudaError_t launch_linear_bwd(const kda_linear_params_t& p, const void* x, const void* w, const void* z,
                               const void* dy, void* dx, void* dw, float* dbias, void* workspace,
                               int32_t* err, cudaStream_t st) {
   const int64_t T = p.tokens, K = p.in_features, N = p.out_features;
-  const bool bf = p.dtype == KDA_DTYPE_BF16;
+  const bool bf = p.dtype == KDA_DTYPE_BF16, any = T > 0;
   const LinearLayout L = linear_layout(p, true);
   char* ws = static_cast<char*>(workspace);
   GemmOperand dz{dy, or_dense(p.y_row_stride, N), false};
   cudaError_t e;
-  const bool form = needs_dz(p) && (dx || dw) && T > 0;
+  const bool form = L.dz != kNone && (dx || dw) && any;
   if (form || dbias) {
     DzArgs A{};
     A.dy = dy; A.z = p.activation != KDA_ACT_NONE ? z : nullptr;
@@ -267,23 +298,27 @@ cudaError_t launch_linear_bwd(const kda_linear_params_t& p, const void* x, const
       return e;
     if (form) dz = {ws + L.dz, L.dz_ld, false};
   }
+  if (any && (dx || dw) && (e = stage(&dz, L.dz_planes, ws, T, N, bf, st)) != cudaSuccess) return e;
   Gemm g{};
   g.bf16 = bf;
   g.err = err;
-  if (dx && T > 0) {
+  g.epi = {nullptr, nullptr, nullptr, nullptr, 0, K, 0, p.scale, KDA_ACT_NONE, false, bf, false};
+  if (dx && any) {
     g.A = {w, or_dense(p.w_row_stride, K), true};
+    if ((e = stage(&g.A, L.w, ws, N, K, bf, st)) != cudaSuccess) return e;
     g.B = dz;
     g.I = K; g.J = T; g.C = N;
-    g.epi = {nullptr, nullptr, dx, nullptr, 0, K, 0, p.scale, KDA_ACT_NONE, false, bf, false};
-    if ((e = run_gemm(g, st)) != cudaSuccess) return e;
+    g.epi.out = dx;
+    if ((e = run_gemm(g, L.tc, st)) != cudaSuccess) return e;
   }
   if (dw) {
     g.A = {x, or_dense(p.x_row_stride, K), true};
+    if (any && (e = stage(&g.A, L.x, ws, T, K, bf, st)) != cudaSuccess) return e;
     g.B = {dz.p, dz.ld, true};
     g.I = K; g.J = N; g.C = T;
-    g.epi = {nullptr, nullptr, dw, nullptr, 0, K, 0, p.scale, KDA_ACT_NONE, false,
-             p.dw_dtype == KDA_DTYPE_BF16, false};
-    if ((e = run_gemm(g, st)) != cudaSuccess) return e;
+    g.epi.out = dw;
+    g.epi.out_bf = p.dw_dtype == KDA_DTYPE_BF16;
+    if ((e = run_gemm(g, L.tc, st)) != cudaSuccess) return e;
   }
   return cudaSuccess;
 }

@@ -100,7 +100,13 @@ def _linear_params(x, weight, activation, scale, y_dtype, flags):
         tokens=T, in_features=K, out_features=N, dtype=dt, y_dtype=_QKV_DTYPES[y_dtype],
         residual_dtype=dt, dw_dtype=dt, activation=_ACTIVATIONS[activation], scale=scale,
         x_row_stride=_rows(x, (T, K), (x.dtype,), "x"),
-        w_row_stride=_rows(weight, (N, K), (x.dtype,), "weight"), flags=flags)
+        w_row_stride=_rows(weight, (N, K), (x.dtype,), "weight"),
+        flags=flags | _unaligned(x, _lib.KDA_FLAG_UNALIGNED_X)
+        | _unaligned(weight, _lib.KDA_FLAG_UNALIGNED_W))
+
+
+def _unaligned(t, flag):
+    return flag if t.data_ptr() % 16 else 0
 
 
 def _linear_workspace(p, backward, workspace, dev):
@@ -123,8 +129,8 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
            workspace: Optional[torch.Tensor] = None):
     """Projection with its epilogue (kda_linear_fwd): residual + scale * act(x weight^T + bias).
 
-    x [T, K] and weight [N, K] in one dtype (bfloat16: tensor cores, fp32 sums; float32: CUDA
-    cores), rows dense with any stride; bias [N] float32; residual [T, N] float32 or bfloat16.
+    x [T, K] and weight [N, K] in one dtype, rows dense with any stride (tensor cores with fp32
+    sums; float32 as three bfloat16 parts; `cuda_cores=True`: fp32 CUDA cores); bias [N] float32; residual [T, N] float32 or bfloat16.
     `activation`: none, relu, silu, gelu (erf form) or sigmoid.  Returns y [T, N] in `out_dtype`
     (default x's), or (y, z) with `save_pre_activation`, z [T, N] in x's dtype being what
     `linear_bwd` needs as `pre_activation`.  `out` may be `residual` itself.
@@ -169,6 +175,7 @@ def linear_bwd(x: torch.Tensor, weight: torch.Tensor, d_y: torch.Tensor, *,
                        _lib.KDA_FLAG_CUDA_CORES if cuda_cores else 0)
     (T, K), N = x.shape, weight.shape[0]
     p.y_row_stride = _rows(d_y, (T, N), (d_y.dtype,), "d_y")
+    p.flags |= _unaligned(d_y, _lib.KDA_FLAG_UNALIGNED_DY)
     if activation != "none":
         if pre_activation is None:
             raise ValueError("an activation's gradient needs pre_activation")

@@ -468,6 +468,13 @@ typedef enum kda_activation {
   KDA_ACT_SIGMOID = 4
 } kda_activation_t;
 
+/* kda_linear_*: the base of x, w or d_y is not 16-byte aligned (a column block at an odd
+ * offset).  Adds an aligned copy of that bf16 operand to the workspace; without it an unaligned
+ * base is KDA_ERR_INVALID_ARG.  Rows that are not a multiple of 16 bytes apart need no flag. */
+#define KDA_FLAG_UNALIGNED_X 16u
+#define KDA_FLAG_UNALIGNED_W 32u
+#define KDA_FLAG_UNALIGNED_DY 64u
+
 typedef struct kda_linear_params {
   int64_t tokens;       /* T: rows of x and y */
   int32_t in_features;  /* K >= 1 */
@@ -480,7 +487,7 @@ typedef struct kda_linear_params {
   float scale;            /* s; any finite value */
   /* elements between rows; 0 means dense.  y_row_stride is y's, or d_y's in the backward. */
   int64_t x_row_stride, w_row_stride, y_row_stride, residual_row_stride;
-  uint32_t flags;         /* 0 or KDA_FLAG_CUDA_CORES (fp32 arithmetic on CUDA cores) */
+  uint32_t flags;         /* KDA_FLAG_CUDA_CORES (fp32 arithmetic on CUDA cores), KDA_FLAG_UNALIGNED_* */
 } kda_linear_params_t;
 
 /*
@@ -494,8 +501,10 @@ typedef struct kda_linear_params {
  *                                   dtype and stride)
  *   y         [T, N], y_dtype       pre_act [T, N] dense, dtype, or NULL: receives z
  *   workspace >= kda_linear_workspace_size(p, 0) bytes, 256-byte aligned (NULL when 0)
- * bf16 operands are multiplied on tensor cores with fp32 accumulation.  Operands whose base
- * or rows are not 16-byte aligned are first copied into aligned rows of the workspace.
+ * bf16 operands are multiplied on tensor cores with fp32 accumulation; those whose base or rows
+ * are not 16-byte aligned are first copied into aligned rows of the workspace.  fp32 operands
+ * are split into three bf16 parts in the workspace (24 bits in all), whose six leading products
+ * the tensor cores sum in fp32.  KDA_FLAG_CUDA_CORES multiplies in fp32 on CUDA cores instead.
  */
 kda_status_t kda_linear_fwd(const kda_linear_params_t *p, const void *x, const void *w,
                             const float *bias, const void *residual, void *y, void *pre_act,

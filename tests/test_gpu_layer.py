@@ -122,6 +122,13 @@ def test_linear_shapes(T, K, N, dtype):
     linear_case(1, T, K, N, dtype, bias=True)
 
 
+@pytest.mark.parametrize("T,K,N", [(1664, 1600, 1664), (1700, 1540, 1603)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_linear_pair_tiles(T, K, N, dtype):
+    """Products of enough 256 x 256 tiles for the persistent kernel, with ragged edges."""
+    linear_case(9, T, K, N, dtype, act="silu", bias=True, res=dtype)
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "sigmoid"])
 @pytest.mark.parametrize("dtype,y,res", [("bf16", "bf16", "bf16"), ("bf16", "f32", "f32"),
                                          ("f32", "f32", "f32"), ("f32", "bf16", "bf16"),
