@@ -92,6 +92,13 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t sdst, const void* map,
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+// Tiled TMA store of one box from shared memory (tracked by the issuing thread's bulk groups);
+// rows and columns past the map's extents are not written.
+__device__ __forceinline__ void tma_store_2d(const void* map, uint32_t ssrc, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
+               "r"(x), "r"(y), "r"(ssrc)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(dst)),
                "r"(ncols)
@@ -121,9 +128,17 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
 
 // ------------------------------------------------------------------ shared pieces
 
+// Tensor maps of the output side: boxes of 128 columns (i) x `rows` rows (j), not swizzled.
+struct OutMaps {
+  CUtensorMap y, z, res;
+};
+
 struct TcArgs {
   GemmEpilogue epi;
   int64_t I, J;
+  bool staged;              // y (and z) leave through shared memory and TMA
+  bool res_staged;          // the residual arrives that way too (it has y's type)
+  int32_t cols;             // pair kernel: columns (j) of a staged chunk
   int32_t kblocks;          // 64-wide steps over c
   int32_t iters;            // kblocks times the products of parts
   int32_t tiles_i, tiles_j;
@@ -147,11 +162,14 @@ __device__ __forceinline__ void part_of(int iters, int kblocks, int it, int& kb,
 // the CTA has.
 template <typename TryWait>
 __device__ __forceinline__ bool wait_bounded(TryWait try_wait, volatile int* abort) {
-  if (try_wait()) return true;
-  const unsigned long long start = now_ns();
-  for (uint32_t i = 1; i < kWaitLimit; ++i) {
+  unsigned long long start = 0;
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
     if (try_wait()) return true;
-    if ((i & 63) == 0 && (*abort || now_ns() - start > kWaitNs)) return false;
+    if ((i & 63) == 63) {
+      const unsigned long long t = now_ns();
+      if (start == 0) start = t;
+      if (*abort || t - start > kWaitNs) return false;
+    }
   }
   return false;
 }
@@ -167,6 +185,19 @@ __device__ __forceinline__ void drain_phase(uint64_t* bar, uint32_t parity) {
   int never = 0;
   wait_phase(bar, parity, &never);
 }
+
+// A position in a ring of N stages and the parity of the pass over it.
+template <int N>
+struct Ring {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == N) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
+};
 
 // Descriptor of 128 (or BN) operand rows staged at `saddr`.  K-major: 8-row groups of 1024 bytes.
 // MN-major: boxes of 64 rows of i (or j) by 64 steps of c, 8192 bytes apart; 8 steps of c are
@@ -191,23 +222,23 @@ __device__ __forceinline__ void load_operand(uint32_t sdst, int64_t r0, int c0, 
   }
 }
 
-// 16 columns (rows j0 .. j0 + 15 of the output) of this thread's element i
-__device__ __forceinline__ void store16(const GemmEpilogue& E, const uint32_t (&r)[16], float bias, int64_t i,
-                                        bool in, int64_t j0, int64_t J) {
-  if (!in || j0 >= J) return;
-  const int n = static_cast<int>(J - j0 < 16 ? J - j0 : 16);
-  float v[16], res[16];
-  if (E.res) {
+// 16 columns (rows j0 .. j0 + n - 1 of the output, n <= 16) of this thread's element i, stored
+// directly: any alignment.  Every load is issued before the first is used.
+template <bool BF>
+__device__ __forceinline__ void gather16(const void* p, int64_t ld, int64_t at, int n, float (&x)[16]) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) res[e] = e < n ? ld_any(E.res, E.res_bf, (j0 + e) * E.res_ld + i) : 0.f;
-  }
+  for (int e = 0; e < 16; ++e) x[e] = e < n ? load_elem<BF>(p, at + e * ld) : 0.f;
+}
+template <bool BF>
+__device__ __forceinline__ void scatter16(void* p, int64_t ld, int64_t at, int n, const float (&x)[16]) {
 #pragma unroll
-  for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(r[e]) + bias;
-  if (E.z) {
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-      if (e < n) st_any(E.z, E.z_bf, (j0 + e) * E.z_ld + i, v[e]);
-  }
+  for (int e = 0; e < 16; ++e)
+    if (e < n) {
+      if constexpr (BF) static_cast<uint16_t*>(p)[at + e * ld] = f32_to_bf16_bits(x[e]);
+      else static_cast<float*>(p)[at + e * ld] = x[e];
+    }
+}
+__device__ __forceinline__ void activate16(const GemmEpilogue& E, float (&v)[16]) {
   if (E.act != KDA_ACT_NONE) {
     if (E.out_bf) {
 #pragma unroll
@@ -219,29 +250,68 @@ __device__ __forceinline__ void store16(const GemmEpilogue& E, const uint32_t (&
   }
 #pragma unroll
   for (int e = 0; e < 16; ++e) v[e] *= E.scale;
+}
+__device__ __forceinline__ void store16(const GemmEpilogue& E, float (&v)[16], int64_t i, int64_t j0, int64_t J) {
+  const int n = static_cast<int>(J - j0 < 16 ? J - j0 : 16);
+  float res[16];
+  if (E.res) {
+    if (E.res_bf) gather16<true>(E.res, E.res_ld, j0 * E.res_ld + i, n, res);
+    else gather16<false>(E.res, E.res_ld, j0 * E.res_ld + i, n, res);
+  }
+  if (E.z) {
+    if (E.z_bf) scatter16<true>(E.z, E.z_ld, j0 * E.z_ld + i, n, v);
+    else scatter16<false>(E.z, E.z_ld, j0 * E.z_ld + i, n, v);
+  }
+  activate16(E, v);
   if (E.res) {
 #pragma unroll
     for (int e = 0; e < 16; ++e) v[e] += res[e];
   }
-  if (E.out_bf) {
-    uint16_t* o = static_cast<uint16_t*>(E.out) + j0 * E.out_ld + i;
+  if (E.out_bf) scatter16<true>(E.out, E.out_ld, j0 * E.out_ld + i, n, v);
+  else scatter16<false>(E.out, E.out_ld, j0 * E.out_ld + i, n, v);
+}
+__device__ __forceinline__ void load16(uint32_t src, float bias, float (&v)[16]) {
+  uint32_t r[16];
+  tc::tmem_ld16(src, r);
+  tc::tmem_wait_ld();
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-      if (e < n) o[e * E.out_ld] = f32_to_bf16_bits(v[e]);
+  for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(r[e]) + bias;
+}
+
+// 16 columns of a staged [column][128] tile at `at` (this thread's element of its first column);
+// the residual, if it is staged, lies where the result goes
+template <bool BF>
+__device__ __forceinline__ void put16(unsigned char* at, bool add, const float (&v)[16]) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    if constexpr (BF) {
+      uint16_t* p = reinterpret_cast<uint16_t*>(at + e * 256);
+      *p = f32_to_bf16_bits(add ? v[e] + bf16_bits_to_f32(*p) : v[e]);
+    } else {
+      float* p = reinterpret_cast<float*>(at + e * 512);
+      *p = add ? v[e] + *p : v[e];
+    }
+  }
+}
+__device__ __forceinline__ void put16(unsigned char* tile, bool bf, int col, int row, bool add, const float (&v)[16]) {
+  if (bf) {
+    unsigned char* at = tile + col * 256 + row * 2;
+    if (add) put16<true>(at, true, v);
+    else put16<true>(at, false, v);
   } else {
-    float* o = static_cast<float*>(E.out) + j0 * E.out_ld + i;
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-      if (e < n) o[e * E.out_ld] = v[e];
+    unsigned char* at = tile + col * 512 + row * 4;
+    if (add) put16<false>(at, true, v);
+    else put16<false>(at, false, v);
   }
 }
 
 // ------------------------------------------------------------------ pairs of CTAs, 256 x 256 tiles
 
 constexpr int kPairStages = 6;
-constexpr int kPairThreads = 384;                  // TMA, MMA, TMEM, idle, 8 epilogue warps
+constexpr int kPairThreads = 384;                  // TMA, MMA, 2 output warps, 8 epilogue warps
 constexpr uint32_t kPairStage = 2 * kOpBytes;
-constexpr size_t kPairSmem = kPairStages * kPairStage + 1024;
+constexpr uint32_t kSlot = 8192;                   // a staged chunk: 128 x 32 bf16 or 128 x 16 fp32
+constexpr size_t kPairSmem = kPairStages * kPairStage + 4 * kSlot + 1024;
 constexpr int kRaster = 8;                         // i tiles taken together, for reuse in L2
 
 // Tile t of the persistent order: groups of kRaster i tiles, j slowest inside a group, so that
@@ -254,12 +324,49 @@ __device__ __forceinline__ void tile_of(int t, int tiles_i, int tiles_j, int& ti
   ti = grp * kRaster + in - tj * width;
 }
 
+// The chunks of one half (128 columns) of this CTA's tiles, in the order the epilogue forms them:
+// per `cols` columns the pre-activation (if it is kept), then y.
+struct Chunk {
+  int t, c;
+  bool z;
+  int64_t i0, j0;
+  __device__ __forceinline__ void place(const TcArgs& A, uint32_t rank, int half, int tiles, int step) {
+    for (; t < tiles; t += step) {
+      int ti, tj;
+      tile_of(t, A.tiles_i, A.tiles_j, ti, tj);
+      i0 = static_cast<int64_t>(ti) * 256 + rank * 128;
+      j0 = static_cast<int64_t>(tj) * 256 + half * 128;
+      if (i0 < A.I && j0 < A.J) return;
+    }
+  }
+  __device__ __forceinline__ void start(const TcArgs& A, uint32_t rank, int half, int first, int tiles, int step) {
+    t = first;
+    c = 0;
+    z = A.epi.z != nullptr;
+    place(A, rank, half, tiles, step);
+  }
+  __device__ __forceinline__ void next(const TcArgs& A, uint32_t rank, int half, int tiles, int step) {
+    if (z) {
+      z = false;
+      return;
+    }
+    z = A.epi.z != nullptr;
+    c += A.cols;
+    if (c >= 128 || j0 + c >= A.J) {
+      c = 0;
+      t += step;
+      place(A, rank, half, tiles, step);
+    }
+  }
+};
+
 template <bool AMN, bool BMN>
 __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
 gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                 const TcArgs A) {
+                 const __grid_constant__ OutMaps maps, const __grid_constant__ TcArgs A) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[kPairStages], empty[kPairStages], acc_full[2], acc_empty[2], drain;
+  __shared__ __align__(8) uint64_t ready[2][2], written[2][2];   // [half][slot] of the staged chunks
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   const uint32_t smem = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -276,6 +383,10 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&acc_full[b], 1);
       tc::mbar_init(&acc_empty[b], 16);            // 8 epilogue warps of both CTAs
+      for (int h = 0; h < 2; ++h) {
+        tc::mbar_init(&ready[h][b], 1);
+        tc::mbar_init(&written[h][b], 128);
+      }
     }
     tc::mbar_init(&drain, 1);
     tc::fence_mbar_init();
@@ -290,23 +401,25 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
 
   if (warp == 0) {
     if (lane == 0) {                               // both CTAs: stage this CTA's rows of A and B
-      int it = 0;
+      Ring<kPairStages> at;
+      int it = 0;                                  // loads issued so far
       bool ok = true;
+      const uint32_t full0 = map_rank(tc::smem_u32(&full[0]), 0);
       for (int t = first; t < tiles && ok; t += step) {
         int ti, tj;
         tile_of(t, A.tiles_i, A.tiles_j, ti, tj);
         const int64_t i0 = static_cast<int64_t>(ti) * 256 + rank * 128;
         const int64_t j0 = static_cast<int64_t>(tj) * 256 + rank * 128;
-        for (int k = 0; k < A.iters; ++k, ++it) {
-          const int s = it % kPairStages;
-          if (!wait_phase(&empty[s], ((it / kPairStages) & 1) ^ 1, &s_abort)) {
+        for (int k = 0; k < A.iters; ++k, ++it, at.next()) {
+          const int s = at.s;
+          if (!wait_phase(&empty[s], at.ph ^ 1, &s_abort)) {
             ok = false;
             break;
           }
           int kb, pa, pb;
           part_of(A.iters, A.kblocks, k, kb, pa, pb);
           if (rank == 0) tc::mbar_arrive_expect_tx(&full[s], 2 * kPairStage);
-          const uint32_t bar = map_rank(tc::smem_u32(&full[s]), 0);
+          const uint32_t bar = full0 + s * 8;
           const uint32_t sa = smem + s * kPairStage, sb = sa + kOpBytes;
           load_operand<AMN, 128>(sa, i0, kb * kBK, [&](uint32_t d, int32_t x, int32_t y) {
             tma_load_3d_pair(d, &map_a, x, y, pa, bar);
@@ -331,7 +444,9 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {                  // the leader multiplies for the pair
       const uint32_t idesc = tc::idesc_f16(256, 256, tc::kBF16, false, AMN, BMN);
-      int it = 0, n = 0;
+      const uint64_t da0 = operand_desc<AMN>(smem), db0 = operand_desc<BMN>(smem + kOpBytes);
+      Ring<kPairStages> at;
+      int n = 0;
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step, ++n) {
         const int b = n & 1;
@@ -341,15 +456,19 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         }
         tc::fence_after_sync();
         const uint32_t d = tmem + b * 256;
-        for (int k = 0; k < A.iters; ++k, ++it) {
-          const int s = it % kPairStages;
-          if (!wait_phase(&full[s], (it / kPairStages) & 1, &s_abort)) {
+        // One stage's products take 512 cycles and only two MMAs queue up behind the running one,
+        // so the next stage's barrier is polled before this stage's products are issued.
+        bool ready = tc::mbar_try_wait(&full[at.s], at.ph);
+        for (int k = 0; k < A.iters; ++k) {
+          const int s = at.s;
+          if (!ready && !wait_phase(&full[s], at.ph, &s_abort)) {
             ok = false;
             break;
           }
           tc::fence_after_sync();
-          const uint64_t da = operand_desc<AMN>(smem + s * kPairStage);
-          const uint64_t db = operand_desc<BMN>(smem + s * kPairStage + kOpBytes);
+          const uint64_t da = tc::desc_add(da0, s * kPairStage), db = tc::desc_add(db0, s * kPairStage);
+          at.next();
+          ready = k + 1 < A.iters && tc::mbar_try_wait(&full[at.s], at.ph);
 #pragma unroll
           for (int q = 0; q < kBK / 16; ++q)
             mma_pair(d, tc::desc_add(da, q * k_advance<AMN>()), tc::desc_add(db, q * k_advance<BMN>()), idesc,
@@ -366,33 +485,122 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
       }
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp < 4) {
+    // One thread a half moves the staged chunks: it hands a slot to the epilogue (with the
+    // residual's values loaded into it, or just free), and stores it once it is written.
+    if (lane == 0 && A.staged) {
+      const int half = warp - 2;
+      const uint32_t bytes = 128u * A.cols * (A.epi.out_bf ? 2 : 4);
+      Chunk cur, ahead;
+      cur.start(A, rank, half, first, tiles, step);
+      ahead = cur;
+      auto hand_over = [&](int q) {
+        if (ahead.t >= tiles) return;
+        uint64_t* bar = &ready[half][q & 1];
+        if (A.res_staged && !ahead.z) {
+          tc::mbar_arrive_expect_tx(bar, bytes);
+          tc::tma_load_2d(smem + kPairStages * kPairStage + (half * 2 + (q & 1)) * kSlot, &maps.res,
+                          static_cast<int32_t>(ahead.i0), static_cast<int32_t>(ahead.j0) + ahead.c, bar);
+        } else {
+          tc::mbar_arrive(bar);
+        }
+        ahead.next(A, rank, half, tiles, step);
+      };
+      hand_over(0);
+      hand_over(1);
+      int q = 0;
+      for (; cur.t < tiles; ++q, cur.next(A, rank, half, tiles, step)) {
+        if (!wait_phase(&written[half][q & 1], (q >> 1) & 1, &s_abort)) {
+          s_abort = 1;
+          raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
+          if (A.res_staged) {                      // loads in flight
+            drain_phase(&ready[half][q & 1], (q >> 1) & 1);
+            drain_phase(&ready[half][(q + 1) & 1], ((q + 1) >> 1) & 1);
+          }
+          break;
+        }
+        tma_store_2d(cur.z ? &maps.z : &maps.y, smem + kPairStages * kPairStage + (half * 2 + (q & 1)) * kSlot,
+                     static_cast<int32_t>(cur.i0), static_cast<int32_t>(cur.j0) + cur.c);
+        tc::bulk_commit();
+        tc::bulk_wait_read();
+        hand_over(q + 2);
+      }
+      tc::bulk_wait_all();
+    }
+    __syncwarp();
+  } else {
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lead = map_rank(tc::smem_u32(&acc_empty[0]), 0);
-    int n = 0;
+    unsigned char* slots = smem_raw + (smem - tc::smem_u32(smem_raw)) + kPairStages * kPairStage + half * 2 * kSlot;
+    // the whole warp takes the same way, as its tensor-memory loads need
+    auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, wait_phase(bar, parity, &s_abort)) != 0;
+    };
+    int n = 0, q = 0;
     for (int t = first; t < tiles; t += step, ++n) {
       int ti, tj;
       tile_of(t, A.tiles_i, A.tiles_j, ti, tj);
       const int b = n & 1;
-      const int64_t i = static_cast<int64_t>(ti) * 256 + rank * 128 + quad * 32 + lane;
+      const int64_t ib = static_cast<int64_t>(ti) * 256 + rank * 128;
+      const int64_t i = ib + quad * 32 + lane;
       const int64_t j0 = static_cast<int64_t>(tj) * 256 + half * 128;
       const bool in = i < A.I;
       const float bias = A.epi.bias && in ? __ldg(A.epi.bias + i) : 0.f;
-      const bool got = wait_phase(&acc_full[b], (n >> 1) & 1, &s_abort);
-      if (__any_sync(0xffffffffu, !got)) {
-        if (!got) raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
-        s_abort = 1;
-        break;
-      }
+      bool got = wait_warp(&acc_full[b], (n >> 1) & 1);
       tc::fence_after_sync();
       const uint32_t src = tmem + b * 256 + half * 128 + (static_cast<uint32_t>(quad * 32) << 16);
+      // the columns of this half that exist (none where the CTA's rows are past the end)
+      const int ncol = ib < A.I ? static_cast<int>(A.J - j0 < 128 ? (A.J > j0 ? A.J - j0 : 0) : 128) : 0;
+      if (!A.staged) {
 #pragma unroll 1
-      for (int c = 0; c < 128; c += 16) {
-        if (j0 + c >= A.J) break;                  // the same for the whole warp
-        uint32_t r[16];
-        tc::tmem_ld16(src + c, r);
-        tc::tmem_wait_ld();
-        store16(A.epi, r, bias, i, in, j0 + c, A.J);
+        for (int c = 0; c < ncol && got; c += 16) {
+          float v[16];
+          load16(src + c, bias, v);
+          if (in) store16(A.epi, v, i, j0 + c, A.J);
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < ncol && got; c += A.cols) {
+          float v[2][16];
+          load16(src + c, bias, v[0]);
+          if (A.cols == 32) load16(src + c + 16, bias, v[1]);
+          if (A.epi.z) {
+            got = got && wait_warp(&ready[half][q & 1], (q >> 1) & 1);
+            unsigned char* tile = slots + (q & 1) * kSlot;
+            put16(tile, A.epi.z_bf, 0, quad * 32 + lane, false, v[0]);
+            if (A.cols == 32) put16(tile, A.epi.z_bf, 16, quad * 32 + lane, false, v[1]);
+            tc::fence_async_smem();
+            tc::mbar_arrive(&written[half][q & 1]);
+            ++q;
+          }
+          activate16(A.epi, v[0]);
+          if (A.cols == 32) activate16(A.epi, v[1]);
+          if (A.epi.res && !A.res_staged && in) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int m = min(16, ncol - c - 16 * u);
+              if (m <= 0 || 16 * u >= A.cols) continue;
+              const int64_t at = (j0 + c + 16 * u) * A.epi.res_ld + i;
+              float r[16];
+              if (A.epi.res_bf) gather16<true>(A.epi.res, A.epi.res_ld, at, m, r);
+              else gather16<false>(A.epi.res, A.epi.res_ld, at, m, r);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[u][e] += r[e];
+            }
+          }
+          got = got && wait_warp(&ready[half][q & 1], (q >> 1) & 1);
+          unsigned char* tile = slots + (q & 1) * kSlot;
+          put16(tile, A.epi.out_bf, 0, quad * 32 + lane, A.res_staged, v[0]);
+          if (A.cols == 32) put16(tile, A.epi.out_bf, 16, quad * 32 + lane, A.res_staged, v[1]);
+          tc::fence_async_smem();
+          tc::mbar_arrive(&written[half][q & 1]);
+          ++q;
+        }
+      }
+      if (!got) {
+        raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
+        s_abort = 1;
+        break;
       }
       tc::fence_before_sync();
       __syncwarp();
@@ -423,7 +631,7 @@ struct SplitShape {
 template <bool AMN, bool BMN, int BN>
 __global__ void __launch_bounds__(kSplitThreads)
 gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                  const TcArgs A, const int splits) {
+                  const __grid_constant__ OutMaps maps, const __grid_constant__ TcArgs A, const int splits) {
   using S = SplitShape<BN>;
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[S::stages], empty[S::stages], acc_full;
@@ -517,25 +725,16 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16);
   bool ready = true;
   if (warp >= 2) {
-    ready = __all_sync(0xffffffffu, wait_phase(&acc_full, 0, &s_abort));
+    ready = !tc::named_sync_or(2, 128, !wait_phase(&acc_full, 0, &s_abort));
     if (!ready) raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
     tc::fence_after_sync();
   }
-  if (splits == 1) {
-    if (warp >= 2 && ready) {
-#pragma unroll 1
-      for (int c = 0; c < BN; c += 16) {
-        if (j0 + c >= A.J) break;
-        uint32_t r[16];
-        tc::tmem_ld16(src + c, r);
-        tc::tmem_wait_ld();
-        store16(A.epi, r, bias, i, in, j0 + c, A.J);
-      }
-    }
-  } else {
-    // every CTA publishes its part of the tile as [column][row]; rank r adds and stores the r-th
-    // share of the columns, the parts in rank order
-    const int ncol = static_cast<int>(A.J - j0 < BN ? A.J - j0 : BN);
+  // The CTA's columns [c0, c1) of the tile.  Split: every CTA publishes its part of the tile as
+  // [column][row], and rank r adds and stores the r-th share of the columns (a multiple of 8),
+  // the parts in rank order.
+  const int ncol = static_cast<int>(A.J - j0 < BN ? A.J - j0 : BN);
+  int c0 = 0, c1 = ncol;
+  if (splits > 1) {
     if (warp >= 2) {
 #pragma unroll 1
       for (int c = 0; c < ncol; c += 16) {
@@ -547,33 +746,73 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       }
     }
     cluster_sync();
-    if (warp >= 2) {
-      const int per = (ncol + splits - 1) / splits;
-      const int c1 = min(ncol, (rank + 1) * per);
-      uint32_t base[8];
+    const int per = ((ncol + splits - 1) / splits + 7) / 8 * 8;
+    c0 = min(ncol, rank * per);
+    c1 = min(ncol, c0 + per);
+  }
+  // the finished tile, [column - c0][128], for TMA: behind the parts if there are any
+  unsigned char* out = smem_raw + (smem - tc::smem_u32(smem_raw)) + (splits > 1 ? 128 * BN * 4 : 0);
+  const int cpad = (c1 - c0 + 15) / 16 * 16;
+  unsigned char* out_z = out + cpad * 128 * (A.epi.out_bf ? 2 : 4);
+  if (warp >= 2 && ready) {
+    const uint32_t mine = smem + (quad * 32 + lane) * 4;
+#pragma unroll 1
+    for (int c = c0; c < c1; c += 16) {
+      float v[16];
+      if (splits == 1) {
+        load16(src + c, bias, v);
+      } else {
 #pragma unroll
-      for (int p = 0; p < 8; ++p)
-        base[p] = map_rank(smem + (quad * 32 + lane) * 4, static_cast<uint32_t>(p < splits ? p : 0));
-      for (int c = rank * per; c < c1; c += 4) {
-        float v[4][8];
+        for (int e = 0; e < 16; ++e) v[e] = 0.f;
+        const int n = min(16, c1 - c);
+#pragma unroll 1
+        for (int p = 0; p < splits; ++p) {
+          const uint32_t at = map_rank(mine, static_cast<uint32_t>(p)) + c * 512;
+          float x[16];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+          for (int e = 0; e < 16; ++e) x[e] = e < n ? ld_cluster(at + e * 512) : 0.f;
 #pragma unroll
-          for (int p = 0; p < 8; ++p)
-            if (p < splits && c + e < c1) v[e][p] = ld_cluster(base[p] + (c + e) * 512);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (c + e >= c1 || !in) continue;
-          float acc = v[e][0];
-#pragma unroll
-          for (int p = 1; p < 8; ++p)
-            if (p < splits) acc += v[e][p];
-          epilogue_store(A.epi, j0 + c + e, i, acc);
+          for (int e = 0; e < 16; ++e) v[e] += x[e];
         }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] += bias;
+      }
+      if (!A.staged) {
+        if (in) store16(A.epi, v, i, j0 + c, j0 + c1);
+      } else {
+        const int m = min(16, c1 - c);
+        float r[16];
+        if (A.epi.res && in) {
+          const int64_t at = (j0 + c) * A.epi.res_ld + i;
+          if (A.epi.res_bf) gather16<true>(A.epi.res, A.epi.res_ld, at, m, r);
+          else gather16<false>(A.epi.res, A.epi.res_ld, at, m, r);
+        }
+        if (A.epi.z) put16(out_z, A.epi.z_bf, c - c0, quad * 32 + lane, false, v);
+        activate16(A.epi, v);
+        if (A.epi.res && in) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] += r[e];
+        }
+        put16(out, A.epi.out_bf, c - c0, quad * 32 + lane, false, v);
       }
     }
-    cluster_sync();                                // the peers are done reading this CTA's part
+    if (A.staged) {
+      tc::fence_async_smem();
+      tc::named_sync(1, 128);
+      if (warp == 2 && lane == 0) {                // boxes of 8 columns
+        for (int c = c0; c < c1; c += 8) {
+          tma_store_2d(&maps.y, tc::smem_u32(out) + (c - c0) * 128 * (A.epi.out_bf ? 2 : 4),
+                       static_cast<int32_t>(i0), static_cast<int32_t>(j0) + c);
+          if (A.epi.z)
+            tma_store_2d(&maps.z, tc::smem_u32(out_z) + (c - c0) * 128 * (A.epi.z_bf ? 2 : 4),
+                         static_cast<int32_t>(i0), static_cast<int32_t>(j0) + c);
+        }
+        tc::bulk_commit();
+        tc::bulk_wait_all();
+      }
+    }
   }
+  if (splits > 1) cluster_sync();                  // the peers are done reading this CTA's part
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 1) {
@@ -640,9 +879,36 @@ bool encode(CUtensorMap* m, const GemmOperand& X, int64_t R, int64_t C, int plan
   return X.mn ? encode_operand(m, X.p, C, R, X.ld, planes, 64) : encode_operand(m, X.p, R, C, X.ld, planes, tile_rows);
 }
 
+// a [J, I] array on the output side, in boxes of 128 columns x `rows` rows
+bool encode_out(CUtensorMap* m, const void* base, bool bf, int64_t I, int64_t J, int64_t ld, int rows) {
+  auto enc = tensor_map_encoder();
+  const cuuint64_t es = bf ? 2 : 4;
+  if (!enc || (reinterpret_cast<uintptr_t>(base) & 15u) || ld * es % 16) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(I), static_cast<cuuint64_t>(J)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * es};
+  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(m, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base),
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The output leaves by TMA where y and z have 16-byte aligned rows; the residual arrives by it
+// (pair kernel) where it has y's type and such rows too.
+void encode_outputs(const Gemm& g, TcArgs* A, OutMaps* m, int rows, bool residual) {
+  const GemmEpilogue& E = g.epi;
+  A->staged = encode_out(&m->y, E.out, E.out_bf, g.I, g.J, E.out_ld, rows) &&
+              (!E.z || encode_out(&m->z, E.z, E.z_bf, g.I, g.J, E.z_ld, rows));
+  A->res_staged = residual && A->staged && E.res && E.res_bf == E.out_bf &&
+                  encode_out(&m->res, E.res, E.res_bf, g.I, g.J, E.res_ld, rows);
+}
+
 template <bool AMN, bool BMN>
 cudaError_t launch_pair(const Gemm& g, TcArgs A, int planes, int pairs, cudaStream_t st) {
   CUtensorMap ma, mb;
+  OutMaps out;
+  A.cols = g.epi.out_bf && (!g.epi.z || g.epi.z_bf) ? 32 : 16;
+  encode_outputs(g, &A, &out, A.cols, true);
   if (!encode(&ma, g.A, g.I, g.C, planes, 128) || !encode(&mb, g.B, g.J, g.C, planes, 128)) return cudaErrorInvalidValue;
   A.tiles_i = static_cast<int32_t>((g.I + 255) / 256);
   A.tiles_j = static_cast<int32_t>((g.J + 255) / 256);
@@ -652,13 +918,20 @@ cudaError_t launch_pair(const Gemm& g, TcArgs A, int planes, int pairs, cudaStre
   const int64_t tiles = static_cast<int64_t>(A.tiles_i) * A.tiles_j;
   if (tiles > 0x3fffffff) return cudaErrorInvalidConfiguration;
   const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(tiles, pairs));
-  k<<<grid, kPairThreads, kPairSmem, st>>>(ma, mb, A);
+  k<<<grid, kPairThreads, kPairSmem, st>>>(ma, mb, out, A);
   return cudaGetLastError();
 }
 
 template <bool AMN, bool BMN, int BN>
 cudaError_t launch_split(const Gemm& g, TcArgs A, int planes, int splits, cudaStream_t st) {
   CUtensorMap ma, mb;
+  OutMaps out;
+  // few columns are stored directly, and so is what does not fit behind the parts
+  const size_t cols = splits == 1 ? BN : ((BN + splits - 1) / splits + 15) / 16 * 16;
+  const size_t bytes = (splits == 1 ? 0 : 128 * BN * 4) +
+                       cols * 128 * ((g.epi.out_bf ? 2 : 4) + (!g.epi.z ? 0 : g.epi.z_bf ? 2 : 4));
+  if (BN >= 64 && bytes <= SplitShape<BN>::smem - 1024) encode_outputs(g, &A, &out, 8, false);
+  else A.staged = A.res_staged = false;
   if (!encode(&ma, g.A, g.I, g.C, planes, 128) || !encode(&mb, g.B, g.J, g.C, planes, BN)) return cudaErrorInvalidValue;
   A.tiles_i = static_cast<int32_t>((g.I + 127) / 128);
   A.tiles_j = static_cast<int32_t>((g.J + BN - 1) / BN);
@@ -677,7 +950,7 @@ cudaError_t launch_split(const Gemm& g, TcArgs A, int planes, int splits, cudaSt
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = splits > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, k, ma, mb, A, splits);
+  e = cudaLaunchKernelEx(&cfg, k, ma, mb, out, A, splits);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
