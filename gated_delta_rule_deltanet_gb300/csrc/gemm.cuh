@@ -54,6 +54,10 @@ __device__ __forceinline__ void epilogue_store(const GemmEpilogue& E, int64_t j,
 
 cudaError_t launch_gemm_simt(const Gemm& g, cudaStream_t st);
 
+// A and B K-major and J at most kRowsMax: CUDA cores, any alignment.
+constexpr int kRowsMax = 8;
+cudaError_t launch_gemm_rows(const Gemm& g, cudaStream_t st);
+
 // The tensor-core product: operands are 16-byte aligned bf16 rows, `planes` (1, or 3 for the parts
 // of fp32) planes of rows * ld elements one after another.  C >= 1.
 cudaError_t launch_gemm_tc(const Gemm& g, int planes, cudaStream_t st);

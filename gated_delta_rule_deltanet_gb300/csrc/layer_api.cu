@@ -14,13 +14,13 @@ cudaError_t launch_linear_bwd(const kda_linear_params_t& p, const void* x, const
                               int32_t* err, cudaStream_t st);
 cudaError_t launch_residual_norm(const kda_norm_params_t& p, const void* x, const void* res,
                                  const void* gate, const float* post_w, const float* w, void* h,
-                                 void* y, cudaStream_t st);
+                                 void* y, int32_t* err, cudaStream_t st);
 size_t residual_norm_bwd_workspace(const kda_norm_params_t& p);
 cudaError_t launch_residual_norm_bwd(const kda_norm_params_t& p, const void* x, const void* h,
                                      const void* gate, const float* post_w, const float* w,
                                      const void* dy, const void* dh, void* dx, void* dres,
                                      void* dgate, float* dpost_w, float* dw, void* workspace,
-                                     cudaStream_t st);
+                                     int32_t* err, cudaStream_t st);
 cudaError_t launch_gated_norm(const kda_norm_params_t& p, const void* o, const void* gate,
                               const float* w, void* y, cudaStream_t st);
 size_t gated_norm_bwd_workspace(const kda_norm_params_t& p);
@@ -175,7 +175,9 @@ kda_status_t kda_residual_norm_fwd(const kda_norm_params_t* p, const void* x, co
       !elem_aligned(y, p->x_dtype) || !elem_aligned(residual, p->h_dtype) || !elem_aligned(h, p->h_dtype) ||
       !elem_aligned(gate, p->gate_per_token ? p->x_dtype : KDA_DTYPE_F32))
     return KDA_ERR_INVALID_ARG;
-  return to_status(kda::launch_residual_norm(*p, x, residual, gate, post_weight, weight, h, y,
+  int32_t* err = kda::layer_error_word();
+  if (!err) return KDA_ERR_CUDA;
+  return to_status(kda::launch_residual_norm(*p, x, residual, gate, post_weight, weight, h, y, err,
                                              static_cast<cudaStream_t>(stream)));
 }
 
@@ -197,8 +199,10 @@ kda_status_t kda_residual_norm_bwd(const kda_norm_params_t* p, const void* x, co
       !elem_aligned(gate, gdt) || !elem_aligned(d_gate, gdt))
     return KDA_ERR_INVALID_ARG;
   if (!workspace_ok(workspace, workspace_bytes, kda::residual_norm_bwd_workspace(*p))) return KDA_ERR_WORKSPACE;
+  int32_t* err = kda::layer_error_word();
+  if (!err) return KDA_ERR_CUDA;
   return to_status(kda::launch_residual_norm_bwd(*p, x, h, gate, post_weight, weight, d_y, d_h, dx,
-                                                 d_residual, d_gate, d_post_weight, d_weight, workspace,
+                                                 d_residual, d_gate, d_post_weight, d_weight, workspace, err,
                                                  static_cast<cudaStream_t>(stream)));
 }
 

@@ -203,10 +203,11 @@ static size_t up256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 
 // What a call keeps in the workspace (offsets; kNone: nothing).  The tensor cores read aligned
 // bf16 rows: bf16 operands as they are where their rows and base are 16-byte aligned, else a
-// copy; fp32 operands always as three planes of parts.
+// copy; fp32 operands always as three planes of parts.  The forward of up to kRowsMax tokens reads
+// everything in place.
 constexpr size_t kNone = ~static_cast<size_t>(0);
 struct LinearLayout {
-  bool tc;
+  bool rows, tc;             // few tokens; tensor cores
   size_t part, dz, x, w, dz_planes, total;
   int64_t dz_ld;
 };
@@ -214,7 +215,8 @@ static LinearLayout linear_layout(const kda_linear_params_t& p, bool bwd) {
   const int64_t T = p.tokens, K = p.in_features, N = p.out_features;
   const bool bf = p.dtype == KDA_DTYPE_BF16;
   LinearLayout L{};
-  L.tc = !(p.flags & KDA_FLAG_CUDA_CORES);
+  L.rows = !bwd && T <= kRowsMax && !(p.flags & KDA_FLAG_CUDA_CORES);
+  L.tc = !L.rows && !(p.flags & KDA_FLAG_CUDA_CORES);
   size_t at = 0;
   auto take = [&](bool yes, size_t bytes) {
     if (!yes) return kNone;
@@ -273,7 +275,7 @@ cudaError_t launch_linear_fwd(const kda_linear_params_t& p, const void* x, const
   g.epi = {bias, res, y, z, or_dense(p.residual_row_stride, N), or_dense(p.y_row_stride, N), N, p.scale,
            p.activation, p.residual_dtype == KDA_DTYPE_BF16, p.y_dtype == KDA_DTYPE_BF16, g.bf16};
   g.err = err;
-  return run_gemm(g, L.tc, st);
+  return L.rows ? launch_gemm_rows(g, st) : run_gemm(g, L.tc, st);
 }
 
 cudaError_t launch_linear_bwd(const kda_linear_params_t& p, const void* x, const void* w, const void* z,

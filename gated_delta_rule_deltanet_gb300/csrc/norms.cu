@@ -1,6 +1,5 @@
-// norms.cu -- the norms around the recurrence: residual_norm (norm of the block's output, gate,
-// residual scale, residual add and the norm before the next block in one pass) and gated_norm
-// (the per-head norm of the recurrence's output times its gate), forward and backward.
+// norms.cu -- residual_norm: the norm of a block's output, its gate and residual scale, the
+// residual add and the norm before the next block in one pass, forward and backward.
 //
 // With rms(a) = a r, r = 1 / sqrt(mean(a^2) + eps), and d the gradient w.r.t. rms(a),
 //
@@ -8,16 +7,15 @@
 //
 // so a row's gradient needs the row's two sums, sum a^2 and sum d a, before any element.
 //
-// All four are bound by HBM: about ten fp32 operations an element against 6 to 20 bytes.  A row
-// of residual_norm belongs to one CTA that keeps it in registers from the load to the store, so
-// every array crosses HBM once; a thread holds 8 to 32 elements as 16-byte vectors, all loaded
-// before the first reduction, and several CTAs share an SM so that one's loads cover another's
-// reductions.  The column sums (gradients of weights and of a learned gate) are kept in
-// registers over all rows of a CTA and written once as partial rows, which a second kernel adds
-// in a fixed order: no atomics, the same bits every time.  Sums and norms are fp32.
+// Bound by HBM: some ten fp32 operations an element forward (25 backward) against 8 to 20 bytes.  A
+// row belongs to one CTA and crosses HBM once: it waits in shared memory (RowRing) or registers
+// from its load to its store.  The column sums (gradients of weights and of a learned gate) are
+// kept in registers over all rows of a CTA and written once as partial rows, which a second
+// kernel adds in a fixed order: no atomics, the same bits every time.  Sums and norms are fp32.
 #include <algorithm>
 
 #include "layer_common.cuh"
+#include "tc_utils.cuh"
 
 namespace kda {
 
@@ -80,6 +78,7 @@ struct ResidualNormArgs {
   int64_t T, gate_stride;
   int32_t N, gate_per_token;
   float eps, scale, inv_n;
+  int32_t* err;
 };
 
 // Sums of K values over the block, the same in every thread.  Buffers alternate between calls,
@@ -184,7 +183,7 @@ residual_norm_kernel(ResidualNormArgs A) {
 }
 
 template <bool XBF, bool HBF, int V, bool VEC>
-__global__ void __launch_bounds__(V == 1 ? 128 : V == 2 ? 256 : 512)
+__global__ void __launch_bounds__(512)
 residual_norm_bwd_kernel(ResidualNormArgs A) {
   __shared__ float s_buf[2][16][3];
   const int nt = blockDim.x, tid = threadIdx.x, step = V * nt;
@@ -319,25 +318,360 @@ residual_norm_bwd_kernel(ResidualNormArgs A) {
   }
 }
 
-// Threads and elements a thread: rows up to 1024 take one chunk a thread, up to 4096 two, up to
-// 16384 four (two chunks of each array in flight a thread, with 64 registers and four CTAs of 256
-// an SM, cover HBM's latency where one chunk and 512 threads did not).
+// ---------------------------------------------------------------- rows through a shared-memory ring
+
+// Rows of a multiple of 8 elements, 16-byte aligned: a CTA walks its rows through a ring of 2 to 4
+// stages, each holding one row of every input array, filled by bulk copies that one thread
+// issues a full ring ahead.  HBM's latency is hidden by the ring instead of by registers and
+// occupancy: with the row in registers the backward ran three CTAs an SM through two reductions
+// each and reached 41% of the measured bandwidth.
+struct RowRing {
+  uint32_t x, r, g, dy, dh;      // byte offsets inside a stage
+  uint32_t stage;                // bytes of a stage
+  uint32_t xrow, hrow;           // bytes of a row of x's and of h's type
+  int32_t stages;
+  int32_t* err;
+};
+constexpr int kMaxStages = 4;
+constexpr size_t kRingBytes = 208 * 1024;
+constexpr uint32_t kRowWait = 1u << 22;
+
+template <bool BF>
+__device__ __forceinline__ Raw8<BF> smem_chunk(const unsigned char* row, int c, int n) {
+  Raw8<BF> r;
+  if (8 * c < n) {
+    const uint4* p = reinterpret_cast<const uint4*>(row + c * (BF ? 16 : 32));
+    const uint4 a = p[0];
+    r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+    if constexpr (!BF) {
+      const uint4 b = p[1];
+      r.w[4] = b.x; r.w[5] = b.y; r.w[6] = b.z; r.w[7] = b.w;
+    }
+  } else {
+    r.zero();
+  }
+  return r;
+}
+
+// One thread's copies of row t into a stage.
+template <bool BWD>
+__device__ __forceinline__ void fetch_row(const ResidualNormArgs& A, const RowRing& R, int64_t t, uint32_t at,
+                                          bool need_x, uint64_t* bar) {
+  auto row = [&](const void* base, int64_t bytes) { return static_cast<const char*>(base) + t * bytes; };
+  uint32_t bytes = 0;
+  if (!BWD || need_x) bytes += R.xrow;
+  if (BWD ? A.dy != nullptr : A.res != nullptr) bytes += R.hrow;
+  if (A.gate_per_token) bytes += R.xrow;
+  if (BWD && A.dy) bytes += R.xrow;
+  if (BWD && A.dh) bytes += R.hrow;
+  tc::mbar_arrive_expect_tx(bar, bytes);
+  if (!BWD || need_x) tc::bulk_load(at + R.x, row(A.x, R.xrow), R.xrow, bar);
+  if (BWD ? A.dy != nullptr : A.res != nullptr) tc::bulk_load(at + R.r, row(A.res, R.hrow), R.hrow, bar);
+  if (A.gate_per_token) tc::bulk_load(at + R.g, row(A.gate, A.gate_stride * (R.xrow / A.N)), R.xrow, bar);
+  if (BWD && A.dy) tc::bulk_load(at + R.dy, row(A.dy, R.xrow), R.xrow, bar);
+  if (BWD && A.dh) tc::bulk_load(at + R.dh, row(A.dh, R.hrow), R.hrow, bar);
+}
+
+// The ring's part of a row loop: `full` holds the row, `empty` says every warp has read it.
+struct RingState {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  int fail;
+};
+
+template <bool BWD>
+__device__ __forceinline__ void ring_start(const ResidualNormArgs& A, const RowRing& R, RingState& S, uint32_t smem,
+                                           bool need_x) {
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < R.stages; ++s) {
+      tc::mbar_init(&S.full[s], 1);
+      tc::mbar_init(&S.empty[s], blockDim.x >> 5);
+    }
+    S.fail = 0;
+    tc::fence_mbar_init();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int64_t t = blockIdx.x;
+    for (int s = 0; s < R.stages && t < A.T; ++s, t += gridDim.x)
+      fetch_row<BWD>(A, R, t, smem + s * R.stage, need_x, &S.full[s]);
+  }
+}
+
+// Before row `it` (stage s): the stage that row it - 1 left is refilled, then row `it` awaited.  A
+// wait that gives up raises the error word and ends the waiting of the whole block, whose
+// remaining rows are then incomplete.
+template <bool BWD>
+__device__ __forceinline__ void ring_row(const ResidualNormArgs& A, const RowRing& R, RingState& S, uint32_t smem,
+                                         bool need_x, int64_t t, int it, int s, uint32_t ph) {
+  volatile int* fail = &S.fail;
+  if (*fail) return;
+  bool ok = true;
+  if (threadIdx.x == 0 && it > 0) {
+    const int64_t next = t + static_cast<int64_t>(R.stages - 1) * gridDim.x;
+    if (next < A.T) {
+      const int p = s == 0 ? R.stages - 1 : s - 1;
+      ok = tc::mbar_wait_bounded(&S.empty[p], s == 0 ? ph ^ 1 : ph, kRowWait);
+      if (ok) fetch_row<BWD>(A, R, next, smem + p * R.stage, need_x, &S.full[p]);
+    }
+  }
+  if (!(tc::mbar_wait_bounded(&S.full[s], ph, kRowWait) && ok)) {
+    raise_device_error(R.err, KDA_DEVERR_TIMEOUT);
+    *fail = 1;
+  }
+}
+
+template <bool XBF, bool HBF, int V>
+__global__ void __launch_bounds__(V == 1 ? 128 : V == 2 ? 256 : 512)
+residual_norm_ring_kernel(const ResidualNormArgs A, const RowRing R) {
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ float s_buf[2][16][1];
+  __shared__ __align__(8) RingState S;
+  const int nt = blockDim.x, tid = threadIdx.x;
+  const int N = A.N;
+  const uint32_t smem = tc::smem_u32(ring);
+  ring_start<false>(A, R, S, smem, true);
+  int par = 0, it = 0, s = 0;
+  uint32_t ph = 0;
+  for (int64_t t = blockIdx.x; t < A.T; t += gridDim.x, ++it) {
+    ring_row<false>(A, R, S, smem, true, t, it, s, ph);
+    const unsigned char* st = ring + s * R.stage;
+    float h[V][8];
+    float a = A.scale;
+    if (A.post_w) {
+      float sum[1] = {0.f};
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const Raw8<XBF> x = smem_chunk<XBF>(st + R.x, tid + v * nt, N);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[0] += x.f32(e) * x.f32(e);
+      }
+      block_sums<1>(sum, s_buf[par]);
+      par ^= 1;
+      a *= 1.f / sqrtf(sum[0] * A.inv_n + A.eps);
+    }
+    float sq[1] = {0.f};
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = tid + v * nt;
+      const Raw8<XBF> x = smem_chunk<XBF>(st + R.x, c, N);
+      float p[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[v][e] = a * x.f32(e);
+      if (A.post_w) {
+        load_params<true>(A.post_w, c, 0, N, p);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[v][e] *= p[e];
+      }
+      if (A.gate_per_token) {
+        const Raw8<XBF> g = smem_chunk<XBF>(st + R.g, c, N);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[v][e] *= g.f32(e);
+      } else if (A.gate) {
+        load_params<true>(static_cast<const float*>(A.gate), c, 0, N, p);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[v][e] *= p[e];
+      }
+      if (A.res) {
+        const Raw8<HBF> r = smem_chunk<HBF>(st + R.r, c, N);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[v][e] += r.f32(e);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sq[0] += h[v][e] * h[v][e];
+      if (A.out_h)
+        store_chunk<HBF, true>(static_cast<char*>(A.out_h) + t * N * (HBF ? 2 : 4), c, 0, N, h[v]);
+    }
+    __syncwarp();
+    if ((tid & 31) == 0) tc::mbar_arrive(&S.empty[s]);
+    if (A.out_y) {
+      block_sums<1>(sq, s_buf[par]);
+      par ^= 1;
+      const float rh = 1.f / sqrtf(sq[0] * A.inv_n + A.eps);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = tid + v * nt;
+        float p[8], y[8];
+        load_params<true>(A.w, c, 0, N, p);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = h[v][e] * rh * p[e];
+        store_chunk<XBF, true>(static_cast<char*>(A.out_y) + t * N * (XBF ? 2 : 4), c, 0, N, y);
+      }
+    }
+    if (++s == R.stages) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
+}
+
+template <bool XBF, bool HBF, int V>
+__global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
+residual_norm_bwd_ring_kernel(const ResidualNormArgs A, const RowRing R) {
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ float s_buf[2][16][3];
+  __shared__ __align__(8) RingState S;
+  const int nt = blockDim.x, tid = threadIdx.x;
+  const int N = A.N;
+  const bool need_x = A.post_w || A.gate;
+  const bool chan = A.gate && !A.gate_per_token;
+  const uint32_t smem = tc::smem_u32(ring);
+  ring_start<true>(A, R, S, smem, need_x);
+  float aw[V][8], ap[V][8], ag[V][8];          // this CTA's column sums
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) aw[v][e] = ap[v][e] = ag[v][e] = 0.f;
+  int par = 0, it = 0, s = 0;
+  uint32_t ph = 0;
+  for (int64_t t = blockIdx.x; t < A.T; t += gridDim.x, ++it) {
+    ring_row<true>(A, R, S, smem, need_x, t, it, s, ph);
+    const unsigned char* st = ring + s * R.stage;
+    const int64_t xo = t * N * (XBF ? 2 : 4), ho = t * N * (HBF ? 2 : 4);
+    float s3[3] = {0.f, 0.f, 0.f};             // sum h^2, sum dy w h, sum x^2
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = tid + v * nt;
+      if (A.dy) {
+        const Raw8<HBF> h = smem_chunk<HBF>(st + R.r, c, N);
+        const Raw8<XBF> dy = smem_chunk<XBF>(st + R.dy, c, N);
+        float p[8];
+        load_params<true>(A.w, c, 0, N, p);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          s3[0] += h.f32(e) * h.f32(e);
+          s3[1] += dy.f32(e) * p[e] * h.f32(e);
+        }
+      }
+      if (A.post_w) {
+        const Raw8<XBF> x = smem_chunk<XBF>(st + R.x, c, N);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s3[2] += x.f32(e) * x.f32(e);
+      }
+    }
+    block_sums<3>(s3, s_buf[par]);
+    par ^= 1;
+    const float rh = 1.f / sqrtf(s3[0] * A.inv_n + A.eps);
+    const float mh = s3[1] * A.inv_n * rh * rh;            // mean(d rms(h)) r
+    const float rx = A.post_w ? 1.f / sqrtf(s3[2] * A.inv_n + A.eps) : 1.f;
+    float d[V][8];                                         // dh, then du post_weight
+    float sx[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = tid + v * nt;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[v][e] = 0.f;
+      if (A.dy) {
+        const Raw8<HBF> h = smem_chunk<HBF>(st + R.r, c, N);
+        const Raw8<XBF> dy = smem_chunk<XBF>(st + R.dy, c, N);
+        float p[8];
+        load_params<true>(A.w, c, 0, N, p);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float hh = h.f32(e), dd = dy.f32(e);
+          aw[v][e] += dd * (hh * rh);
+          d[v][e] = rh * (dd * p[e] - hh * mh);
+        }
+      }
+      if (A.dh) {
+        const Raw8<HBF> dh = smem_chunk<HBF>(st + R.dh, c, N);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[v][e] += dh.f32(e);
+      }
+      if (A.out_h) store_chunk<HBF, true>(static_cast<char*>(A.out_h) + ho, c, 0, N, d[v]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[v][e] *= A.scale;
+      if (need_x) {
+        const Raw8<XBF> x = smem_chunk<XBF>(st + R.x, c, N);
+        float pw[8];
+        if (A.post_w) {
+          load_params<true>(A.post_w, c, 0, N, pw);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) pw[e] = 1.f;
+        }
+        if (A.gate) {                                      // d_gate = scale dh u, du = scale dh gate
+          float dg[8], gg[8];
+          if (chan) {
+            load_params<true>(static_cast<const float*>(A.gate), c, 0, N, gg);
+          } else {
+            const Raw8<XBF> g = smem_chunk<XBF>(st + R.g, c, N);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) gg[e] = g.f32(e);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            dg[e] = d[v][e] * (x.f32(e) * rx * pw[e]);
+            if (chan) ag[v][e] += dg[e];
+            d[v][e] *= gg[e];
+          }
+          if (!chan) store_chunk<XBF, true>(static_cast<char*>(A.dgate) + xo, c, 0, N, dg);
+        }
+        if (A.post_w) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            ap[v][e] += d[v][e] * (x.f32(e) * rx);
+            d[v][e] *= pw[e];
+            sx[0] += d[v][e] * x.f32(e);
+          }
+        }
+      }
+      if (!A.post_w) store_chunk<XBF, true>(static_cast<char*>(A.out_y) + xo, c, 0, N, d[v]);
+    }
+    if (A.post_w) {
+      block_sums<3>(sx, s_buf[par]);
+      par ^= 1;
+      const float mx = sx[0] * A.inv_n * rx * rx;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = tid + v * nt;
+        const Raw8<XBF> x = smem_chunk<XBF>(st + R.x, c, N);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[v][e] = rx * (d[v][e] - x.f32(e) * mx);
+        store_chunk<XBF, true>(static_cast<char*>(A.out_y) + xo, c, 0, N, d[v]);
+      }
+    }
+    __syncwarp();
+    if ((tid & 31) == 0) tc::mbar_arrive(&S.empty[s]);
+    if (++s == R.stages) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
+  float* part = A.part + static_cast<int64_t>(blockIdx.x) * 3 * N;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = tid + v * nt;
+    if (8 * c >= N) continue;
+    if (A.dy) store_chunk<false, true>(part, c, 0, N, aw[v]);
+    if (A.post_w) store_chunk<false, true>(part + N, c, 0, N, ap[v]);
+    if (chan) store_chunk<false, true>(part + 2 * N, c, 0, N, ag[v]);
+  }
+}
+
+// Threads and elements a thread.  Forward: rows up to 1024 take one chunk a thread, up to 4096 two, up
+// to 16384 four, so that a row's reductions cross few warps.  Backward: one chunk up to 4096, two up
+// to 8192, four above: with 24 column sums a chunk beside the row, one chunk a thread leaves room for
+// 32 warps an SM.
 struct RowShape {
   int V, threads;
 };
-static RowShape row_shape(int N) {
+static RowShape row_shape(int N, bool bwd) {
   const int chunks = (N + 7) / 8;
-  const int V = chunks <= 128 ? 1 : chunks <= 512 ? 2 : 4;
+  const int V = bwd ? (chunks <= 512 ? 1 : chunks <= 1024 ? 2 : 4) : (chunks <= 128 ? 1 : chunks <= 512 ? 2 : 4);
   const int th = ((chunks + V - 1) / V + 31) / 32 * 32;
   return {V, th};
 }
 
 static bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// CTAs an SM that walk the rows: bounded by registers (64 a thread; 128 backward above one chunk)
+static int rows_per_sm(int N, bool bwd) {
+  const RowShape s = row_shape(N, bwd);
+  return std::max(1, (bwd && s.V > 1 ? 512 : 1024) / s.threads);
+}
+
 static int residual_norm_bwd_grid(int64_t T, int N) {
-  const RowShape s = row_shape(N);
-  const int per_sm = std::max(1, 512 / s.threads);
-  return static_cast<int>(std::min<int64_t>(std::max<int64_t>(T, 1), static_cast<int64_t>(sm_count()) * per_sm));
+  return static_cast<int>(std::min<int64_t>(std::max<int64_t>(T, 1), static_cast<int64_t>(sm_count()) * rows_per_sm(N, true)));
 }
 
 static bool residual_vec(const ResidualNormArgs& A, bool xbf) {
@@ -347,10 +681,54 @@ static bool residual_vec(const ResidualNormArgs& A, bool xbf) {
          (!A.gate_per_token || A.gate_stride * es % 16 == 0);
 }
 
+// The ring of a call, or stages = 0 where rows are better read directly: with fewer than three
+// rows a CTA there is nothing to run ahead of (256 rows of 4096: 4.6 us directly, 5.6 us through the
+// ring), and a stage has to fit twice.
+static RowRing row_ring(const ResidualNormArgs& A, bool xbf, bool hbf, bool bwd, int grid) {
+  RowRing R{};
+  R.xrow = static_cast<uint32_t>(A.N) * (xbf ? 2 : 4);
+  R.hrow = static_cast<uint32_t>(A.N) * (hbf ? 2 : 4);
+  R.err = A.err;
+  uint32_t at = 0;
+  auto take = [&](bool yes, uint32_t bytes) {
+    const uint32_t here = at;
+    if (yes) at += bytes;
+    return here;
+  };
+  R.x = take(!bwd || A.post_w || A.gate, R.xrow);
+  R.r = take(bwd ? A.dy != nullptr : A.res != nullptr, R.hrow);
+  R.g = take(A.gate_per_token, R.xrow);
+  R.dy = take(bwd && A.dy, R.xrow);
+  R.dh = take(bwd && A.dh, R.hrow);
+  R.stage = (at + 127) / 128 * 128;
+  const size_t share = kRingBytes / rows_per_sm(A.N, bwd);
+  R.stages = static_cast<int>(std::min<size_t>(kMaxStages, share / R.stage));
+  if (R.stages < 2 || A.T < 3 * static_cast<int64_t>(grid)) R.stages = 0;
+  return R;
+}
+
+template <typename Kernel>
+static cudaError_t launch_ring(Kernel k, unsigned grid, int threads, const ResidualNormArgs& A, const RowRing& R,
+                               cudaStream_t st) {
+  const size_t smem = static_cast<size_t>(R.stage) * R.stages;
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  k<<<grid, threads, smem, st>>>(A, R);
+  return cudaGetLastError();
+}
+
 template <bool XBF, bool HBF, int V, bool VEC>
 static cudaError_t run_residual_norm(const ResidualNormArgs& A, bool bwd, int threads, cudaStream_t st) {
+  const int grid = bwd ? residual_norm_bwd_grid(A.T, A.N)
+                       : static_cast<int>(std::min<int64_t>(A.T, static_cast<int64_t>(sm_count()) * rows_per_sm(A.N, false)));
+  if constexpr (VEC) {
+    const RowRing R = row_ring(A, XBF, HBF, bwd, grid);
+    if (R.stages)
+      return bwd ? launch_ring(residual_norm_bwd_ring_kernel<XBF, HBF, V>, grid, threads, A, R, st)
+                 : launch_ring(residual_norm_ring_kernel<XBF, HBF, V>, grid, threads, A, R, st);
+  }
   if (bwd) {
-    residual_norm_bwd_kernel<XBF, HBF, V, VEC><<<residual_norm_bwd_grid(A.T, A.N), threads, 0, st>>>(A);
+    residual_norm_bwd_kernel<XBF, HBF, V, VEC><<<grid, threads, 0, st>>>(A);
   } else {
     const int64_t cap = static_cast<int64_t>(sm_count()) * std::max(1, 2048 / threads);
     residual_norm_kernel<XBF, HBF, V, VEC><<<static_cast<unsigned>(std::min(A.T, cap)), threads, 0, st>>>(A);
@@ -360,7 +738,7 @@ static cudaError_t run_residual_norm(const ResidualNormArgs& A, bool bwd, int th
 
 template <bool XBF, bool HBF>
 static cudaError_t pick_residual_norm(const ResidualNormArgs& A, bool bwd, cudaStream_t st) {
-  const RowShape s = row_shape(A.N);
+  const RowShape s = row_shape(A.N, bwd);
   if (residual_vec(A, XBF)) {
     if (s.V == 1) return run_residual_norm<XBF, HBF, 1, true>(A, bwd, s.threads, st);
     if (s.V == 2) return run_residual_norm<XBF, HBF, 2, true>(A, bwd, s.threads, st);
@@ -378,13 +756,14 @@ static cudaError_t launch_residual(const ResidualNormArgs& A, bool xbf, bool hbf
 
 cudaError_t launch_residual_norm(const kda_norm_params_t& p, const void* x, const void* res,
                                  const void* gate, const float* post_w, const float* w, void* h,
-                                 void* y, cudaStream_t st) {
+                                 void* y, int32_t* err, cudaStream_t st) {
   ResidualNormArgs A{};
   A.x = x; A.res = res; A.gate = gate; A.post_w = post_w; A.w = w; A.out_h = h; A.out_y = y;
   A.T = p.tokens; A.N = p.features;
   A.gate_per_token = gate && p.gate_per_token;
   A.gate_stride = p.gate_row_stride ? p.gate_row_stride : p.features;
   A.eps = p.eps; A.scale = p.scale; A.inv_n = 1.f / static_cast<float>(p.features);
+  A.err = err;
   return launch_residual(A, p.x_dtype == KDA_DTYPE_BF16, p.h_dtype == KDA_DTYPE_BF16, false, st);
 }
 
@@ -396,7 +775,7 @@ cudaError_t launch_residual_norm_bwd(const kda_norm_params_t& p, const void* x, 
                                      const void* gate, const float* post_w, const float* w,
                                      const void* dy, const void* dh, void* dx, void* dres,
                                      void* dgate, float* dpost_w, float* dw, void* workspace,
-                                     cudaStream_t st) {
+                                     int32_t* err, cudaStream_t st) {
   ResidualNormArgs A{};
   A.x = x; A.res = h; A.gate = gate; A.post_w = post_w; A.w = w; A.dy = dy; A.dh = dh;
   A.out_h = dres; A.out_y = dx;
@@ -405,6 +784,7 @@ cudaError_t launch_residual_norm_bwd(const kda_norm_params_t& p, const void* x, 
   A.dgate = A.gate_per_token ? dgate : nullptr;
   A.gate_stride = p.gate_row_stride ? p.gate_row_stride : p.features;
   A.eps = p.eps; A.scale = p.scale; A.inv_n = 1.f / static_cast<float>(p.features);
+  A.err = err;
   A.part = static_cast<float*>(workspace);
   if (p.tokens == 0) {                          // sums over no tokens
     const size_t bytes = static_cast<size_t>(p.features) * 4;
@@ -420,260 +800,6 @@ cudaError_t launch_residual_norm_bwd(const kda_norm_params_t& p, const void* x, 
   const SumOuts outs{{dy ? dw : nullptr, post_w ? dpost_w : nullptr,
                       gate && !A.gate_per_token ? static_cast<float*>(dgate) : nullptr}};
   return launch_sum_parts(A.part, parts, p.features, 3, 1.f, outs, st);
-}
-
-// ---------------------------------------------------------------- gated_norm
-
-struct GatedNormArgs {
-  const void* o;
-  const void* gate;
-  const float* w;
-  const void* dy;
-  void* out;                // forward: y; backward: d_o
-  void* dgate;
-  float* part;              // [grid][D]
-  int64_t gate_stride;      // elements between tokens
-  uint32_t rows;            // T * H
-  int32_t H, D, act, lpr;   // lpr: lanes of a row, a power of two <= 32
-  float eps, inv_d;
-};
-
-// A row is read by `lpr` lanes of a warp (8 elements a lane and chunk, VPL chunks a lane), so a
-// warp works on 32 / lpr rows at a time and U such groups at once: with the head size 128 that
-// is 8 rows, 12 16-byte loads a lane in flight (o fp32, gate bf16) before the first reduction.
-// LPR = 16 (head sizes 65..128) fixes the lane count at compile time; LPR = 0 reads it from the
-// arguments (other head sizes).
-template <int LPR>
-__device__ __forceinline__ float row_sum(float v, int lpr) {
-  if constexpr (LPR > 0) {
-#pragma unroll
-    for (int off = LPR / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  } else {
-    for (int off = lpr / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  }
-  return v;
-}
-
-template <bool OBF, bool GBF, bool YBF, int LPR, int VPL, bool VEC>
-__global__ void __launch_bounds__(256) gated_norm_kernel(GatedNormArgs A) {
-  constexpr int U = VPL == 1 ? 4 : 1;
-  const int lpr = LPR > 0 ? LPR : A.lpr;
-  const int lane = threadIdx.x & 31;
-  const int rpw = 32 / lpr, sub = lane / lpr, c0 = lane % lpr;
-  const int D = A.D, step = VPL * lpr;
-  float w[VPL][8];
-#pragma unroll
-  for (int v = 0; v < VPL; ++v) load_params<VEC>(A.w, c0 + v * lpr, step, D, w[v]);
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
-  for (int64_t base = (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * (rpw * U); base < A.rows;
-       base += warps * (rpw * U)) {
-    Raw8<OBF> o[U][VPL];
-    Raw8<GBF> g[U][VPL];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t row = base + u * rpw + sub;
-      const bool in = row < A.rows;
-      const uint32_t r = in ? static_cast<uint32_t>(row) : 0u;
-      const uint32_t t = r / static_cast<uint32_t>(A.H);
-      const int64_t go = t * A.gate_stride + static_cast<int64_t>(r - t * A.H) * D;
-#pragma unroll
-      for (int v = 0; v < VPL; ++v) {
-        o[u][v] = load_chunk<OBF, VEC>(static_cast<const char*>(A.o) + static_cast<int64_t>(r) * D * (OBF ? 2 : 4),
-                                       c0 + v * lpr, step, in ? D : 0);
-        g[u][v] = load_chunk<GBF, VEC>(static_cast<const char*>(A.gate) + go * (GBF ? 2 : 4), c0 + v * lpr, step, in ? D : 0);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t row = base + u * rpw + sub;
-      float sq = 0.f;
-#pragma unroll
-      for (int v = 0; v < VPL; ++v)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sq += o[u][v].f32(e) * o[u][v].f32(e);
-      sq = row_sum<LPR>(sq, lpr);
-      const float rs = 1.f / sqrtf(sq * A.inv_d + A.eps);
-      if (row < A.rows) {
-#pragma unroll
-        for (int v = 0; v < VPL; ++v) {
-          float y[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            y[e] = o[u][v].f32(e) * rs * w[v][e] * act_f<YBF>(A.act, g[u][v].f32(e));
-          store_chunk<YBF, VEC>(static_cast<char*>(A.out) + row * D * (YBF ? 2 : 4), c0 + v * lpr, step, D, y);
-        }
-      }
-    }
-  }
-}
-
-template <bool OBF, bool GBF, bool YBF, int LPR, int VPL, bool VEC>
-__global__ void __launch_bounds__(256) gated_norm_bwd_kernel(GatedNormArgs A) {
-  constexpr int U = VPL == 1 ? 2 : 1;
-  __shared__ float s_dw[1024];
-  const int lpr = LPR > 0 ? LPR : A.lpr;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rpw = 32 / lpr, sub = lane / lpr, c0 = lane % lpr;
-  const int D = A.D, step = VPL * lpr;
-  float w[VPL][8], aw[VPL][8];
-#pragma unroll
-  for (int v = 0; v < VPL; ++v) {
-    load_params<VEC>(A.w, c0 + v * lpr, step, D, w[v]);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) aw[v][e] = 0.f;
-  }
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
-  for (int64_t base = (static_cast<int64_t>(blockIdx.x) * 8 + warp) * (rpw * U); base < A.rows;
-       base += warps * (rpw * U)) {
-    Raw8<OBF> o[U][VPL];
-    Raw8<GBF> g[U][VPL];
-    Raw8<YBF> dy[U][VPL];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t row = base + u * rpw + sub;
-      const bool in = row < A.rows;
-      const uint32_t r = in ? static_cast<uint32_t>(row) : 0u;
-      const uint32_t t = r / static_cast<uint32_t>(A.H);
-      const int64_t go = t * A.gate_stride + static_cast<int64_t>(r - t * A.H) * D;
-      const int n = in ? D : 0;                // rows past the end add zeros
-#pragma unroll
-      for (int v = 0; v < VPL; ++v) {
-        const int c = c0 + v * lpr;
-        o[u][v] = load_chunk<OBF, VEC>(static_cast<const char*>(A.o) + static_cast<int64_t>(r) * D * (OBF ? 2 : 4), c, step, n);
-        g[u][v] = load_chunk<GBF, VEC>(static_cast<const char*>(A.gate) + go * (GBF ? 2 : 4), c, step, n);
-        dy[u][v] = load_chunk<YBF, VEC>(static_cast<const char*>(A.dy) + static_cast<int64_t>(r) * D * (YBF ? 2 : 4), c, step, n);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t row = base + u * rpw + sub;
-      const bool in = row < A.rows;
-      float dn[VPL][8], dg[VPL][8];            // d act(gate), then its product with weight
-      float sq = 0.f, dot = 0.f;
-#pragma unroll
-      for (int v = 0; v < VPL; ++v)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float oo = o[u][v].f32(e), gg = g[u][v].f32(e), d = dy[u][v].f32(e);
-          float a, da;
-          if (A.act == KDA_ACT_NONE) {
-            a = gg; da = 1.f;
-          } else {
-            const float p = sigmoid_f<GBF>(gg), q = sigmoid_f<GBF>(-gg);
-            const bool silu = A.act == KDA_ACT_SILU;
-            a = silu ? (gg == -INFINITY ? 0.f : gg * p) : p;
-            da = silu ? (fabsf(gg) > 3e38f ? p : p * (1.f + gg * q)) : p * q;
-          }
-          sq += oo * oo;
-          dn[v][e] = d * a;
-          dot += dn[v][e] * w[v][e] * oo;
-          dg[v][e] = d * da * w[v][e] * oo;
-        }
-      sq = row_sum<LPR>(sq, lpr);
-      dot = row_sum<LPR>(dot, lpr);
-      const float rs = 1.f / sqrtf(sq * A.inv_d + A.eps);
-      const float m = dot * A.inv_d * rs * rs;
-#pragma unroll
-      for (int v = 0; v < VPL; ++v) {
-        float d_o[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float oo = o[u][v].f32(e);
-          aw[v][e] += dn[v][e] * (oo * rs);
-          d_o[e] = rs * (dn[v][e] * w[v][e] - oo * m);
-          dg[v][e] *= rs;
-        }
-        if (in) {
-          store_chunk<OBF, VEC>(static_cast<char*>(A.out) + row * D * (OBF ? 2 : 4), c0 + v * lpr, step, D, d_o);
-          store_chunk<GBF, VEC>(static_cast<char*>(A.dgate) + row * D * (GBF ? 2 : 4), c0 + v * lpr, step, D, dg[v]);
-        }
-      }
-    }
-  }
-  // this block's partial row of d_weight: lanes of the same columns, then the warps in order
-  for (int wv = 0; wv < 8; ++wv) {
-    if (warp == wv) {
-#pragma unroll
-      for (int v = 0; v < VPL; ++v)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float t = aw[v][e];
-          for (int off = lpr; off < 32; off <<= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-          const int i = chunk_index<VEC>(c0 + v * lpr, step, e);
-          if (sub == 0 && i < D) s_dw[i] = wv == 0 ? t : s_dw[i] + t;
-        }
-    }
-    __syncthreads();
-  }
-  for (int i = threadIdx.x; i < D; i += blockDim.x) A.part[static_cast<int64_t>(blockIdx.x) * D + i] = s_dw[i];
-}
-
-static int lanes_per_row(int D) {
-  int l = 1;
-  while (l < 32 && l * 8 < D) l *= 2;
-  return l;
-}
-
-static int gated_grid(int64_t rows, int D, bool bwd) {
-  const int lpr = lanes_per_row(D);
-  const int64_t per_block = static_cast<int64_t>(32 / lpr) * 8 * (D <= 256 ? (bwd ? 2 : 4) : 1);
-  const int64_t blocks = (rows + per_block - 1) / per_block;
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(blocks, static_cast<int64_t>(sm_count()) * (bwd ? 4 : 8))));
-}
-
-template <bool OBF, bool GBF, bool YBF, int LPR, int VPL, bool VEC>
-static cudaError_t run_gated(const GatedNormArgs& A, bool bwd, cudaStream_t st) {
-  const int grid = gated_grid(A.rows, A.D, bwd);
-  if (bwd) gated_norm_bwd_kernel<OBF, GBF, YBF, LPR, VPL, VEC><<<grid, 256, 0, st>>>(A);
-  else gated_norm_kernel<OBF, GBF, YBF, LPR, VPL, VEC><<<grid, 256, 0, st>>>(A);
-  return cudaGetLastError();
-}
-
-template <bool OBF, bool GBF, bool YBF>
-static cudaError_t pick_gated(const GatedNormArgs& A, bool bwd, cudaStream_t st) {
-  const bool vec = A.D % 8 == 0 && al16(A.o) && al16(A.gate) && al16(A.w) && al16(A.dy) && al16(A.out) &&
-                   al16(A.dgate) && A.gate_stride * (GBF ? 2 : 4) % 16 == 0;
-  if (A.D > 256) return vec ? run_gated<OBF, GBF, YBF, 0, 4, true>(A, bwd, st) : run_gated<OBF, GBF, YBF, 0, 4, false>(A, bwd, st);
-  if (!vec) return run_gated<OBF, GBF, YBF, 0, 1, false>(A, bwd, st);
-  return A.lpr == 16 ? run_gated<OBF, GBF, YBF, 16, 1, true>(A, bwd, st) : run_gated<OBF, GBF, YBF, 0, 1, true>(A, bwd, st);
-}
-
-static cudaError_t launch_gated(const kda_norm_params_t& p, GatedNormArgs A, bool bwd, cudaStream_t st) {
-  A.rows = static_cast<uint32_t>(p.tokens * p.num_heads);
-  A.H = p.num_heads; A.D = p.features; A.act = p.activation;
-  A.lpr = lanes_per_row(p.features);
-  A.gate_stride = p.gate_row_stride ? p.gate_row_stride : static_cast<int64_t>(p.num_heads) * p.features;
-  A.eps = p.eps; A.inv_d = 1.f / static_cast<float>(p.features);
-  const bool ob = p.x_dtype == KDA_DTYPE_BF16, gb = p.gate_dtype == KDA_DTYPE_BF16, yb = p.y_dtype == KDA_DTYPE_BF16;
-  if (ob) {
-    if (gb) return yb ? pick_gated<true, true, true>(A, bwd, st) : pick_gated<true, true, false>(A, bwd, st);
-    return yb ? pick_gated<true, false, true>(A, bwd, st) : pick_gated<true, false, false>(A, bwd, st);
-  }
-  if (gb) return yb ? pick_gated<false, true, true>(A, bwd, st) : pick_gated<false, true, false>(A, bwd, st);
-  return yb ? pick_gated<false, false, true>(A, bwd, st) : pick_gated<false, false, false>(A, bwd, st);
-}
-
-cudaError_t launch_gated_norm(const kda_norm_params_t& p, const void* o, const void* gate,
-                              const float* w, void* y, cudaStream_t st) {
-  GatedNormArgs A{};
-  A.o = o; A.gate = gate; A.w = w; A.out = y;
-  return launch_gated(p, A, false, st);
-}
-
-size_t gated_norm_bwd_workspace(const kda_norm_params_t& p) {
-  return static_cast<size_t>(gated_grid(p.tokens * p.num_heads, p.features, true)) * p.features * 4;
-}
-
-cudaError_t launch_gated_norm_bwd(const kda_norm_params_t& p, const void* o, const void* gate,
-                                  const float* w, const void* dy, void* d_o, void* dgate, float* dw,
-                                  void* workspace, cudaStream_t st) {
-  GatedNormArgs A{};
-  A.o = o; A.gate = gate; A.w = w; A.dy = dy; A.out = d_o; A.dgate = dgate;
-  A.part = static_cast<float*>(workspace);
-  const cudaError_t e = launch_gated(p, A, true, st);
-  if (e != cudaSuccess) return e;
-  return launch_sum_parts(A.part, gated_grid(p.tokens * p.num_heads, p.features, true), p.features, 1,
-                          1.f, SumOuts{{dw, nullptr, nullptr}}, st);
 }
 
 }  // namespace kda

@@ -5,8 +5,6 @@ kda_gated_norm_*).  Argument marshalling only, as in `kda.py`.
 from __future__ import annotations
 
 import ctypes
-import functools
-import inspect
 from typing import Optional
 
 import torch
@@ -18,6 +16,45 @@ from .kda import _QKV_DTYPES, _workspace
 _ACTIVATIONS = {"none": _lib.KDA_ACT_NONE, "relu": _lib.KDA_ACT_RELU, "silu": _lib.KDA_ACT_SILU,
                 "gelu": _lib.KDA_ACT_GELU, "sigmoid": _lib.KDA_ACT_SIGMOID}
 _NORM_GATES = ("sigmoid", "silu", "none")
+
+
+# A call's checks and parameter record depend only on its tensors' shapes, strides, types and
+# devices and on its scalars, so they are made once for each combination of those (`_sig`) and kept:
+# a decode step repeats the same few thousands of times, and the checks would cost more than its
+# kernels.  Nothing is kept by a tensor's address or contents.
+_PLANS: dict = {}
+_MAX_PLANS = 4096
+
+
+class _Plan:
+    __slots__ = ("fn", "params", "ref", "device", "index", "nbytes", "shape", "dtype", "dtype2")
+
+    def __init__(self, name, params, device, nbytes=0, shape=None, dtype=None, dtype2=None):
+        self.fn = getattr(_lib.load(), name)
+        self.params = params
+        self.ref = ctypes.byref(params)
+        self.device = device
+        self.index = device.index
+        self.nbytes = nbytes
+        self.shape = shape
+        self.dtype = dtype
+        self.dtype2 = dtype2
+
+
+def _sig(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+def _sig16(t):
+    """The same with the address's place within 16 bytes, where a copy depends on it."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device(), t.data_ptr() & 15)
+
+
+def _keep(key, plan):
+    if len(_PLANS) >= _MAX_PLANS:
+        _PLANS.clear()
+    _PLANS[key] = plan
+    return plan
 
 
 def _device(*ts):
@@ -38,32 +75,48 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _on_stream(fn):
+def _raw_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the handle of the current stream without building a Stream object (2 us a call), and the current
+# device without the check for initialisation, where torch has them
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _on(stream, t):
     """With `stream=`, the whole call runs with that stream current, so that the outputs and the
     workspace it allocates belong to the stream that uses them."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        with torch.cuda.stream(stream):
-            return fn(*args, **kw)
-    call.__signature__ = inspect.signature(fn).replace(parameters=[
-        *inspect.signature(fn).parameters.values(),
-        inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None,
-                          annotation=Optional[torch.cuda.Stream])])
-    return call
+    if stream.device != t.device:
+        raise ValueError("the stream is on another device than the tensors")
+    return torch.cuda.stream(stream)
 
 
-def _call(name, dev, *args):
-    """Calls entry point `name` on the current stream of the tensors' device, `dev` current."""
-    fn = getattr(_lib.load(), name)
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+def _call(plan, *args):
+    """Calls the plan's entry point on the current stream of its device, that device current."""
+    index = plan.index
+    if _current_device() == index:
+        st = plan.fn(plan.ref, *args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        with torch.cuda.device(index):
+            st = plan.fn(plan.ref, *args, _raw_stream(index))
     if st != _lib.KDA_OK:
-        raise KdaError(st, name)
+        raise KdaError(st, plan.fn.__name__)
+
+
+def _space(plan, workspace):
+    """The call's workspace: (tensor or None, its address or None, its bytes)."""
+    need = plan.nbytes
+    if need == 0:
+        return None, None, 0
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=plan.device)
+        return workspace, workspace.data_ptr(), need
+    if workspace.device != plan.device:
+        raise ValueError("all tensors must be on the same device")
+    _workspace(need, workspace, plan.device)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _rows(t, shape, dtypes, name):
@@ -109,32 +162,16 @@ def _unaligned(t, flag):
     return flag if t.data_ptr() % 16 else 0
 
 
-def _linear_workspace(p, backward, workspace, dev):
+def _linear_plan(key, p, backward, dev, shape, y_dtype, dw_dtype=None):
     n = ctypes.c_size_t(0)
     st = _lib.load().kda_linear_workspace_size(ctypes.byref(p), backward, ctypes.byref(n))
     if st != _lib.KDA_OK:
         raise KdaError(st, "kda_linear_workspace_size")
-    if n.value == 0:
-        return None, 0
-    workspace = _workspace(n.value, workspace, dev)
-    _device(workspace)
-    return workspace, workspace.numel() * workspace.element_size()
+    return _keep(key, _Plan("kda_linear_bwd" if backward else "kda_linear_fwd", p, dev, n.value, shape,
+                            y_dtype, dw_dtype))
 
 
-@_on_stream
-def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
-           activation: str = "none", residual: Optional[torch.Tensor] = None, scale: float = 1.0,
-           out_dtype: Optional[torch.dtype] = None, save_pre_activation: bool = False,
-           cuda_cores: bool = False, out: Optional[torch.Tensor] = None,
-           workspace: Optional[torch.Tensor] = None):
-    """Projection with its epilogue (kda_linear_fwd): residual + scale * act(x weight^T + bias).
-
-    x [T, K] and weight [N, K] in one dtype, rows dense with any stride (tensor cores with fp32
-    sums; float32 as three bfloat16 parts; `cuda_cores=True`: fp32 CUDA cores); bias [N] float32; residual [T, N] float32 or bfloat16.
-    `activation`: none, relu, silu, gelu (erf form) or sigmoid.  Returns y [T, N] in `out_dtype`
-    (default x's), or (y, z) with `save_pre_activation`, z [T, N] in x's dtype being what
-    `linear_bwd` needs as `pre_activation`.  `out` may be `residual` itself.
-    """
+def _plan_linear(key, x, weight, bias, activation, residual, scale, out_dtype, out, cuda_cores):
     dev = _device(x, weight, bias, residual, out)
     y_dtype = out.dtype if out is not None else (out_dtype or x.dtype)
     if out is not None and out_dtype is not None and out.dtype != out_dtype:
@@ -147,33 +184,53 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
     if residual is not None:
         p.residual_row_stride = _rows(residual, (T, N), tuple(_QKV_DTYPES), "residual")
         p.residual_dtype = _QKV_DTYPES[residual.dtype]
-    if out is None:
-        out = torch.empty((T, N), dtype=y_dtype, device=dev)
-    else:
+    if out is not None:
         p.y_row_stride = _rows(out, (T, N), (y_dtype,), "out")
-    z = torch.empty((T, N), dtype=x.dtype, device=dev) if save_pre_activation else None
-    workspace, nbytes = _linear_workspace(p, 0, workspace, dev)
-    _call("kda_linear_fwd", dev, ctypes.byref(p), _p(x), _p(weight), _p(bias),
-          _p(residual), _p(out), _p(z), _p(workspace), nbytes)
+    return _linear_plan(key, p, 0, dev, (T, N), y_dtype)
+
+
+def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
+           activation: str = "none", residual: Optional[torch.Tensor] = None, scale: float = 1.0,
+           out_dtype: Optional[torch.dtype] = None, save_pre_activation: bool = False,
+           cuda_cores: bool = False, out: Optional[torch.Tensor] = None,
+           workspace: Optional[torch.Tensor] = None,
+           stream: Optional[torch.cuda.Stream] = None):
+    """Projection with its epilogue (kda_linear_fwd): residual + scale * act(x weight^T + bias).
+
+    x [T, K] and weight [N, K] in one dtype, rows dense with any stride (tensor cores with fp32
+    sums; float32 as three bfloat16 parts; `cuda_cores=True`: fp32 CUDA cores); bias [N] float32;
+    residual [T, N] float32 or bfloat16.  `activation`: none, relu, silu, gelu (erf form) or
+    sigmoid.  Returns y [T, N] in `out_dtype` (default x's), or (y, z) with
+    `save_pre_activation`, z [T, N] in x's dtype being what `linear_bwd` needs as
+    `pre_activation`.  `out` may be `residual` itself.
+    """
+    if stream is not None:
+        with _on(stream, x):
+            return linear(x, weight, bias, activation=activation, residual=residual, scale=scale,
+                          out_dtype=out_dtype, save_pre_activation=save_pre_activation,
+                          cuda_cores=cuda_cores, out=out, workspace=workspace)
+    key = ("linear", x.shape, x.stride(), x.dtype, x.get_device(), x.data_ptr() & 15, _sig16(weight),
+           _sig(bias), activation, _sig(residual), scale, out_dtype, _sig(out), cuda_cores)
+    plan = _PLANS.get(key)
+    if plan is None:
+        plan = _plan_linear(key, x, weight, bias, activation, residual, scale, out_dtype, out,
+                            cuda_cores)
+    if out is None:
+        out = torch.empty(plan.shape, dtype=plan.dtype, device=plan.device)
+    z = x.new_empty(plan.shape) if save_pre_activation else None
+    space, address, nbytes = _space(plan, workspace)
+    _call(plan, x.data_ptr(), weight.data_ptr(), _p(bias), _p(residual),
+          out.data_ptr(), _p(z), address, nbytes)
     return (out, z) if save_pre_activation else out
 
 
-@_on_stream
-def linear_bwd(x: torch.Tensor, weight: torch.Tensor, d_y: torch.Tensor, *,
-               activation: str = "none", pre_activation: Optional[torch.Tensor] = None,
-               scale: float = 1.0, need_dx: bool = True, need_dw: bool = True,
-               need_bias: bool = False, dw_dtype: Optional[torch.dtype] = None,
-               cuda_cores: bool = False, workspace: Optional[torch.Tensor] = None):
-    """Backward of `linear` (kda_linear_bwd).  d_y [T, N] float32 or bfloat16; `pre_activation`
-    as `linear` returned it (needed with an activation).  Returns (dx [T, K] in x's dtype,
-    dw [N, K] in `dw_dtype` (default x's), dbias [N] float32), None for those not needed.
-    The residual's gradient is d_y itself."""
+def _plan_linear_bwd(key, x, weight, d_y, activation, pre_activation, scale, dw_dtype, cuda_cores):
     dev = _device(x, weight, d_y, pre_activation)
     if d_y.dtype not in _QKV_DTYPES:
         raise ValueError("d_y must be float32 or bfloat16")
     p = _linear_params(x, weight, activation, scale, d_y.dtype,
                        _lib.KDA_FLAG_CUDA_CORES if cuda_cores else 0)
-    (T, K), N = x.shape, weight.shape[0]
+    T, N = x.shape[0], weight.shape[0]
     p.y_row_stride = _rows(d_y, (T, N), (d_y.dtype,), "d_y")
     p.flags |= _unaligned(d_y, _lib.KDA_FLAG_UNALIGNED_DY)
     if activation != "none":
@@ -184,13 +241,38 @@ def linear_bwd(x: torch.Tensor, weight: torch.Tensor, d_y: torch.Tensor, *,
     if dw_dtype not in _QKV_DTYPES:
         raise ValueError("dw_dtype must be float32 or bfloat16")
     p.dw_dtype = _QKV_DTYPES[dw_dtype]
-    dx = torch.empty((T, K), dtype=x.dtype, device=dev) if need_dx else None
-    dw = torch.empty((N, K), dtype=dw_dtype, device=dev) if need_dw else None
-    dbias = torch.empty((N,), dtype=torch.float32, device=dev) if need_bias else None
-    workspace, nbytes = _linear_workspace(p, 1, workspace, dev)
-    _call("kda_linear_bwd", dev, ctypes.byref(p), _p(x), _p(weight),
-          _p(pre_activation) if activation != "none" else None, _p(d_y), _p(dx), _p(dw), _p(dbias),
-          _p(workspace), nbytes)
+    return _linear_plan(key, p, 1, dev, (T, N), d_y.dtype, dw_dtype)
+
+
+def linear_bwd(x: torch.Tensor, weight: torch.Tensor, d_y: torch.Tensor, *,
+               activation: str = "none", pre_activation: Optional[torch.Tensor] = None,
+               scale: float = 1.0, need_dx: bool = True, need_dw: bool = True,
+               need_bias: bool = False, dw_dtype: Optional[torch.dtype] = None,
+               cuda_cores: bool = False, workspace: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None):
+    """Backward of `linear` (kda_linear_bwd).  d_y [T, N] float32 or bfloat16; `pre_activation`
+    as `linear` returned it (needed with an activation).  Returns (dx [T, K] in x's dtype,
+    dw [N, K] in `dw_dtype` (default x's), dbias [N] float32), None for those not needed.
+    The residual's gradient is d_y itself."""
+    if stream is not None:
+        with _on(stream, x):
+            return linear_bwd(x, weight, d_y, activation=activation, pre_activation=pre_activation,
+                              scale=scale, need_dx=need_dx, need_dw=need_dw, need_bias=need_bias,
+                              dw_dtype=dw_dtype, cuda_cores=cuda_cores, workspace=workspace)
+    if activation == "none":
+        pre_activation = None
+    key = ("linear_bwd", _sig16(x), _sig16(weight), _sig16(d_y), activation, _sig(pre_activation),
+           scale, dw_dtype, cuda_cores)
+    plan = _PLANS.get(key)
+    if plan is None:
+        plan = _plan_linear_bwd(key, x, weight, d_y, activation, pre_activation, scale, dw_dtype,
+                                cuda_cores)
+    dx = x.new_empty(x.shape) if need_dx else None
+    dw = weight.new_empty(weight.shape, dtype=plan.dtype2) if need_dw else None
+    dbias = x.new_empty(plan.shape[1:], dtype=torch.float32) if need_bias else None
+    space, address, nbytes = _space(plan, workspace)
+    _call(plan, x.data_ptr(), weight.data_ptr(), _p(pre_activation),
+          d_y.data_ptr(), _p(dx), _p(dw), _p(dbias), address, nbytes)
     return dx, dw, dbias
 
 
@@ -206,14 +288,12 @@ def _norm_gate(gate, x, p, N):
         p.gate_row_stride = _rows(gate, tuple(x.shape), (x.dtype,), "a per-token gate")
 
 
-def _norm_workspace(p, gated, workspace, dev):
+def _norm_bytes(p, gated):
     n = ctypes.c_size_t(0)
     st = _lib.load().kda_norm_workspace_size(ctypes.byref(p), gated, ctypes.byref(n))
     if st != _lib.KDA_OK:
         raise KdaError(st, "kda_norm_workspace_size")
-    workspace = _workspace(n.value, workspace, dev)
-    _device(workspace)
-    return workspace, workspace.numel() * workspace.element_size()
+    return n.value
 
 
 def _residual_params(x, h_dtype, scale, eps):
@@ -224,22 +304,7 @@ def _residual_params(x, h_dtype, scale, eps):
                          h_dtype=_QKV_DTYPES[h_dtype], y_dtype=dt, eps=eps, scale=scale)
 
 
-@_on_stream
-def residual_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
-                  residual: Optional[torch.Tensor] = None,
-                  post_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
-                  scale: float = 1.0, eps: float = 1e-6, out: Optional[torch.Tensor] = None,
-                  h_out: Optional[torch.Tensor] = None):
-    """The norms around a block in one pass (kda_residual_norm_fwd).  With
-    rms(a) = a / sqrt(mean(a^2) + eps) over each row:
-
-        u = rms(x) * post_weight (x without one);  h = residual + scale * gate * u;
-        y = rms(h) * weight
-
-    x [T, N]; residual [T, N] (float32 or bfloat16: h's dtype); gate [N] float32 or [T, N] in x's
-    dtype (row stride free); weights [N] float32.  Returns (y in x's dtype, or None without
-    `weight`; h in the residual's dtype, x's without one).  `h_out` may be `residual`.
-    """
+def _plan_residual_norm(key, x, weight, residual, post_weight, gate, scale, eps, out, h_out):
     dev = _device(x, weight, residual, post_weight, gate, out, h_out)
     h_dtype = residual.dtype if residual is not None else x.dtype
     if h_dtype not in _QKV_DTYPES:
@@ -252,32 +317,51 @@ def residual_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
         if t is not None:
             _dense(t, (N,), torch.float32, name)
     _norm_gate(gate, x, p, N)
-    if h_out is None:
-        h_out = torch.empty(shape, dtype=h_dtype, device=dev)
-    else:
+    if h_out is not None:
         _dense(h_out, shape, h_dtype, "h_out")
-    if weight is None:
-        if out is not None:
+    if out is not None:
+        if weight is None:
             raise ValueError("out needs a weight")
-    elif out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=dev)
-    else:
         _dense(out, shape, x.dtype, "out")
-    _call("kda_residual_norm_fwd", dev, ctypes.byref(p), _p(x), _p(residual), _p(gate),
-          _p(post_weight), _p(weight), _p(h_out), _p(out))
+    return _keep(key, _Plan("kda_residual_norm_fwd", p, dev, 0, shape, h_dtype))
+
+
+def residual_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
+                  residual: Optional[torch.Tensor] = None,
+                  post_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                  scale: float = 1.0, eps: float = 1e-6, out: Optional[torch.Tensor] = None,
+                  h_out: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None):
+    """The norms around a block in one pass (kda_residual_norm_fwd).  With
+    rms(a) = a / sqrt(mean(a^2) + eps) over each row:
+
+        u = rms(x) * post_weight (x without one);  h = residual + scale * gate * u;
+        y = rms(h) * weight
+
+    x [T, N]; residual [T, N] (float32 or bfloat16: h's dtype); gate [N] float32 or [T, N] in x's
+    dtype (row stride free); weights [N] float32.  Returns (y in x's dtype, or None without
+    `weight`; h in the residual's dtype, x's without one).  `h_out` may be `residual`.
+    """
+    if stream is not None:
+        with _on(stream, x):
+            return residual_norm(x, weight, residual=residual, post_weight=post_weight, gate=gate,
+                                 scale=scale, eps=eps, out=out, h_out=h_out)
+    key = ("residual_norm", _sig(x), _sig(weight), _sig(residual), _sig(post_weight), _sig(gate),
+           scale, eps, _sig(out), _sig(h_out))
+    plan = _PLANS.get(key)
+    if plan is None:
+        plan = _plan_residual_norm(key, x, weight, residual, post_weight, gate, scale, eps, out,
+                                   h_out)
+    if h_out is None:
+        h_out = torch.empty(plan.shape, dtype=plan.dtype, device=plan.device)
+    if out is None and weight is not None:
+        out = x.new_empty(plan.shape)
+    _call(plan, x.data_ptr(), _p(residual), _p(gate), _p(post_weight),
+          _p(weight), h_out.data_ptr(), _p(out))
     return out, h_out
 
 
-@_on_stream
-def residual_norm_bwd(x: torch.Tensor, h: torch.Tensor, weight: Optional[torch.Tensor],
-                      d_y: Optional[torch.Tensor], d_h: Optional[torch.Tensor] = None, *,
-                      post_weight: Optional[torch.Tensor] = None,
-                      gate: Optional[torch.Tensor] = None, scale: float = 1.0, eps: float = 1e-6,
-                      workspace: Optional[torch.Tensor] = None):
-    """Backward of `residual_norm` (kda_residual_norm_bwd).  h as the forward returned it; d_y
-    [T, N] in x's dtype (None exactly without `weight`) and d_h [T, N] in h's dtype (None: zero)
-    are the gradients of y and h.  Returns (dx, d_residual in h's dtype, d_weight, d_post_weight,
-    d_gate), None where the forward had no such argument (d_residual is always formed)."""
+def _plan_residual_norm_bwd(key, x, h, weight, d_y, d_h, post_weight, gate, scale, eps):
     dev = _device(x, h, weight, d_y, d_h, post_weight, gate)
     if h.dtype not in _QKV_DTYPES:
         raise ValueError("h must be float32 or bfloat16")
@@ -296,18 +380,37 @@ def residual_norm_bwd(x: torch.Tensor, h: torch.Tensor, weight: Optional[torch.T
         if t is not None:
             _dense(t, (N,), torch.float32, name)
     _norm_gate(gate, x, p, N)
-    dx = torch.empty_like(x)
-    d_residual = torch.empty_like(h)
-    f32 = dict(dtype=torch.float32, device=dev)
-    d_weight = torch.empty((N,), **f32) if weight is not None else None
-    d_post = torch.empty((N,), **f32) if post_weight is not None else None
-    d_gate = None
-    if gate is not None:
-        d_gate = torch.empty(gate.shape, dtype=gate.dtype, device=dev)
-    workspace, nbytes = _norm_workspace(p, 0, workspace, dev)
-    _call("kda_residual_norm_bwd", dev, ctypes.byref(p), _p(x), _p(h), _p(gate),
-          _p(post_weight), _p(weight), _p(d_y), _p(d_h), _p(dx), _p(d_residual), _p(d_gate),
-          _p(d_post), _p(d_weight), _p(workspace), nbytes)
+    return _keep(key, _Plan("kda_residual_norm_bwd", p, dev, _norm_bytes(p, 0), (N,)))
+
+
+def residual_norm_bwd(x: torch.Tensor, h: torch.Tensor, weight: Optional[torch.Tensor],
+                      d_y: Optional[torch.Tensor], d_h: Optional[torch.Tensor] = None, *,
+                      post_weight: Optional[torch.Tensor] = None,
+                      gate: Optional[torch.Tensor] = None, scale: float = 1.0, eps: float = 1e-6,
+                      workspace: Optional[torch.Tensor] = None,
+                      stream: Optional[torch.cuda.Stream] = None):
+    """Backward of `residual_norm` (kda_residual_norm_bwd).  h as the forward returned it; d_y
+    [T, N] in x's dtype (None exactly without `weight`) and d_h [T, N] in h's dtype (None: zero)
+    are the gradients of y and h.  Returns (dx, d_residual in h's dtype, d_weight, d_post_weight,
+    d_gate), None where the forward had no such argument (d_residual is always formed)."""
+    if stream is not None:
+        with _on(stream, x):
+            return residual_norm_bwd(x, h, weight, d_y, d_h, post_weight=post_weight, gate=gate,
+                                     scale=scale, eps=eps, workspace=workspace)
+    key = ("residual_norm_bwd", _sig(x), _sig(h), _sig(weight), _sig(d_y), _sig(d_h),
+           _sig(post_weight), _sig(gate), scale, eps)
+    plan = _PLANS.get(key)
+    if plan is None:
+        plan = _plan_residual_norm_bwd(key, x, h, weight, d_y, d_h, post_weight, gate, scale, eps)
+    dx = x.new_empty(x.shape)
+    d_residual = h.new_empty(h.shape)
+    d_weight = weight.new_empty(plan.shape) if weight is not None else None
+    d_post = post_weight.new_empty(plan.shape) if post_weight is not None else None
+    d_gate = gate.new_empty(gate.shape) if gate is not None else None
+    space, address, nbytes = _space(plan, workspace)
+    _call(plan, x.data_ptr(), h.data_ptr(), _p(gate), _p(post_weight),
+          _p(weight), _p(d_y), _p(d_h), dx.data_ptr(), d_residual.data_ptr(), _p(d_gate),
+          _p(d_post), _p(d_weight), address, nbytes)
     return dx, d_residual, d_weight, d_post, d_gate
 
 
@@ -336,39 +439,64 @@ def _gated_params(o, gate, weight, y_dtype, activation, eps):
                          gate_row_stride=stride)
 
 
-@_on_stream
-def gated_norm(o: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, *,
-               activation: str = "sigmoid", eps: float = 1e-6,
-               out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """The output norm of the recurrence (kda_gated_norm_fwd): the RMS norm of each token's and
-    head's o row, times weight [D], times act(gate).  o [T, H, D] as `prefill` and `decode_step`
-    return it; gate [T, H, D] in either dtype, a column block of a packed projection if need be;
-    `activation` of the gate: sigmoid, silu or none.  Returns y [T, H, D] (default the gate's
-    dtype), ready as [T, H * D] for the output projection."""
+def _plan_gated_norm(key, o, gate, weight, activation, eps, out_dtype, out):
     dev = _device(o, gate, weight, out)
     y_dtype = out.dtype if out is not None else (out_dtype or gate.dtype)
     p = _gated_params(o, gate, weight, y_dtype, activation, eps)
-    if out is None:
-        out = torch.empty(o.shape, dtype=y_dtype, device=dev)
-    else:
+    if out is not None:
         _dense(out, o.shape, out_dtype or out.dtype, "out")
-    _call("kda_gated_norm_fwd", dev, ctypes.byref(p), _p(o), _p(gate), _p(weight), _p(out))
+    return _keep(key, _Plan("kda_gated_norm_fwd", p, dev, 0, o.shape, y_dtype))
+
+
+def gated_norm(o: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, *,
+               activation: str = "sigmoid", eps: float = 1e-6,
+               out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The output norm of the recurrence (kda_gated_norm_fwd): the RMS norm of each token's and
+    head's o row, times weight [D], times act(gate).  o [T, H, D] as `prefill` and `decode_step`
+    return it; gate [T, H, D] in either dtype, a column block of a packed projection if need be;
+    `activation` of the gate: sigmoid, silu or none (the gate itself).  Returns y [T, H, D]
+    (default the gate's dtype), ready as [T, H * D] for the output projection."""
+    if stream is not None:
+        with _on(stream, o):
+            return gated_norm(o, gate, weight, activation=activation, eps=eps, out_dtype=out_dtype,
+                              out=out)
+    key = ("gated_norm", _sig(o), _sig(gate), _sig(weight), activation, eps, out_dtype, _sig(out))
+    plan = _PLANS.get(key)
+    if plan is None:
+        plan = _plan_gated_norm(key, o, gate, weight, activation, eps, out_dtype, out)
+    if out is None:
+        out = torch.empty(plan.shape, dtype=plan.dtype, device=plan.device)
+    _call(plan, o.data_ptr(), gate.data_ptr(), weight.data_ptr(),
+          out.data_ptr())
     return out
 
 
-@_on_stream
-def gated_norm_bwd(o: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, d_y: torch.Tensor, *,
-                   activation: str = "sigmoid", eps: float = 1e-6,
-                   workspace: Optional[torch.Tensor] = None):
-    """Backward of `gated_norm` (kda_gated_norm_bwd).  Returns (d_o in o's dtype -- `prefill_bwd`'s
-    d_o for the fp32 o of `prefill` --, d_gate dense in the gate's dtype, d_weight [D] float32)."""
+def _plan_gated_norm_bwd(key, o, gate, weight, d_y, activation, eps):
     dev = _device(o, gate, weight, d_y)
     p = _gated_params(o, gate, weight, d_y.dtype, activation, eps)
     _dense(d_y, o.shape, d_y.dtype, "d_y")
-    d_o = torch.empty_like(o)
-    d_gate = torch.empty(gate.shape, dtype=gate.dtype, device=dev)
-    d_weight = torch.empty(weight.shape, dtype=torch.float32, device=dev)
-    workspace, nbytes = _norm_workspace(p, 1, workspace, dev)
-    _call("kda_gated_norm_bwd", dev, ctypes.byref(p), _p(o), _p(gate), _p(weight), _p(d_y),
-          _p(d_o), _p(d_gate), _p(d_weight), _p(workspace), nbytes)
+    return _keep(key, _Plan("kda_gated_norm_bwd", p, dev, _norm_bytes(p, 1)))
+
+
+def gated_norm_bwd(o: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, d_y: torch.Tensor, *,
+                   activation: str = "sigmoid", eps: float = 1e-6,
+                   workspace: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None):
+    """Backward of `gated_norm` (kda_gated_norm_bwd).  Returns (d_o in o's dtype -- `prefill_bwd`'s
+    d_o for the fp32 o of `prefill` --, d_gate dense in the gate's dtype, d_weight [D] float32)."""
+    if stream is not None:
+        with _on(stream, o):
+            return gated_norm_bwd(o, gate, weight, d_y, activation=activation, eps=eps,
+                                  workspace=workspace)
+    key = ("gated_norm_bwd", _sig(o), _sig(gate), _sig(weight), _sig(d_y), activation, eps)
+    plan = _PLANS.get(key)
+    if plan is None:
+        plan = _plan_gated_norm_bwd(key, o, gate, weight, d_y, activation, eps)
+    d_o = o.new_empty(o.shape)
+    d_gate = gate.new_empty(gate.shape)
+    d_weight = weight.new_empty(weight.shape)
+    space, address, nbytes = _space(plan, workspace)
+    _call(plan, o.data_ptr(), gate.data_ptr(), weight.data_ptr(),
+          d_y.data_ptr(), d_o.data_ptr(), d_gate.data_ptr(), d_weight.data_ptr(), address, nbytes)
     return d_o, d_gate, d_weight
