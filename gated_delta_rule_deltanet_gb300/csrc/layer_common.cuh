@@ -32,6 +32,7 @@ struct Raw8 {               // the chunk as loaded: no arithmetic waits on it un
     else
       return __uint_as_float(w[e]);
   }
+  __device__ __forceinline__ float2 f2(int e) const { return make_float2(f32(2 * e), f32(2 * e + 1)); }
   __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int i = 0; i < (BF ? 4 : 8); ++i) w[i] = 0;
@@ -117,6 +118,19 @@ __device__ __forceinline__ void load_params(const float* p, int c, int step, int
       x[e] = i < n ? __ldg(p + i) : 0.f;
     }
   }
+}
+
+// aligned forms on pairs
+__device__ __forceinline__ void load_params2(const float* p, int c, int n, float2 (&x)[4]) {
+  float v[8];
+  load_params<true>(p, c, 0, n, v);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = make_float2(v[2 * e], v[2 * e + 1]);
+}
+template <bool BF>
+__device__ __forceinline__ void store_pairs(void* row, int c, int n, const float2 (&x)[4]) {
+  const float v[8] = {x[0].x, x[0].y, x[1].x, x[1].y, x[2].x, x[2].y, x[3].x, x[3].y};
+  store_chunk<BF, true>(row, c, 0, n, v);
 }
 
 // ---------------------------------------------------------------- activations

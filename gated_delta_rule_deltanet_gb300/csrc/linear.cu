@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(256) dz_kernel(DzArgs A) {
 static int dz_rows(int64_t T, int N) {                    // blocks along the tokens
   const int64_t cols = (N + 255) / 256;
   const int64_t want = std::max<int64_t>(1, static_cast<int64_t>(sm_count()) * 6 / cols);
-  return static_cast<int>(std::max<int64_t>(1, std::min(want, (T + 31) / 32)));
+  return static_cast<int>(std::max<int64_t>(1, std::min(want, (T + 7) / 8)));
 }
 
 static bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }

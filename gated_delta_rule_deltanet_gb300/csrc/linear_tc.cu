@@ -17,10 +17,11 @@
 //                      accumulators alternate, one being multiplied into while eight warps
 //                      store the other.  Bound by the tensor pipe and, over seconds, by power.
 //   gemm_split_kernel  small products, mostly few rows (decode: the weight is the work).  One CTA
-//                      holds a 128 x BN tile; a cluster of S CTAs splits the sum over c and adds
-//                      its parts through distributed shared memory in rank order, so the
-//                      result does not depend on timing and needs no workspace.  Bound by HBM
-//                      for few rows: a deep TMA ring keeps the weight streaming.
+//                      holds a 128 x BN tile; a cluster of S CTAs splits the sum over c: each
+//                      pushes its part of every other CTA's columns into that CTA's shared
+//                      memory and adds what it receives in rank order, so the result does not
+//                      depend on timing and needs no workspace.  Bound by HBM for few rows: a deep
+//                      TMA ring keeps the weight streaming.
 //
 // fp32 operands are split into three bf16 parts, x = hi + mid + lo with every part rounded to
 // nearest, which hold all 24 bits; the six products of parts above 2^-27 relative are summed,
@@ -51,6 +52,18 @@ __device__ __forceinline__ unsigned long long now_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
+// One lane of the (converged) warp.  The role loops below run on whole warps with only the
+// asynchronous instructions under this predicate: loop state and descriptors then live in uniform
+// registers, where a loop inside a one-lane branch moves them there for every instruction.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -65,10 +78,13 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+// Bulk copy of `bytes` (a multiple of 16) from this CTA's shared memory to `dst` in another CTA's,
+// completing on that CTA's barrier `bar` (both shared::cluster addresses).
+__device__ __forceinline__ void push_cluster(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "r"(src), "r"(bytes), "r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -401,28 +417,28 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
   tc::fence_after_sync();
   const uint32_t tmem = s_tmem;
 
-  if (warp == 0) {
-    if (lane == 0) {                               // both CTAs: stage this CTA's rows of A and B
-      Ring<kPairStages> at;
-      int it = 0;                                  // loads issued so far
-      bool ok = true;
-      const uint32_t full0 = map_rank(tc::smem_u32(&full[0]), 0);
-      for (int t = first; t < tiles && ok; t += step) {
-        int ti, tj;
-        tile_of(t, A.tiles_i, A.tiles_j, ti, tj);
-        const int64_t i0 = static_cast<int64_t>(ti) * 256 + rank * 128;
-        const int64_t j0 = static_cast<int64_t>(tj) * 256 + rank * 128;
-        for (int k = 0; k < A.iters; ++k, ++it, at.next()) {
-          const int s = at.s;
-          if (!wait_phase(&empty[s], at.ph ^ 1, &s_abort)) {
-            ok = false;
-            break;
-          }
-          int kb, pa, pb;
-          part_of(A.iters, A.kblocks, k, kb, pa, pb);
+  if (warp == 0) {                                 // both CTAs: stage this CTA's rows of A and B
+    Ring<kPairStages> at;
+    int it = 0;                                    // loads issued so far
+    bool ok = true;
+    const uint32_t full0 = map_rank(tc::smem_u32(&full[0]), 0);
+    for (int t = first; t < tiles && ok; t += step) {
+      int ti, tj;
+      tile_of(t, A.tiles_i, A.tiles_j, ti, tj);
+      const int64_t i0 = static_cast<int64_t>(ti) * 256 + rank * 128;
+      const int64_t j0 = static_cast<int64_t>(tj) * 256 + rank * 128;
+      for (int k = 0; k < A.iters; ++k, ++it, at.next()) {
+        const int s = at.s;
+        if (!__all_sync(0xffffffffu, wait_phase(&empty[s], at.ph ^ 1, &s_abort))) {
+          ok = false;
+          break;
+        }
+        int kb, pa, pb;
+        part_of(A.iters, A.kblocks, k, kb, pa, pb);
+        const uint32_t bar = full0 + s * 8;
+        const uint32_t sa = smem + s * kPairStage, sb = sa + kOpBytes;
+        if (elect_one()) {
           if (rank == 0) tc::mbar_arrive_expect_tx(&full[s], 2 * kPairStage);
-          const uint32_t bar = full0 + s * 8;
-          const uint32_t sa = smem + s * kPairStage, sb = sa + kOpBytes;
           load_operand<AMN, 128>(sa, i0, kb * kBK, [&](uint32_t d, int32_t x, int32_t y) {
             tma_load_3d_pair(d, &map_a, x, y, pa, bar);
           });
@@ -430,13 +446,14 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             tma_load_3d_pair(d, &map_b, x, y, pb, bar);
           });
         }
+        __syncwarp();
       }
-      if (!ok) {
-        s_abort = 1;
-        raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
-      }
-      // after a timeout: the copies still in flight (their bytes count on the leader's barriers)
-      if (!ok && rank == 0) {
+    }
+    if (!ok && lane == 0) {
+      s_abort = 1;
+      raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
+      // the copies still in flight (their bytes count on the leader's barriers)
+      if (rank == 0) {
         const int from = it > kPairStages ? it - kPairStages : 0;
         for (int j = from; j < it; ++j)
           drain_phase(&full[j % kPairStages], (j / kPairStages) & 1);
@@ -444,7 +461,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {                  // the leader multiplies for the pair
+    if (rank == 0) {                               // the leader multiplies for the pair
       const uint32_t idesc = tc::idesc_f16(256, 256, tc::kBF16, false, AMN, BMN);
       const uint64_t da0 = operand_desc<AMN>(smem), db0 = operand_desc<BMN>(smem + kOpBytes);
       Ring<kPairStages> at;
@@ -452,34 +469,34 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step, ++n) {
         const int b = n & 1;
-        if (!wait_phase_cluster(&acc_empty[b], ((n >> 1) & 1) ^ 1, &s_abort)) {
+        if (!__all_sync(0xffffffffu, wait_phase_cluster(&acc_empty[b], ((n >> 1) & 1) ^ 1, &s_abort))) {
           ok = false;
           break;
         }
         tc::fence_after_sync();
         const uint32_t d = tmem + b * 256;
-        // One stage's products take 512 cycles and only two MMAs queue up behind the running one,
-        // so the next stage's barrier is polled before this stage's products are issued.
-        bool ready = tc::mbar_try_wait(&full[at.s], at.ph);
         for (int k = 0; k < A.iters; ++k) {
           const int s = at.s;
-          if (!ready && !wait_phase(&full[s], at.ph, &s_abort)) {
+          if (!__all_sync(0xffffffffu, wait_phase(&full[s], at.ph, &s_abort))) {
             ok = false;
             break;
           }
           tc::fence_after_sync();
           const uint64_t da = tc::desc_add(da0, s * kPairStage), db = tc::desc_add(db0, s * kPairStage);
           at.next();
-          ready = k + 1 < A.iters && tc::mbar_try_wait(&full[at.s], at.ph);
+          if (elect_one()) {
 #pragma unroll
-          for (int q = 0; q < kBK / 16; ++q)
-            mma_pair(d, tc::desc_add(da, q * k_advance<AMN>()), tc::desc_add(db, q * k_advance<BMN>()), idesc,
-                     (k | q) != 0);
-          commit_pair(&empty[s]);
+            for (int q = 0; q < kBK / 16; ++q)
+              mma_pair(d, tc::desc_add(da, q * k_advance<AMN>()), tc::desc_add(db, q * k_advance<BMN>()), idesc,
+                       (k | q) != 0);
+            commit_pair(&empty[s]);
+          }
+          __syncwarp();
         }
-        if (ok) commit_pair(&acc_full[b]);
+        if (ok && elect_one()) commit_pair(&acc_full[b]);
+        __syncwarp();
       }
-      if (!ok) {
+      if (!ok && lane == 0) {
         s_abort = 1;
         raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
         commit_pair(&drain);                       // the products still in flight
@@ -627,7 +644,9 @@ struct SplitShape {
   static constexpr int stages = BN <= 32 ? 5 : BN == 64 ? 4 : BN == 128 ? 6 : 4;
   static constexpr size_t smem = static_cast<size_t>(stage) * stages + 1024;
   static constexpr uint32_t cols = BN < 32 ? 32 : BN;
-  static_assert(static_cast<size_t>(stage) * stages >= 128 * BN * 4, "the partial tile reuses the ring");
+  // a split's own part and those received (7 shares of up to BN / 8 + 7 columns, or one of BN / 2)
+  static_assert(BN == 256 || static_cast<size_t>(stage) * stages >= 128 * 4 * (BN + 7 * 8 + BN),
+                "the parts reuse the ring");
 };
 
 template <bool AMN, bool BMN, int BN>
@@ -636,7 +655,7 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                   const __grid_constant__ OutMaps maps, const __grid_constant__ TcArgs A, const int splits) {
   using S = SplitShape<BN>;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t full[S::stages], empty[S::stages], acc_full;
+  __shared__ __align__(8) uint64_t full[S::stages], empty[S::stages], acc_full, received;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   const uint32_t smem = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -654,6 +673,7 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       tc::mbar_init(&empty[s], 1);
     }
     tc::mbar_init(&acc_full, 1);
+    tc::mbar_init(&received, 1);
     tc::fence_mbar_init();
     s_abort = 0;
   }
@@ -731,12 +751,15 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     if (!ready) raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
     tc::fence_after_sync();
   }
-  // The CTA's columns [c0, c1) of the tile.  Split: every CTA publishes its part of the tile as
-  // [column][row], and rank r adds and stores the r-th share of the columns (a multiple of 8),
-  // the parts in rank order.
+  // The CTA's columns [c0, c1) of the tile.  Split: every CTA lays its part of the tile out as
+  // [column][row]; rank r gets the r-th share of the columns (a multiple of 8) of every other
+  // part, one stretch of memory each, behind its own, and adds the parts in rank order.
   const int ncol = static_cast<int>(A.J - j0 < BN ? A.J - j0 : BN);
+  const int per = ((ncol + splits - 1) / splits + 7) / 8 * 8;
   int c0 = 0, c1 = ncol;
   if (splits > 1) {
+    c0 = min(ncol, rank * per);
+    c1 = min(ncol, c0 + per);
     if (warp >= 2) {
 #pragma unroll 1
       for (int c = 0; c < ncol; c += 16) {
@@ -746,18 +769,34 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 #pragma unroll
         for (int e = 0; e < 16; ++e) part[(c + e) * 128 + quad * 32 + lane] = __uint_as_float(r[e]);
       }
+      tc::fence_async_smem();
     }
-    cluster_sync();
-    const int per = ((ncol + splits - 1) / splits + 7) / 8 * 8;
-    c0 = min(ncol, rank * per);
-    c1 = min(ncol, c0 + per);
+    cluster_sync();                                // every ring is free, every part laid out
+    if (threadIdx.x == 0) {
+      if (c1 > c0) tc::mbar_arrive_expect_tx(&received, static_cast<uint32_t>((splits - 1) * (c1 - c0)) * 512);
+      for (int d = 1; d < splits; ++d) {           // the next ranks first, so that no CTA is everyone's target
+        const int to = rank + d < splits ? rank + d : rank + d - splits;
+        const int p0 = min(ncol, to * per), n = min(ncol, p0 + per) - p0;
+        // the sender's place among the receiver's others, in rank order
+        const int place = rank < to ? rank : rank - 1;
+        if (n > 0)
+          push_cluster(map_rank(smem + 128 * BN * 4 + place * per * 512, static_cast<uint32_t>(to)), smem + p0 * 512,
+                       static_cast<uint32_t>(n) * 512, map_rank(tc::smem_u32(&received), static_cast<uint32_t>(to)));
+      }
+      tc::bulk_commit();
+    }
+    if (warp >= 2 && c1 > c0) {
+      ready = !tc::named_sync_or(2, 128, !wait_phase_cluster(&received, 0, &s_abort)) && ready;
+      if (!ready) raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
+    }
   }
   // the finished tile, [column - c0][128], for TMA: behind the parts if there are any
-  unsigned char* out = smem_raw + (smem - tc::smem_u32(smem_raw)) + (splits > 1 ? 128 * BN * 4 : 0);
+  unsigned char* out = smem_raw + (smem - tc::smem_u32(smem_raw)) +
+                       (splits > 1 ? 128 * BN * 4 + (splits - 1) * per * 512 : 0);
   const int cpad = (c1 - c0 + 15) / 16 * 16;
   unsigned char* out_z = out + cpad * 128 * (A.epi.out_bf ? 2 : 4);
   if (warp >= 2 && ready) {
-    const uint32_t mine = smem + (quad * 32 + lane) * 4;
+    const float* mine = part + quad * 32 + lane;
 #pragma unroll 1
     for (int c = c0; c < c1; c += 16) {
       float v[16];
@@ -769,12 +808,10 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         const int n = min(16, c1 - c);
 #pragma unroll 1
         for (int p = 0; p < splits; ++p) {
-          const uint32_t at = map_rank(mine, static_cast<uint32_t>(p)) + c * 512;
-          float x[16];
+          const float* at = p == rank ? mine + c * 128
+                                      : mine + 128 * BN + ((p < rank ? p : p - 1) * per + c - c0) * 128;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = e < n ? ld_cluster(at + e * 512) : 0.f;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] += x[e];
+          for (int e = 0; e < 16; ++e) v[e] += e < n ? at[e * 128] : 0.f;
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] += bias;
@@ -814,7 +851,7 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       }
     }
   }
-  if (splits > 1) cluster_sync();                  // the peers are done reading this CTA's part
+  if (splits > 1 && threadIdx.x == 0) tc::bulk_wait_all();   // this CTA's pushes have left
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 1) {
@@ -944,7 +981,7 @@ cudaError_t launch_split(const Gemm& g, TcArgs A, int planes, int splits, cudaSt
   OutMaps out;
   // few columns are stored directly, and so is what does not fit behind the parts
   const size_t cols = splits == 1 ? BN : ((BN + splits - 1) / splits + 15) / 16 * 16;
-  const size_t bytes = (splits == 1 ? 0 : 128 * BN * 4) +
+  const size_t bytes = (splits == 1 ? 0 : 128 * BN * 4 + (splits - 1) * cols * 512) +
                        cols * 128 * ((g.epi.out_bf ? 2 : 4) + (!g.epi.z ? 0 : g.epi.z_bf ? 2 : 4));
   if (BN >= 64 && bytes <= SplitShape<BN>::smem - 1024) encode_outputs(g, &A, &out, 8, false);
   else A.staged = A.res_staged = false;
@@ -975,17 +1012,18 @@ cudaError_t launch_shape(const Gemm& g, const TcArgs& A, int planes, cudaStream_
   const int sms = sm_count();
   const int64_t big = ((g.I + 255) / 256) * ((g.J + 255) / 256);
   if (big >= sms / 4 && g.J > 128) return launch_pair<AMN, BMN>(g, A, planes, sms / 2, st);
-  // Few tiles: the narrowest tile that holds the rows (MN-major boxes are 64 wide), and enough
+  // Few tiles: the narrowest tile that holds the rows (MN-major boxes are 64 wide; 256 columns only
+  // without a split, whose parts would not fit), halved while too few CTAs would run, and enough
   // CTAs along c to fill the SMs, each with at least four steps.
   int bn = 16;
   while (bn < 256 && bn < g.J) bn *= 2;
   if (BMN) bn = std::max(bn, 64);
   auto tiles_for = [&](int n) { return ((g.I + 127) / 128) * ((g.J + n - 1) / n); };
-  while (bn > 64 && tiles_for(bn) * 8 < sms) bn /= 2;
+  auto room = [&](int n) { return static_cast<int64_t>(sms) * (n <= 64 ? 2 : 1); };   // CTAs that run at once
+  while (bn > 64 && tiles_for(bn) * 2 <= room(bn)) bn /= 2;
   const int64_t tiles = tiles_for(bn);
-  const int64_t room = static_cast<int64_t>(sms) * (bn <= 64 ? 2 : 1);   // CTAs that run at once
-  int splits = static_cast<int>(std::min<int64_t>(8, std::max<int64_t>(1, room / tiles)));
-  splits = std::max(1, std::min(splits, A.iters / 4));
+  int splits = static_cast<int>(std::min<int64_t>(8, std::max<int64_t>(1, room(bn) / tiles)));
+  splits = bn == 256 ? 1 : std::max(1, std::min(splits, A.iters / 4));
   if (tiles * splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   switch (bn) {
     case 16: if constexpr (!BMN) return launch_split<AMN, BMN, 16>(g, A, planes, splits, st);

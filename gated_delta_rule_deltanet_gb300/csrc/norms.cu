@@ -21,32 +21,34 @@ namespace kda {
 
 // ---------------------------------------------------------------- partial rows
 
+// A block adds 8 columns (one sector of each partial row) with 32 row lanes: some 20 loads a thread
+// for the 608 partial rows of the longest sums, 8 of them in flight (15 us with 32 columns and
+// 8 row lanes, 4 us so).
 __global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict__ part, int parts,
                                                         int64_t cols, float alpha, SumOuts outs) {
-  __shared__ float s[8][33];
-  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+  __shared__ float s[32][9];
+  const int col = threadIdx.x & 7, row = threadIdx.x >> 3;
   float* out = outs.p[blockIdx.y];
   if (!out) return;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + col;
   const int64_t stride = cols * gridDim.y;
   const float* src = part + blockIdx.y * cols + c;
-  float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+  float a = 0.f;
   if (c < cols) {
-    int p = row;
-    for (; p + 24 < parts; p += 32) {
-      a0 += src[p * stride];
-      a1 += src[(p + 8) * stride];
-      a2 += src[(p + 16) * stride];
-      a3 += src[(p + 24) * stride];
+    for (int p = row; p < parts; p += 32 * 8) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = p + 32 * u < parts ? src[(p + 32 * u) * stride] : 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) a += v[u];
     }
-    for (; p < parts; p += 8) a0 += src[p * stride];
   }
-  s[row][lane] = (a0 + a1) + (a2 + a3);
+  s[row][col] = a;
   __syncthreads();
   if (row == 0 && c < cols) {
     float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t += s[i][lane];
+    for (int i = 0; i < 32; ++i) t += s[i][col];
     out[c] = alpha * t;
   }
 }
@@ -56,7 +58,7 @@ cudaError_t launch_sum_parts(const float* part, int parts, int64_t cols, int seg
   bool any = false;
   for (int i = 0; i < segments; ++i) any = any || outs.p[i];
   if (!any || cols == 0) return cudaSuccess;
-  const dim3 grid(static_cast<unsigned>((cols + 31) / 32), static_cast<unsigned>(segments));
+  const dim3 grid(static_cast<unsigned>((cols + 7) / 8), static_cast<unsigned>(segments));
   sum_parts_kernel<<<grid, 256, 0, st>>>(part, parts, cols, alpha, outs);
   return cudaGetLastError();
 }
@@ -183,7 +185,7 @@ residual_norm_kernel(ResidualNormArgs A) {
 }
 
 template <bool XBF, bool HBF, int V, bool VEC>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(V == 1 ? 128 : V == 2 ? 256 : 512)
 residual_norm_bwd_kernel(ResidualNormArgs A) {
   __shared__ float s_buf[2][16][3];
   const int nt = blockDim.x, tid = threadIdx.x, step = V * nt;
@@ -505,7 +507,7 @@ residual_norm_ring_kernel(const ResidualNormArgs A, const RowRing R) {
 }
 
 template <bool XBF, bool HBF, int V>
-__global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
+__global__ void __launch_bounds__(V == 1 ? 128 : V == 2 ? 256 : 512, V == 1 ? 4 : V == 2 ? 2 : 1)
 residual_norm_bwd_ring_kernel(const ResidualNormArgs A, const RowRing R) {
   extern __shared__ __align__(128) unsigned char ring[];
   __shared__ float s_buf[2][16][3];
@@ -516,118 +518,121 @@ residual_norm_bwd_ring_kernel(const ResidualNormArgs A, const RowRing R) {
   const bool chan = A.gate && !A.gate_per_token;
   const uint32_t smem = tc::smem_u32(ring);
   ring_start<true>(A, R, S, smem, need_x);
-  float aw[V][8], ap[V][8], ag[V][8];          // this CTA's column sums
+  float2 aw[V][4], ap[V][4], ag[V][4];         // this CTA's column sums
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) aw[v][e] = ap[v][e] = ag[v][e] = 0.f;
+    for (int e = 0; e < 4; ++e) aw[v][e] = ap[v][e] = ag[v][e] = make_float2(0.f, 0.f);
   int par = 0, it = 0, s = 0;
   uint32_t ph = 0;
   for (int64_t t = blockIdx.x; t < A.T; t += gridDim.x, ++it) {
     ring_row<true>(A, R, S, smem, need_x, t, it, s, ph);
     const unsigned char* st = ring + s * R.stage;
     const int64_t xo = t * N * (XBF ? 2 : 4), ho = t * N * (HBF ? 2 : 4);
-    float s3[3] = {0.f, 0.f, 0.f};             // sum h^2, sum dy w h, sum x^2
+    // the row's arithmetic runs on fp32 pairs (f2: two elements an instruction)
+    float2 q0 = make_float2(0.f, 0.f), q1 = q0, q2 = q0;   // sum h^2, sum dy w h, sum x^2
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = tid + v * nt;
       if (A.dy) {
         const Raw8<HBF> h = smem_chunk<HBF>(st + R.r, c, N);
         const Raw8<XBF> dy = smem_chunk<XBF>(st + R.dy, c, N);
-        float p[8];
-        load_params<true>(A.w, c, 0, N, p);
+        float2 p[4];
+        load_params2(A.w, c, N, p);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          s3[0] += h.f32(e) * h.f32(e);
-          s3[1] += dy.f32(e) * p[e] * h.f32(e);
+        for (int e = 0; e < 4; ++e) {
+          q0 = fma2(h.f2(e), h.f2(e), q0);
+          q1 = fma2(mul2(dy.f2(e), p[e]), h.f2(e), q1);
         }
       }
       if (A.post_w) {
         const Raw8<XBF> x = smem_chunk<XBF>(st + R.x, c, N);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s3[2] += x.f32(e) * x.f32(e);
+        for (int e = 0; e < 4; ++e) q2 = fma2(x.f2(e), x.f2(e), q2);
       }
     }
+    float s3[3] = {q0.x + q0.y, q1.x + q1.y, q2.x + q2.y};
     block_sums<3>(s3, s_buf[par]);
     par ^= 1;
     const float rh = 1.f / sqrtf(s3[0] * A.inv_n + A.eps);
     const float mh = s3[1] * A.inv_n * rh * rh;            // mean(d rms(h)) r
     const float rx = A.post_w ? 1.f / sqrtf(s3[2] * A.inv_n + A.eps) : 1.f;
-    float d[V][8];                                         // dh, then du post_weight
-    float sx[3] = {0.f, 0.f, 0.f};
+    const float2 rh2 = make_float2(rh, rh), mh2 = make_float2(-mh, -mh), rx2 = make_float2(rx, rx);
+    const float2 scale2 = make_float2(A.scale, A.scale);
+    float2 d[V][4];                                        // dh, then du post_weight
+    float2 qx = make_float2(0.f, 0.f);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = tid + v * nt;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[v][e] = 0.f;
+      for (int e = 0; e < 4; ++e) d[v][e] = make_float2(0.f, 0.f);
       if (A.dy) {
         const Raw8<HBF> h = smem_chunk<HBF>(st + R.r, c, N);
         const Raw8<XBF> dy = smem_chunk<XBF>(st + R.dy, c, N);
-        float p[8];
-        load_params<true>(A.w, c, 0, N, p);
+        float2 p[4];
+        load_params2(A.w, c, N, p);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float hh = h.f32(e), dd = dy.f32(e);
-          aw[v][e] += dd * (hh * rh);
-          d[v][e] = rh * (dd * p[e] - hh * mh);
+        for (int e = 0; e < 4; ++e) {
+          const float2 hh = h.f2(e), dd = dy.f2(e);
+          aw[v][e] = fma2(dd, mul2(hh, rh2), aw[v][e]);
+          d[v][e] = mul2(rh2, fma2(hh, mh2, mul2(dd, p[e])));
         }
       }
       if (A.dh) {
         const Raw8<HBF> dh = smem_chunk<HBF>(st + R.dh, c, N);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[v][e] += dh.f32(e);
+        for (int e = 0; e < 4; ++e) d[v][e] = add2(d[v][e], dh.f2(e));
       }
-      if (A.out_h) store_chunk<HBF, true>(static_cast<char*>(A.out_h) + ho, c, 0, N, d[v]);
+      if (A.out_h) store_pairs<HBF>(static_cast<char*>(A.out_h) + ho, c, N, d[v]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[v][e] *= A.scale;
+      for (int e = 0; e < 4; ++e) d[v][e] = mul2(d[v][e], scale2);
       if (need_x) {
         const Raw8<XBF> x = smem_chunk<XBF>(st + R.x, c, N);
-        float pw[8];
-        if (A.post_w) {
-          load_params<true>(A.post_w, c, 0, N, pw);
-        } else {
+        float2 xn[4], pw[4];                               // rms(x) (x without a norm)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) pw[e] = 1.f;
-        }
+        for (int e = 0; e < 4; ++e) xn[e] = mul2(x.f2(e), rx2);
+        if (A.post_w) load_params2(A.post_w, c, N, pw);
         if (A.gate) {                                      // d_gate = scale dh u, du = scale dh gate
-          float dg[8], gg[8];
+          float2 dg[4], gg[4];
           if (chan) {
-            load_params<true>(static_cast<const float*>(A.gate), c, 0, N, gg);
+            load_params2(static_cast<const float*>(A.gate), c, N, gg);
           } else {
             const Raw8<XBF> g = smem_chunk<XBF>(st + R.g, c, N);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) gg[e] = g.f32(e);
+            for (int e = 0; e < 4; ++e) gg[e] = g.f2(e);
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            dg[e] = d[v][e] * (x.f32(e) * rx * pw[e]);
-            if (chan) ag[v][e] += dg[e];
-            d[v][e] *= gg[e];
+          for (int e = 0; e < 4; ++e) {
+            dg[e] = mul2(d[v][e], A.post_w ? mul2(xn[e], pw[e]) : xn[e]);
+            if (chan) ag[v][e] = add2(ag[v][e], dg[e]);
+            d[v][e] = mul2(d[v][e], gg[e]);
           }
-          if (!chan) store_chunk<XBF, true>(static_cast<char*>(A.dgate) + xo, c, 0, N, dg);
+          if (!chan) store_pairs<XBF>(static_cast<char*>(A.dgate) + xo, c, N, dg);
         }
         if (A.post_w) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            ap[v][e] += d[v][e] * (x.f32(e) * rx);
-            d[v][e] *= pw[e];
-            sx[0] += d[v][e] * x.f32(e);
+          for (int e = 0; e < 4; ++e) {
+            ap[v][e] = fma2(d[v][e], xn[e], ap[v][e]);
+            d[v][e] = mul2(d[v][e], pw[e]);
+            qx = fma2(d[v][e], x.f2(e), qx);
           }
         }
       }
-      if (!A.post_w) store_chunk<XBF, true>(static_cast<char*>(A.out_y) + xo, c, 0, N, d[v]);
+      if (!A.post_w) store_pairs<XBF>(static_cast<char*>(A.out_y) + xo, c, N, d[v]);
     }
     if (A.post_w) {
+      float sx[3] = {qx.x + qx.y, 0.f, 0.f};
       block_sums<3>(sx, s_buf[par]);
       par ^= 1;
-      const float mx = sx[0] * A.inv_n * rx * rx;
+      const float mx = -sx[0] * A.inv_n * rx * rx;
+      const float2 mx2 = make_float2(mx, mx);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int c = tid + v * nt;
         const Raw8<XBF> x = smem_chunk<XBF>(st + R.x, c, N);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[v][e] = rx * (d[v][e] - x.f32(e) * mx);
-        store_chunk<XBF, true>(static_cast<char*>(A.out_y) + xo, c, 0, N, d[v]);
+        for (int e = 0; e < 4; ++e) d[v][e] = mul2(rx2, fma2(x.f2(e), mx2, d[v][e]));
+        store_pairs<XBF>(static_cast<char*>(A.out_y) + xo, c, N, d[v]);
       }
     }
     __syncwarp();
@@ -641,34 +646,29 @@ residual_norm_bwd_ring_kernel(const ResidualNormArgs A, const RowRing R) {
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = tid + v * nt;
-    if (8 * c >= N) continue;
-    if (A.dy) store_chunk<false, true>(part, c, 0, N, aw[v]);
-    if (A.post_w) store_chunk<false, true>(part + N, c, 0, N, ap[v]);
-    if (chan) store_chunk<false, true>(part + 2 * N, c, 0, N, ag[v]);
+    if (A.dy) store_pairs<false>(part, c, N, aw[v]);
+    if (A.post_w) store_pairs<false>(part + N, c, N, ap[v]);
+    if (chan) store_pairs<false>(part + 2 * N, c, N, ag[v]);
   }
 }
 
-// Threads and elements a thread.  Forward: rows up to 1024 take one chunk a thread, up to 4096 two, up
-// to 16384 four, so that a row's reductions cross few warps.  Backward: one chunk up to 4096, two up
-// to 8192, four above: with 24 column sums a chunk beside the row, one chunk a thread leaves room for
-// 32 warps an SM.
+// Threads and elements a thread: rows up to 1024 take one chunk a thread, up to 4096 two, up to
+// 16384 four, so that a row's two reductions cross few warps (backward of 16384 x 2048 with one
+// chunk and twice the threads: 116 against 106 us).
 struct RowShape {
   int V, threads;
 };
-static RowShape row_shape(int N, bool bwd) {
+static RowShape row_shape(int N) {
   const int chunks = (N + 7) / 8;
-  const int V = bwd ? (chunks <= 512 ? 1 : chunks <= 1024 ? 2 : 4) : (chunks <= 128 ? 1 : chunks <= 512 ? 2 : 4);
+  const int V = chunks <= 128 ? 1 : chunks <= 512 ? 2 : 4;
   const int th = ((chunks + V - 1) / V + 31) / 32 * 32;
   return {V, th};
 }
 
 static bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// CTAs an SM that walk the rows: bounded by registers (64 a thread; 128 backward above one chunk)
-static int rows_per_sm(int N, bool bwd) {
-  const RowShape s = row_shape(N, bwd);
-  return std::max(1, (bwd && s.V > 1 ? 512 : 1024) / s.threads);
-}
+// CTAs an SM that walk the rows: bounded by registers (64 a thread forward, 128 backward)
+static int rows_per_sm(int N, bool bwd) { return std::max(1, (bwd ? 512 : 1024) / row_shape(N).threads); }
 
 static int residual_norm_bwd_grid(int64_t T, int N) {
   return static_cast<int>(std::min<int64_t>(std::max<int64_t>(T, 1), static_cast<int64_t>(sm_count()) * rows_per_sm(N, true)));
@@ -738,7 +738,7 @@ static cudaError_t run_residual_norm(const ResidualNormArgs& A, bool bwd, int th
 
 template <bool XBF, bool HBF>
 static cudaError_t pick_residual_norm(const ResidualNormArgs& A, bool bwd, cudaStream_t st) {
-  const RowShape s = row_shape(A.N, bwd);
+  const RowShape s = row_shape(A.N);
   if (residual_vec(A, XBF)) {
     if (s.V == 1) return run_residual_norm<XBF, HBF, 1, true>(A, bwd, s.threads, st);
     if (s.V == 2) return run_residual_norm<XBF, HBF, 2, true>(A, bwd, s.threads, st);

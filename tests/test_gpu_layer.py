@@ -122,6 +122,13 @@ def test_linear_shapes(T, K, N, dtype):
     linear_case(1, T, K, N, dtype, bias=True)
 
 
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("K,N", [(520, 70), (4096, 40), (37, 261)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_linear_few_tokens(T, K, N, dtype):
+    linear_case(10, T, K, N, dtype, act="silu", bias=True, res=dtype, scale=0.5)
+
+
 @pytest.mark.parametrize("T,K,N", [(1664, 1600, 1664), (1700, 1540, 1603)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_linear_pair_tiles(T, K, N, dtype):
@@ -309,8 +316,13 @@ def test_residual_norm_unaligned(N):
     residual_case(4, 9, N, "f32", "f32", post=True, gate="token", shift=1)
 
 
-def test_residual_norm_many_rows():
-    residual_case(5, 5000, 96, "bf16", "f32", post=True, gate="channel")
+@pytest.mark.parametrize("T,N", [(7500, 96), (2000, 2048), (1000, 4096), (470, 8200), (460, 16384)])
+@pytest.mark.parametrize("dtype,h_dtype,post,gate", [
+    ("bf16", "bf16", True, "token"), ("bf16", "f32", True, "channel"), ("f32", "f32", False, None),
+    ("bf16", "bf16", False, "token")])
+def test_residual_norm_many_rows(T, N, dtype, h_dtype, post, gate):
+    """Enough rows that each CTA walks several of them through its ring."""
+    residual_case(5, T, N, dtype, h_dtype, post=post, gate=gate, scale=0.5)
 
 
 def test_residual_norm_zero_rows_and_no_tokens():
