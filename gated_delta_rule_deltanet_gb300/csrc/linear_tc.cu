@@ -155,6 +155,7 @@ struct TcArgs {
   int64_t I, J;
   bool staged;              // y (and z) leave through shared memory and TMA
   bool res_staged;          // the residual arrives that way too (it has y's type)
+  int32_t bn;               // pair kernel: columns (j) of a tile, a multiple of 32 from 128 to 256
   int32_t cols;             // pair kernel: columns (j) of a staged chunk
   int32_t kblocks;          // 64-wide steps over c
   int32_t iters;            // kblocks times the products of parts
@@ -342,10 +343,10 @@ __device__ __forceinline__ void tile_of(int t, int tiles_i, int tiles_j, int& ti
   ti = grp * kRaster + in - tj * width;
 }
 
-// The chunks of one half (128 columns) of this CTA's tiles, in the order the epilogue forms them:
+// The chunks of one half (columns 0 .. 127 or 128 .. bn - 1) of this CTA's tiles, in the order the epilogue forms them:
 // per `cols` columns the pre-activation (if it is kept), then y.
 struct Chunk {
-  int t, c;
+  int t, c, width;
   bool z;
   int64_t i0, j0;
   __device__ __forceinline__ void place(const TcArgs& A, uint32_t rank, int half, int tiles, int step) {
@@ -353,8 +354,9 @@ struct Chunk {
       int ti, tj;
       tile_of(t, A.tiles_i, A.tiles_j, ti, tj);
       i0 = static_cast<int64_t>(ti) * 256 + rank * 128;
-      j0 = static_cast<int64_t>(tj) * 256 + half * 128;
-      if (i0 < A.I && j0 < A.J) return;
+      j0 = static_cast<int64_t>(tj) * A.bn + half * 128;
+      width = half ? A.bn - 128 : 128;
+      if (i0 < A.I && j0 < A.J && width > 0) return;
     }
   }
   __device__ __forceinline__ void start(const TcArgs& A, uint32_t rank, int half, int first, int tiles, int step) {
@@ -370,7 +372,7 @@ struct Chunk {
     }
     z = A.epi.z != nullptr;
     c += A.cols;
-    if (c >= 128 || j0 + c >= A.J) {
+    if (c >= width || j0 + c >= A.J) {
       c = 0;
       t += step;
       place(A, rank, half, tiles, step);
@@ -422,11 +424,13 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     int it = 0;                                    // loads issued so far
     bool ok = true;
     const uint32_t full0 = map_rank(tc::smem_u32(&full[0]), 0);
+    // both CTAs' rows (an MN-major operand comes in boxes of 64 columns, all 128 of them)
+    const uint32_t stage_bytes = 2 * (kOpBytes + (BMN ? kOpBytes : A.bn / 2 * kBK * 2));
     for (int t = first; t < tiles && ok; t += step) {
       int ti, tj;
       tile_of(t, A.tiles_i, A.tiles_j, ti, tj);
       const int64_t i0 = static_cast<int64_t>(ti) * 256 + rank * 128;
-      const int64_t j0 = static_cast<int64_t>(tj) * 256 + rank * 128;
+      const int64_t j0 = static_cast<int64_t>(tj) * A.bn + rank * (A.bn / 2);
       for (int k = 0; k < A.iters; ++k, ++it, at.next()) {
         const int s = at.s;
         if (!__all_sync(0xffffffffu, wait_phase(&empty[s], at.ph ^ 1, &s_abort))) {
@@ -438,7 +442,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         const uint32_t bar = full0 + s * 8;
         const uint32_t sa = smem + s * kPairStage, sb = sa + kOpBytes;
         if (elect_one()) {
-          if (rank == 0) tc::mbar_arrive_expect_tx(&full[s], 2 * kPairStage);
+          if (rank == 0) tc::mbar_arrive_expect_tx(&full[s], stage_bytes);
           load_operand<AMN, 128>(sa, i0, kb * kBK, [&](uint32_t d, int32_t x, int32_t y) {
             tma_load_3d_pair(d, &map_a, x, y, pa, bar);
           });
@@ -462,7 +466,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0) {                               // the leader multiplies for the pair
-      const uint32_t idesc = tc::idesc_f16(256, 256, tc::kBF16, false, AMN, BMN);
+      const uint32_t idesc = tc::idesc_f16(256, A.bn, tc::kBF16, false, AMN, BMN);
       const uint64_t da0 = operand_desc<AMN>(smem), db0 = operand_desc<BMN>(smem + kOpBytes);
       Ring<kPairStages> at;
       int n = 0;
@@ -562,14 +566,15 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
       const int b = n & 1;
       const int64_t ib = static_cast<int64_t>(ti) * 256 + rank * 128;
       const int64_t i = ib + quad * 32 + lane;
-      const int64_t j0 = static_cast<int64_t>(tj) * 256 + half * 128;
+      const int64_t j0 = static_cast<int64_t>(tj) * A.bn + half * 128;
+      const int width = half ? A.bn - 128 : 128;
       const bool in = i < A.I;
       const float bias = A.epi.bias && in ? __ldg(A.epi.bias + i) : 0.f;
       bool got = wait_warp(&acc_full[b], (n >> 1) & 1);
       tc::fence_after_sync();
       const uint32_t src = tmem + b * 256 + half * 128 + (static_cast<uint32_t>(quad * 32) << 16);
       // the columns of this half that exist (none where the CTA's rows are past the end)
-      const int ncol = ib < A.I ? static_cast<int>(A.J - j0 < 128 ? (A.J > j0 ? A.J - j0 : 0) : 128) : 0;
+      const int ncol = ib < A.I ? static_cast<int>(A.J - j0 < width ? (A.J > j0 ? A.J - j0 : 0) : width) : 0;
       if (!A.staged) {
 #pragma unroll 1
         for (int c = 0; c < ncol && got; c += 16) {
@@ -687,19 +692,20 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   const uint32_t tmem = s_tmem;
 
   if (warp == 0) {
-    if (lane == 0) {
-      bool ok = true;
-      int it = 0;
-      for (int k = k0; k < k1; ++k, ++it) {
-        const int s = it % S::stages;
-        if (!wait_phase(&empty[s], ((it / S::stages) & 1) ^ 1, &s_abort)) {
-          ok = false;
-          break;
-        }
-        int kb, pa, pb;
-        part_of(A.iters, A.kblocks, k, kb, pa, pb);
+    Ring<S::stages> at;
+    bool ok = true;
+    int k = k0;
+    for (; k < k1; ++k, at.next()) {
+      const int s = at.s;
+      if (!__all_sync(0xffffffffu, wait_phase(&empty[s], at.ph ^ 1, &s_abort))) {
+        ok = false;
+        break;
+      }
+      int kb, pa, pb;
+      part_of(A.iters, A.kblocks, k, kb, pa, pb);
+      const uint32_t sa = smem + s * S::stage, sb = sa + kOpBytes;
+      if (elect_one()) {
         tc::mbar_arrive_expect_tx(&full[s], S::stage);
-        const uint32_t sa = smem + s * S::stage, sb = sa + kOpBytes;
         load_operand<AMN, 128>(sa, i0, kb * kBK, [&](uint32_t d, int32_t x, int32_t y) {
           tc::tma_load_3d(d, &map_a, x, y, pa, &full[s]);
         });
@@ -707,37 +713,39 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
           tc::tma_load_3d(d, &map_b, x, y, pb, &full[s]);
         });
       }
-      if (!ok) {                                   // wait for the copies in flight
-        s_abort = 1;
-        raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
-        const int from = it > S::stages ? it - S::stages : 0;
-        for (int j = from; j < it; ++j)
-          drain_phase(&full[j % S::stages], (j / S::stages) & 1);
-      }
+      __syncwarp();
+    }
+    if (!ok && lane == 0) {                        // wait for the copies in flight
+      s_abort = 1;
+      raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
+      for (int j = max(0, k - k0 - S::stages); j < k - k0; ++j)
+        drain_phase(&full[j % S::stages], (j / S::stages) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = tc::idesc_f16(128, BN, tc::kBF16, false, AMN, BMN);
-      int it = 0;
-      for (int k = k0; k < k1; ++k, ++it) {
-        const int s = it % S::stages;
-        if (!wait_phase(&full[s], (it / S::stages) & 1, &s_abort)) {
-          s_abort = 1;
-          raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
-          break;
-        }
-        tc::fence_after_sync();
-        const uint64_t da = operand_desc<AMN>(smem + s * S::stage);
-        const uint64_t db = operand_desc<BMN>(smem + s * S::stage + kOpBytes);
+    const uint32_t idesc = tc::idesc_f16(128, BN, tc::kBF16, false, AMN, BMN);
+    const uint64_t da0 = operand_desc<AMN>(smem), db0 = operand_desc<BMN>(smem + kOpBytes);
+    Ring<S::stages> at;
+    for (int k = k0; k < k1; ++k) {
+      const int s = at.s;
+      if (!__all_sync(0xffffffffu, wait_phase(&full[s], at.ph, &s_abort))) {
+        s_abort = 1;
+        raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
+        break;
+      }
+      tc::fence_after_sync();
+      const uint64_t da = tc::desc_add(da0, s * S::stage), db = tc::desc_add(db0, s * S::stage);
+      at.next();
+      if (elect_one()) {
 #pragma unroll
         for (int q = 0; q < kBK / 16; ++q)
           tc::mma_ss(tmem, tc::desc_add(da, q * k_advance<AMN>()), tc::desc_add(db, q * k_advance<BMN>()), idesc,
                      (k > k0 || q > 0) ? 1u : 0u);
         tc::mma_commit(&empty[s]);
       }
-      tc::mma_commit(&acc_full);                   // also after a timeout: the products in flight
+      __syncwarp();
     }
+    if (elect_one()) tc::mma_commit(&acc_full);    // also after a timeout: the products in flight
     __syncwarp();
   }
   const int quad = warp & 3;
@@ -961,9 +969,23 @@ cudaError_t launch_pair(const Gemm& g, TcArgs A, int planes, int pairs, cudaStre
   OutMaps out;
   A.cols = g.epi.out_bf && (!g.epi.z || g.epi.z_bf) ? 32 : 16;
   encode_outputs(g, &A, &out, A.cols, true);
-  if (!encode(&ma, g.A, g.I, g.C, planes, 128) || !encode(&mb, g.B, g.J, g.C, planes, 128)) return cudaErrorInvalidValue;
+  // The width that wastes least in the last wave.  A narrower tile moves more bytes for its
+  // products, so it takes longer than its share of a wide one's time (measured on 16384 x 4096 x
+  // 4096, in thousandths).  dw of 16384 x 2048 -> 6144, 2.53 waves of 256 columns: 233 us, 2.95
+  // waves of 224: 218 us.
+  constexpr int kWidth[5] = {256, 224, 192, 160, 128}, kCost[5] = {1000, 885, 820, 760, 730};
+  int64_t best = 0;
+  for (int c = 0; c < 5; ++c) {
+    const int64_t tiles = ((g.I + 255) / 256) * ((g.J + kWidth[c] - 1) / kWidth[c]);
+    const int64_t cost = (tiles + pairs - 1) / pairs * kCost[c];
+    if (best == 0 || cost < best) {
+      best = cost;
+      A.bn = kWidth[c];
+    }
+  }
+  if (!encode(&ma, g.A, g.I, g.C, planes, 128) || !encode(&mb, g.B, g.J, g.C, planes, A.bn / 2)) return cudaErrorInvalidValue;
   A.tiles_i = static_cast<int32_t>((g.I + 255) / 256);
-  A.tiles_j = static_cast<int32_t>((g.J + 255) / 256);
+  A.tiles_j = static_cast<int32_t>((g.J + A.bn - 1) / A.bn);
   auto k = gemm_pair_kernel<AMN, BMN>;
   static std::atomic<uint64_t> raised{0};
   const cudaError_t e = raise_smem(k, kPairSmem, raised);
