@@ -61,8 +61,9 @@ cudaError_t launch_gemm_rows(const Gemm& g, cudaStream_t st);
 // The tensor-core product: operands are 16-byte aligned bf16 rows, `planes` (1, or 3 for the parts
 // of fp32) planes of rows * ld elements one after another.  C >= 1.
 cudaError_t launch_gemm_tc(const Gemm& g, int planes, cudaStream_t st);
-// rows of `cols` elements copied into rows of a multiple of 8 elements: bf16 as they are, fp32 as
-// three planes of bf16 parts
+// rows of `cols` elements copied into rows of `padded(cols)`: bf16 as they are, fp32 as three planes
+// of bf16 parts.  The rows are whole 128-byte lines, so that a box's rows cross none.
+inline int64_t padded(int64_t cols) { return (cols + 63) / 64 * 64; }
 size_t repacked_bytes(int64_t rows, int64_t cols, bool bf16);
 cudaError_t launch_repack(const void* src, int64_t src_ld, int64_t rows, int64_t cols, bool bf16, void* dst,
                           cudaStream_t st);

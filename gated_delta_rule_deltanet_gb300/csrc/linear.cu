@@ -233,7 +233,7 @@ static LinearLayout linear_layout(const kda_linear_params_t& p, bool bwd) {
     L.part = take(true, static_cast<size_t>(dz_rows(T, p.out_features)) * N * 4);
     // dz is formed unless the products can read d_y itself
     const bool unaligned = L.tc && bf && ((p.flags & KDA_FLAG_UNALIGNED_DY) || or_dense(p.y_row_stride, N) % 8);
-    L.dz_ld = (N + 7) / 8 * 8;
+    L.dz_ld = padded(N);
     L.dz = take(p.activation != KDA_ACT_NONE || p.y_dtype != p.dtype || unaligned,
                 static_cast<size_t>(T) * L.dz_ld * dtype_bytes(p.dtype));
     L.dz_planes = take(L.tc && !bf, repacked_bytes(T, N, false));
@@ -249,7 +249,7 @@ static cudaError_t stage(GemmOperand* X, size_t at, char* ws, int64_t rows, int6
   if (at == kNone) return cudaSuccess;
   const cudaError_t e = launch_repack(X->p, X->ld, rows, cols, bf16, ws + at, st);
   X->p = ws + at;
-  X->ld = (cols + 7) / 8 * 8;
+  X->ld = padded(cols);
   return e;
 }
 

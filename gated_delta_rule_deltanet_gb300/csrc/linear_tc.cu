@@ -645,10 +645,9 @@ constexpr int kSplitThreads = 192;                 // TMA, MMA, 4 epilogue warps
 template <int BN>
 struct SplitShape {
   static constexpr uint32_t stage = kOpBytes + BN * kBK * 2;
-  // the ring: as deep as 2 CTAs an SM allow for narrow tiles, 200 KB for the widest
-  static constexpr int stages = BN <= 32 ? 5 : BN == 64 ? 4 : BN == 128 ? 6 : 4;
+  // the ring: as deep as two CTAs an SM allow for the narrow tile, 200 KB for the others
+  static constexpr int stages = BN == 128 ? 6 : 4;
   static constexpr size_t smem = static_cast<size_t>(stage) * stages + 1024;
-  static constexpr uint32_t cols = BN < 32 ? 32 : BN;
   // a split's own part and those received (7 shares of up to BN / 8 + 7 columns, or one of BN / 2)
   static_assert(BN == 256 || static_cast<size_t>(stage) * stages >= 128 * 4 * (BN + 7 * 8 + BN),
                 "the parts reuse the ring");
@@ -683,7 +682,7 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     s_abort = 0;
   }
   if (warp == 1) {
-    tc::tmem_alloc(&s_tmem, S::cols);
+    tc::tmem_alloc(&s_tmem, BN);
     tc::tmem_relinquish();
   }
   tc::fence_before_sync();
@@ -864,7 +863,7 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   __syncthreads();
   if (warp == 1) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, S::cols);
+    tc::tmem_dealloc(tmem, BN);
   }
 }
 
@@ -880,8 +879,8 @@ __device__ __forceinline__ void split3(float x, uint16_t (&p)[3]) {
   p[2] = f32_to_bf16_bits(r - bf16_bits_to_f32(p[1]));
 }
 
-// rows of `cols` elements copied into rows of ld (a multiple of 8) elements: bf16 as they are,
-// fp32 as three planes of parts
+// rows of `cols` elements copied into rows of ld elements: bf16 as they are, fp32 as three planes
+// of parts
 template <bool BF>
 __global__ void __launch_bounds__(256) repack_kernel(const void* src, int64_t src_ld, int64_t rows, int64_t cols,
                                                      int64_t ld, uint16_t* dst) {
@@ -1001,11 +1000,11 @@ template <bool AMN, bool BMN, int BN>
 cudaError_t launch_split(const Gemm& g, TcArgs A, int planes, int splits, cudaStream_t st) {
   CUtensorMap ma, mb;
   OutMaps out;
-  // few columns are stored directly, and so is what does not fit behind the parts
+  // what does not fit behind the parts is stored directly
   const size_t cols = splits == 1 ? BN : ((BN + splits - 1) / splits + 15) / 16 * 16;
   const size_t bytes = (splits == 1 ? 0 : 128 * BN * 4 + (splits - 1) * cols * 512) +
                        cols * 128 * ((g.epi.out_bf ? 2 : 4) + (!g.epi.z ? 0 : g.epi.z_bf ? 2 : 4));
-  if (BN >= 64 && bytes <= SplitShape<BN>::smem - 1024) encode_outputs(g, &A, &out, 8, false);
+  if (bytes <= SplitShape<BN>::smem - 1024) encode_outputs(g, &A, &out, 8, false);
   else A.staged = A.res_staged = false;
   if (!encode(&ma, g.A, g.I, g.C, planes, 128) || !encode(&mb, g.B, g.J, g.C, planes, BN)) return cudaErrorInvalidValue;
   A.tiles_i = static_cast<int32_t>((g.I + 127) / 128);
@@ -1034,22 +1033,20 @@ cudaError_t launch_shape(const Gemm& g, const TcArgs& A, int planes, cudaStream_
   const int sms = sm_count();
   const int64_t big = ((g.I + 255) / 256) * ((g.J + 255) / 256);
   if (big >= sms / 4 && g.J > 128) return launch_pair<AMN, BMN>(g, A, planes, sms / 2, st);
-  // Few tiles: the narrowest tile that holds the rows (MN-major boxes are 64 wide; 256 columns only
-  // without a split, whose parts would not fit), halved while too few CTAs would run, and enough
-  // CTAs along c to fill the SMs, each with at least four steps.
-  int bn = 16;
+  // Few tiles.  64 columns at least (narrower tiles were no faster even for 16 rows), the tile halved
+  // while too few CTAs would run; 256 columns only unsplit, as the parts would not fit.
+  int bn = 64;
   while (bn < 256 && bn < g.J) bn *= 2;
-  if (BMN) bn = std::max(bn, 64);
   auto tiles_for = [&](int n) { return ((g.I + 127) / 128) * ((g.J + n - 1) / n); };
   auto room = [&](int n) { return static_cast<int64_t>(sms) * (n <= 64 ? 2 : 1); };   // CTAs that run at once
   while (bn > 64 && tiles_for(bn) * 2 <= room(bn)) bn /= 2;
   const int64_t tiles = tiles_for(bn);
-  int splits = static_cast<int>(std::min<int64_t>(8, std::max<int64_t>(1, room(bn) / tiles)));
+  // Splits fill the SMs, with four steps a CTA at least; beyond four ways the exchange costs more than
+  // it saves unless c is long (16 x 4096 -> 4096: 4 ways 8.4 us, 8 ways 9.5 us).
+  int splits = static_cast<int>(std::min<int64_t>(A.iters >= 128 ? 8 : 4, std::max<int64_t>(1, room(bn) / tiles)));
   splits = bn == 256 ? 1 : std::max(1, std::min(splits, A.iters / 4));
   if (tiles * splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   switch (bn) {
-    case 16: if constexpr (!BMN) return launch_split<AMN, BMN, 16>(g, A, planes, splits, st);
-    case 32: if constexpr (!BMN) return launch_split<AMN, BMN, 32>(g, A, planes, splits, st);
     case 64: return launch_split<AMN, BMN, 64>(g, A, planes, splits, st);
     case 128: return launch_split<AMN, BMN, 128>(g, A, planes, splits, st);
     default: return launch_split<AMN, BMN, 256>(g, A, planes, splits, st);
@@ -1059,13 +1056,13 @@ cudaError_t launch_shape(const Gemm& g, const TcArgs& A, int planes, cudaStream_
 }  // namespace
 
 size_t repacked_bytes(int64_t rows, int64_t cols, bool bf16) {
-  return static_cast<size_t>(rows) * ((cols + 7) / 8 * 8) * 2 * (bf16 ? 1 : 3);
+  return static_cast<size_t>(rows) * padded(cols) * 2 * (bf16 ? 1 : 3);
 }
 
 cudaError_t launch_repack(const void* src, int64_t src_ld, int64_t rows, int64_t cols, bool bf16, void* dst,
                           cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
-  const int64_t ld = (cols + 7) / 8 * 8, units = rows * ((cols + 1023) / 1024);
+  const int64_t ld = padded(cols), units = rows * ((cols + 1023) / 1024);
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, static_cast<int64_t>(sm_count()) * 16));
   if (bf16) repack_kernel<true><<<grid, 256, 0, st>>>(src, src_ld, rows, cols, ld, static_cast<uint16_t*>(dst));
   else repack_kernel<false><<<grid, 256, 0, st>>>(src, src_ld, rows, cols, ld, static_cast<uint16_t*>(dst));
