@@ -25,7 +25,10 @@
 //
 // fp32 operands are split into three bf16 parts, x = hi + mid + lo with every part rounded to
 // nearest, which hold all 24 bits; the six products of parts above 2^-27 relative are summed,
-// smallest first (the sum then rounds like an fp32 sum).
+// smallest first.  The tensor cores cut the accumulator's low bits at every step of 16 instead of
+// rounding them, always towards zero, so a long sum would lose several times fp32's rounding
+// (1.2e-6 relative at c = 1000, growing with c): the split kernel therefore moves the accumulator
+// into registers every 128 steps of c, where it is added with rounding (PROMOTE).
 //
 // Every wait is bounded; one that gives up raises KDA_DEVERR_TIMEOUT, and the CTAs leave through
 // the same barriers as otherwise.
@@ -158,23 +161,13 @@ struct TcArgs {
   int32_t bn;               // pair kernel: columns (j) of a tile, a multiple of 32 from 128 to 256
   int32_t cols;             // pair kernel: columns (j) of a staged chunk
   int32_t kblocks;          // 64-wide steps over c
-  int32_t iters;            // kblocks times the products of parts
   int32_t tiles_i, tiles_j;
   int32_t* err;
 };
 
-// Step `it` of the sum: with three parts (0 = hi, 1 = mid, 2 = lo) the products of parts follow one
-// another, smallest first; a is the part of A, b of B.
-__device__ __forceinline__ void part_of(int iters, int kblocks, int it, int& kb, int& a, int& b) {
-  if (iters == kblocks) {
-    kb = it; a = b = 0;
-    return;
-  }
-  const int q = it / kblocks;
-  kb = it - q * kblocks;
-  a = (0x201100 >> (4 * (5 - q))) & 15;          // (lo, hi) (hi, lo) (mid, mid) (mid, hi)
-  b = (0x021010 >> (4 * (5 - q))) & 15;          // (hi, mid) (hi, hi)
-}
+// The products of parts of one stretch of c, smallest first (0 = hi, 1 = mid, 2 = lo).
+__device__ __forceinline__ int part_a(int q) { return (0x201100 >> (4 * (5 - q))) & 15; }   // lo hi mid mid hi hi
+__device__ __forceinline__ int part_b(int q) { return (0x021010 >> (4 * (5 - q))) & 15; }   // hi lo mid hi mid hi
 
 // Waits for a phase; gives up after kWaitNs (far beyond any kernel's run) or once another role of
 // the CTA has.
@@ -431,23 +424,21 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
       tile_of(t, A.tiles_i, A.tiles_j, ti, tj);
       const int64_t i0 = static_cast<int64_t>(ti) * 256 + rank * 128;
       const int64_t j0 = static_cast<int64_t>(tj) * A.bn + rank * (A.bn / 2);
-      for (int k = 0; k < A.iters; ++k, ++it, at.next()) {
+      for (int k = 0; k < A.kblocks; ++k, ++it, at.next()) {
         const int s = at.s;
         if (!__all_sync(0xffffffffu, wait_phase(&empty[s], at.ph ^ 1, &s_abort))) {
           ok = false;
           break;
         }
-        int kb, pa, pb;
-        part_of(A.iters, A.kblocks, k, kb, pa, pb);
         const uint32_t bar = full0 + s * 8;
         const uint32_t sa = smem + s * kPairStage, sb = sa + kOpBytes;
         if (elect_one()) {
           if (rank == 0) tc::mbar_arrive_expect_tx(&full[s], stage_bytes);
-          load_operand<AMN, 128>(sa, i0, kb * kBK, [&](uint32_t d, int32_t x, int32_t y) {
-            tma_load_3d_pair(d, &map_a, x, y, pa, bar);
+          load_operand<AMN, 128>(sa, i0, k * kBK, [&](uint32_t d, int32_t x, int32_t y) {
+            tma_load_3d_pair(d, &map_a, x, y, 0, bar);
           });
-          load_operand<BMN, 128>(sb, j0, kb * kBK, [&](uint32_t d, int32_t x, int32_t y) {
-            tma_load_3d_pair(d, &map_b, x, y, pb, bar);
+          load_operand<BMN, 128>(sb, j0, k * kBK, [&](uint32_t d, int32_t x, int32_t y) {
+            tma_load_3d_pair(d, &map_b, x, y, 0, bar);
           });
         }
         __syncwarp();
@@ -479,7 +470,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         }
         tc::fence_after_sync();
         const uint32_t d = tmem + b * 256;
-        for (int k = 0; k < A.iters; ++k) {
+        for (int k = 0; k < A.kblocks; ++k) {
           const int s = at.s;
           if (!__all_sync(0xffffffffu, wait_phase(&full[s], at.ph, &s_abort))) {
             ok = false;
@@ -641,6 +632,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
 // ------------------------------------------------------------------ one CTA a tile, split over c
 
 constexpr int kSplitThreads = 192;                 // TMA, MMA, 4 epilogue warps
+constexpr int kStretch = 2;                        // 64-wide steps between promotions
 
 template <int BN>
 struct SplitShape {
@@ -653,13 +645,13 @@ struct SplitShape {
                 "the parts reuse the ring");
 };
 
-template <bool AMN, bool BMN, int BN>
+template <bool AMN, bool BMN, int BN, bool PROMOTE>
 __global__ void __launch_bounds__(kSplitThreads)
 gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                   const __grid_constant__ OutMaps maps, const __grid_constant__ TcArgs A, const int splits) {
   using S = SplitShape<BN>;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t full[S::stages], empty[S::stages], acc_full, received;
+  __shared__ __align__(8) uint64_t full[S::stages], empty[S::stages], acc_full[2], acc_empty[2], received;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   const uint32_t smem = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -668,21 +660,28 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   const int rank = splits > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int tile = blockIdx.x / splits;
   const int64_t i0 = static_cast<int64_t>(tile % A.tiles_i) * 128, j0 = static_cast<int64_t>(tile / A.tiles_i) * BN;
-  const int k0 = static_cast<int>(static_cast<int64_t>(A.iters) * rank / splits);
-  const int k1 = static_cast<int>(static_cast<int64_t>(A.iters) * (rank + 1) / splits);
+  const int k0 = static_cast<int>(static_cast<int64_t>(A.kblocks) * rank / splits);
+  const int k1 = static_cast<int>(static_cast<int64_t>(A.kblocks) * (rank + 1) / splits);
+  // the stretches of c that one accumulator takes, and the products of parts of each
+  const int stretch = PROMOTE ? kStretch : k1 - k0;
+  constexpr int kParts = PROMOTE ? 6 : 1;
+  constexpr uint32_t kCols = PROMOTE ? 2 * BN : BN;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::stages; ++s) {
       tc::mbar_init(&full[s], 1);
       tc::mbar_init(&empty[s], 1);
     }
-    tc::mbar_init(&acc_full, 1);
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(&acc_full[b], 1);
+      tc::mbar_init(&acc_empty[b], 4);             // the epilogue warps
+    }
     tc::mbar_init(&received, 1);
     tc::fence_mbar_init();
     s_abort = 0;
   }
   if (warp == 1) {
-    tc::tmem_alloc(&s_tmem, BN);
+    tc::tmem_alloc(&s_tmem, kCols);
     tc::tmem_relinquish();
   }
   tc::fence_before_sync();
@@ -692,32 +691,34 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 
   if (warp == 0) {
     Ring<S::stages> at;
+    int it = 0;
     bool ok = true;
-    int k = k0;
-    for (; k < k1; ++k, at.next()) {
-      const int s = at.s;
-      if (!__all_sync(0xffffffffu, wait_phase(&empty[s], at.ph ^ 1, &s_abort))) {
-        ok = false;
-        break;
+    for (int base = k0; base < k1 && ok; base += stretch)
+      for (int q = 0; q < kParts && ok; ++q) {
+        const int pa = PROMOTE ? part_a(q) : 0, pb = PROMOTE ? part_b(q) : 0;
+        for (int k = base; k < min(base + stretch, k1); ++k, ++it, at.next()) {
+          const int s = at.s;
+          if (!__all_sync(0xffffffffu, wait_phase(&empty[s], at.ph ^ 1, &s_abort))) {
+            ok = false;
+            break;
+          }
+          const uint32_t sa = smem + s * S::stage, sb = sa + kOpBytes;
+          if (elect_one()) {
+            tc::mbar_arrive_expect_tx(&full[s], S::stage);
+            load_operand<AMN, 128>(sa, i0, k * kBK, [&](uint32_t d, int32_t x, int32_t y) {
+              tc::tma_load_3d(d, &map_a, x, y, pa, &full[s]);
+            });
+            load_operand<BMN, BN>(sb, j0, k * kBK, [&](uint32_t d, int32_t x, int32_t y) {
+              tc::tma_load_3d(d, &map_b, x, y, pb, &full[s]);
+            });
+          }
+          __syncwarp();
+        }
       }
-      int kb, pa, pb;
-      part_of(A.iters, A.kblocks, k, kb, pa, pb);
-      const uint32_t sa = smem + s * S::stage, sb = sa + kOpBytes;
-      if (elect_one()) {
-        tc::mbar_arrive_expect_tx(&full[s], S::stage);
-        load_operand<AMN, 128>(sa, i0, kb * kBK, [&](uint32_t d, int32_t x, int32_t y) {
-          tc::tma_load_3d(d, &map_a, x, y, pa, &full[s]);
-        });
-        load_operand<BMN, BN>(sb, j0, kb * kBK, [&](uint32_t d, int32_t x, int32_t y) {
-          tc::tma_load_3d(d, &map_b, x, y, pb, &full[s]);
-        });
-      }
-      __syncwarp();
-    }
     if (!ok && lane == 0) {                        // wait for the copies in flight
       s_abort = 1;
       raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
-      for (int j = max(0, k - k0 - S::stages); j < k - k0; ++j)
+      for (int j = max(0, it - S::stages); j < it; ++j)
         drain_phase(&full[j % S::stages], (j / S::stages) & 1);
     }
     __syncwarp();
@@ -725,27 +726,41 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     const uint32_t idesc = tc::idesc_f16(128, BN, tc::kBF16, false, AMN, BMN);
     const uint64_t da0 = operand_desc<AMN>(smem), db0 = operand_desc<BMN>(smem + kOpBytes);
     Ring<S::stages> at;
-    for (int k = k0; k < k1; ++k) {
-      const int s = at.s;
-      if (!__all_sync(0xffffffffu, wait_phase(&full[s], at.ph, &s_abort))) {
-        s_abort = 1;
-        raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
+    bool ok = true;
+    int n = 0;
+    for (int base = k0; base < k1 && ok; base += stretch, ++n) {
+      const int b = n & 1;
+      const uint32_t d = tmem + (PROMOTE ? b * BN : 0);
+      if (PROMOTE && !__all_sync(0xffffffffu, wait_phase(&acc_empty[b], ((n >> 1) & 1) ^ 1, &s_abort))) {
+        ok = false;
         break;
       }
-      tc::fence_after_sync();
-      const uint64_t da = tc::desc_add(da0, s * S::stage), db = tc::desc_add(db0, s * S::stage);
-      at.next();
-      if (elect_one()) {
+      const int steps = kParts * (min(base + stretch, k1) - base);
+      for (int k = 0; k < steps; ++k) {
+        const int s = at.s;
+        if (!__all_sync(0xffffffffu, wait_phase(&full[s], at.ph, &s_abort))) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        const uint64_t da = tc::desc_add(da0, s * S::stage), db = tc::desc_add(db0, s * S::stage);
+        at.next();
+        if (elect_one()) {
 #pragma unroll
-        for (int q = 0; q < kBK / 16; ++q)
-          tc::mma_ss(tmem, tc::desc_add(da, q * k_advance<AMN>()), tc::desc_add(db, q * k_advance<BMN>()), idesc,
-                     (k > k0 || q > 0) ? 1u : 0u);
-        tc::mma_commit(&empty[s]);
+          for (int q = 0; q < kBK / 16; ++q)
+            tc::mma_ss(d, tc::desc_add(da, q * k_advance<AMN>()), tc::desc_add(db, q * k_advance<BMN>()), idesc,
+                       (k | q) != 0);
+          tc::mma_commit(&empty[s]);
+        }
+        __syncwarp();
       }
+      if (elect_one()) tc::mma_commit(&acc_full[b]);   // also after a timeout: the products in flight
       __syncwarp();
     }
-    if (elect_one()) tc::mma_commit(&acc_full);    // also after a timeout: the products in flight
-    __syncwarp();
+    if (!ok) {
+      s_abort = 1;
+      raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
+    }
   }
   const int quad = warp & 3;
   const int64_t i = i0 + quad * 32 + lane;
@@ -753,8 +768,31 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   const float bias = warp >= 2 && A.epi.bias && in ? __ldg(A.epi.bias + i) : 0.f;
   const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16);
   bool ready = true;
+  float sum[PROMOTE ? BN : 1];                     // PROMOTE: this thread's row of the tile
   if (warp >= 2) {
-    ready = !tc::named_sync_or(2, 128, !wait_phase(&acc_full, 0, &s_abort));
+    int n = 0;
+    if constexpr (PROMOTE) {
+#pragma unroll
+      for (int c = 0; c < BN; ++c) sum[c] = 0.f;
+      for (int base = k0; base < k1 && ready; base += stretch, ++n) {
+        ready = __all_sync(0xffffffffu, wait_phase(&acc_full[n & 1], (n >> 1) & 1, &s_abort));
+        if (!ready) break;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < BN; c += 16) {
+          float v[16];
+          load16(src + (n & 1) * BN + c, 0.f, v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sum[c + e] += v[e];
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&acc_empty[n & 1]);
+      }
+      ready = !tc::named_sync_or(2, 128, !ready);
+    } else {
+      ready = !tc::named_sync_or(2, 128, !wait_phase(&acc_full[0], 0, &s_abort));
+    }
     if (!ready) raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
     tc::fence_after_sync();
   }
@@ -768,13 +806,19 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     c0 = min(ncol, rank * per);
     c1 = min(ncol, c0 + per);
     if (warp >= 2) {
-#pragma unroll 1
-      for (int c = 0; c < ncol; c += 16) {
-        uint32_t r[16];
-        tc::tmem_ld16(src + c, r);
-        tc::tmem_wait_ld();
+      float* at = part + quad * 32 + lane;
+      if constexpr (PROMOTE) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) part[(c + e) * 128 + quad * 32 + lane] = __uint_as_float(r[e]);
+        for (int c = 0; c < BN; ++c)
+          if (c < ncol) at[c * 128] = sum[c];
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < ncol; c += 16) {
+          float v[16];
+          load16(src + c, 0.f, v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) at[(c + e) * 128] = v[e];
+        }
       }
       tc::fence_async_smem();
     }
@@ -804,11 +848,19 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   unsigned char* out_z = out + cpad * 128 * (A.epi.out_bf ? 2 : 4);
   if (warp >= 2 && ready) {
     const float* mine = part + quad * 32 + lane;
-#pragma unroll 1
-    for (int c = c0; c < c1; c += 16) {
+    // (unrolled where the tile is in registers, whose places are fixed at compile time)
+#pragma unroll (PROMOTE ? BN / 16 : 1)
+    for (int cc = 0; cc < BN; cc += 16) {
+      const int c = c0 + cc;
+      if (c >= c1) break;
       float v[16];
       if (splits == 1) {
-        load16(src + c, bias, v);
+        if constexpr (PROMOTE) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = sum[cc + e] + bias;
+        } else {
+          load16(src + c, bias, v);
+        }
       } else {
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = 0.f;
@@ -863,7 +915,7 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   __syncthreads();
   if (warp == 1) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, BN);
+    tc::tmem_dealloc(tmem, kCols);
   }
 }
 
@@ -996,7 +1048,7 @@ cudaError_t launch_pair(const Gemm& g, TcArgs A, int planes, int pairs, cudaStre
   return cudaGetLastError();
 }
 
-template <bool AMN, bool BMN, int BN>
+template <bool AMN, bool BMN, int BN, bool PROMOTE>
 cudaError_t launch_split(const Gemm& g, TcArgs A, int planes, int splits, cudaStream_t st) {
   CUtensorMap ma, mb;
   OutMaps out;
@@ -1009,7 +1061,7 @@ cudaError_t launch_split(const Gemm& g, TcArgs A, int planes, int splits, cudaSt
   if (!encode(&ma, g.A, g.I, g.C, planes, 128) || !encode(&mb, g.B, g.J, g.C, planes, BN)) return cudaErrorInvalidValue;
   A.tiles_i = static_cast<int32_t>((g.I + 127) / 128);
   A.tiles_j = static_cast<int32_t>((g.J + BN - 1) / BN);
-  auto k = gemm_split_kernel<AMN, BMN, BN>;
+  auto k = gemm_split_kernel<AMN, BMN, BN, PROMOTE>;
   static std::atomic<uint64_t> raised{0};
   cudaError_t e = raise_smem(k, SplitShape<BN>::smem, raised);
   if (e != cudaSuccess) return e;
@@ -1032,24 +1084,28 @@ template <bool AMN, bool BMN>
 cudaError_t launch_shape(const Gemm& g, const TcArgs& A, int planes, cudaStream_t st) {
   const int sms = sm_count();
   const int64_t big = ((g.I + 255) / 256) * ((g.J + 255) / 256);
-  if (big >= sms / 4 && g.J > 128) return launch_pair<AMN, BMN>(g, A, planes, sms / 2, st);
+  if (planes == 1 && big >= sms / 4 && g.J > 128) return launch_pair<AMN, BMN>(g, A, planes, sms / 2, st);
   // Few tiles.  64 columns at least (narrower tiles were no faster even for 16 rows), the tile halved
   // while too few CTAs would run; 256 columns only unsplit, as the parts would not fit.
   int bn = 64;
-  while (bn < 256 && bn < g.J) bn *= 2;
+  while (bn < (planes == 1 ? 256 : 128) && bn < g.J) bn *= 2;
   auto tiles_for = [&](int n) { return ((g.I + 127) / 128) * ((g.J + n - 1) / n); };
   auto room = [&](int n) { return static_cast<int64_t>(sms) * (n <= 64 ? 2 : 1); };   // CTAs that run at once
   while (bn > 64 && tiles_for(bn) * 2 <= room(bn)) bn /= 2;
   const int64_t tiles = tiles_for(bn);
   // Splits fill the SMs, with four steps a CTA at least; beyond four ways the exchange costs more than
   // it saves unless c is long (16 x 4096 -> 4096: 4 ways 8.4 us, 8 ways 9.5 us).
-  int splits = static_cast<int>(std::min<int64_t>(A.iters >= 128 ? 8 : 4, std::max<int64_t>(1, room(bn) / tiles)));
-  splits = bn == 256 ? 1 : std::max(1, std::min(splits, A.iters / 4));
+  const int steps = A.kblocks * (planes == 1 ? 1 : 6);
+  int splits = static_cast<int>(std::min<int64_t>(steps >= 128 ? 8 : 4, std::max<int64_t>(1, room(bn) / tiles)));
+  splits = bn == 256 ? 1 : std::max(1, std::min(splits, std::min(steps / 4, A.kblocks)));
   if (tiles * splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  if (planes == 3)
+    return bn == 64 ? launch_split<AMN, BMN, 64, true>(g, A, planes, splits, st)
+                    : launch_split<AMN, BMN, 128, true>(g, A, planes, splits, st);
   switch (bn) {
-    case 64: return launch_split<AMN, BMN, 64>(g, A, planes, splits, st);
-    case 128: return launch_split<AMN, BMN, 128>(g, A, planes, splits, st);
-    default: return launch_split<AMN, BMN, 256>(g, A, planes, splits, st);
+    case 64: return launch_split<AMN, BMN, 64, false>(g, A, planes, splits, st);
+    case 128: return launch_split<AMN, BMN, 128, false>(g, A, planes, splits, st);
+    default: return launch_split<AMN, BMN, 256, false>(g, A, planes, splits, st);
   }
 }
 
@@ -1076,7 +1132,6 @@ cudaError_t launch_gemm_tc(const Gemm& g, int planes, cudaStream_t st) {
   A.epi = g.epi;
   A.I = g.I; A.J = g.J;
   A.kblocks = static_cast<int32_t>((g.C + kBK - 1) / kBK);
-  A.iters = A.kblocks * (planes == 3 ? 6 : 1);
   A.err = g.err;
   if (g.A.mn) return g.B.mn ? launch_shape<true, true>(g, A, planes, st) : launch_shape<true, false>(g, A, planes, st);
   return launch_shape<false, false>(g, A, planes, st);
