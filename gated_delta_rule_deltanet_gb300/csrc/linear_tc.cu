@@ -28,7 +28,10 @@
 // smallest first.  The tensor cores cut the accumulator's low bits at every step of 16 instead of
 // rounding them, always towards zero, so a long sum would lose several times fp32's rounding
 // (1.2e-6 relative at c = 1000, growing with c): the split kernel therefore moves the accumulator
-// into registers every 128 steps of c, where it is added with rounding (PROMOTE).
+// into registers every 128 steps of c, where it is added with rounding (PROMOTE).  The pair kernel
+// does the same every 512 steps, into a third stretch of tensor memory, where bf16 operands have
+// an fp32 result over more than 1024 steps (c = 4096: 4.4e-6 of the norm without, 4.8e-7 with; the tile is then 160
+// columns wide, three of which fit).  A bf16 result rounds by far more than the truncation.
 //
 // Every wait is bounded; one that gives up raises KDA_DEVERR_TIMEOUT, and the CTAs leave through
 // the same barriers as otherwise.
@@ -159,8 +162,10 @@ struct TcArgs {
   bool staged;              // y (and z) leave through shared memory and TMA
   bool res_staged;          // the residual arrives that way too (it has y's type)
   int32_t bn;               // pair kernel: columns (j) of a tile, a multiple of 32 from 128 to 256
+  int32_t first_half;       // and those of them that the first four epilogue warps store
   int32_t cols;             // pair kernel: columns (j) of a staged chunk
   int32_t kblocks;          // 64-wide steps over c
+  int32_t parts;            // products of parts: 6 for fp32 operands, else 1
   int32_t tiles_i, tiles_j;
   int32_t* err;
 };
@@ -319,6 +324,8 @@ __device__ __forceinline__ void put16(unsigned char* tile, bool bf, int col, int
 // ------------------------------------------------------------------ pairs of CTAs, 256 x 256 tiles
 
 constexpr int kPairStages = 6;
+constexpr int kPairStretch = 8;                    // PROMOTE: 64-wide steps in one accumulator
+constexpr int kPromoteBN = 160;
 constexpr int kPairThreads = 384;                  // TMA, MMA, 2 output warps, 8 epilogue warps
 constexpr uint32_t kPairStage = 2 * kOpBytes;
 constexpr uint32_t kSlot = 8192;                   // a staged chunk: 128 x 32 bf16 or 128 x 16 fp32
@@ -336,7 +343,7 @@ __device__ __forceinline__ void tile_of(int t, int tiles_i, int tiles_j, int& ti
   ti = grp * kRaster + in - tj * width;
 }
 
-// The chunks of one half (columns 0 .. 127 or 128 .. bn - 1) of this CTA's tiles, in the order the epilogue forms them:
+// The chunks of one half (the first columns or the others) of this CTA's tiles, in the order the epilogue forms them:
 // per `cols` columns the pre-activation (if it is kept), then y.
 struct Chunk {
   int t, c, width;
@@ -347,8 +354,8 @@ struct Chunk {
       int ti, tj;
       tile_of(t, A.tiles_i, A.tiles_j, ti, tj);
       i0 = static_cast<int64_t>(ti) * 256 + rank * 128;
-      j0 = static_cast<int64_t>(tj) * A.bn + half * 128;
-      width = half ? A.bn - 128 : 128;
+      j0 = static_cast<int64_t>(tj) * A.bn + half * A.first_half;
+      width = half ? A.bn - A.first_half : A.first_half;
       if (i0 < A.I && j0 < A.J && width > 0) return;
     }
   }
@@ -373,7 +380,7 @@ struct Chunk {
   }
 };
 
-template <bool AMN, bool BMN>
+template <bool AMN, bool BMN, bool PROMOTE>
 __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
 gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                  const __grid_constant__ OutMaps maps, const __grid_constant__ TcArgs A) {
@@ -387,6 +394,9 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
   const uint32_t rank = cluster_rank();
   const int tiles = A.tiles_i * A.tiles_j;
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  // columns of an accumulator, and the steps of c that one takes
+  constexpr int kAcc = PROMOTE ? kPromoteBN : 256;
+  const int stretch = PROMOTE ? kPairStretch : A.kblocks;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPairStages; ++s) {
@@ -462,34 +472,37 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
       Ring<kPairStages> at;
       int n = 0;
       bool ok = true;
-      for (int t = first; t < tiles && ok; t += step, ++n) {
-        const int b = n & 1;
-        if (!__all_sync(0xffffffffu, wait_phase_cluster(&acc_empty[b], ((n >> 1) & 1) ^ 1, &s_abort))) {
-          ok = false;
-          break;
-        }
-        tc::fence_after_sync();
-        const uint32_t d = tmem + b * 256;
-        for (int k = 0; k < A.kblocks; ++k) {
-          const int s = at.s;
-          if (!__all_sync(0xffffffffu, wait_phase(&full[s], at.ph, &s_abort))) {
+      for (int t = first; t < tiles && ok; t += step) {
+        for (int base = 0; base < A.kblocks && ok; base += stretch, ++n) {
+          const int b = n & 1;
+          if (!__all_sync(0xffffffffu, wait_phase_cluster(&acc_empty[b], ((n >> 1) & 1) ^ 1, &s_abort))) {
             ok = false;
             break;
           }
           tc::fence_after_sync();
-          const uint64_t da = tc::desc_add(da0, s * kPairStage), db = tc::desc_add(db0, s * kPairStage);
-          at.next();
-          if (elect_one()) {
+          const uint32_t d = tmem + b * kAcc;
+          const int k1 = min(A.kblocks, base + stretch);
+          for (int k = base; k < k1; ++k) {
+            const int s = at.s;
+            if (!__all_sync(0xffffffffu, wait_phase(&full[s], at.ph, &s_abort))) {
+              ok = false;
+              break;
+            }
+            tc::fence_after_sync();
+            const uint64_t da = tc::desc_add(da0, s * kPairStage), db = tc::desc_add(db0, s * kPairStage);
+            at.next();
+            if (elect_one()) {
 #pragma unroll
-            for (int q = 0; q < kBK / 16; ++q)
-              mma_pair(d, tc::desc_add(da, q * k_advance<AMN>()), tc::desc_add(db, q * k_advance<BMN>()), idesc,
-                       (k | q) != 0);
-            commit_pair(&empty[s]);
+              for (int q = 0; q < kBK / 16; ++q)
+                mma_pair(d, tc::desc_add(da, q * k_advance<AMN>()), tc::desc_add(db, q * k_advance<BMN>()), idesc,
+                         k > base || q > 0);
+              commit_pair(&empty[s]);
+            }
+            __syncwarp();
           }
+          if (ok && elect_one()) commit_pair(&acc_full[b]);
           __syncwarp();
         }
-        if (ok && elect_one()) commit_pair(&acc_full[b]);
-        __syncwarp();
       }
       if (!ok && lane == 0) {
         s_abort = 1;
@@ -554,31 +567,69 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     for (int t = first; t < tiles; t += step, ++n) {
       int ti, tj;
       tile_of(t, A.tiles_i, A.tiles_j, ti, tj);
-      const int b = n & 1;
       const int64_t ib = static_cast<int64_t>(ti) * 256 + rank * 128;
       const int64_t i = ib + quad * 32 + lane;
-      const int64_t j0 = static_cast<int64_t>(tj) * A.bn + half * 128;
-      const int width = half ? A.bn - 128 : 128;
+      const int64_t j0 = static_cast<int64_t>(tj) * A.bn + half * A.first_half;
+      const int width = half ? A.bn - A.first_half : A.first_half;
       const bool in = i < A.I;
       const float bias = A.epi.bias && in ? __ldg(A.epi.bias + i) : 0.f;
-      bool got = wait_warp(&acc_full[b], (n >> 1) & 1);
+      bool got = wait_warp(&acc_full[n & 1], (n >> 1) & 1);
       tc::fence_after_sync();
-      const uint32_t src = tmem + b * 256 + half * 128 + (static_cast<uint32_t>(quad * 32) << 16);
+      const uint32_t mine = tmem + half * A.first_half + (static_cast<uint32_t>(quad * 32) << 16);
+      const uint32_t sum = mine + 2 * kAcc;
+      if constexpr (PROMOTE) {                     // all stretches but the last go into the sum
+        for (int base = stretch; base < A.kblocks && got; base += stretch) {
+#pragma unroll 1
+          for (int c = 0; c < width; c += 16) {
+            float v[16];
+            load16(mine + (n & 1) * kAcc + c, 0.f, v);
+            if (base > stretch) {
+              float u[16];
+              load16(sum + c, 0.f, u);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] += u[e];
+            }
+            uint32_t r[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(v[e]);
+            tc::tmem_st16(sum + c, r);
+          }
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) arrive_remote(lead + (n & 1) * 8);
+          ++n;
+          got = wait_warp(&acc_full[n & 1], (n >> 1) & 1);
+          tc::fence_after_sync();
+        }
+      }
+      const int b = n & 1;
+      const uint32_t src = mine + b * kAcc;
+      const bool summed = PROMOTE && A.kblocks > stretch;
+      auto load_cols = [&](int c, float (&v)[16]) {
+        load16(src + c, bias, v);
+        if (summed) {
+          float u[16];
+          load16(sum + c, 0.f, u);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] += u[e];
+        }
+      };
       // the columns of this half that exist (none where the CTA's rows are past the end)
       const int ncol = ib < A.I ? static_cast<int>(A.J - j0 < width ? (A.J > j0 ? A.J - j0 : 0) : width) : 0;
       if (!A.staged) {
 #pragma unroll 1
         for (int c = 0; c < ncol && got; c += 16) {
           float v[16];
-          load16(src + c, bias, v);
+          load_cols(c, v);
           if (in) store16(A.epi, v, i, j0 + c, A.J);
         }
       } else {
 #pragma unroll 1
         for (int c = 0; c < ncol && got; c += A.cols) {
           float v[2][16];
-          load16(src + c, bias, v[0]);
-          if (A.cols == 32) load16(src + c + 16, bias, v[1]);
+          load_cols(c, v[0]);
+          if (A.cols == 32) load_cols(c + 16, v[1]);
           if (A.epi.z) {
             got = got && wait_warp(&ready[half][q & 1], (q >> 1) & 1);
             unsigned char* tile = slots + (q & 1) * kSlot;
@@ -663,8 +714,8 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   const int k0 = static_cast<int>(static_cast<int64_t>(A.kblocks) * rank / splits);
   const int k1 = static_cast<int>(static_cast<int64_t>(A.kblocks) * (rank + 1) / splits);
   // the stretches of c that one accumulator takes, and the products of parts of each
-  const int stretch = PROMOTE ? kStretch : k1 - k0;
-  constexpr int kParts = PROMOTE ? 6 : 1;
+  const int parts = PROMOTE ? A.parts : 1;
+  const int stretch = PROMOTE ? (parts == 6 ? kStretch : kPairStretch) : k1 - k0;
   constexpr uint32_t kCols = PROMOTE ? 2 * BN : BN;
 
   if (threadIdx.x == 0) {
@@ -694,8 +745,8 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     int it = 0;
     bool ok = true;
     for (int base = k0; base < k1 && ok; base += stretch)
-      for (int q = 0; q < kParts && ok; ++q) {
-        const int pa = PROMOTE ? part_a(q) : 0, pb = PROMOTE ? part_b(q) : 0;
+      for (int q = 0; q < parts && ok; ++q) {
+        const int pa = parts == 6 ? part_a(q) : 0, pb = parts == 6 ? part_b(q) : 0;
         for (int k = base; k < min(base + stretch, k1); ++k, ++it, at.next()) {
           const int s = at.s;
           if (!__all_sync(0xffffffffu, wait_phase(&empty[s], at.ph ^ 1, &s_abort))) {
@@ -735,7 +786,7 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         ok = false;
         break;
       }
-      const int steps = kParts * (min(base + stretch, k1) - base);
+      const int steps = parts * (min(base + stretch, k1) - base);
       for (int k = 0; k < steps; ++k) {
         const int s = at.s;
         if (!__all_sync(0xffffffffu, wait_phase(&full[s], at.ph, &s_abort))) {
@@ -1014,7 +1065,7 @@ cudaError_t raise_smem(Kernel k, size_t bytes, std::atomic<uint64_t>& done) {
   return e;
 }
 
-template <bool AMN, bool BMN>
+template <bool AMN, bool BMN, bool PROMOTE>
 cudaError_t launch_pair(const Gemm& g, TcArgs A, int planes, int pairs, cudaStream_t st) {
   CUtensorMap ma, mb;
   OutMaps out;
@@ -1034,10 +1085,12 @@ cudaError_t launch_pair(const Gemm& g, TcArgs A, int planes, int pairs, cudaStre
       A.bn = kWidth[c];
     }
   }
+  if (PROMOTE) A.bn = kPromoteBN;
+  A.first_half = PROMOTE ? kPromoteBN / 2 : 128;
   if (!encode(&ma, g.A, g.I, g.C, planes, 128) || !encode(&mb, g.B, g.J, g.C, planes, A.bn / 2)) return cudaErrorInvalidValue;
   A.tiles_i = static_cast<int32_t>((g.I + 255) / 256);
   A.tiles_j = static_cast<int32_t>((g.J + A.bn - 1) / A.bn);
-  auto k = gemm_pair_kernel<AMN, BMN>;
+  auto k = gemm_pair_kernel<AMN, BMN, PROMOTE>;
   static std::atomic<uint64_t> raised{0};
   const cudaError_t e = raise_smem(k, kPairSmem, raised);
   if (e != cudaSuccess) return e;
@@ -1084,22 +1137,25 @@ template <bool AMN, bool BMN>
 cudaError_t launch_shape(const Gemm& g, const TcArgs& A, int planes, cudaStream_t st) {
   const int sms = sm_count();
   const int64_t big = ((g.I + 255) / 256) * ((g.J + 255) / 256);
-  if (planes == 1 && big >= sms / 4 && g.J > 128) return launch_pair<AMN, BMN>(g, A, planes, sms / 2, st);
+  const bool promote = planes == 3 || (!g.epi.out_bf && A.kblocks > 16);
+  if (planes == 1 && big >= sms / 4 && g.J > 128)
+    return promote ? launch_pair<AMN, BMN, true>(g, A, planes, sms / 2, st)
+                   : launch_pair<AMN, BMN, false>(g, A, planes, sms / 2, st);
   // Few tiles.  64 columns at least (narrower tiles were no faster even for 16 rows), the tile halved
   // while too few CTAs would run; 256 columns only unsplit, as the parts would not fit.
   int bn = 64;
-  while (bn < (planes == 1 ? 256 : 128) && bn < g.J) bn *= 2;
+  while (bn < (promote ? 128 : 256) && bn < g.J) bn *= 2;
   auto tiles_for = [&](int n) { return ((g.I + 127) / 128) * ((g.J + n - 1) / n); };
   auto room = [&](int n) { return static_cast<int64_t>(sms) * (n <= 64 ? 2 : 1); };   // CTAs that run at once
   while (bn > 64 && tiles_for(bn) * 2 <= room(bn)) bn /= 2;
   const int64_t tiles = tiles_for(bn);
   // Splits fill the SMs, with four steps a CTA at least; beyond four ways the exchange costs more than
   // it saves unless c is long (16 x 4096 -> 4096: 4 ways 8.4 us, 8 ways 9.5 us).
-  const int steps = A.kblocks * (planes == 1 ? 1 : 6);
+  const int steps = A.kblocks * A.parts;
   int splits = static_cast<int>(std::min<int64_t>(steps >= 128 ? 8 : 4, std::max<int64_t>(1, room(bn) / tiles)));
   splits = bn == 256 ? 1 : std::max(1, std::min(splits, std::min(steps / 4, A.kblocks)));
   if (tiles * splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  if (planes == 3)
+  if (promote)
     return bn == 64 ? launch_split<AMN, BMN, 64, true>(g, A, planes, splits, st)
                     : launch_split<AMN, BMN, 128, true>(g, A, planes, splits, st);
   switch (bn) {
@@ -1132,6 +1188,7 @@ cudaError_t launch_gemm_tc(const Gemm& g, int planes, cudaStream_t st) {
   A.epi = g.epi;
   A.I = g.I; A.J = g.J;
   A.kblocks = static_cast<int32_t>((g.C + kBK - 1) / kBK);
+  A.parts = planes == 3 ? 6 : 1;
   A.err = g.err;
   if (g.A.mn) return g.B.mn ? launch_shape<true, true>(g, A, planes, st) : launch_shape<true, false>(g, A, planes, st);
   return launch_shape<false, false>(g, A, planes, st);

@@ -122,6 +122,25 @@ def test_linear_shapes(T, K, N, dtype):
     linear_case(1, T, K, N, dtype, bias=True)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,K,N", [(64, 4096, 64), (1500, 2112, 1600), (300, 1100, 200)])
+def test_linear_fp32_results_round_like_fp32_sums(T, K, N, dtype):
+    """A long sum with an fp32 result is not left to the truncating accumulators: relative to the
+    result's norm it stays within sqrt(K) roundings (an fp32 chain's random walk), 2 of them
+    for the systematic part."""
+    r = rng(11, T, K)
+    x, x64 = dev(r.standard_normal((T, K)), dtype)
+    w, w64 = dev(r.standard_normal((N, K)) / np.sqrt(K), dtype)
+    d, d64 = dev(r.standard_normal((T, N)), dtype)
+    y = host(kda.linear(x, w, out_dtype=torch.float32))
+    dw = host(kda.linear_bwd(x, w, d, need_dx=False, dw_dtype=torch.float32)[1])
+    no_error()
+    for got, ref, c in ((y, x64 @ w64.T, K), (dw, d64.T @ x64, T)):
+        # up to 1024 steps stay in one accumulator: 64 truncations of up to 2 U each, half on average
+        lim = 2 * np.sqrt(c) * U if c > 1024 else max(2 * np.sqrt(c), c / 16) * U
+        assert np.linalg.norm(got - ref) <= lim * np.linalg.norm(ref)
+
+
 @pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 8, 9])
 @pytest.mark.parametrize("K,N", [(520, 70), (4096, 40), (37, 261)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
