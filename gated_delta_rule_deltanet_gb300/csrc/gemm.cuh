@@ -65,7 +65,23 @@ cudaError_t launch_gemm_tc(const Gemm& g, int planes, cudaStream_t st);
 // of bf16 parts.  The rows are whole 128-byte lines, so that a box's rows cross none.
 inline int64_t padded(int64_t cols) { return (cols + 63) / 64 * 64; }
 size_t repacked_bytes(int64_t rows, int64_t cols, bool bf16);
-cudaError_t launch_repack(const void* src, int64_t src_ld, int64_t rows, int64_t cols, bool bf16, void* dst,
-                          cudaStream_t st);
+struct Repack {
+  const void* src;
+  int64_t src_ld, rows, cols;
+  void* dst;
+};
+cudaError_t launch_repack(const Repack* arrays, int count, bool bf16, cudaStream_t st);   // up to 3
+
+// the three bf16 parts of an fp32 value
+__device__ __forceinline__ void split3(float x, uint16_t (&p)[3]) {
+  // rounded to nearest at each step; a finite x whose rounding would overflow is cut instead
+  p[0] = f32_to_bf16_bits(x);
+  if ((p[0] & 0x7fff) == 0x7f80) p[0] = static_cast<uint16_t>(__float_as_uint(x) >> 16);
+  const float hi = bf16_bits_to_f32(p[0]);
+  const float r = (p[0] & 0x7f80) == 0x7f80 ? 0.f : x - hi;     // infinities and NaN have no rest
+  p[1] = f32_to_bf16_bits(r);
+  p[2] = f32_to_bf16_bits(r - bf16_bits_to_f32(p[1]));
+}
+
 
 }  // namespace kda

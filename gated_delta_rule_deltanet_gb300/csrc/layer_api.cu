@@ -44,10 +44,10 @@ bool f32_aligned(const void* p) { return elem_aligned(p, KDA_DTYPE_F32); }
 
 kda_status_t to_status(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
 
-// row strides are 0 (dense) or at least the row; every array stays below 2^62 bytes
+// row strides are 0 (dense) or at least the row; strides stay below what a tensor map can say
 bool stride_ok(int64_t stride, int64_t cols, int64_t rows) {
   const int64_t s = stride ? stride : cols;
-  return s >= cols && s <= (int64_t{1} << 40) && rows <= (int64_t{1} << 60) / s;
+  return s >= cols && s <= (int64_t{1} << 36) && rows <= (int64_t{1} << 60) / s;
 }
 
 constexpr uint32_t kLinearFlags =

@@ -119,6 +119,7 @@ struct DzArgs {
   const void* dy;
   const void* z;        // null: no activation
   void* dz;             // null: only the column sums
+  int64_t plane;        // > 0: dz is three planes of bf16 parts, this many elements apart
   float* part;          // [gridDim.y][N] or null
   int64_t T, dy_ld, dz_ld;
   int32_t N, act;
@@ -156,7 +157,21 @@ __global__ void __launch_bounds__(256) dz_kernel(DzArgs A) {
         if (A.z) d[e] *= act_grad_f<ZBF>(A.act, z[u].f32(e));
         sum[e] += chunk_index<VEC>(lane, 32, e) < n ? d[e] : 0.f;
       }
-      if (A.dz) store_chunk<ZBF, VEC>(static_cast<char*>(A.dz) + (tu * A.dz_ld + n0) * (ZBF ? 2 : 4), lane, 32, n, d);
+      if (A.dz && (ZBF || A.plane == 0)) {
+        store_chunk<ZBF, VEC>(static_cast<char*>(A.dz) + (tu * A.dz_ld + n0) * (ZBF ? 2 : 4), lane, 32, n, d);
+      } else if (A.dz) {
+        float part[3][8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          uint16_t q[3];
+          split3(d[e], q);
+#pragma unroll
+          for (int p = 0; p < 3; ++p) part[p][e] = bf16_bits_to_f32(q[p]);
+        }
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+          store_chunk<true, VEC>(static_cast<uint16_t*>(A.dz) + p * A.plane + tu * A.dz_ld + n0, lane, 32, n, part[p]);
+      }
     }
   }
   if (!A.part) return;
@@ -184,7 +199,7 @@ static bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) =
 template <bool DYBF, bool ZBF>
 static cudaError_t launch_dz_t(const DzArgs& A, cudaStream_t st) {
   const bool vec = A.N % 8 == 0 && al16(A.dy) && al16(A.z) && al16(A.dz) &&
-                   A.dy_ld * (DYBF ? 2 : 4) % 16 == 0 && A.dz_ld * (ZBF ? 2 : 4) % 16 == 0;
+                   A.dy_ld * (DYBF ? 2 : 4) % 16 == 0 && A.dz_ld * (ZBF ? 2 : 4) % 16 == 0 && A.plane % 8 == 0;
   const dim3 grid(static_cast<unsigned>((A.N + 255) / 256), static_cast<unsigned>(dz_rows(A.T, A.N)));
   if (vec) dz_kernel<DYBF, ZBF, true><<<grid, 256, 0, st>>>(A);
   else dz_kernel<DYBF, ZBF, false><<<grid, 256, 0, st>>>(A);
@@ -208,8 +223,8 @@ static size_t up256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 constexpr size_t kNone = ~static_cast<size_t>(0);
 struct LinearLayout {
   bool rows, tc;             // few tokens; tensor cores
-  size_t part, dz, x, w, dz_planes, total;
-  int64_t dz_ld;
+  size_t part, dz, x, w, total;
+  int64_t dz_ld, dz_plane;
 };
 static LinearLayout linear_layout(const kda_linear_params_t& p, bool bwd) {
   const int64_t T = p.tokens, K = p.in_features, N = p.out_features;
@@ -228,15 +243,15 @@ static LinearLayout linear_layout(const kda_linear_params_t& p, bool bwd) {
              repacked_bytes(T, K, bf));
   L.w = take(L.tc && (!bf || (p.flags & KDA_FLAG_UNALIGNED_W) || or_dense(p.w_row_stride, K) % 8),
              repacked_bytes(N, K, bf));
-  L.dz = L.part = L.dz_planes = kNone;
+  L.dz = L.part = kNone;
   if (bwd) {
     L.part = take(true, static_cast<size_t>(dz_rows(T, p.out_features)) * N * 4);
     // dz is formed unless the products can read d_y itself
     const bool unaligned = L.tc && bf && ((p.flags & KDA_FLAG_UNALIGNED_DY) || or_dense(p.y_row_stride, N) % 8);
     L.dz_ld = padded(N);
-    L.dz = take(p.activation != KDA_ACT_NONE || p.y_dtype != p.dtype || unaligned,
-                static_cast<size_t>(T) * L.dz_ld * dtype_bytes(p.dtype));
-    L.dz_planes = take(L.tc && !bf, repacked_bytes(T, N, false));
+    L.dz_plane = L.tc && !bf ? T * L.dz_ld : 0;
+    L.dz = take(p.activation != KDA_ACT_NONE || p.y_dtype != p.dtype || unaligned || L.dz_plane,
+                L.dz_plane ? repacked_bytes(T, N, false) : static_cast<size_t>(T) * L.dz_ld * dtype_bytes(p.dtype));
   }
   L.total = at;
   return L;
@@ -244,14 +259,19 @@ static LinearLayout linear_layout(const kda_linear_params_t& p, bool bwd) {
 
 size_t linear_workspace_bytes(const kda_linear_params_t& p, bool bwd) { return linear_layout(p, bwd).total; }
 
-// The operand as the product reads it: copied into the workspace where the layout says so.
-static cudaError_t stage(GemmOperand* X, size_t at, char* ws, int64_t rows, int64_t cols, bool bf16, cudaStream_t st) {
-  if (at == kNone) return cudaSuccess;
-  const cudaError_t e = launch_repack(X->p, X->ld, rows, cols, bf16, ws + at, st);
-  X->p = ws + at;
-  X->ld = padded(cols);
-  return e;
-}
+// The operands as the products read them: copied into the workspace where the layout says so, in
+// one launch.
+struct Stage {
+  Repack a[2];
+  int n = 0;
+  void add(GemmOperand* X, size_t at, char* ws, int64_t rows, int64_t cols) {
+    if (at == kNone) return;
+    a[n++] = {X->p, X->ld, rows, cols, ws + at};
+    X->p = ws + at;
+    X->ld = padded(cols);
+  }
+  cudaError_t run(bool bf16, cudaStream_t st) const { return n ? launch_repack(a, n, bf16, st) : cudaSuccess; }
+};
 
 static cudaError_t run_gemm(const Gemm& g, bool tc, cudaStream_t st) {
   return tc && g.C > 0 ? launch_gemm_tc(g, g.bf16 ? 1 : 3, st) : launch_gemm_simt(g, st);
@@ -269,8 +289,10 @@ cudaError_t launch_linear_fwd(const kda_linear_params_t& p, const void* x, const
   g.bf16 = p.dtype == KDA_DTYPE_BF16;
   g.A = {w, or_dense(p.w_row_stride, K), false};
   g.B = {x, or_dense(p.x_row_stride, K), false};
-  if ((e = stage(&g.A, L.w, ws, N, K, g.bf16, st)) != cudaSuccess) return e;
-  if ((e = stage(&g.B, L.x, ws, T, K, g.bf16, st)) != cudaSuccess) return e;
+  Stage copies;
+  copies.add(&g.A, L.w, ws, N, K);
+  copies.add(&g.B, L.x, ws, T, K);
+  if ((e = copies.run(g.bf16, st)) != cudaSuccess) return e;
   g.I = N; g.J = T; g.C = K;
   g.epi = {bias, res, y, z, or_dense(p.residual_row_stride, N), or_dense(p.y_row_stride, N), N, p.scale,
            p.activation, p.residual_dtype == KDA_DTYPE_BF16, p.y_dtype == KDA_DTYPE_BF16, g.bf16};
@@ -294,28 +316,31 @@ cudaError_t launch_linear_bwd(const kda_linear_params_t& p, const void* x, const
     A.dz = form ? ws + L.dz : nullptr;
     A.part = dbias ? reinterpret_cast<float*>(ws + L.part) : nullptr;
     A.T = T; A.dy_ld = dz.ld; A.dz_ld = L.dz_ld; A.N = p.out_features; A.act = p.activation;
+    A.plane = L.dz_plane;
     if ((e = launch_dz(A, p.y_dtype == KDA_DTYPE_BF16, bf, st)) != cudaSuccess) return e;
     if (dbias && (e = launch_sum_parts(A.part, dz_rows(T, p.out_features), N, 1, p.scale,
                                        SumOuts{{dbias, nullptr, nullptr}}, st)) != cudaSuccess)
       return e;
     if (form) dz = {ws + L.dz, L.dz_ld, false};
   }
-  if (any && (dx || dw) && (e = stage(&dz, L.dz_planes, ws, T, N, bf, st)) != cudaSuccess) return e;
+  GemmOperand wt{w, or_dense(p.w_row_stride, K), true}, xt{x, or_dense(p.x_row_stride, K), true};
+  Stage copies;
+  if (dx && any) copies.add(&wt, L.w, ws, N, K);
+  if (dw && any) copies.add(&xt, L.x, ws, T, K);
+  if ((e = copies.run(bf, st)) != cudaSuccess) return e;
   Gemm g{};
   g.bf16 = bf;
   g.err = err;
   g.epi = {nullptr, nullptr, nullptr, nullptr, 0, K, 0, p.scale, KDA_ACT_NONE, false, bf, false};
   if (dx && any) {
-    g.A = {w, or_dense(p.w_row_stride, K), true};
-    if ((e = stage(&g.A, L.w, ws, N, K, bf, st)) != cudaSuccess) return e;
+    g.A = wt;
     g.B = dz;
     g.I = K; g.J = T; g.C = N;
     g.epi.out = dx;
     if ((e = run_gemm(g, L.tc, st)) != cudaSuccess) return e;
   }
   if (dw) {
-    g.A = {x, or_dense(p.x_row_stride, K), true};
-    if (any && (e = stage(&g.A, L.x, ws, T, K, bf, st)) != cudaSuccess) return e;
+    g.A = xt;
     g.B = {dz.p, dz.ld, true};
     g.I = K; g.J = N; g.C = T;
     g.epi.out = dw;

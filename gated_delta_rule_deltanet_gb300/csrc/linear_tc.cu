@@ -28,7 +28,7 @@
 // smallest first.  The tensor cores cut the accumulator's low bits at every step of 16 instead of
 // rounding them, always towards zero, so a long sum would lose several times fp32's rounding
 // (1.2e-6 relative at c = 1000, growing with c): the split kernel therefore moves the accumulator
-// into registers every 128 steps of c, where it is added with rounding (PROMOTE).  The pair kernel
+// into registers every 64 steps of c, where it is added with rounding.  The pair kernel
 // does the same every 512 steps, into a third stretch of tensor memory, where bf16 operands have
 // an fp32 result over more than 1024 steps (c = 4096: 4.4e-6 of the norm without, 4.8e-7 with; the tile is then 160
 // columns wide, three of which fit).  A bf16 result rounds by far more than the truncation.
@@ -47,7 +47,6 @@ namespace kda {
 namespace {
 
 constexpr uint32_t kWaitLimit = 1u << 30;
-constexpr unsigned long long kWaitNs = 2000000000ull;
 constexpr int kBK = 64;                            // c per stage: one 128-byte swizzled row
 constexpr uint32_t kOpBytes = 128 * kBK * 2;       // 128 rows of an operand
 
@@ -165,41 +164,40 @@ struct TcArgs {
   int32_t first_half;       // and those of them that the first four epilogue warps store
   int32_t cols;             // pair kernel: columns (j) of a staged chunk
   int32_t kblocks;          // 64-wide steps over c
-  int32_t parts;            // products of parts: 6 for fp32 operands, else 1
   int32_t tiles_i, tiles_j;
   int32_t* err;
+  unsigned long long wait_ns;   // what a wait may take: far beyond the kernel's run
 };
 
-// The products of parts of one stretch of c, smallest first (0 = hi, 1 = mid, 2 = lo).
-__device__ __forceinline__ int part_a(int q) { return (0x201100 >> (4 * (5 - q))) & 15; }   // lo hi mid mid hi hi
-__device__ __forceinline__ int part_b(int q) { return (0x021010 >> (4 * (5 - q))) & 15; }   // hi lo mid hi mid hi
+// The products of parts of one step of c, smallest first (0 = hi, 1 = mid, 2 = lo).
+__device__ __forceinline__ constexpr int part_a(int q) { return (0x201100 >> (4 * (5 - q))) & 15; }   // lo hi mid mid hi hi
+__device__ __forceinline__ constexpr int part_b(int q) { return (0x021010 >> (4 * (5 - q))) & 15; }   // hi lo mid hi mid hi
 
-// Waits for a phase; gives up after kWaitNs (far beyond any kernel's run) or once another role of
-// the CTA has.
+// Waits for a phase; gives up after `limit` ns or once another role of the CTA has.
 template <typename TryWait>
-__device__ __forceinline__ bool wait_bounded(TryWait try_wait, volatile int* abort) {
+__device__ __forceinline__ bool wait_bounded(TryWait try_wait, unsigned long long limit, volatile int* abort) {
   unsigned long long start = 0;
   for (uint32_t i = 0; i < kWaitLimit; ++i) {
     if (try_wait()) return true;
     if ((i & 63) == 63) {
       const unsigned long long t = now_ns();
       if (start == 0) start = t;
-      if (*abort || t - start > kWaitNs) return false;
+      if (*abort || t - start > limit) return false;
     }
   }
   return false;
 }
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return wait_bounded([&] { return tc::mbar_try_wait(bar, parity); }, abort);
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, unsigned long long limit, volatile int* abort) {
+  return wait_bounded([&] { return tc::mbar_try_wait(bar, parity); }, limit, abort);
 }
 // the same for a barrier that the other CTA of the pair arrives on
-__device__ __forceinline__ bool wait_phase_cluster(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return wait_bounded([&] { return try_wait_cluster(bar, parity); }, abort);
+__device__ __forceinline__ bool wait_phase_cluster(uint64_t* bar, uint32_t parity, unsigned long long limit, volatile int* abort) {
+  return wait_bounded([&] { return try_wait_cluster(bar, parity); }, limit, abort);
 }
 // after a timeout: the copies or products in flight
 __device__ __forceinline__ void drain_phase(uint64_t* bar, uint32_t parity) {
   int never = 0;
-  wait_phase(bar, parity, &never);
+  wait_phase(bar, parity, 100000000ull, &never);
 }
 
 // A position in a ring of N stages and the parity of the pass over it.
@@ -216,11 +214,11 @@ struct Ring {
 };
 
 // Descriptor of 128 (or BN) operand rows staged at `saddr`.  K-major: 8-row groups of 1024 bytes.
-// MN-major: boxes of 64 rows of i (or j) by 64 steps of c, 8192 bytes apart; 8 steps of c are
-// 1024 bytes apart.
-template <bool MN>
+// MN-major: boxes of 64 rows of i (or j) by 64 steps of c (of every plane), 8192 bytes a plane; 8
+// steps of c are 1024 bytes apart.
+template <bool MN, int PLANES = 1>
 __device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
-  return MN ? (tc::smem_desc(saddr, 8192, 1024) | (static_cast<uint64_t>(2) << 61))
+  return MN ? (tc::smem_desc(saddr, PLANES * 8192, 1024) | (static_cast<uint64_t>(2) << 61))
             : tc::smem_desc_sw128(saddr, 1024);
 }
 // bytes from one MMA's 16 steps of c to the next
@@ -228,11 +226,11 @@ template <bool MN>
 __device__ __forceinline__ constexpr uint32_t k_advance() { return MN ? 2048 : 32; }
 
 // `ROWS` rows of an operand from row r0 and step c0: one box K-major, ROWS / 64 boxes MN-major
-template <bool MN, int ROWS, typename Load>
+template <bool MN, int ROWS, int PLANES = 1, typename Load>
 __device__ __forceinline__ void load_operand(uint32_t sdst, int64_t r0, int c0, Load load) {
   if constexpr (MN) {
 #pragma unroll
-    for (int b = 0; b < ROWS / 64; ++b) load(sdst + b * 8192, static_cast<int32_t>(r0) + 64 * b, c0);
+    for (int b = 0; b < ROWS / 64; ++b) load(sdst + b * PLANES * 8192, static_cast<int32_t>(r0) + 64 * b, c0);
   } else {
     load(sdst, c0, static_cast<int32_t>(r0));
   }
@@ -436,7 +434,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
       const int64_t j0 = static_cast<int64_t>(tj) * A.bn + rank * (A.bn / 2);
       for (int k = 0; k < A.kblocks; ++k, ++it, at.next()) {
         const int s = at.s;
-        if (!__all_sync(0xffffffffu, wait_phase(&empty[s], at.ph ^ 1, &s_abort))) {
+        if (!__all_sync(0xffffffffu, wait_phase(&empty[s], at.ph ^ 1, A.wait_ns, &s_abort))) {
           ok = false;
           break;
         }
@@ -475,7 +473,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
       for (int t = first; t < tiles && ok; t += step) {
         for (int base = 0; base < A.kblocks && ok; base += stretch, ++n) {
           const int b = n & 1;
-          if (!__all_sync(0xffffffffu, wait_phase_cluster(&acc_empty[b], ((n >> 1) & 1) ^ 1, &s_abort))) {
+          if (!__all_sync(0xffffffffu, wait_phase_cluster(&acc_empty[b], ((n >> 1) & 1) ^ 1, A.wait_ns, &s_abort))) {
             ok = false;
             break;
           }
@@ -484,7 +482,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
           const int k1 = min(A.kblocks, base + stretch);
           for (int k = base; k < k1; ++k) {
             const int s = at.s;
-            if (!__all_sync(0xffffffffu, wait_phase(&full[s], at.ph, &s_abort))) {
+            if (!__all_sync(0xffffffffu, wait_phase(&full[s], at.ph, A.wait_ns, &s_abort))) {
               ok = false;
               break;
             }
@@ -537,7 +535,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
       hand_over(1);
       int q = 0;
       for (; cur.t < tiles; ++q, cur.next(A, rank, half, tiles, step)) {
-        if (!wait_phase(&written[half][q & 1], (q >> 1) & 1, &s_abort)) {
+        if (!wait_phase(&written[half][q & 1], (q >> 1) & 1, A.wait_ns, &s_abort)) {
           s_abort = 1;
           raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
           if (A.res_staged) {                      // loads in flight
@@ -561,7 +559,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     unsigned char* slots = smem_raw + (smem - tc::smem_u32(smem_raw)) + kPairStages * kPairStage + half * 2 * kSlot;
     // the whole warp takes the same way, as its tensor-memory loads need
     auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, wait_phase(bar, parity, &s_abort)) != 0;
+      return __all_sync(0xffffffffu, wait_phase(bar, parity, A.wait_ns, &s_abort)) != 0;
     };
     int n = 0, q = 0;
     for (int t = first; t < tiles; t += step, ++n) {
@@ -683,24 +681,29 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
 // ------------------------------------------------------------------ one CTA a tile, split over c
 
 constexpr int kSplitThreads = 192;                 // TMA, MMA, 4 epilogue warps
-constexpr int kStretch = 2;                        // 64-wide steps between promotions
 
-template <int BN>
+// PARTS: how the sum over c is kept.  0: in one accumulator.  1: promoted every kPairStretch steps.
+// 6: fp32 operands; a stage holds all three parts of both, so that they are read once for
+// their six products, and every step of c is promoted.
+template <int BN, int PARTS>
 struct SplitShape {
-  static constexpr uint32_t stage = kOpBytes + BN * kBK * 2;
+  static constexpr int planes = PARTS == 6 ? 3 : 1;
+  static constexpr uint32_t a_bytes = planes * kOpBytes;
+  static constexpr uint32_t stage = a_bytes + planes * BN * kBK * 2;
   // the ring: as deep as two CTAs an SM allow for the narrow tile, 200 KB for the others
-  static constexpr int stages = BN == 128 ? 6 : 4;
+  static constexpr int stages = PARTS == 6 ? (BN == 64 ? 3 : 2) : BN == 128 ? 6 : 4;
   static constexpr size_t smem = static_cast<size_t>(stage) * stages + 1024;
   // a split's own part and those received (7 shares of up to BN / 8 + 7 columns, or one of BN / 2)
   static_assert(BN == 256 || static_cast<size_t>(stage) * stages >= 128 * 4 * (BN + 7 * 8 + BN),
                 "the parts reuse the ring");
 };
 
-template <bool AMN, bool BMN, int BN, bool PROMOTE>
+template <bool AMN, bool BMN, int BN, int PARTS>
 __global__ void __launch_bounds__(kSplitThreads)
 gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                   const __grid_constant__ OutMaps maps, const __grid_constant__ TcArgs A, const int splits) {
-  using S = SplitShape<BN>;
+  using S = SplitShape<BN, PARTS>;
+  constexpr bool PROMOTE = PARTS > 0;
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[S::stages], empty[S::stages], acc_full[2], acc_empty[2], received;
   __shared__ uint32_t s_tmem;
@@ -713,9 +716,8 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   const int64_t i0 = static_cast<int64_t>(tile % A.tiles_i) * 128, j0 = static_cast<int64_t>(tile / A.tiles_i) * BN;
   const int k0 = static_cast<int>(static_cast<int64_t>(A.kblocks) * rank / splits);
   const int k1 = static_cast<int>(static_cast<int64_t>(A.kblocks) * (rank + 1) / splits);
-  // the stretches of c that one accumulator takes, and the products of parts of each
-  const int parts = PROMOTE ? A.parts : 1;
-  const int stretch = PROMOTE ? (parts == 6 ? kStretch : kPairStretch) : k1 - k0;
+  // the steps of c that one accumulator takes
+  const int stretch = PARTS == 6 ? 1 : PARTS == 1 ? kPairStretch : k1 - k0;
   constexpr uint32_t kCols = PROMOTE ? 2 * BN : BN;
 
   if (threadIdx.x == 0) {
@@ -744,28 +746,24 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     Ring<S::stages> at;
     int it = 0;
     bool ok = true;
-    for (int base = k0; base < k1 && ok; base += stretch)
-      for (int q = 0; q < parts && ok; ++q) {
-        const int pa = parts == 6 ? part_a(q) : 0, pb = parts == 6 ? part_b(q) : 0;
-        for (int k = base; k < min(base + stretch, k1); ++k, ++it, at.next()) {
-          const int s = at.s;
-          if (!__all_sync(0xffffffffu, wait_phase(&empty[s], at.ph ^ 1, &s_abort))) {
-            ok = false;
-            break;
-          }
-          const uint32_t sa = smem + s * S::stage, sb = sa + kOpBytes;
-          if (elect_one()) {
-            tc::mbar_arrive_expect_tx(&full[s], S::stage);
-            load_operand<AMN, 128>(sa, i0, k * kBK, [&](uint32_t d, int32_t x, int32_t y) {
-              tc::tma_load_3d(d, &map_a, x, y, pa, &full[s]);
-            });
-            load_operand<BMN, BN>(sb, j0, k * kBK, [&](uint32_t d, int32_t x, int32_t y) {
-              tc::tma_load_3d(d, &map_b, x, y, pb, &full[s]);
-            });
-          }
-          __syncwarp();
-        }
+    for (int k = k0; k < k1; ++k, ++it, at.next()) {
+      const int s = at.s;
+      if (!__all_sync(0xffffffffu, wait_phase(&empty[s], at.ph ^ 1, A.wait_ns, &s_abort))) {
+        ok = false;
+        break;
       }
+      const uint32_t sa = smem + s * S::stage, sb = sa + S::a_bytes;
+      if (elect_one()) {
+        tc::mbar_arrive_expect_tx(&full[s], S::stage);
+        load_operand<AMN, 128, S::planes>(sa, i0, k * kBK, [&](uint32_t d, int32_t x, int32_t y) {
+          tc::tma_load_3d(d, &map_a, x, y, 0, &full[s]);
+        });
+        load_operand<BMN, BN, S::planes>(sb, j0, k * kBK, [&](uint32_t d, int32_t x, int32_t y) {
+          tc::tma_load_3d(d, &map_b, x, y, 0, &full[s]);
+        });
+      }
+      __syncwarp();
+    }
     if (!ok && lane == 0) {                        // wait for the copies in flight
       s_abort = 1;
       raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
@@ -775,21 +773,21 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     __syncwarp();
   } else if (warp == 1) {
     const uint32_t idesc = tc::idesc_f16(128, BN, tc::kBF16, false, AMN, BMN);
-    const uint64_t da0 = operand_desc<AMN>(smem), db0 = operand_desc<BMN>(smem + kOpBytes);
+    const uint64_t da0 = operand_desc<AMN, S::planes>(smem), db0 = operand_desc<BMN, S::planes>(smem + S::a_bytes);
     Ring<S::stages> at;
     bool ok = true;
     int n = 0;
     for (int base = k0; base < k1 && ok; base += stretch, ++n) {
       const int b = n & 1;
       const uint32_t d = tmem + (PROMOTE ? b * BN : 0);
-      if (PROMOTE && !__all_sync(0xffffffffu, wait_phase(&acc_empty[b], ((n >> 1) & 1) ^ 1, &s_abort))) {
+      if (PROMOTE && !__all_sync(0xffffffffu, wait_phase(&acc_empty[b], ((n >> 1) & 1) ^ 1, A.wait_ns, &s_abort))) {
         ok = false;
         break;
       }
-      const int steps = parts * (min(base + stretch, k1) - base);
-      for (int k = 0; k < steps; ++k) {
+      const int last = min(base + stretch, k1);
+      for (int k = base; k < last; ++k) {
         const int s = at.s;
-        if (!__all_sync(0xffffffffu, wait_phase(&full[s], at.ph, &s_abort))) {
+        if (!__all_sync(0xffffffffu, wait_phase(&full[s], at.ph, A.wait_ns, &s_abort))) {
           ok = false;
           break;
         }
@@ -798,9 +796,15 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         at.next();
         if (elect_one()) {
 #pragma unroll
-          for (int q = 0; q < kBK / 16; ++q)
-            tc::mma_ss(d, tc::desc_add(da, q * k_advance<AMN>()), tc::desc_add(db, q * k_advance<BMN>()), idesc,
-                       (k | q) != 0);
+          for (int p = 0; p < (PARTS == 6 ? 6 : 1); ++p) {
+            // a part's place in the stage
+            const uint32_t pa = PARTS == 6 ? part_a(p) * (AMN ? 8192 : kOpBytes) : 0;
+            const uint32_t pb = PARTS == 6 ? part_b(p) * (BMN ? 8192 : BN * kBK * 2) : 0;
+#pragma unroll
+            for (int q = 0; q < kBK / 16; ++q)
+              tc::mma_ss(d, tc::desc_add(da, pa + q * k_advance<AMN>()), tc::desc_add(db, pb + q * k_advance<BMN>()),
+                         idesc, k > base || p > 0 || q > 0);
+          }
           tc::mma_commit(&empty[s]);
         }
         __syncwarp();
@@ -826,7 +830,7 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 #pragma unroll
       for (int c = 0; c < BN; ++c) sum[c] = 0.f;
       for (int base = k0; base < k1 && ready; base += stretch, ++n) {
-        ready = __all_sync(0xffffffffu, wait_phase(&acc_full[n & 1], (n >> 1) & 1, &s_abort));
+        ready = __all_sync(0xffffffffu, wait_phase(&acc_full[n & 1], (n >> 1) & 1, A.wait_ns, &s_abort));
         if (!ready) break;
         tc::fence_after_sync();
 #pragma unroll
@@ -842,7 +846,7 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       }
       ready = !tc::named_sync_or(2, 128, !ready);
     } else {
-      ready = !tc::named_sync_or(2, 128, !wait_phase(&acc_full[0], 0, &s_abort));
+      ready = !tc::named_sync_or(2, 128, !wait_phase(&acc_full[0], 0, A.wait_ns, &s_abort));
     }
     if (!ready) raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
     tc::fence_after_sync();
@@ -888,7 +892,7 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       tc::bulk_commit();
     }
     if (warp >= 2 && c1 > c0) {
-      ready = !tc::named_sync_or(2, 128, !wait_phase_cluster(&received, 0, &s_abort)) && ready;
+      ready = !tc::named_sync_or(2, 128, !wait_phase_cluster(&received, 0, A.wait_ns, &s_abort)) && ready;
       if (!ready) raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
     }
   }
@@ -972,36 +976,34 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 
 // ------------------------------------------------------------------ aligned copies, fp32 parts
 
-__device__ __forceinline__ void split3(float x, uint16_t (&p)[3]) {
-  // rounded to nearest at each step; a finite x whose rounding would overflow is cut instead
-  p[0] = f32_to_bf16_bits(x);
-  if ((p[0] & 0x7fff) == 0x7f80) p[0] = static_cast<uint16_t>(__float_as_uint(x) >> 16);
-  const float hi = bf16_bits_to_f32(p[0]);
-  const float r = (p[0] & 0x7f80) == 0x7f80 ? 0.f : x - hi;     // infinities and NaN have no rest
-  p[1] = f32_to_bf16_bits(r);
-  p[2] = f32_to_bf16_bits(r - bf16_bits_to_f32(p[1]));
-}
-
 // rows of `cols` elements copied into rows of ld elements: bf16 as they are, fp32 as three planes
-// of parts
+// of parts; blockIdx.y picks the array
+struct RepackArgs {
+  struct {
+    const void* src;
+    uint16_t* dst;
+    int64_t src_ld, rows, cols, ld;
+  } a[3];
+};
+
 template <bool BF>
-__global__ void __launch_bounds__(256) repack_kernel(const void* src, int64_t src_ld, int64_t rows, int64_t cols,
-                                                     int64_t ld, uint16_t* dst) {
-  const int64_t plane = rows * ld;
-  const int64_t cb = (cols + 1023) / 1024;
-  for (int64_t u = blockIdx.x; u < rows * cb; u += gridDim.x) {
+__global__ void __launch_bounds__(256) repack_kernel(const RepackArgs R) {
+  const auto& a = R.a[blockIdx.y];
+  const int64_t plane = a.rows * a.ld;
+  const int64_t cb = (a.cols + 1023) / 1024;
+  for (int64_t u = blockIdx.x; u < a.rows * cb; u += gridDim.x) {
     const int64_t r = u / cb;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int64_t c = (u - r * cb) * 1024 + e * 256 + threadIdx.x;
-      if (c >= cols) continue;
+      if (c >= a.cols) continue;
       if constexpr (BF) {
-        dst[r * ld + c] = static_cast<const uint16_t*>(src)[r * src_ld + c];
+        a.dst[r * a.ld + c] = static_cast<const uint16_t*>(a.src)[r * a.src_ld + c];
       } else {
         uint16_t p[3];
-        split3(static_cast<const float*>(src)[r * src_ld + c], p);
+        split3(static_cast<const float*>(a.src)[r * a.src_ld + c], p);
 #pragma unroll
-        for (int q = 0; q < 3; ++q) dst[q * plane + r * ld + c] = p[q];
+        for (int q = 0; q < 3; ++q) a.dst[q * plane + r * a.ld + c] = p[q];
       }
     }
   }
@@ -1009,14 +1011,14 @@ __global__ void __launch_bounds__(256) repack_kernel(const void* src, int64_t sr
 
 // ------------------------------------------------------------------ tensor maps, launches
 
-// boxes of 64 columns (128 bytes, swizzled) x box_rows rows of one plane
+// boxes of 64 columns (128 bytes, swizzled) x box_rows rows x every plane
 bool encode_operand(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t planes,
                     uint32_t box_rows) {
   auto enc = tensor_map_encoder();
   if (!enc || rows == 0 || (reinterpret_cast<uintptr_t>(base) & 15u) || (ld & 7u)) return false;
   const cuuint64_t dims[3] = {cols, rows, planes};
   const cuuint64_t strides[2] = {ld * 2, rows * ld * 2};
-  const cuuint32_t box[3] = {64, box_rows, 1};
+  const cuuint32_t box[3] = {64, box_rows, planes};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1101,7 +1103,7 @@ cudaError_t launch_pair(const Gemm& g, TcArgs A, int planes, int pairs, cudaStre
   return cudaGetLastError();
 }
 
-template <bool AMN, bool BMN, int BN, bool PROMOTE>
+template <bool AMN, bool BMN, int BN, int PARTS>
 cudaError_t launch_split(const Gemm& g, TcArgs A, int planes, int splits, cudaStream_t st) {
   CUtensorMap ma, mb;
   OutMaps out;
@@ -1109,19 +1111,19 @@ cudaError_t launch_split(const Gemm& g, TcArgs A, int planes, int splits, cudaSt
   const size_t cols = splits == 1 ? BN : ((BN + splits - 1) / splits + 15) / 16 * 16;
   const size_t bytes = (splits == 1 ? 0 : 128 * BN * 4 + (splits - 1) * cols * 512) +
                        cols * 128 * ((g.epi.out_bf ? 2 : 4) + (!g.epi.z ? 0 : g.epi.z_bf ? 2 : 4));
-  if (bytes <= SplitShape<BN>::smem - 1024) encode_outputs(g, &A, &out, 8, false);
+  if (bytes <= (SplitShape<BN, PARTS>::smem) - 1024) encode_outputs(g, &A, &out, 8, false);
   else A.staged = A.res_staged = false;
   if (!encode(&ma, g.A, g.I, g.C, planes, 128) || !encode(&mb, g.B, g.J, g.C, planes, BN)) return cudaErrorInvalidValue;
   A.tiles_i = static_cast<int32_t>((g.I + 127) / 128);
   A.tiles_j = static_cast<int32_t>((g.J + BN - 1) / BN);
-  auto k = gemm_split_kernel<AMN, BMN, BN, PROMOTE>;
+  auto k = gemm_split_kernel<AMN, BMN, BN, PARTS>;
   static std::atomic<uint64_t> raised{0};
-  cudaError_t e = raise_smem(k, SplitShape<BN>::smem, raised);
+  cudaError_t e = raise_smem(k, (SplitShape<BN, PARTS>::smem), raised);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(A.tiles_i) * A.tiles_j * splits));
   cfg.blockDim = dim3(kSplitThreads);
-  cfg.dynamicSmemBytes = SplitShape<BN>::smem;
+  cfg.dynamicSmemBytes = (SplitShape<BN, PARTS>::smem);
   cfg.stream = st;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;
@@ -1146,22 +1148,26 @@ cudaError_t launch_shape(const Gemm& g, const TcArgs& A, int planes, cudaStream_
   int bn = 64;
   while (bn < (promote ? 128 : 256) && bn < g.J) bn *= 2;
   auto tiles_for = [&](int n) { return ((g.I + 127) / 128) * ((g.J + n - 1) / n); };
-  auto room = [&](int n) { return static_cast<int64_t>(sms) * (n <= 64 ? 2 : 1); };   // CTAs that run at once
-  while (bn > 64 && tiles_for(bn) * 2 <= room(bn)) bn /= 2;
+  // CTAs that run at once
+  auto room = [&](int n) { return static_cast<int64_t>(sms) * (n <= 64 && planes == 1 ? 2 : 1); };
+  while (bn > 64 && tiles_for(bn) * (planes == 3 ? std::min(4, A.kblocks) : 2) <= room(bn)) bn /= 2;
   const int64_t tiles = tiles_for(bn);
   // Splits fill the SMs, with four steps a CTA at least; beyond four ways the exchange costs more than
   // it saves unless c is long (16 x 4096 -> 4096: 4 ways 8.4 us, 8 ways 9.5 us).
-  const int steps = A.kblocks * A.parts;
+  const int steps = A.kblocks * (planes == 3 ? 6 : 1);
   int splits = static_cast<int>(std::min<int64_t>(steps >= 128 ? 8 : 4, std::max<int64_t>(1, room(bn) / tiles)));
   splits = bn == 256 ? 1 : std::max(1, std::min(splits, std::min(steps / 4, A.kblocks)));
   if (tiles * splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  if (planes == 3)
+    return bn == 64 ? launch_split<AMN, BMN, 64, 6>(g, A, planes, splits, st)
+                    : launch_split<AMN, BMN, 128, 6>(g, A, planes, splits, st);
   if (promote)
-    return bn == 64 ? launch_split<AMN, BMN, 64, true>(g, A, planes, splits, st)
-                    : launch_split<AMN, BMN, 128, true>(g, A, planes, splits, st);
+    return bn == 64 ? launch_split<AMN, BMN, 64, 1>(g, A, planes, splits, st)
+                    : launch_split<AMN, BMN, 128, 1>(g, A, planes, splits, st);
   switch (bn) {
-    case 64: return launch_split<AMN, BMN, 64, false>(g, A, planes, splits, st);
-    case 128: return launch_split<AMN, BMN, 128, false>(g, A, planes, splits, st);
-    default: return launch_split<AMN, BMN, 256, false>(g, A, planes, splits, st);
+    case 64: return launch_split<AMN, BMN, 64, 0>(g, A, planes, splits, st);
+    case 128: return launch_split<AMN, BMN, 128, 0>(g, A, planes, splits, st);
+    default: return launch_split<AMN, BMN, 256, 0>(g, A, planes, splits, st);
   }
 }
 
@@ -1171,13 +1177,19 @@ size_t repacked_bytes(int64_t rows, int64_t cols, bool bf16) {
   return static_cast<size_t>(rows) * padded(cols) * 2 * (bf16 ? 1 : 3);
 }
 
-cudaError_t launch_repack(const void* src, int64_t src_ld, int64_t rows, int64_t cols, bool bf16, void* dst,
-                          cudaStream_t st) {
-  if (rows == 0) return cudaSuccess;
-  const int64_t ld = padded(cols), units = rows * ((cols + 1023) / 1024);
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, static_cast<int64_t>(sm_count()) * 16));
-  if (bf16) repack_kernel<true><<<grid, 256, 0, st>>>(src, src_ld, rows, cols, ld, static_cast<uint16_t*>(dst));
-  else repack_kernel<false><<<grid, 256, 0, st>>>(src, src_ld, rows, cols, ld, static_cast<uint16_t*>(dst));
+cudaError_t launch_repack(const Repack* arrays, int count, bool bf16, cudaStream_t st) {
+  RepackArgs R{};
+  int64_t units = 0;
+  for (int i = 0; i < count; ++i) {
+    const Repack& a = arrays[i];
+    R.a[i] = {a.src, static_cast<uint16_t*>(a.dst), a.src_ld, a.rows, a.cols, padded(a.cols)};
+    units = std::max(units, a.rows * ((a.cols + 1023) / 1024));
+  }
+  if (units == 0) return cudaSuccess;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(units, static_cast<int64_t>(sm_count()) * 16)),
+                  static_cast<unsigned>(count));
+  if (bf16) repack_kernel<true><<<grid, 256, 0, st>>>(R);
+  else repack_kernel<false><<<grid, 256, 0, st>>>(R);
   return cudaGetLastError();
 }
 
@@ -1188,8 +1200,8 @@ cudaError_t launch_gemm_tc(const Gemm& g, int planes, cudaStream_t st) {
   A.epi = g.epi;
   A.I = g.I; A.J = g.J;
   A.kblocks = static_cast<int32_t>((g.C + kBK - 1) / kBK);
-  A.parts = planes == 3 ? 6 : 1;
   A.err = g.err;
+  A.wait_ns = 2000000000ull + static_cast<unsigned long long>(A.kblocks) * 4000ull;
   if (g.A.mn) return g.B.mn ? launch_shape<true, true>(g, A, planes, st) : launch_shape<true, false>(g, A, planes, st);
   return launch_shape<false, false>(g, A, planes, st);
 }
