@@ -122,6 +122,56 @@ def test_linear_shapes(T, K, N, dtype):
     linear_case(1, T, K, N, dtype, bias=True)
 
 
+@pytest.mark.parametrize("dtype,y,res,K", [("bf16", "bf16", "f32", 200), ("bf16", "f32", "f32", 1100),
+                                           ("bf16", "f32", "bf16", 1100), ("bf16", "f32", None, 1100)])
+def test_linear_pair_tiles_of_other_types(dtype, y, res, K):
+    """Residuals that are and are not of y's type, and fp32 results, at the persistent kernel's
+    sizes (its backward then has an fp32 d_y)."""
+    linear_case(12, 1601, K, 1608, dtype, act="sigmoid", bias=True, res=res, y=y, scale=-1.5)
+
+
+def test_linear_pair_tiles_in_place():
+    r = rng(13)
+    T, K, N = 1700, 128, 1600
+    x, x64 = dev(r.standard_normal((T, K)), "bf16")
+    w, w64 = dev(r.standard_normal((N, K)), "bf16")
+    for dtype in ("bf16", "f32"):
+        h, h64 = dev(r.standard_normal((T, N)), dtype)
+        y = kda.linear(x, w, residual=h, out=h, scale=0.5)
+        no_error()
+        assert y is h
+        ref = ol.linear(x64, w64, None, "none", h64, 0.5)[0]
+        check("y", h, ref, product_tol(x64, w64.T, K, "bf16") + 4 * U * np.abs(ref))
+
+
+def test_arrays_past_2_to_the_31():
+    """More than 2^31 elements: the last rows equal those of a call on the last rows alone."""
+    T, N = 530000, 4160                                    # 2.2e9 elements
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    x = torch.randn((T, 64), generator=g, device=DEV, dtype=torch.bfloat16)
+    w = torch.randn((N, 64), generator=g, device=DEV, dtype=torch.bfloat16)
+    y = kda.linear(x, w)
+    tail = slice(T - 300, T)
+    assert torch.equal(y[tail], kda.linear(x[tail].contiguous(), w))
+    dx = kda.linear_bwd(x, w, y, need_dw=False)[0]
+    ref = y[tail].float() @ w.float()
+    assert (dx[tail].float() - ref).abs().max() <= 2 * R(torch.bfloat16) * ref.abs().max()
+    del dx
+    v = torch.randn(N, generator=g, device=DEV)
+    n, h = kda.residual_norm(y, v, residual=y)
+    yt = y[tail].contiguous()
+    nt, ht = kda.residual_norm(yt, v, residual=yt)
+    # another kernel (rows read directly): the order of a row's sum may differ, a bf16 step then
+    assert torch.equal(h[tail], ht) and (n[tail].float() - nt.float()).abs().max() <= 2 * R(torch.bfloat16) * nt.abs().max()
+    del n, h
+    o = y.view(-1)[:T * N // 128 * 128].view(-1, 1, 128)
+    z = kda.gated_norm(o, o, v[:128].contiguous())
+    zt = kda.gated_norm(o[-500:].contiguous(), o[-500:].contiguous(), v[:128].contiguous())
+    no_error()
+    assert torch.equal(z[-500:], zt)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T,K,N", [(64, 4096, 64), (1500, 2112, 1600), (300, 1100, 200)])
 def test_linear_fp32_results_round_like_fp32_sums(T, K, N, dtype):
