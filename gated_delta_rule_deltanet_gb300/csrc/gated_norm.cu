@@ -54,10 +54,8 @@ __device__ __forceinline__ void gate_grad_f(float z, float& a, float& da) {
     a = z;
     da = 1.f;
   } else {
-    // p = sigmoid(z) and q = 1 - p from one exponential of -|z|: neither cancels
-    const float e = FAST ? __expf(-fabsf(z)) : expf(-fabsf(z));
-    const float r = __fdividef(1.f, 1.f + e);
-    const float p = z < 0.f ? e * r : r, q = z < 0.f ? r : e * r;
+    float p, q;
+    sigmoid_pair<FAST>(z, p, q);
     if constexpr (ACT == KDA_ACT_SIGMOID) {
       a = p;
       da = p * q;

@@ -153,22 +153,29 @@ __device__ __forceinline__ float act_f(int act, float z) {
   }
 }
 
+// p = sigmoid(z) and q = 1 - p from one exponential of -|z|: neither cancels
 template <bool FAST>
-__device__ __forceinline__ float act_grad_f(int act, float z) {
-  switch (act) {
-    case KDA_ACT_RELU: return z > 0.f ? 1.f : (z == z ? 0.f : z);
-    case KDA_ACT_SILU: {
-      // p (1 + z (1 - p)), 1 - p = sigmoid(-z): no cancellation, and 0 / 1 at the infinities
-      if (fabsf(z) > 3e38f) return z > 0.f ? 1.f : 0.f;
-      const float p = sigmoid_f<FAST>(z);
-      return p * (1.f + z * sigmoid_f<FAST>(-z));
-    }
-    case KDA_ACT_GELU: {
-      if (fabsf(z) > 20.f) return z > 0.f ? 1.f : 0.f;
-      return 0.5f * erfcf(-0.70710678f * z) + 0.39894228f * z * expf(-0.5f * z * z);
-    }
-    case KDA_ACT_SIGMOID: return sigmoid_f<FAST>(z) * sigmoid_f<FAST>(-z);
-    default: return 1.f;
+__device__ __forceinline__ void sigmoid_pair(float z, float& p, float& q) {
+  const float e = FAST ? __expf(-fabsf(z)) : expf(-fabsf(z));
+  const float r = __fdividef(1.f, 1.f + e);
+  p = z < 0.f ? e * r : r;
+  q = z < 0.f ? r : e * r;
+}
+
+template <int ACT, bool FAST>
+__device__ __forceinline__ float act_grad_f(float z) {
+  if constexpr (ACT == KDA_ACT_RELU) {
+    return z > 0.f ? 1.f : (z == z ? 0.f : z);
+  } else if constexpr (ACT == KDA_ACT_SILU || ACT == KDA_ACT_SIGMOID) {
+    float p, q;
+    sigmoid_pair<FAST>(z, p, q);
+    if constexpr (ACT == KDA_ACT_SIGMOID) return p * q;
+    return fabsf(z) > 100.f ? p : p * (1.f + z * q);      // 0 / 1 at the infinities
+  } else if constexpr (ACT == KDA_ACT_GELU) {
+    if (fabsf(z) > 20.f) return z > 0.f ? 1.f : 0.f;
+    return 0.5f * erfcf(-0.70710678f * z) + 0.39894228f * z * (FAST ? __expf(-0.5f * z * z) : expf(-0.5f * z * z));
+  } else {
+    return 1.f;
   }
 }
 

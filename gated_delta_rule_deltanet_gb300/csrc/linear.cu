@@ -2,6 +2,7 @@
 // gradients: the fp32 product on CUDA cores, the element-wise gradient of the epilogue with the
 // bias's column sums, and the choice of path.  The tensor-core product is in linear_tc.cu.
 #include <algorithm>
+#include <type_traits>
 
 #include "gemm.cuh"
 
@@ -125,8 +126,9 @@ struct DzArgs {
   int32_t N, act;
 };
 
-// ACT = false: the sums alone or a copy, with few registers and eight rows in flight.
-template <bool DYBF, bool ZBF, bool VEC, bool ACT>
+// The activation is fixed at compile time; without one (the sums alone, or a copy) eight rows are in
+// flight instead of four.
+template <bool DYBF, bool ZBF, bool VEC, int ACT>
 __global__ void __launch_bounds__(256) dz_kernel(DzArgs A) {
   __shared__ float s[8][256 + 8];
   const int lane = threadIdx.x & 31, ry = threadIdx.x >> 5;
@@ -135,7 +137,7 @@ __global__ void __launch_bounds__(256) dz_kernel(DzArgs A) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) sum[e] = 0.f;
   const int64_t stride = static_cast<int64_t>(gridDim.y) * 8;
-  constexpr int U = ACT ? 4 : 8;
+  constexpr int U = ACT != KDA_ACT_NONE ? 4 : 8;
   for (int64_t t = static_cast<int64_t>(blockIdx.y) * 8 + ry; t < A.T; t += U * stride) {
     Raw8<DYBF> dy[U];
     Raw8<ZBF> z[U];
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(256) dz_kernel(DzArgs A) {
       const int m = tu < A.T ? n : 0;
       const int64_t tt = tu < A.T ? tu : 0;
       dy[u] = load_chunk<DYBF, VEC>(static_cast<const char*>(A.dy) + (tt * A.dy_ld + n0) * (DYBF ? 2 : 4), lane, 32, m);
-      if constexpr (ACT) z[u] = load_chunk<ZBF, VEC>(static_cast<const char*>(A.z) + (tt * A.N + n0) * (ZBF ? 2 : 4), lane, 32, m);
+      if constexpr (ACT != KDA_ACT_NONE) z[u] = load_chunk<ZBF, VEC>(static_cast<const char*>(A.z) + (tt * A.N + n0) * (ZBF ? 2 : 4), lane, 32, m);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -155,7 +157,7 @@ __global__ void __launch_bounds__(256) dz_kernel(DzArgs A) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         d[e] = dy[u].f32(e);
-        if constexpr (ACT) d[e] *= act_grad_f<ZBF>(A.act, z[u].f32(e));
+        if constexpr (ACT != KDA_ACT_NONE) d[e] *= act_grad_f<ACT, ZBF>(z[u].f32(e));
         sum[e] += chunk_index<VEC>(lane, 32, e) < n ? d[e] : 0.f;
       }
       if (A.dz && (ZBF || A.plane == 0)) {
@@ -202,12 +204,17 @@ static cudaError_t launch_dz_t(const DzArgs& A, cudaStream_t st) {
   const bool vec = A.N % 8 == 0 && al16(A.dy) && al16(A.z) && al16(A.dz) &&
                    A.dy_ld * (DYBF ? 2 : 4) % 16 == 0 && A.dz_ld * (ZBF ? 2 : 4) % 16 == 0 && A.plane % 8 == 0;
   const dim3 grid(static_cast<unsigned>((A.N + 255) / 256), static_cast<unsigned>(dz_rows(A.T, A.N)));
-  if (A.z) {
-    if (vec) dz_kernel<DYBF, ZBF, true, true><<<grid, 256, 0, st>>>(A);
-    else dz_kernel<DYBF, ZBF, false, true><<<grid, 256, 0, st>>>(A);
-  } else {
-    if (vec) dz_kernel<DYBF, ZBF, true, false><<<grid, 256, 0, st>>>(A);
-    else dz_kernel<DYBF, ZBF, false, false><<<grid, 256, 0, st>>>(A);
+  auto run = [&](auto act) {
+    constexpr int ACT = decltype(act)::value;
+    if (vec) dz_kernel<DYBF, ZBF, true, ACT><<<grid, 256, 0, st>>>(A);
+    else dz_kernel<DYBF, ZBF, false, ACT><<<grid, 256, 0, st>>>(A);
+  };
+  switch (A.z ? A.act : KDA_ACT_NONE) {
+    case KDA_ACT_RELU: run(std::integral_constant<int, KDA_ACT_RELU>()); break;
+    case KDA_ACT_SILU: run(std::integral_constant<int, KDA_ACT_SILU>()); break;
+    case KDA_ACT_GELU: run(std::integral_constant<int, KDA_ACT_GELU>()); break;
+    case KDA_ACT_SIGMOID: run(std::integral_constant<int, KDA_ACT_SIGMOID>()); break;
+    default: run(std::integral_constant<int, KDA_ACT_NONE>()); break;
   }
   return cudaGetLastError();
 }

@@ -22,24 +22,58 @@ struct RepackArgs {
   } a[3];
 };
 
+// Bound by HBM: two elements a thread and step, four steps in flight.  bf16 rows that start in the
+// middle of a 4-byte word are read as the words that hold them (each holds at least one element
+// of the row) and shifted by one element against the next lane's word.
 template <bool BF>
 __global__ void __launch_bounds__(256) repack_kernel(const RepackArgs R) {
   const auto& a = R.a[blockIdx.y];
   const int64_t plane = a.rows * a.ld;
-  const int64_t cb = (a.cols + 1023) / 1024;
+  const int64_t cb = (a.cols + 2047) / 2048;
+  const int lane = threadIdx.x & 31;
   for (int64_t u = blockIdx.x; u < a.rows * cb; u += gridDim.x) {
     const int64_t r = u / cb;
+    const int64_t c0 = (u - r * cb) * 2048 + 2 * threadIdx.x;
+    if constexpr (BF) {
+      const uint16_t* row = static_cast<const uint16_t*>(a.src) + r * a.src_ld;
+      const int odd = (reinterpret_cast<uintptr_t>(row) >> 1) & 1;
+      const uint32_t* words = reinterpret_cast<const uint32_t*>(row - odd);
+      const int64_t nw = (a.cols + odd + 1) / 2;       // words that hold elements of the row
+      uint32_t lo[4], hi[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int64_t c = (u - r * cb) * 1024 + e * 256 + threadIdx.x;
-      if (c >= a.cols) continue;
-      if constexpr (BF) {
-        a.dst[r * a.ld + c] = static_cast<const uint16_t*>(a.src)[r * a.src_ld + c];
-      } else {
-        uint16_t p[3];
-        split3(static_cast<const float*>(a.src)[r * a.src_ld + c], p);
+      for (int e = 0; e < 4; ++e) {
+        const int64_t w = (c0 >> 1) + e * 256;
+        lo[e] = w < nw ? words[w] : 0;
+        hi[e] = odd && lane == 31 && w + 1 < nw ? words[w + 1] : 0;
+      }
 #pragma unroll
-        for (int q = 0; q < 3; ++q) a.dst[q * plane + r * a.ld + c] = p[q];
+      for (int e = 0; e < 4; ++e) {
+        if (odd) {                                     // the same for the whole warp
+          const uint32_t next = __shfl_down_sync(0xffffffffu, lo[e], 1);
+          lo[e] = (lo[e] >> 16) | ((lane == 31 ? hi[e] : next) << 16);
+        }
+        const int64_t c = c0 + e * 512;
+        if (c < a.cols) *reinterpret_cast<uint32_t*>(a.dst + r * a.ld + c) = lo[e];   // (the padding takes the rest)
+      }
+    } else {
+      const float* row = static_cast<const float*>(a.src) + r * a.src_ld;
+      float x[4][2];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t c = c0 + e * 512;
+        x[e][0] = c < a.cols ? row[c] : 0.f;
+        x[e][1] = c + 1 < a.cols ? row[c + 1] : 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t c = c0 + e * 512;
+        if (c >= a.cols) continue;
+        uint16_t p[3], q[3];
+        split3(x[e][0], p);
+        split3(x[e][1], q);
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          *reinterpret_cast<uint32_t*>(a.dst + k * plane + r * a.ld + c) = p[k] | static_cast<uint32_t>(q[k]) << 16;
       }
     }
   }
@@ -57,7 +91,7 @@ cudaError_t launch_repack(const Repack* arrays, int count, bool bf16, cudaStream
   for (int i = 0; i < count; ++i) {
     const Repack& a = arrays[i];
     R.a[i] = {a.src, static_cast<uint16_t*>(a.dst), a.src_ld, a.rows, a.cols, padded(a.cols)};
-    units = std::max(units, a.rows * ((a.cols + 1023) / 1024));
+    units = std::max(units, a.rows * ((a.cols + 2047) / 2048));
   }
   if (units == 0) return cudaSuccess;
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(units, static_cast<int64_t>(sm_count()) * 16)),

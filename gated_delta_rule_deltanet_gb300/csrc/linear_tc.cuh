@@ -157,11 +157,17 @@ struct OutMaps {
   CUtensorMap y, z, res;
 };
 
+// The residual is loaded by the storing threads, or by TMA: into the chunk of y that it is added to
+// (y's type), or as a chunk of its own.
+enum : int32_t { kResDirect = 0, kResInPlace = 1, kResChunk = 2 };
+// The kinds of staged chunks, in the order they follow one another for the same columns.
+enum : int { kChunkZ = 0, kChunkRes = 1, kChunkY = 2 };
+
 struct TcArgs {
   GemmEpilogue epi;
   int64_t I, J;
   bool staged;              // y (and z) leave through shared memory and TMA
-  bool res_staged;          // the residual arrives that way too (it has y's type)
+  int32_t res_mode;         // pair kernel: how the residual comes, kRes*
   int32_t bn;               // pair kernel: columns (j) of a tile, a multiple of 32 from 128 to 256
   int32_t first_half;       // and those of them that the first four epilogue warps store
   int32_t cols;             // pair kernel: columns (j) of a staged chunk
@@ -325,6 +331,17 @@ __device__ __forceinline__ void put16(unsigned char* tile, bool bf, int col, int
   }
 }
 
+__device__ __forceinline__ void add16(const unsigned char* tile, bool bf, int col, int row, float (&v)[16]) {
+  if (bf) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      v[e] += bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(tile + (col + e) * 256 + row * 2));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] += *reinterpret_cast<const float*>(tile + (col + e) * 512 + row * 4);
+  }
+}
+
 // ------------------------------------------------------------------ pairs of CTAs, 256 x 256 tiles
 
 constexpr int kPairStages = 6;
@@ -348,11 +365,13 @@ __device__ __forceinline__ void tile_of(int t, int tiles_i, int tiles_j, int& ti
 }
 
 // The chunks of one half (the first columns or the others) of this CTA's tiles, in the order the epilogue forms them:
-// per `cols` columns the pre-activation (if it is kept), then y.
+// per `cols` columns the pre-activation (if it is kept), a residual of another type than y's, then y.
 struct Chunk {
-  int t, c, width;
-  bool z;
+  int t, c, width, kind;
   int64_t i0, j0;
+  __device__ __forceinline__ static int first_kind(const TcArgs& A) {
+    return A.epi.z ? kChunkZ : A.res_mode == kResChunk ? kChunkRes : kChunkY;
+  }
   __device__ __forceinline__ void place(const TcArgs& A, uint32_t rank, int half, int tiles, int step) {
     for (; t < tiles; t += step) {
       int ti, tj;
@@ -366,15 +385,15 @@ struct Chunk {
   __device__ __forceinline__ void start(const TcArgs& A, uint32_t rank, int half, int first, int tiles, int step) {
     t = first;
     c = 0;
-    z = A.epi.z != nullptr;
+    kind = first_kind(A);
     place(A, rank, half, tiles, step);
   }
   __device__ __forceinline__ void next(const TcArgs& A, uint32_t rank, int half, int tiles, int step) {
-    if (z) {
-      z = false;
+    if (kind != kChunkY) {
+      kind = kind == kChunkZ && A.res_mode == kResChunk ? kChunkRes : kChunkY;
       return;
     }
-    z = A.epi.z != nullptr;
+    kind = first_kind(A);
     c += A.cols;
     if (c >= width || j0 + c >= A.J) {
       c = 0;
@@ -522,14 +541,14 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     // residual's values loaded into it, or just free), and stores it once it is written.
     if (lane == 0 && A.staged) {
       const int half = warp - 2;
-      const uint32_t bytes = 128u * A.cols * (A.epi.out_bf ? 2 : 4);
+      const uint32_t bytes = 128u * A.cols * (A.epi.res_bf ? 2 : 4);
       Chunk cur, ahead;
       cur.start(A, rank, half, first, tiles, step);
       ahead = cur;
       auto hand_over = [&](int q) {
         if (ahead.t >= tiles) return;
         uint64_t* bar = &ready[half][q & 1];
-        if (A.res_staged && !ahead.z) {
+        if (ahead.kind == kChunkRes || (ahead.kind == kChunkY && A.res_mode == kResInPlace)) {
           tc::mbar_arrive_expect_tx(bar, bytes);
           tc::tma_load_2d(smem + kPairStages * kPairStage + (half * 2 + (q & 1)) * kSlot, &maps.res,
                           static_cast<int32_t>(ahead.i0), static_cast<int32_t>(ahead.j0) + ahead.c, bar);
@@ -545,16 +564,19 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         if (!wait_phase(&written[half][q & 1], (q >> 1) & 1, A.wait_ns, &s_abort)) {
           s_abort = 1;
           raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
-          if (A.res_staged) {                      // loads in flight
+          if (A.res_mode != kResDirect) {          // loads in flight
             drain_phase(&ready[half][q & 1], (q >> 1) & 1);
             drain_phase(&ready[half][(q + 1) & 1], ((q + 1) >> 1) & 1);
           }
           break;
         }
-        tma_store_2d(cur.z ? &maps.z : &maps.y, smem + kPairStages * kPairStage + (half * 2 + (q & 1)) * kSlot,
-                     static_cast<int32_t>(cur.i0), static_cast<int32_t>(cur.j0) + cur.c);
-        tc::bulk_commit();
-        tc::bulk_wait_read();
+        if (cur.kind != kChunkRes) {
+          tma_store_2d(cur.kind == kChunkZ ? &maps.z : &maps.y,
+                       smem + kPairStages * kPairStage + (half * 2 + (q & 1)) * kSlot, static_cast<int32_t>(cur.i0),
+                       static_cast<int32_t>(cur.j0) + cur.c);
+          tc::bulk_commit();
+          tc::bulk_wait_read();
+        }
         hand_over(q + 2);
       }
       tc::bulk_wait_all();
@@ -654,7 +676,14 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
               v[1][e] *= A.epi.scale;
             }
           }
-          if (FULL && A.epi.res && !A.res_staged && in) {
+          if (FULL && A.res_mode == kResChunk) {
+            got = got && wait_warp(&ready[half][q & 1], (q >> 1) & 1);
+            const unsigned char* tile = slots + (q & 1) * kSlot;
+            add16(tile, A.epi.res_bf, 0, quad * 32 + lane, v[0]);
+            if (A.cols == 32) add16(tile, A.epi.res_bf, 16, quad * 32 + lane, v[1]);
+            tc::mbar_arrive(&written[half][q & 1]);
+            ++q;
+          } else if (FULL && A.epi.res && A.res_mode == kResDirect && in) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               const int m = min(16, ncol - c - 16 * u);
@@ -669,8 +698,8 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
           }
           got = got && wait_warp(&ready[half][q & 1], (q >> 1) & 1);
           unsigned char* tile = slots + (q & 1) * kSlot;
-          put16(tile, A.epi.out_bf, 0, quad * 32 + lane, FULL && A.res_staged, v[0]);
-          if (A.cols == 32) put16(tile, A.epi.out_bf, 16, quad * 32 + lane, FULL && A.res_staged, v[1]);
+          put16(tile, A.epi.out_bf, 0, quad * 32 + lane, FULL && A.res_mode == kResInPlace, v[0]);
+          if (A.cols == 32) put16(tile, A.epi.out_bf, 16, quad * 32 + lane, FULL && A.res_mode == kResInPlace, v[1]);
           tc::fence_async_smem();
           tc::mbar_arrive(&written[half][q & 1]);
           ++q;
@@ -695,7 +724,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
 
 // ------------------------------------------------------------------ one CTA a tile, split over c
 
-constexpr int kSplitThreads = 192;                 // TMA, MMA, 4 epilogue warps
+constexpr int kSplitThreads = 320;                 // TMA, MMA, 8 epilogue warps
 
 // PARTS: how the sum over c is kept.  0: in one accumulator.  1: promoted every kPairStretch steps.
 // 6: fp32 operands; a stage holds all three parts of both, so that they are read once for
@@ -742,7 +771,7 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&acc_full[b], 1);
-      tc::mbar_init(&acc_empty[b], 4);             // the epilogue warps
+      tc::mbar_init(&acc_empty[b], 8);             // the epilogue warps
     }
     tc::mbar_init(&received, 1);
     tc::fence_mbar_init();
@@ -832,27 +861,33 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
     }
   }
-  const int quad = warp & 3;
+  // Epilogue warps: 32 lanes of the tile (quad), every other 16 columns (half).
+  const int quad = warp & 3, half = (warp - 2) >> 2;
   const int64_t i = i0 + quad * 32 + lane;
   const bool in = i < A.I;
   constexpr bool FULL = !AMN;
   const float bias = FULL && warp >= 2 && A.epi.bias && in ? __ldg(A.epi.bias + i) : 0.f;
   const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+  if (FULL && warp >= 2 && A.epi.res && i0 + quad * 32 < A.I) {   // the residual, towards L2 meanwhile
+    const char* r = static_cast<const char*>(A.epi.res) + (i0 + quad * 32) * (A.epi.res_bf ? 2 : 4);
+    for (int c = half * 32 + lane; c < BN && j0 + c < A.J; c += 64)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(r + (j0 + c) * A.epi.res_ld * (A.epi.res_bf ? 2 : 4)));
+  }
   bool ready = true;
-  float sum[PROMOTE ? BN : 1];                     // PROMOTE: this thread's row of the tile
+  float sum[PROMOTE ? BN / 2 : 1];                 // PROMOTE: this thread's half row of the tile
   if (warp >= 2) {
     int n = 0;
     if constexpr (PROMOTE) {
 #pragma unroll
-      for (int c = 0; c < BN; ++c) sum[c] = 0.f;
+      for (int c = 0; c < BN / 2; ++c) sum[c] = 0.f;
       for (int base = k0; base < k1 && ready; base += stretch, ++n) {
         ready = __all_sync(0xffffffffu, wait_phase(&acc_full[n & 1], (n >> 1) & 1, A.wait_ns, &s_abort));
         if (!ready) break;
         tc::fence_after_sync();
 #pragma unroll
-        for (int c = 0; c < BN; c += 16) {
+        for (int c = 0; c < BN / 2; c += 16) {
           float v[16];
-          load16(src + (n & 1) * BN + c, 0.f, v);
+          load16(src + (n & 1) * BN + 2 * c + half * 16, 0.f, v);
 #pragma unroll
           for (int e = 0; e < 16; ++e) sum[c + e] += v[e];
         }
@@ -860,9 +895,9 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&acc_empty[n & 1]);
       }
-      ready = !tc::named_sync_or(2, 128, !ready);
+      ready = !tc::named_sync_or(2, 256, !ready);
     } else {
-      ready = !tc::named_sync_or(2, 128, !wait_phase(&acc_full[0], 0, A.wait_ns, &s_abort));
+      ready = !tc::named_sync_or(2, 256, !wait_phase(&acc_full[0], 0, A.wait_ns, &s_abort));
     }
     if (!ready) raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
     tc::fence_after_sync();
@@ -880,11 +915,13 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       float* at = part + quad * 32 + lane;
       if constexpr (PROMOTE) {
 #pragma unroll
-        for (int c = 0; c < BN; ++c)
-          if (c < ncol) at[c * 128] = sum[c];
+        for (int c = 0; c < BN / 2; ++c) {
+          const int col = (c / 16) * 32 + half * 16 + c % 16;
+          if (col < ncol) at[col * 128] = sum[c];
+        }
       } else {
 #pragma unroll 1
-        for (int c = 0; c < ncol; c += 16) {
+        for (int c = half * 16; c < ncol; c += 32) {
           float v[16];
           load16(src + c, 0.f, v);
 #pragma unroll
@@ -908,7 +945,7 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       tc::bulk_commit();
     }
     if (warp >= 2 && c1 > c0) {
-      ready = !tc::named_sync_or(2, 128, !wait_phase_cluster(&received, 0, A.wait_ns, &s_abort)) && ready;
+      ready = !tc::named_sync_or(2, 256, !wait_phase_cluster(&received, 0, A.wait_ns, &s_abort)) && ready;
       if (!ready) raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
     }
   }
@@ -920,9 +957,9 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   if (warp >= 2 && ready) {
     const float* mine = part + quad * 32 + lane;
     // (unrolled where the tile is in registers, whose places are fixed at compile time)
-#pragma unroll (PROMOTE ? BN / 16 : 1)
-    for (int cc = 0; cc < BN; cc += 16) {
-      const int c = c0 + cc;
+#pragma unroll (PROMOTE ? BN / 32 : 1)
+    for (int cc = 0; cc < BN / 2; cc += 16) {
+      const int c = c0 + 2 * cc + half * 16;
       if (c >= c1) break;
       float v[16];
       if (splits == 1) {
@@ -972,7 +1009,7 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     }
     if (A.staged) {
       tc::fence_async_smem();
-      tc::named_sync(1, 128);
+      tc::named_sync(1, 256);
       if (warp == 2 && lane == 0) {                // boxes of 8 columns
         for (int c = c0; c < c1; c += 8) {
           tma_store_2d(&maps.y, tc::smem_u32(out) + (c - c0) * 128 * (A.epi.out_bf ? 2 : 4),
@@ -1031,13 +1068,14 @@ bool encode_out(CUtensorMap* m, const void* base, bool bf, int64_t I, int64_t J,
 }
 
 // The output leaves by TMA where y and z have 16-byte aligned rows; the residual arrives by it
-// (pair kernel) where it has y's type and such rows too.
+// (pair kernel) where it has such rows too.
 void encode_outputs(const Gemm& g, TcArgs* A, OutMaps* m, int rows, bool residual) {
   const GemmEpilogue& E = g.epi;
   A->staged = encode_out(&m->y, E.out, E.out_bf, g.I, g.J, E.out_ld, rows) &&
               (!E.z || encode_out(&m->z, E.z, E.z_bf, g.I, g.J, E.z_ld, rows));
-  A->res_staged = residual && A->staged && E.res && E.res_bf == E.out_bf &&
-                  encode_out(&m->res, E.res, E.res_bf, g.I, g.J, E.res_ld, rows);
+  A->res_mode = kResDirect;
+  if (residual && A->staged && E.res && encode_out(&m->res, E.res, E.res_bf, g.I, g.J, E.res_ld, rows))
+    A->res_mode = E.res_bf == E.out_bf ? kResInPlace : kResChunk;
 }
 
 // The kernel's shared-memory limit, raised once for each device.
@@ -1057,7 +1095,7 @@ template <bool AMN, bool BMN, bool PROMOTE>
 cudaError_t launch_pair(const Gemm& g, TcArgs A, int planes, int pairs, cudaStream_t st) {
   CUtensorMap ma, mb;
   OutMaps out;
-  A.cols = g.epi.out_bf && (!g.epi.z || g.epi.z_bf) ? 32 : 16;
+  A.cols = g.epi.out_bf && (!g.epi.z || g.epi.z_bf) && (!g.epi.res || g.epi.res_bf) ? 32 : 16;
   encode_outputs(g, &A, &out, A.cols, true);
   // The width that wastes least in the last wave.  A narrower tile moves more bytes for its
   // products, so it takes longer than its share of a wide one's time (measured on 16384 x 4096 x
@@ -1098,7 +1136,7 @@ cudaError_t launch_split(const Gemm& g, TcArgs A, int planes, int splits, cudaSt
   const size_t bytes = (splits == 1 ? 0 : 128 * BN * 4 + (splits - 1) * cols * 512) +
                        cols * 128 * ((g.epi.out_bf ? 2 : 4) + (!g.epi.z ? 0 : g.epi.z_bf ? 2 : 4));
   if (bytes <= (SplitShape<BN, PARTS>::smem) - 1024) encode_outputs(g, &A, &out, 8, false);
-  else A.staged = A.res_staged = false;
+  else A.staged = false;
   if (!encode(&ma, g.A, g.I, g.C, planes, 128) || !encode(&mb, g.B, g.J, g.C, planes, BN)) return cudaErrorInvalidValue;
   A.tiles_i = static_cast<int32_t>((g.I + 127) / 128);
   A.tiles_j = static_cast<int32_t>((g.J + BN - 1) / BN);

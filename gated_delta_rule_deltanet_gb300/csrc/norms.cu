@@ -21,18 +21,24 @@ namespace kda {
 
 // ---------------------------------------------------------------- partial rows
 
+// the stretches that have an output, and their places in a partial row
+struct LiveOuts {
+  float* p[3];
+  int at[3];
+};
+
 // A block adds 8 columns (one sector of each partial row) with 32 row lanes: some 20 loads a thread
 // for the 608 partial rows of the longest sums, 8 of them in flight (15 us with 32 columns and
 // 8 row lanes, 4 us so).
 __global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict__ part, int parts,
-                                                        int64_t cols, float alpha, SumOuts outs) {
+                                                        int64_t cols, int segments, float alpha,
+                                                        LiveOuts outs) {
   __shared__ float s[32][9];
   const int col = threadIdx.x & 7, row = threadIdx.x >> 3;
   float* out = outs.p[blockIdx.y];
-  if (!out) return;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + col;
-  const int64_t stride = cols * gridDim.y;
-  const float* src = part + blockIdx.y * cols + c;
+  const int64_t stride = cols * segments;
+  const float* src = part + outs.at[blockIdx.y] * cols + c;
   float a = 0.f;
   if (c < cols) {
     for (int p = row; p < parts; p += 32 * 8) {
@@ -55,11 +61,16 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict_
 
 cudaError_t launch_sum_parts(const float* part, int parts, int64_t cols, int segments, float alpha,
                              const SumOuts& outs, cudaStream_t st) {
-  bool any = false;
-  for (int i = 0; i < segments; ++i) any = any || outs.p[i];
-  if (!any || cols == 0) return cudaSuccess;
-  const dim3 grid(static_cast<unsigned>((cols + 7) / 8), static_cast<unsigned>(segments));
-  sum_parts_kernel<<<grid, 256, 0, st>>>(part, parts, cols, alpha, outs);
+  LiveOuts live{};
+  int n = 0;
+  for (int i = 0; i < segments; ++i)
+    if (outs.p[i]) {
+      live.p[n] = outs.p[i];
+      live.at[n++] = i;
+    }
+  if (n == 0 || cols == 0) return cudaSuccess;
+  const dim3 grid(static_cast<unsigned>((cols + 7) / 8), static_cast<unsigned>(n));
+  sum_parts_kernel<<<grid, 256, 0, st>>>(part, parts, cols, segments, alpha, live);
   return cudaGetLastError();
 }
 
@@ -703,6 +714,8 @@ static RowRing row_ring(const ResidualNormArgs& A, bool xbf, bool hbf, bool bwd,
   R.stage = (at + 127) / 128 * 128;
   const size_t share = kRingBytes / rows_per_sm(A.N, bwd);
   R.stages = static_cast<int>(std::min<size_t>(kMaxStages, share / R.stage));
+  // (backward rows above 4096: four chunks a thread do not fit the registers beside the sums)
+  if (bwd && row_shape(A.N).V == 4) return R;
   if (R.stages < 2 || A.T < 3 * static_cast<int64_t>(grid)) R.stages = 0;
   return R;
 }
