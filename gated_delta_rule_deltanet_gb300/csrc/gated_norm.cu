@@ -1,7 +1,9 @@
 // gated_norm.cu -- the output norm of the recurrence: the RMS norm of every token's and head's row
 // of o, times weight, times act(gate), forward and backward (rms' as in norms.cu).
 //
-// Bound by HBM: 8 bytes an element forward with an fp32 o and bf16 gate and y, 14 backward.
+// Bound by HBM: 8 bytes an element forward with an fp32 o and bf16 gate and y, 14 backward.  32768
+// tokens x 32 heads x 128: 172 us, 92% of the measured copy rate; backward of 16384 x 16 x 128: 86 us,
+// 80% (60% of the issue slots go to the gate's exponential and the conversions).
 #include <algorithm>
 
 #include "layer_common.cuh"

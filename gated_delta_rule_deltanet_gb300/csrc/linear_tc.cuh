@@ -10,28 +10,32 @@
 //
 // Two kernels.
 //
-//   gemm_pair_kernel   large products.  A pair of CTAs (cta_group::2) works on a 256 x 256 tile: each
-//                      stages its own 128 rows of A and of B, so a 64-wide step of c moves 32 KB
-//                      into each SM for 512 tensor cycles, half of what two single CTAs with
-//                      the same accumulators would move.  Persistent: the two 256-column
-//                      accumulators alternate, one being multiplied into while eight warps
-//                      store the other.  Bound by the tensor pipe and, over seconds, by power.
+//   gemm_pair_kernel   large products.  A pair of CTAs (cta_group::2) works on a 256 x BN tile (BN
+//                      128 to 256, see launch_pair): each stages its own half of the rows of A and
+//                      of B, so a 64-wide step of c moves 32 KB into each SM for 512 tensor
+//                      cycles, half of what two single CTAs with the same accumulators would
+//                      move.  Persistent: the two accumulators alternate, one being multiplied
+//                      into while eight warps store the other through shared memory and TMA.
+//                      Bound by the tensor pipe and, over seconds, by power: 32768 x 4096 x 4096
+//                      535 us, 2.06 PFLOP/s (the vendor library's product: 532 us).
 //   gemm_split_kernel  small products, mostly few rows (decode: the weight is the work).  One CTA
 //                      holds a 128 x BN tile; a cluster of S CTAs splits the sum over c: each
 //                      pushes its part of every other CTA's columns into that CTA's shared
 //                      memory and adds what it receives in rank order, so the result does not
-//                      depend on timing and needs no workspace.  Bound by HBM for few rows: a deep
-//                      TMA ring keeps the weight streaming.
+//                      depend on timing and needs no workspace.  Bound by HBM and by set-up: 64
+//                      rows through 4096 -> 12288 15.7 us (6.5 TB/s, the weight largely in L2),
+//                      16 through 4096 -> 4096 9.1 us.
 //
 // fp32 operands are split into three bf16 parts, x = hi + mid + lo with every part rounded to
 // nearest, which hold all 24 bits; the six products of parts above 2^-27 relative are summed,
 // smallest first.  The tensor cores cut the accumulator's low bits at every step of 16 instead of
-// rounding them, always towards zero, so a long sum would lose several times fp32's rounding
-// (1.2e-6 relative at c = 1000, growing with c): the split kernel therefore moves the accumulator
-// into registers every 64 steps of c, where it is added with rounding.  The pair kernel
-// does the same every 512 steps, into a third stretch of tensor memory, where bf16 operands have
-// an fp32 result over more than 1024 steps (c = 4096: 4.4e-6 of the norm without, 4.8e-7 with; the tile is then 160
-// columns wide, three of which fit).  A bf16 result rounds by far more than the truncation.
+// rounding them, always towards zero, so a long sum would lose several times fp32's rounding.
+// The split kernel therefore moves the accumulator into registers every 64 steps of c, where it is
+// added with rounding (c = 4096: 1.7e-7 of the norm, an fp32 product on CUDA cores 1.1e-6, at 2.6
+// times its speed).  Where bf16 operands have an fp32 result over more than 1024 steps both kernels
+// do the same every 512, the pair kernel into a third stretch of tensor memory of 160 columns
+// (c = 4096: 4.8e-7 against 4.4e-6 without; 4096 x 8192 x 4096 245 us against 154).  A bf16 result
+// rounds by far more than the truncation.
 //
 // Every wait is bounded; one that gives up raises KDA_DEVERR_TIMEOUT, and the CTAs leave through
 // the same barriers as otherwise.
@@ -262,8 +266,7 @@ __device__ __forceinline__ void scatter16(void* p, int64_t ld, int64_t at, int n
 }
 // scale act(v), the choice of activation outside the loops: with two epilogue warps a scheduler a
 // test an element set the pace of the persistent kernel (SiLU with the pre-activation kept on 6731
-// x 4096 -> 8192: 323 us, so 300 us).  bf16 results take the
-// faster functions.
+// x 4096 -> 8192: 323 us, now 293 us).  bf16 results take the faster functions.
 template <typename F>
 __device__ __forceinline__ void map16(float (&v)[16], float scale, F f) {
 #pragma unroll
@@ -361,7 +364,7 @@ __device__ __forceinline__ void add16(const unsigned char* tile, bool bf, int co
   }
 }
 
-// ------------------------------------------------------------------ pairs of CTAs, 256 x 256 tiles
+// ------------------------------------------------------------------ pairs of CTAs
 
 constexpr int kPairStages = 6;
 constexpr int kPairStretch = 8;                    // PROMOTE: 64-wide steps in one accumulator

