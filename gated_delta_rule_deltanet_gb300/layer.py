@@ -217,7 +217,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
                             cuda_cores)
     if out is None:
         out = torch.empty(plan.shape, dtype=plan.dtype, device=plan.device)
-    z = x.new_empty(plan.shape) if save_pre_activation else None
+    z = torch.empty(plan.shape, dtype=x.dtype, device=plan.device) if save_pre_activation else None
     space, address, nbytes = _space(plan, workspace)
     _call(plan, x.data_ptr(), weight.data_ptr(), _p(bias), _p(residual),
           out.data_ptr(), _p(z), address, nbytes)
@@ -267,9 +267,10 @@ def linear_bwd(x: torch.Tensor, weight: torch.Tensor, d_y: torch.Tensor, *,
     if plan is None:
         plan = _plan_linear_bwd(key, x, weight, d_y, activation, pre_activation, scale, dw_dtype,
                                 cuda_cores)
-    dx = x.new_empty(x.shape) if need_dx else None
-    dw = weight.new_empty(weight.shape, dtype=plan.dtype2) if need_dw else None
-    dbias = x.new_empty(plan.shape[1:], dtype=torch.float32) if need_bias else None
+    dev = plan.device
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if need_dx else None
+    dw = torch.empty(weight.shape, dtype=plan.dtype2, device=dev) if need_dw else None
+    dbias = torch.empty(plan.shape[1:], dtype=torch.float32, device=dev) if need_bias else None
     space, address, nbytes = _space(plan, workspace)
     _call(plan, x.data_ptr(), weight.data_ptr(), _p(pre_activation),
           d_y.data_ptr(), _p(dx), _p(dw), _p(dbias), address, nbytes)
@@ -355,7 +356,7 @@ def residual_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
     if h_out is None:
         h_out = torch.empty(plan.shape, dtype=plan.dtype, device=plan.device)
     if out is None and weight is not None:
-        out = x.new_empty(plan.shape)
+        out = torch.empty_like(x)
     _call(plan, x.data_ptr(), _p(residual), _p(gate), _p(post_weight),
           _p(weight), h_out.data_ptr(), _p(out))
     return out, h_out
@@ -402,11 +403,13 @@ def residual_norm_bwd(x: torch.Tensor, h: torch.Tensor, weight: Optional[torch.T
     plan = _PLANS.get(key)
     if plan is None:
         plan = _plan_residual_norm_bwd(key, x, h, weight, d_y, d_h, post_weight, gate, scale, eps)
-    dx = x.new_empty(x.shape)
-    d_residual = h.new_empty(h.shape)
-    d_weight = weight.new_empty(plan.shape) if weight is not None else None
-    d_post = post_weight.new_empty(plan.shape) if post_weight is not None else None
-    d_gate = gate.new_empty(gate.shape) if gate is not None else None
+    dx = torch.empty_like(x)
+    d_residual = torch.empty_like(h)
+    d_weight = torch.empty_like(weight) if weight is not None else None
+    d_post = torch.empty_like(post_weight) if post_weight is not None else None
+    d_gate = None
+    if gate is not None:
+        d_gate = torch.empty(gate.shape, dtype=gate.dtype, device=plan.device)
     space, address, nbytes = _space(plan, workspace)
     _call(plan, x.data_ptr(), h.data_ptr(), _p(gate), _p(post_weight),
           _p(weight), _p(d_y), _p(d_h), dx.data_ptr(), d_residual.data_ptr(), _p(d_gate),
@@ -493,9 +496,9 @@ def gated_norm_bwd(o: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, d_
     plan = _PLANS.get(key)
     if plan is None:
         plan = _plan_gated_norm_bwd(key, o, gate, weight, d_y, activation, eps)
-    d_o = o.new_empty(o.shape)
-    d_gate = gate.new_empty(gate.shape)
-    d_weight = weight.new_empty(weight.shape)
+    d_o = torch.empty_like(o)
+    d_gate = torch.empty(gate.shape, dtype=gate.dtype, device=plan.device)
+    d_weight = torch.empty_like(weight)
     space, address, nbytes = _space(plan, workspace)
     _call(plan, o.data_ptr(), gate.data_ptr(), weight.data_ptr(),
           d_y.data_ptr(), d_o.data_ptr(), d_gate.data_ptr(), d_weight.data_ptr(), address, nbytes)
