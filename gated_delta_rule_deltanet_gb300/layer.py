@@ -162,12 +162,19 @@ def _unaligned(t, flag):
     return flag if t.data_ptr() % 16 else 0
 
 
-def _linear_plan(key, p, backward, dev, shape, y_dtype, dw_dtype=None):
+def _bytes(name, p, flag, dev):
+    """A workspace size, asked for with the tensors' device current (it depends on its SMs)."""
     n = ctypes.c_size_t(0)
-    st = _lib.load().kda_linear_workspace_size(ctypes.byref(p), backward, ctypes.byref(n))
+    with torch.cuda.device(dev):
+        st = getattr(_lib.load(), name)(ctypes.byref(p), flag, ctypes.byref(n))
     if st != _lib.KDA_OK:
-        raise KdaError(st, "kda_linear_workspace_size")
-    return _keep(key, _Plan("kda_linear_bwd" if backward else "kda_linear_fwd", p, dev, n.value, shape,
+        raise KdaError(st, name)
+    return n.value
+
+
+def _linear_plan(key, p, backward, dev, shape, y_dtype, dw_dtype=None):
+    nbytes = _bytes("kda_linear_workspace_size", p, backward, dev)
+    return _keep(key, _Plan("kda_linear_bwd" if backward else "kda_linear_fwd", p, dev, nbytes, shape,
                             y_dtype, dw_dtype))
 
 
@@ -289,14 +296,6 @@ def _norm_gate(gate, x, p, N):
         p.gate_row_stride = _rows(gate, tuple(x.shape), (x.dtype,), "a per-token gate")
 
 
-def _norm_bytes(p, gated):
-    n = ctypes.c_size_t(0)
-    st = _lib.load().kda_norm_workspace_size(ctypes.byref(p), gated, ctypes.byref(n))
-    if st != _lib.KDA_OK:
-        raise KdaError(st, "kda_norm_workspace_size")
-    return n.value
-
-
 def _residual_params(x, h_dtype, scale, eps):
     if x.dim() != 2 or x.dtype not in _QKV_DTYPES or not x.is_contiguous():
         raise ValueError("x must be contiguous [T, N] float32 or bfloat16")
@@ -381,7 +380,8 @@ def _plan_residual_norm_bwd(key, x, h, weight, d_y, d_h, post_weight, gate, scal
         if t is not None:
             _dense(t, (N,), torch.float32, name)
     _norm_gate(gate, x, p, N)
-    return _keep(key, _Plan("kda_residual_norm_bwd", p, dev, _norm_bytes(p, 0), (N,)))
+    nbytes = _bytes("kda_norm_workspace_size", p, 0, dev)
+    return _keep(key, _Plan("kda_residual_norm_bwd", p, dev, nbytes, (N,)))
 
 
 def residual_norm_bwd(x: torch.Tensor, h: torch.Tensor, weight: Optional[torch.Tensor],
@@ -479,7 +479,8 @@ def _plan_gated_norm_bwd(key, o, gate, weight, d_y, activation, eps):
     dev = _device(o, gate, weight, d_y)
     p = _gated_params(o, gate, weight, d_y.dtype, activation, eps)
     _dense(d_y, o.shape, d_y.dtype, "d_y")
-    return _keep(key, _Plan("kda_gated_norm_bwd", p, dev, _norm_bytes(p, 1)))
+    nbytes = _bytes("kda_norm_workspace_size", p, 1, dev)
+    return _keep(key, _Plan("kda_gated_norm_bwd", p, dev, nbytes))
 
 
 def gated_norm_bwd(o: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, d_y: torch.Tensor, *,

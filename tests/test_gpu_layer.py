@@ -217,6 +217,20 @@ def test_linear_cuda_cores_path():
     linear_case(3, 140, 96, 150, "bf16", act="silu", bias=True, cuda_cores=True)
 
 
+@pytest.mark.parametrize("K", [1, 3, 66, 2047, 2049, 4161])
+@pytest.mark.parametrize("off", [0, 1, 2, 5])
+def test_linear_copies_of_unaligned_rows(K, off):
+    """Widths around the copy's word and stretch sizes, from even and odd elements."""
+    r = rng(14, K, off)
+    T, N = 20, 24
+    wide, wide64 = dev(r.standard_normal((T, K + 11)), "bf16")
+    w, w64 = dev(r.standard_normal((N, K)), "bf16")
+    x64 = wide64[:, off:off + K]
+    y = kda.linear(wide[:, off:off + K], w, out_dtype=torch.float32)
+    no_error()
+    check("y", y, x64 @ w64.T, product_tol(x64, w64.T, K, "bf16"))
+
+
 @pytest.mark.parametrize("off,pad", [(0, 8), (8, 24), (1, 3), (3, 8)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_linear_column_blocks(off, pad, dtype):
@@ -271,10 +285,11 @@ def test_linear_wide_values(dtype):
     assert not y[3].any()
 
 
-def test_linear_infinite_token_stays_in_its_row():
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_linear_infinite_token_stays_in_its_row(dtype):
     r = rng(7)
-    x, _ = dev(r.standard_normal((150, 64)), "bf16")
-    w, _ = dev(r.standard_normal((64, 64)), "bf16")
+    x, _ = dev(r.standard_normal((150, 64)), dtype)
+    w, _ = dev(r.standard_normal((64, 64)), dtype)
     clean = kda.linear(x, w)
     x[5, 9] = float("inf")
     x[77, 0] = float("nan")
