@@ -120,6 +120,9 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t sdst, const void* map,
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+__device__ __forceinline__ void prefetch_map(const void* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 // Tiled TMA store of one box from shared memory (tracked by the issuing thread's bulk groups);
 // rows and columns past the map's extents are not written.
 __device__ __forceinline__ void tma_store_2d(const void* map, uint32_t ssrc, int32_t x, int32_t y) {
@@ -444,6 +447,10 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
   constexpr bool FULL = !AMN;
   const int stretch = PROMOTE ? kPairStretch : A.kblocks;
 
+  if (threadIdx.x == 32) {
+    prefetch_map(&map_a);
+    prefetch_map(&map_b);
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPairStages; ++s) {
       tc::mbar_init(&full[s], 1);
@@ -601,7 +608,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         }
         hand_over(q + 2);
       }
-      tc::bulk_wait_all();
+      tc::bulk_wait_read();                        // (the stores themselves end with the kernel)
     }
     __syncwarp();
   } else {
@@ -756,8 +763,9 @@ struct SplitShape {
   static constexpr int planes = PARTS == 6 ? 3 : 1;
   static constexpr uint32_t a_bytes = planes * kOpBytes;
   static constexpr uint32_t stage = a_bytes + planes * BN * kBK * 2;
-  // the ring: as deep as two CTAs an SM allow for the narrow tile, 200 KB for the others
-  static constexpr int stages = PARTS == 6 ? (BN == 64 ? 3 : 2) : BN == 128 ? 6 : 4;
+  // the ring: some 200 KB, one CTA an SM (with 96 KB and two CTAs the narrow tile's loads waited on
+  // the ring: 16 x 4096 -> 16384 from HBM 32.6 us, so 25.2 us)
+  static constexpr int stages = PARTS == 6 ? (BN == 64 ? 3 : 2) : BN == 64 ? 8 : BN == 128 ? 6 : 4;
   static constexpr size_t smem = static_cast<size_t>(stage) * stages + 1024;
   // a split's own part and those received (7 shares of up to BN / 8 + 7 columns, or one of BN / 2)
   static_assert(BN == 256 || static_cast<size_t>(stage) * stages >= 128 * 4 * (BN + 7 * 8 + BN),
@@ -786,6 +794,18 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   const int stretch = PARTS == 6 ? 1 : PARTS == 1 ? kPairStretch : k1 - k0;
   constexpr uint32_t kCols = PROMOTE ? 2 * BN : BN;
 
+  auto load_stage = [&](int s, int k) {
+    const uint32_t sa = smem + s * S::stage, sb = sa + S::a_bytes;
+    tc::mbar_arrive_expect_tx(&full[s], S::stage);
+    load_operand<AMN, 128, S::planes>(sa, i0, k * kBK, [&](uint32_t d, int32_t x, int32_t y) {
+      tc::tma_load_3d(d, &map_a, x, y, 0, &full[s]);
+    });
+    load_operand<BMN, BN, S::planes>(sb, j0, k * kBK, [&](uint32_t d, int32_t x, int32_t y) {
+      tc::tma_load_3d(d, &map_b, x, y, 0, &full[s]);
+    });
+  };
+  // The first stages are requested before the block meets: the loads need nothing but their barriers.
+  const int early = min(S::stages, k1 - k0);
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::stages; ++s) {
       tc::mbar_init(&full[s], 1);
@@ -798,6 +818,7 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     tc::mbar_init(&received, 1);
     tc::fence_mbar_init();
     s_abort = 0;
+    for (int s = 0; s < early; ++s) load_stage(s, k0 + s);
   }
   if (warp == 1) {
     tc::tmem_alloc(&s_tmem, kCols);
@@ -809,25 +830,17 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   const uint32_t tmem = s_tmem;
 
   if (warp == 0) {
-    Ring<S::stages> at;
-    int it = 0;
+    Ring<S::stages> at;                            // after a first pass over the ring
+    at.ph = 1;
+    int it = early;
     bool ok = true;
-    for (int k = k0; k < k1; ++k, ++it, at.next()) {
+    for (int k = k0 + early; k < k1; ++k, ++it, at.next()) {
       const int s = at.s;
       if (!__all_sync(0xffffffffu, wait_phase(&empty[s], at.ph ^ 1, A.wait_ns, &s_abort))) {
         ok = false;
         break;
       }
-      const uint32_t sa = smem + s * S::stage, sb = sa + S::a_bytes;
-      if (elect_one()) {
-        tc::mbar_arrive_expect_tx(&full[s], S::stage);
-        load_operand<AMN, 128, S::planes>(sa, i0, k * kBK, [&](uint32_t d, int32_t x, int32_t y) {
-          tc::tma_load_3d(d, &map_a, x, y, 0, &full[s]);
-        });
-        load_operand<BMN, BN, S::planes>(sb, j0, k * kBK, [&](uint32_t d, int32_t x, int32_t y) {
-          tc::tma_load_3d(d, &map_b, x, y, 0, &full[s]);
-        });
-      }
+      if (elect_one()) load_stage(s, k);
       __syncwarp();
     }
     if (!ok && lane == 0) {                        // wait for the copies in flight
@@ -1041,11 +1054,11 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                          static_cast<int32_t>(i0), static_cast<int32_t>(j0) + c);
         }
         tc::bulk_commit();
-        tc::bulk_wait_all();
+        tc::bulk_wait_read();                      // (the stores themselves end with the kernel)
       }
     }
   }
-  if (splits > 1 && threadIdx.x == 0) tc::bulk_wait_all();   // this CTA's pushes have left
+  if (splits > 1 && threadIdx.x == 0) tc::bulk_wait_read();   // this CTA's pushes have left
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 1) {
@@ -1149,10 +1162,48 @@ cudaError_t launch_pair(const Gemm& g, TcArgs A, int planes, int pairs, cudaStre
   return cudaGetLastError();
 }
 
+// How many clusters of `size` CTAs of kernel k run at once on the current device (asked once).
+template <typename Kernel>
+int active_clusters(Kernel k, int size, size_t smem, std::atomic<int> (&known)[16][9]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16) return 0;
+  int n = known[dev][size].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(size));
+    cfg.blockDim = dim3(kSplitThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = static_cast<unsigned>(size);
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess) n = 0;
+    n = std::max(n, 1);
+    known[dev][size].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// `splits`: the most ways that pay; fewer where their clusters would not all run at once (a cluster
+// lies within a group of SMs: 48 clusters of three on 152 SMs took two waves, 14.2 us against 9.9
+// for 48 of two).
 template <bool AMN, bool BMN, int BN, int PARTS>
 cudaError_t launch_split(const Gemm& g, TcArgs A, int planes, int splits, cudaStream_t st) {
   CUtensorMap ma, mb;
   OutMaps out;
+  A.tiles_i = static_cast<int32_t>((g.I + 127) / 128);
+  A.tiles_j = static_cast<int32_t>((g.J + BN - 1) / BN);
+  const int64_t tiles = static_cast<int64_t>(A.tiles_i) * A.tiles_j;
+  auto k = gemm_split_kernel<AMN, BMN, BN, PARTS>;
+  static std::atomic<uint64_t> raised{0};
+  cudaError_t e = raise_smem(k, (SplitShape<BN, PARTS>::smem), raised);
+  if (e != cudaSuccess) return e;
+  static std::atomic<int> active[16][9];
+  while (splits > 1 &&
+         (tiles * splits > sm_count() || tiles > active_clusters(k, splits, (SplitShape<BN, PARTS>::smem), active)))
+    --splits;
   // what does not fit behind the parts is stored directly
   const size_t cols = splits == 1 ? BN : ((BN + splits - 1) / splits + 15) / 16 * 16;
   const size_t bytes = (splits == 1 ? 0 : 128 * BN * 4 + (splits - 1) * cols * 512) +
@@ -1160,14 +1211,8 @@ cudaError_t launch_split(const Gemm& g, TcArgs A, int planes, int splits, cudaSt
   if (bytes <= (SplitShape<BN, PARTS>::smem) - 1024) encode_outputs(g, &A, &out, 8, false);
   else A.staged = false;
   if (!encode(&ma, g.A, g.I, g.C, planes, 128) || !encode(&mb, g.B, g.J, g.C, planes, BN)) return cudaErrorInvalidValue;
-  A.tiles_i = static_cast<int32_t>((g.I + 127) / 128);
-  A.tiles_j = static_cast<int32_t>((g.J + BN - 1) / BN);
-  auto k = gemm_split_kernel<AMN, BMN, BN, PARTS>;
-  static std::atomic<uint64_t> raised{0};
-  cudaError_t e = raise_smem(k, (SplitShape<BN, PARTS>::smem), raised);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(A.tiles_i) * A.tiles_j * splits));
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
   cfg.blockDim = dim3(kSplitThreads);
   cfg.dynamicSmemBytes = (SplitShape<BN, PARTS>::smem);
   cfg.stream = st;
@@ -1195,21 +1240,17 @@ cudaError_t launch_shape(const Gemm& g, int planes, cudaStream_t st) {
   if (planes == 1 && big >= sms / 4 && g.J > 128)
     return promote ? launch_pair<AMN, BMN, true>(g, A, planes, sms / 2, st)
                    : launch_pair<AMN, BMN, false>(g, A, planes, sms / 2, st);
-  // Few tiles.  64 columns at least (narrower tiles were no faster even for 16 rows), the tile halved
-  // while too few CTAs would run; 256 columns only unsplit, as the parts would not fit.
-  int bn = 64;
-  while (bn < (promote ? 128 : 256) && bn < g.J) bn *= 2;
+  // Few tiles.  128 columns, 64 where there are no more rows or too few tiles to fill the SMs with a
+  // split, 256 (unsplit, as the parts would not fit) where 128 would take a second wave.  An SM takes
+  // in some 90 GB/s, so a weight streams at HBM's rate only into most of them: splits as many as
+  // run at once (launch_split), with four steps a CTA at least; beyond four ways the exchange costs
+  // more than it saves unless c is long (16 x 4096 -> 4096: 4 ways 8.4 us, 8 ways 9.5 us).
   auto tiles_for = [&](int n) { return ((g.I + 127) / 128) * ((g.J + n - 1) / n); };
-  // CTAs that run at once
-  auto room = [&](int n) { return static_cast<int64_t>(sms) * (n <= 64 && planes == 1 ? 2 : 1); };
-  while (bn > 64 && tiles_for(bn) * (planes == 3 ? std::min(4, A.kblocks) : 2) <= room(bn)) bn /= 2;
-  const int64_t tiles = tiles_for(bn);
-  // Splits fill the SMs, with four steps a CTA at least; beyond four ways the exchange costs more than
-  // it saves unless c is long (16 x 4096 -> 4096: 4 ways 8.4 us, 8 ways 9.5 us).
+  int bn = g.J <= 64 || tiles_for(128) * 8 <= sms ? 64 : 128;
+  if (bn == 128 && !promote && tiles_for(128) > sms) bn = 256;
   const int steps = A.kblocks * (planes == 3 ? 6 : 1);
-  int splits = static_cast<int>(std::min<int64_t>(steps >= 128 ? 8 : 4, std::max<int64_t>(1, room(bn) / tiles)));
-  splits = bn == 256 ? 1 : std::max(1, std::min(splits, std::min(steps / 4, A.kblocks)));
-  if (tiles * splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const int splits = bn == 256 ? 1 : std::max(1, std::min(std::min(steps >= 128 ? 8 : 4, steps / 4), A.kblocks));
+  if (tiles_for(bn) * splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   if (planes == 3)
     return bn == 64 ? launch_split<AMN, BMN, 64, 6>(g, A, planes, splits, st)
                     : launch_split<AMN, BMN, 128, 6>(g, A, planes, splits, st);

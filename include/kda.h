@@ -506,8 +506,8 @@ typedef struct kda_linear_params {
  * are split into three bf16 parts in the workspace (24 bits in all), whose six leading products
  * the tensor cores sum in fp32; there a sum with an infinite term may come out as NaN, and values
  * below 2^-109 keep fewer than 24 bits (their last part is subnormal and counts as zero).
- * KDA_FLAG_CUDA_CORES multiplies in fp32 on CUDA cores instead.  Up to 8 tokens the forward runs on
- * CUDA cores and reads both operands in place.
+ * KDA_FLAG_CUDA_CORES multiplies in fp32 on CUDA cores instead.  The forward of up to 2 tokens, or
+ * of up to 8 where w would have to be copied, runs on CUDA cores and reads both operands in place.
  */
 kda_status_t kda_linear_fwd(const kda_linear_params_t *p, const void *x, const void *w,
                             const float *bias, const void *residual, void *y, void *pre_act,
