@@ -1,4 +1,5 @@
-// linear_rows.cu -- the projection of a few tokens (decode): out[j, i] for j < 8.
+// linear_rows.cu -- the projection of a few tokens (decode): out[j, i] for j < 2, or j < 8 where the
+// tensor cores would need a copy of the weight.
 //
 // Bound by HBM: every weight is read once for at most 8 multiply-adds, which the CUDA cores do as
 // fp32 pairs.  A warp owns R = 4 rows of the weight (4 outputs a token) and walks them together, 16

@@ -22,18 +22,19 @@ struct RepackArgs {
   } a[3];
 };
 
-// Bound by HBM: two elements a thread and step, four steps in flight.  bf16 rows that start in the
-// middle of a 4-byte word are read as the words that hold them (each holds at least one element
-// of the row) and shifted by one element against the next lane's word.
+// Bound by HBM.  A warp copies 256 elements of a row, two a lane and step, four steps in flight.  bf16
+// rows that start in the middle of a 4-byte word are read as the words that hold them (each
+// holds at least one element of the row) and shifted by one element against the next lane's word.
 template <bool BF>
 __global__ void __launch_bounds__(256) repack_kernel(const RepackArgs R) {
   const auto& a = R.a[blockIdx.y];
   const int64_t plane = a.rows * a.ld;
-  const int64_t cb = (a.cols + 2047) / 2048;
+  const int64_t cb = (a.cols + 255) / 256;
   const int lane = threadIdx.x & 31;
-  for (int64_t u = blockIdx.x; u < a.rows * cb; u += gridDim.x) {
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); u < a.rows * cb; u += warps) {
     const int64_t r = u / cb;
-    const int64_t c0 = (u - r * cb) * 2048 + 2 * threadIdx.x;
+    const int64_t c0 = (u - r * cb) * 256 + 2 * lane;
     if constexpr (BF) {
       const uint16_t* row = static_cast<const uint16_t*>(a.src) + r * a.src_ld;
       const int odd = (reinterpret_cast<uintptr_t>(row) >> 1) & 1;
@@ -42,7 +43,7 @@ __global__ void __launch_bounds__(256) repack_kernel(const RepackArgs R) {
       uint32_t lo[4], hi[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int64_t w = (c0 >> 1) + e * 256;
+        const int64_t w = (c0 >> 1) + e * 32;
         lo[e] = w < nw ? words[w] : 0;
         hi[e] = odd && lane == 31 && w + 1 < nw ? words[w + 1] : 0;
       }
@@ -52,7 +53,7 @@ __global__ void __launch_bounds__(256) repack_kernel(const RepackArgs R) {
           const uint32_t next = __shfl_down_sync(0xffffffffu, lo[e], 1);
           lo[e] = (lo[e] >> 16) | ((lane == 31 ? hi[e] : next) << 16);
         }
-        const int64_t c = c0 + e * 512;
+        const int64_t c = c0 + e * 64;
         if (c < a.cols) *reinterpret_cast<uint32_t*>(a.dst + r * a.ld + c) = lo[e];   // (the padding takes the rest)
       }
     } else {
@@ -60,13 +61,13 @@ __global__ void __launch_bounds__(256) repack_kernel(const RepackArgs R) {
       float x[4][2];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int64_t c = c0 + e * 512;
+        const int64_t c = c0 + e * 64;
         x[e][0] = c < a.cols ? row[c] : 0.f;
         x[e][1] = c + 1 < a.cols ? row[c + 1] : 0.f;
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int64_t c = c0 + e * 512;
+        const int64_t c = c0 + e * 64;
         if (c >= a.cols) continue;
         uint16_t p[3], q[3];
         split3(x[e][0], p);
@@ -91,7 +92,7 @@ cudaError_t launch_repack(const Repack* arrays, int count, bool bf16, cudaStream
   for (int i = 0; i < count; ++i) {
     const Repack& a = arrays[i];
     R.a[i] = {a.src, static_cast<uint16_t*>(a.dst), a.src_ld, a.rows, a.cols, padded(a.cols)};
-    units = std::max(units, a.rows * ((a.cols + 2047) / 2048));
+    units = std::max(units, (a.rows * ((a.cols + 255) / 256) + 7) / 8);   // blocks of eight warps
   }
   if (units == 0) return cudaSuccess;
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(units, static_cast<int64_t>(sm_count()) * 16)),
