@@ -22,9 +22,9 @@
 //                      holds a 128 x BN tile; a cluster of S CTAs splits the sum over c: each
 //                      pushes its part of every other CTA's columns into that CTA's shared
 //                      memory and adds what it receives in rank order, so the result does not
-//                      depend on timing and needs no workspace.  Bound by HBM and by set-up: 64
-//                      rows through 4096 -> 12288 15.7 us (6.5 TB/s, the weight largely in L2),
-//                      16 through 4096 -> 4096 9.1 us.
+//                      depend on timing and needs no workspace.  Bound by HBM and by set-up: 16
+//                      rows through 4096 -> 16384 from HBM 25.7 us (5.2 TB/s), 64 through 4096
+//                      -> 4096 11.4 us.
 //
 // fp32 operands are split into three bf16 parts, x = hi + mid + lo with every part rounded to
 // nearest, which hold all 24 bits; the six products of parts above 2^-27 relative are summed,
