@@ -125,7 +125,8 @@ kda_status_t kda_linear_fwd(const kda_linear_params_t* p, const void* x, const v
   const int64_t K = p->in_features;
   if (!operand_ok(p, x, p->x_row_stride ? p->x_row_stride : K, KDA_FLAG_UNALIGNED_X) ||
       !operand_ok(p, w, p->w_row_stride ? p->w_row_stride : K, KDA_FLAG_UNALIGNED_W) ||
-      !elem_aligned(pre_act, p->dtype) || !elem_aligned(y, p->y_dtype) || !elem_aligned(residual, p->residual_dtype) || !f32_aligned(bias))
+      !elem_aligned(pre_act, p->dtype) || !elem_aligned(y, p->y_dtype) ||
+      !elem_aligned(residual, p->residual_dtype) || !f32_aligned(bias))
     return KDA_ERR_INVALID_ARG;
   if (!workspace_ok(workspace, workspace_bytes, kda::linear_workspace_bytes(*p, false))) return KDA_ERR_WORKSPACE;
   int32_t* err = kda::layer_error_word();
@@ -146,7 +147,8 @@ kda_status_t kda_linear_bwd(const kda_linear_params_t* p, const void* x, const v
       !operand_ok(p, w, p->w_row_stride ? p->w_row_stride : K, KDA_FLAG_UNALIGNED_W) ||
       !elem_aligned(pre_act, p->dtype) || !elem_aligned(d_y, p->y_dtype) ||
       (p->activation == KDA_ACT_NONE && p->y_dtype == p->dtype &&
-       !operand_ok(p, d_y, p->y_row_stride ? p->y_row_stride : N, KDA_FLAG_UNALIGNED_DY)) || !elem_aligned(dx, p->dtype) || !elem_aligned(dw, p->dw_dtype) ||
+       !operand_ok(p, d_y, p->y_row_stride ? p->y_row_stride : N, KDA_FLAG_UNALIGNED_DY)) ||
+      !elem_aligned(dx, p->dtype) || !elem_aligned(dw, p->dw_dtype) ||
       !f32_aligned(dbias))
     return KDA_ERR_INVALID_ARG;
   if (!workspace_ok(workspace, workspace_bytes, kda::linear_workspace_bytes(*p, true))) return KDA_ERR_WORKSPACE;

@@ -114,9 +114,10 @@ cudaError_t launch_gemm_simt(const Gemm& g, cudaStream_t st) {
 // ---------------------------------------------------------------- gradient of the epilogue
 
 // dz = act'(z) d_y (the scale is applied to the sums), rounded to the operand type where a
-// product reads it, and the column sums of the unrounded dz for the bias.  Bound by HBM: d_y and
-// z read once, dz written once (the sums alone over 16384 x 6144: 40 us, 5 TB/s).  A block walks 256 columns (8 a lane) with eight row lanes whose
-// sums meet in shared memory; it writes one partial row, added in a fixed order afterwards.
+// product reads it, or as the three parts of fp32, and the column sums of the unrounded dz for the
+// bias.  Bound by HBM: d_y and z read once, dz written once (the sums alone over 16384 x 6144: 40 us,
+// 5 TB/s).  A block walks 256 columns (8 a lane) with eight row lanes whose sums meet in shared
+// memory; it writes one partial row, added in a fixed order afterwards.
 struct DzArgs {
   const void* dy;
   const void* z;        // null: no activation
@@ -148,7 +149,8 @@ __global__ void __launch_bounds__(256) dz_kernel(DzArgs A) {
       const int m = tu < A.T ? n : 0;
       const int64_t tt = tu < A.T ? tu : 0;
       dy[u] = load_chunk<DYBF, VEC>(static_cast<const char*>(A.dy) + (tt * A.dy_ld + n0) * (DYBF ? 2 : 4), lane, 32, m);
-      if constexpr (ACT != KDA_ACT_NONE) z[u] = load_chunk<ZBF, VEC>(static_cast<const char*>(A.z) + (tt * A.N + n0) * (ZBF ? 2 : 4), lane, 32, m);
+      if constexpr (ACT != KDA_ACT_NONE)
+        z[u] = load_chunk<ZBF, VEC>(static_cast<const char*>(A.z) + (tt * A.N + n0) * (ZBF ? 2 : 4), lane, 32, m);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {

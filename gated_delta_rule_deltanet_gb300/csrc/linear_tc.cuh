@@ -206,7 +206,8 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, unsig
   return wait_bounded([&] { return tc::mbar_try_wait(bar, parity); }, limit, abort);
 }
 // the same for a barrier that the other CTA of the pair arrives on
-__device__ __forceinline__ bool wait_phase_cluster(uint64_t* bar, uint32_t parity, unsigned long long limit, volatile int* abort) {
+__device__ __forceinline__ bool wait_phase_cluster(uint64_t* bar, uint32_t parity, unsigned long long limit,
+                                                   volatile int* abort) {
   return wait_bounded([&] { return try_wait_cluster(bar, parity); }, limit, abort);
 }
 // after a timeout: the copies or products in flight
