@@ -21,7 +21,8 @@ _NORM_GATES = ("sigmoid", "silu", "none")
 # A call's checks and parameter record depend only on its tensors' shapes, strides, types and
 # devices and on its scalars, so they are made once for each combination of those (`_sig`) and kept:
 # a decode step repeats the same few thousands of times, and the checks would cost more than its
-# kernels.  Nothing is kept by a tensor's address or contents.
+# kernels.  Nothing is kept by a tensor's address or contents: a scalar given as a tensor is read
+# on each call.
 _PLANS: dict = {}
 _MAX_PLANS = 4096
 
@@ -216,6 +217,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
             return linear(x, weight, bias, activation=activation, residual=residual, scale=scale,
                           out_dtype=out_dtype, save_pre_activation=save_pre_activation,
                           cuda_cores=cuda_cores, out=out, workspace=workspace)
+    scale = float(scale)
     key = ("linear", x.shape, x.stride(), x.dtype, x.get_device(), x.data_ptr() & 15, _sig16(weight),
            _sig(bias), activation, _sig(residual), scale, out_dtype, _sig(out), cuda_cores)
     plan = _PLANS.get(key)
@@ -268,6 +270,7 @@ def linear_bwd(x: torch.Tensor, weight: torch.Tensor, d_y: torch.Tensor, *,
                               dw_dtype=dw_dtype, cuda_cores=cuda_cores, workspace=workspace)
     if activation == "none":
         pre_activation = None
+    scale = float(scale)
     key = ("linear_bwd", _sig16(x), _sig16(weight), _sig16(d_y), activation, _sig(pre_activation),
            scale, dw_dtype, cuda_cores)
     plan = _PLANS.get(key)
@@ -346,6 +349,7 @@ def residual_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
         with _on(stream, x):
             return residual_norm(x, weight, residual=residual, post_weight=post_weight, gate=gate,
                                  scale=scale, eps=eps, out=out, h_out=h_out)
+    scale, eps = float(scale), float(eps)
     key = ("residual_norm", _sig(x), _sig(weight), _sig(residual), _sig(post_weight), _sig(gate),
            scale, eps, _sig(out), _sig(h_out))
     plan = _PLANS.get(key)
@@ -398,6 +402,7 @@ def residual_norm_bwd(x: torch.Tensor, h: torch.Tensor, weight: Optional[torch.T
         with _on(stream, x):
             return residual_norm_bwd(x, h, weight, d_y, d_h, post_weight=post_weight, gate=gate,
                                      scale=scale, eps=eps, workspace=workspace)
+    scale, eps = float(scale), float(eps)
     key = ("residual_norm_bwd", _sig(x), _sig(h), _sig(weight), _sig(d_y), _sig(d_h),
            _sig(post_weight), _sig(gate), scale, eps)
     plan = _PLANS.get(key)
@@ -464,6 +469,7 @@ def gated_norm(o: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, *,
         with _on(stream, o):
             return gated_norm(o, gate, weight, activation=activation, eps=eps, out_dtype=out_dtype,
                               out=out)
+    eps = float(eps)
     key = ("gated_norm", _sig(o), _sig(gate), _sig(weight), activation, eps, out_dtype, _sig(out))
     plan = _PLANS.get(key)
     if plan is None:
@@ -493,6 +499,7 @@ def gated_norm_bwd(o: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, d_
         with _on(stream, o):
             return gated_norm_bwd(o, gate, weight, d_y, activation=activation, eps=eps,
                                   workspace=workspace)
+    eps = float(eps)
     key = ("gated_norm_bwd", _sig(o), _sig(gate), _sig(weight), _sig(d_y), activation, eps)
     plan = _PLANS.get(key)
     if plan is None:

@@ -345,3 +345,32 @@ def test_device_error_word_stays_clear_and_status_raises():
         kda.linear(t["x"], t["w"].cpu())
     with pytest.raises(kda.KdaError):
         kda.residual_norm(t["x"], t["kw"], eps=0.0)
+
+
+def test_scalars_given_as_tensors_are_read_each_call():
+    """A scale or eps held in a tensor that changes between calls: as with the numbers themselves."""
+    g = torch.Generator().manual_seed(11)
+    x = torch.randn(5, 64, generator=g).to(DEV)
+    w = torch.randn(48, 64, generator=g).to(DEV)
+    kw = torch.randn(64, generator=g).to(DEV)
+    s, eps = torch.tensor(0.5), torch.tensor(1e-6)
+    for a, e in [(0.5, 2.0 ** -20), (2.0, 0.25)]:
+        s.fill_(a)
+        eps.fill_(e)
+        y = kda.linear(x, w, scale=a)
+        assert torch.equal(kda.linear(x, w, scale=s), y)
+        for got, want in zip(kda.linear_bwd(x, w, y, scale=s), kda.linear_bwd(x, w, y, scale=a)):
+            assert got is want or torch.equal(got, want)
+        n, h = kda.residual_norm(x, kw, scale=a, eps=e)
+        for got, want in zip(kda.residual_norm(x, kw, scale=s, eps=eps), (n, h)):
+            assert torch.equal(got, want)
+        for got, want in zip(kda.residual_norm_bwd(x, h, kw, n, scale=s, eps=eps),
+                             kda.residual_norm_bwd(x, h, kw, n, scale=a, eps=e)):
+            assert got is want or torch.equal(got, want)
+        o = x.view(5, 2, 32)
+        v = kda.gated_norm(o, o, kw[:32], eps=e)
+        assert torch.equal(kda.gated_norm(o, o, kw[:32], eps=eps), v)
+        for got, want in zip(kda.gated_norm_bwd(o, o, kw[:32], v, eps=eps),
+                             kda.gated_norm_bwd(o, o, kw[:32], v, eps=e)):
+            assert torch.equal(got, want)
+    no_error()
