@@ -80,8 +80,15 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 // the shared::cluster address of `saddr` in CTA `rank` of the cluster
 __device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
@@ -90,7 +97,8 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
   return r;
 }
 // Bulk copy of `bytes` (a multiple of 16) from this CTA's shared memory to `dst` in another CTA's,
-// completing on that CTA's barrier `bar` (both shared::cluster addresses).
+// completing on that CTA's barrier `bar` (both shared::cluster addresses).  Only that barrier
+// tells when the source has been read: such a copy belongs to no bulk group of the issuing thread.
 __device__ __forceinline__ void push_cluster(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -978,12 +986,13 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
           push_cluster(map_rank(smem + 128 * BN * 4 + place * per * 512, static_cast<uint32_t>(to)), smem + p0 * 512,
                        static_cast<uint32_t>(n) * 512, map_rank(tc::smem_u32(&received), static_cast<uint32_t>(to)));
       }
-      tc::bulk_commit();
     }
+    __syncwarp();
     if (warp >= 2 && c1 > c0) {
       ready = !tc::named_sync_or(2, 256, !wait_phase_cluster(&received, 0, A.wait_ns, &s_abort)) && ready;
       if (!ready) raise_device_error(A.err, KDA_DEVERR_TIMEOUT);
     }
+    cluster_arrive();                              // this CTA has received what it waits for
   }
   // the finished tile, [column - c0][128], for TMA: behind the parts if there are any
   unsigned char* out = smem_raw + (smem - tc::smem_u32(smem_raw)) +
@@ -1059,7 +1068,10 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       }
     }
   }
-  if (splits > 1 && threadIdx.x == 0) tc::bulk_wait_read();   // this CTA's pushes have left
+  // Every CTA has received its shares, so this one's pushes have read its shared memory: it may leave.
+  // (The arrival comes before the epilogue, which hides the wait.)
+  __syncwarp();
+  if (splits > 1) cluster_wait();
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 1) {
