@@ -349,7 +349,11 @@ struct RowRing {
 };
 constexpr int kMaxStages = 4;
 constexpr size_t kRingBytes = 208 * 1024;
-constexpr uint32_t kRowWait = 1u << 22;
+#ifndef KDA_ROW_WAIT
+#define KDA_ROW_WAIT (1u << 22)
+#endif
+constexpr uint32_t kRowWait = KDA_ROW_WAIT;      // polls of a wait for a row (tests compile one that gives up)
+constexpr uint32_t kDrainWait = 1u << 22;        // and of a wait for copies in flight after one gave up
 
 template <bool BF>
 __device__ __forceinline__ Raw8<BF> smem_chunk(const unsigned char* row, int c, int n) {
@@ -391,6 +395,7 @@ __device__ __forceinline__ void fetch_row(const ResidualNormArgs& A, const RowRi
 struct RingState {
   uint64_t full[kMaxStages], empty[kMaxStages];
   int fail;
+  int fetched;                   // rows requested so far (thread 0's)
 };
 
 template <bool BWD>
@@ -407,8 +412,10 @@ __device__ __forceinline__ void ring_start(const ResidualNormArgs& A, const RowR
   __syncthreads();
   if (threadIdx.x == 0) {
     int64_t t = blockIdx.x;
-    for (int s = 0; s < R.stages && t < A.T; ++s, t += gridDim.x)
+    int s = 0;
+    for (; s < R.stages && t < A.T; ++s, t += gridDim.x)
       fetch_row<BWD>(A, R, t, smem + s * R.stage, need_x, &S.full[s]);
+    S.fetched = s;
   }
 }
 
@@ -426,13 +433,26 @@ __device__ __forceinline__ void ring_row(const ResidualNormArgs& A, const RowRin
     if (next < A.T) {
       const int p = s == 0 ? R.stages - 1 : s - 1;
       ok = tc::mbar_wait_bounded(&S.empty[p], s == 0 ? ph ^ 1 : ph, kRowWait);
-      if (ok) fetch_row<BWD>(A, R, next, smem + p * R.stage, need_x, &S.full[p]);
+      if (ok) {
+        fetch_row<BWD>(A, R, next, smem + p * R.stage, need_x, &S.full[p]);
+        ++S.fetched;
+      }
     }
   }
   if (!(tc::mbar_wait_bounded(&S.full[s], ph, kRowWait) && ok)) {
     raise_device_error(R.err, KDA_DEVERR_TIMEOUT);
     *fail = 1;
   }
+}
+
+// After the last row.  Every copy has been awaited then, unless a wait gave up: the thread that
+// issued the copies stays until the last ones have landed, as the block's shared memory is someone
+// else's once its threads are gone.
+__device__ __forceinline__ void ring_end(const RowRing& R, RingState& S) {
+  volatile int* fail = &S.fail;
+  if (threadIdx.x != 0 || !*fail) return;
+  for (int j = S.fetched > R.stages ? S.fetched - R.stages : 0; j < S.fetched; ++j)
+    tc::mbar_wait_bounded(&S.full[j % R.stages], (j / R.stages) & 1, kDrainWait);
 }
 
 template <bool XBF, bool HBF, int V>
@@ -517,6 +537,7 @@ residual_norm_ring_kernel(const ResidualNormArgs A, const RowRing R) {
       ph ^= 1;
     }
   }
+  ring_end(R, S);
 }
 
 template <bool XBF, bool HBF, int V>
@@ -655,6 +676,7 @@ residual_norm_bwd_ring_kernel(const ResidualNormArgs A, const RowRing R) {
       ph ^= 1;
     }
   }
+  ring_end(R, S);
   float* part = A.part + static_cast<int64_t>(blockIdx.x) * 3 * N;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
