@@ -3,6 +3,8 @@
 // their derivatives, and the fixed-order sum over partial rows.
 #pragma once
 
+#include <atomic>
+
 #include "kda_common.cuh"
 
 namespace kda {
@@ -11,6 +13,23 @@ namespace kda {
 int32_t* layer_error_word();
 
 inline size_t dtype_bytes(int32_t dt) { return dt == KDA_DTYPE_BF16 ? 2 : 4; }
+
+// ---------------------------------------------------------------- launches
+
+// The kernel's dynamic shared-memory limit, raised once for each device to the most that any call takes: the
+// limit belongs to the process, so a call that set its own could lower another thread's between that one's
+// setting and launch.
+template <typename Kernel>
+inline cudaError_t raise_smem(Kernel k, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // ---------------------------------------------------------------- eight elements of a row
 

@@ -42,7 +42,6 @@
 #pragma once
 
 #include <algorithm>
-#include <atomic>
 
 #include "gemm.cuh"
 #include "tc_utils.cuh"
@@ -1124,19 +1123,6 @@ void encode_outputs(const Gemm& g, TcArgs* A, OutMaps* m, int rows, bool residua
   A->res_mode = kResDirect;
   if (residual && A->staged && E.res && encode_out(&m->res, E.res, E.res_bf, g.I, g.J, E.res_ld, rows))
     A->res_mode = E.res_bf == E.out_bf ? kResInPlace : kResChunk;
-}
-
-// The kernel's shared-memory limit, raised once for each device.
-template <typename Kernel>
-cudaError_t raise_smem(Kernel k, size_t bytes, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
-  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
 }
 
 template <bool AMN, bool BMN, bool PROMOTE>

@@ -745,10 +745,10 @@ static RowRing row_ring(const ResidualNormArgs& A, bool xbf, bool hbf, bool bwd,
 }
 
 template <typename Kernel>
-static cudaError_t launch_ring(Kernel k, unsigned grid, int threads, const ResidualNormArgs& A, const RowRing& R,
-                               cudaStream_t st) {
-  const size_t smem = static_cast<size_t>(R.stage) * R.stages;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+static cudaError_t launch_ring(Kernel k, std::atomic<uint64_t>& raised, unsigned grid, int threads,
+                               const ResidualNormArgs& A, const RowRing& R, cudaStream_t st) {
+  const size_t smem = static_cast<size_t>(R.stage) * R.stages;      // at most kRingBytes (row_ring)
+  const cudaError_t e = raise_smem(k, kRingBytes, raised);
   if (e != cudaSuccess) return e;
   k<<<grid, threads, smem, st>>>(A, R);
   return cudaGetLastError();
@@ -760,9 +760,10 @@ static cudaError_t run_residual_norm(const ResidualNormArgs& A, bool bwd, int th
                        : static_cast<int>(std::min<int64_t>(A.T, static_cast<int64_t>(sm_count()) * rows_per_sm(A.N, false)));
   if constexpr (VEC) {
     const RowRing R = row_ring(A, XBF, HBF, bwd, grid);
+    static std::atomic<uint64_t> raised[2];      // of this instance's two kernels
     if (R.stages)
-      return bwd ? launch_ring(residual_norm_bwd_ring_kernel<XBF, HBF, V>, grid, threads, A, R, st)
-                 : launch_ring(residual_norm_ring_kernel<XBF, HBF, V>, grid, threads, A, R, st);
+      return bwd ? launch_ring(residual_norm_bwd_ring_kernel<XBF, HBF, V>, raised[1], grid, threads, A, R, st)
+                 : launch_ring(residual_norm_ring_kernel<XBF, HBF, V>, raised[0], grid, threads, A, R, st);
   }
   if (bwd) {
     residual_norm_bwd_kernel<XBF, HBF, V, VEC><<<grid, threads, 0, st>>>(A);

@@ -75,3 +75,47 @@ def test_rows_whose_wait_gives_up_end_with_their_copies(giving_up, T, N, backwar
         assert word.item() == _lib.KDA_DEVERR_TIMEOUT
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+class ThreadArgs(ctypes.Structure):
+    """Mirror of Args in call_from_threads.cpp."""
+
+    _fields_ = ([("p", ctypes.POINTER(_lib.KdaNormParams))] + [(n, ctypes.c_void_p) for n in (
+        "x", "h", "gate", "post_weight", "weight", "d_y", "d_h", "dx", "d_residual", "d_gate",
+        "d_post_weight", "d_weight", "workspace")] + [("workspace_bytes", ctypes.c_size_t),
+                                                      ("stream", ctypes.c_void_p)])
+
+
+def test_two_widths_from_two_threads(tmp_path):
+    """Host threads that call one kernel with rings of different sizes (2048 columns: 40 KB, 4096: 80
+    KB) do not disturb each other."""
+    so = str(tmp_path / "libthreads.so")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-pthread", "-I", kbuild.INCLUDE, "-o", so,
+                    os.path.join(os.path.dirname(__file__), "call_from_threads.cpp")], check=True)
+    run = ctypes.CDLL(so).call_from_threads
+    lib = _lib.load()
+    args, want, got, keep = (ThreadArgs * 4)(), [], [], []
+    for i in range(4):
+        T, N = 2500, (2048, 4096)[i % 2]
+        r = rng(32, i)
+        x, _ = dev(r.standard_normal((T, N)), "bf16")
+        g, _ = dev(r.standard_normal((T, N)), "bf16")
+        w, _ = dev(r.standard_normal(N), "f32")
+        want.append(kda.residual_norm_bwd(x, x, w, x, x, post_weight=w, gate=g))
+        p = _lib.KdaNormParams(tokens=T, features=N, x_dtype=1, h_dtype=1, y_dtype=1, gate_per_token=1, eps=1e-6,
+                               scale=1.0)
+        n = ctypes.c_size_t(0)
+        assert lib.kda_norm_workspace_size(ctypes.byref(p), 0, ctypes.byref(n)) == 0
+        ws = torch.empty(n.value, dtype=torch.uint8, device=DEV)
+        out = [torch.empty_like(t) for t in want[-1]]
+        s = torch.cuda.Stream()
+        a, c, e = x.data_ptr(), w.data_ptr(), [t.data_ptr() for t in out]
+        args[i] = ThreadArgs(ctypes.pointer(p), a, a, g.data_ptr(), c, c, a, a, e[0], e[1], e[4], e[3], e[2],
+                             ws.data_ptr(), n.value, s.cuda_stream)
+        got.append(out)
+        keep.append((p, x, g, w, ws, s))
+    torch.cuda.synchronize()
+    assert run(ctypes.cast(lib.kda_residual_norm_bwd, ctypes.c_void_p), args, 4, 2000) == 0
+    no_error()
+    for a, b in zip(got, want):
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
