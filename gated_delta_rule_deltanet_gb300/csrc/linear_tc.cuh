@@ -773,10 +773,10 @@ struct SplitShape {
   static constexpr uint32_t stage = a_bytes + planes * BN * kBK * 2;
   // the ring: some 200 KB, one CTA an SM (with 96 KB and two CTAs the narrow tile's loads waited on
   // the ring: 16 x 4096 -> 16384 from HBM 32.6 us, so 25.2 us)
-  static constexpr int stages = PARTS == 6 ? (BN == 64 ? 3 : 2) : BN == 64 ? 8 : BN == 128 ? 6 : 4;
+  static constexpr int stages = PARTS == 6 ? (BN == 64 ? 3 : 2) : BN == 64 ? 8 : 6;
   static constexpr size_t smem = static_cast<size_t>(stage) * stages + 1024;
   // a split's own part and those received (7 shares of up to BN / 8 + 7 columns, or one of BN / 2)
-  static_assert(BN == 256 || static_cast<size_t>(stage) * stages >= 128 * 4 * (BN + 7 * 8 + BN),
+  static_assert(static_cast<size_t>(stage) * stages >= 128 * 4 * (BN + 7 * 8 + BN),
                 "the parts reuse the ring");
 };
 
@@ -1239,16 +1239,14 @@ cudaError_t launch_shape(const Gemm& g, int planes, cudaStream_t st) {
   if (planes == 1 && big >= sms / 4 && g.J > 128)
     return promote ? launch_pair<AMN, BMN, true>(g, A, planes, sms / 2, st)
                    : launch_pair<AMN, BMN, false>(g, A, planes, sms / 2, st);
-  // Few tiles.  128 columns, 64 where there are no more rows or too few tiles to fill the SMs with a
-  // split, 256 (unsplit, as the parts would not fit) where 128 would take a second wave.  An SM takes
-  // in some 90 GB/s, so a weight streams at HBM's rate only into most of them: splits as many as
+  // Few tiles, or few rows.  128 columns, 64 where there are no more rows or too few tiles to fill the
+  // SMs with a split.  An SM takes in some 90 GB/s, so a weight streams at HBM's rate only into most of them: splits as many as
   // run at once (launch_split), with four steps a CTA at least; beyond four ways the exchange costs
   // more than it saves unless c is long (16 x 4096 -> 4096: 4 ways 8.4 us, 8 ways 9.5 us).
   auto tiles_for = [&](int n) { return ((g.I + 127) / 128) * ((g.J + n - 1) / n); };
-  int bn = g.J <= 64 || tiles_for(128) * 8 <= sms ? 64 : 128;
-  if (bn == 128 && !promote && tiles_for(128) > sms) bn = 256;
+  const int bn = g.J <= 64 || tiles_for(128) * 8 <= sms ? 64 : 128;
   const int steps = A.kblocks * (planes == 3 ? 6 : 1);
-  const int splits = bn == 256 ? 1 : std::max(1, std::min(std::min(steps >= 128 ? 8 : 4, steps / 4), A.kblocks));
+  const int splits = std::max(1, std::min(std::min(steps >= 128 ? 8 : 4, steps / 4), A.kblocks));
   if (tiles_for(bn) * splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   if (planes == 3)
     return bn == 64 ? launch_split<AMN, BMN, 64, 6>(g, A, planes, splits, st)
@@ -1256,11 +1254,8 @@ cudaError_t launch_shape(const Gemm& g, int planes, cudaStream_t st) {
   if (promote)
     return bn == 64 ? launch_split<AMN, BMN, 64, 1>(g, A, planes, splits, st)
                     : launch_split<AMN, BMN, 128, 1>(g, A, planes, splits, st);
-  switch (bn) {
-    case 64: return launch_split<AMN, BMN, 64, 0>(g, A, planes, splits, st);
-    case 128: return launch_split<AMN, BMN, 128, 0>(g, A, planes, splits, st);
-    default: return launch_split<AMN, BMN, 256, 0>(g, A, planes, splits, st);
-  }
+  return bn == 64 ? launch_split<AMN, BMN, 64, 0>(g, A, planes, splits, st)
+                  : launch_split<AMN, BMN, 128, 0>(g, A, planes, splits, st);
 }
 
 }  // namespace

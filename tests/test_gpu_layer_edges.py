@@ -13,7 +13,7 @@ import torch
 import gated_delta_rule_deltanet_gb300 as kda
 from gated_delta_rule_deltanet_gb300 import _lib, build as kbuild
 from oracle import layer as ol
-from test_gpu_layer import DEV, U, check, dev, host, no_error, product_tol, rng
+from test_gpu_layer import DEV, U, check, dev, host, linear_case, no_error, product_tol, rng
 
 pytestmark = pytest.mark.gpu
 
@@ -119,3 +119,11 @@ def test_two_widths_from_two_threads(tmp_path):
     no_error()
     for a, b in zip(got, want):
         assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+@pytest.mark.parametrize("T", [65, 100, 128])
+@pytest.mark.parametrize("dtype,y", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+def test_few_tokens_onto_more_rows_than_one_wave(T, dtype, y):
+    """A vocabulary-sized weight: more 128-row tiles than SMs."""
+    N = 128 * torch.cuda.get_device_properties(0).multi_processor_count + 136
+    linear_case(33, T, 136, N, dtype, act="silu", bias=True, res=y, y=y, scale=0.5)
