@@ -4,6 +4,7 @@ threads.  Tolerances as there.
 """
 import ctypes
 import os
+import re
 import subprocess
 
 import numpy as np
@@ -127,3 +128,83 @@ def test_few_tokens_onto_more_rows_than_one_wave(T, dtype, y):
     """A vocabulary-sized weight: more 128-row tiles than SMs."""
     N = 128 * torch.cuda.get_device_properties(0).multi_processor_count + 136
     linear_case(33, T, 136, N, dtype, act="silu", bias=True, res=y, y=y, scale=0.5)
+
+
+# ------------------------------------------------------- tile widths of the persistent product
+
+WIDTHS = (256, 224, 192, 160, 128)
+
+
+def width_rule():
+    """The widths and their costs as the library's source states them."""
+    src = open(os.path.join(kbuild.CSRC, "linear_tc.cuh")).read()
+    w, c = re.search(r"kWidth\[5\] = \{([\d, ]+)\}, kCost\[5\] = \{([\d, ]+)\}", src).groups()
+    return [int(v) for v in w.split(",")], [int(v) for v in c.split(",")]
+
+
+def shape_of_width(want):
+    """Output columns and rows (I, J), odd in both tiles, for which the library takes tiles `want` wide:
+    at least two whole ones and a ragged one along J."""
+    widths, costs = width_rule()
+    assert tuple(widths) == WIDTHS
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    best = None
+    for ti in range(2, 24):
+        I = 256 * ti - 104
+        for J in range(2 * want + 10, 4000, 14):
+            if ti * -(-J // 256) < sms // 4 or best and I * J >= best[0] * best[1]:
+                continue
+            waves = [-(-ti * -(-J // w) // (sms // 2)) * c for w, c in zip(widths, costs)]
+            if widths[waves.index(min(waves))] == want:
+                best = I, J
+    assert best, want
+    return best
+
+
+@pytest.mark.parametrize("width", WIDTHS)
+@pytest.mark.parametrize("form", ["plain", "z", "in place", "fp32 residual", "fp32"])
+def test_forward_at_each_tile_width(width, form):
+    N, T = shape_of_width(width)
+    K = 200
+    r = rng(34, width)
+    x, x64 = dev(r.standard_normal((T, K)), "bf16")
+    w, w64 = dev(r.standard_normal((N, K)) / np.sqrt(K), "bf16")
+    b, b64 = dev(r.standard_normal(N), "f32")
+    kw = dict(activation="silu", scale=0.5, out_dtype=torch.float32 if form == "fp32" else torch.bfloat16)
+    rs, rs64, z = None, None, None
+    if form in ("in place", "fp32 residual"):
+        rs, rs64 = dev(r.standard_normal((T, N)), "bf16" if form == "in place" else "f32")
+    if form in ("z", "fp32 residual"):
+        y, z = kda.linear(x, w, b, residual=rs, save_pre_activation=True, **kw)
+    else:
+        y = kda.linear(x, w, b, residual=rs, out=rs if form == "in place" else None, **kw)
+    no_error()
+    y_ref, z_ref = ol.linear(x64, w64, b64, "silu", rs64, 0.5)
+    ez = product_tol(x64, w64.T, K, "bf16") + 2 * U * np.abs(z_ref)
+    check("y", y, y_ref, 0.5 * (1.13 * ez + 16 * U * np.maximum(1, np.abs(z_ref))) + 4 * U * np.abs(y_ref))
+    if z is not None:
+        check("z", z, z_ref, ez)
+
+
+@pytest.mark.parametrize("width", WIDTHS)
+@pytest.mark.parametrize("dw_dtype", ["bf16", "f32"])
+def test_gradients_at_each_tile_width(width, dw_dtype):
+    I, J = shape_of_width(width)
+    C = 328
+    r = rng(35, width)
+    # dx [T = J, K = I], summed over N = C
+    w, w64 = dev(r.standard_normal((C, I)), "bf16")
+    d, d64 = dev(r.standard_normal((J, C)), "bf16")
+    x, _ = dev(r.standard_normal((J, I)), "bf16")
+    dx = kda.linear_bwd(x, w, d, need_dw=False, scale=-1.5)[0]
+    no_error()
+    ref = -1.5 * (d64 @ w64)
+    check("dx", dx, ref, 1.5 * product_tol(d64, w64, C, "bf16") + 2 * U * np.abs(ref))
+    # dw [N = J, K = I], summed over T = C
+    x, x64 = w, w64
+    d, d64 = dev(r.standard_normal((C, J)), "bf16")
+    w, _ = dev(r.standard_normal((J, I)), "bf16")
+    dw = kda.linear_bwd(x, w, d, need_dx=False, dw_dtype=torch.float32 if dw_dtype == "f32" else torch.bfloat16)[1]
+    no_error()
+    ref = d64.T @ x64
+    check("dw", dw, ref, product_tol(d64.T, x64, C, "bf16") + 2 * U * np.abs(ref))
