@@ -3,6 +3,7 @@ shares of a split sum, tile widths, tails of the activations, infinities, calls 
 threads.  Tolerances as there.
 """
 import ctypes
+import math
 import os
 import re
 import subprocess
@@ -17,6 +18,7 @@ from oracle import layer as ol
 from test_gpu_layer import DEV, U, check, dev, host, linear_case, no_error, product_tol, rng
 
 pytestmark = pytest.mark.gpu
+erfc64 = np.vectorize(math.erfc, otypes=[np.float64])
 
 
 @pytest.mark.parametrize("T", [3, 8, 9, 16, 17, 64])
@@ -208,3 +210,40 @@ def test_gradients_at_each_tile_width(width, dw_dtype):
     no_error()
     ref = d64.T @ x64
     check("dw", dw, ref, product_tol(d64.T, x64, C, "bf16") + 2 * U * np.abs(ref))
+
+
+# ------------------------------------------------------------------- the far side of the activations
+
+@pytest.mark.parametrize("act", ["gelu", "silu", "sigmoid"])
+@pytest.mark.parametrize("T", [1, 9, 600])
+def test_activation_tails_keep_their_relative_size(act, T):
+    """Far below zero gelu, silu and sigmoid are tiny and still right to their type's rounding: half a
+    bf16 step, plus 2e-4 (the normal distribution's approximation 1e-4; exp of an argument a up to 78
+    that is itself rounded, (2 + 1.2 a) 2^-23 + 4 a 2^-24 < 3e-5).  One row, few rows and many take
+    three kernels."""
+    N, K = 4096, 64
+    z = np.linspace(-12.5, 9, N).astype(np.float32)
+    b = torch.from_numpy(z).to(DEV)
+    x = torch.zeros((T, K), dtype=torch.bfloat16, device=DEV)
+    w = torch.zeros((N, K), dtype=torch.bfloat16, device=DEV)
+    y = kda.linear(x, w, b, activation=act)
+    no_error()
+    ref = z * 0.5 * erfc64(-z / math.sqrt(2)) if act == "gelu" else ol.act(act, z)
+    check("y", y, np.broadcast_to(ref, (T, N)), 2e-4 * np.abs(ref))
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu", "sigmoid"])
+def test_activation_gradient_tails_keep_their_relative_size(act):
+    """The same of the slopes of a bf16 pre-activation below -2, where no two terms cancel but gelu's
+    two (each within 2e-4, the smaller at most a fifth of the difference)."""
+    N, K = 1024, 64
+    z = torch.linspace(-12.5, -2, N, device=DEV).to(torch.bfloat16)[None]
+    x = torch.zeros((1, K), dtype=torch.bfloat16, device=DEV)
+    w = torch.zeros((N, K), dtype=torch.bfloat16, device=DEV)
+    db = kda.linear_bwd(x, w, torch.ones_like(z), activation=act, pre_activation=z, need_dx=False, need_dw=False,
+                        need_bias=True)[2]
+    no_error()
+    z64 = host(z)[0]
+    ref = (0.5 * erfc64(-z64 / math.sqrt(2)) + z64 * np.exp(-z64 * z64 / 2) / math.sqrt(2 * math.pi)
+           if act == "gelu" else ol.act_grad(act, z64))
+    check("db", db, ref, 3e-4 * np.abs(ref))
