@@ -177,8 +177,16 @@ enum : int32_t { kResDirect = 0, kResInPlace = 1, kResChunk = 2 };
 // The kinds of staged chunks, in the order they follow one another for the same columns.
 enum : int { kChunkZ = 0, kChunkRes = 1, kChunkY = 2 };
 
+// The three planes of parts that fp32 operands are split into.
+struct PartPlanes {
+  const uint16_t *a, *b;
+  int64_t lda, ldb, plane_a, plane_b;   // elements between stored rows, and between planes
+  int64_t C;
+};
+
 struct TcArgs {
   GemmEpilogue epi;
+  PartPlanes parts;
   int64_t I, J;
   bool staged;              // y (and z) leave through shared memory and TMA
   int32_t res_mode;         // pair kernel: how the residual comes, kRes*
@@ -194,6 +202,40 @@ struct TcArgs {
 // The products of parts of one step of c, smallest first (0 = hi, 1 = mid, 2 = lo).
 __device__ __forceinline__ constexpr int part_a(int q) { return (0x201100 >> (4 * (5 - q))) & 15; }   // lo hi mid mid hi hi
 __device__ __forceinline__ constexpr int part_b(int q) { return (0x021010 >> (4 * (5 - q))) & 15; }   // hi lo mid hi mid hi
+
+// Eight steps of c of one row or column, put together again; zeros past the last step.
+template <bool MN>
+__device__ __forceinline__ void join8(const uint16_t* p, int64_t ld, int64_t plane, int64_t r, int64_t c, int64_t C,
+                                      float (&x)[8]) {
+  if constexpr (MN) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint16_t* at = p + (c + e) * ld + r;
+      x[e] = c + e < C ? bf16_bits_to_f32(at[0]) + bf16_bits_to_f32(at[plane]) + bf16_bits_to_f32(at[2 * plane]) : 0.f;
+    }
+  } else {                                         // (rows are whole 128-byte lines)
+    const Raw8<true> hi = load_chunk<true, true>(p + r * ld + c, 0, 0, 8), mid = load_chunk<true, true>(p + plane + r * ld + c, 0, 0, 8),
+                     lo = load_chunk<true, true>(p + 2 * plane + r * ld + c, 0, 0, 8);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = c + e < C ? hi.f32(e) + mid.f32(e) + lo.f32(e) : 0.f;
+  }
+}
+// The sum of element (i, j) as fp32 makes it, from the operands themselves.  The parts of an infinity are
+// itself, 0 and 0, and its products with another operand's parts have either sign, so that the sum of
+// the six products is NaN where fp32's is infinite.  Only sums that are not finite come here, one thread a
+// sum (1024 x 2048 -> 2048 with one infinity in every row: REPLACE ms where finite rows take 57 us).
+template <bool AMN, bool BMN>
+__device__ __noinline__ float sum_again(const PartPlanes& P, int64_t i, int64_t j) {
+  float s = 0.f;
+  for (int64_t c = 0; c < P.C && s == s; c += 8) {
+    float a[8], b[8];
+    join8<AMN>(P.a, P.lda, P.plane_a, i, c, P.C, a);
+    join8<BMN>(P.b, P.ldb, P.plane_b, j, c, P.C, b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fmaf(a[e], b[e], s);
+  }
+  return s;
+}
 
 // Waits for a phase; gives up after `limit` ns or once another role of the CTA has.
 template <typename TryWait>
@@ -1000,6 +1042,18 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   unsigned char* out_z = out + cpad * 128 * (A.epi.out_bf ? 2 : 4);
   if (warp >= 2 && ready) {
     const float* mine = part + quad * 32 + lane;
+    // sums of parts that are not finite: 16 columns of the tile from c
+    auto mend = [&](float (&v)[16], int c) {
+      if constexpr (PARTS == 6) {
+        float zero = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) zero = fmaf(v[e], 0.f, zero);
+        if (zero == 0.f) return;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (!(fabsf(v[e]) < INFINITY) && in && c + e < c1) v[e] = sum_again<AMN, BMN>(A.parts, i, j0 + c + e);
+      }
+    };
     // (unrolled where the tile is in registers, whose places are fixed at compile time)
 #pragma unroll (PROMOTE ? BN / 32 : 1)
     for (int cc = 0; cc < BN / 2; cc += 16) {
@@ -1009,7 +1063,10 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       if (splits == 1) {
         if constexpr (PROMOTE) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = sum[cc + e] + bias;
+          for (int e = 0; e < 16; ++e) v[e] = sum[cc + e];
+          mend(v, c);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] += bias;
         } else {
           load16(src + c, bias, v);
         }
@@ -1024,6 +1081,7 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] += e < n ? at[e * 128] : 0.f;
         }
+        mend(v, c);
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] += bias;
       }
@@ -1232,6 +1290,9 @@ cudaError_t launch_shape(const Gemm& g, int planes, cudaStream_t st) {
   A.I = g.I; A.J = g.J;
   A.kblocks = static_cast<int32_t>((g.C + kBK - 1) / kBK);
   A.err = g.err;
+  if (planes == 3)
+    A.parts = {static_cast<const uint16_t*>(g.A.p), static_cast<const uint16_t*>(g.B.p), g.A.ld, g.B.ld,
+               (AMN ? g.C : g.I) * g.A.ld, (BMN ? g.C : g.J) * g.B.ld, g.C};
   A.wait_ns = 2000000000ull + static_cast<unsigned long long>(A.kblocks) * 4000ull;
   const int sms = sm_count();
   const int64_t big = ((g.I + 255) / 256) * ((g.J + 255) / 256);

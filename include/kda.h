@@ -504,8 +504,9 @@ typedef struct kda_linear_params {
  * bf16 operands are multiplied on tensor cores with fp32 accumulation; those whose base or rows
  * are not 16-byte aligned are first copied into aligned rows of the workspace.  fp32 operands
  * are split into three bf16 parts in the workspace (24 bits in all), whose six leading products
- * the tensor cores sum in fp32; there a sum with an infinite term may come out as NaN, and values
- * below 2^-109 keep fewer than 24 bits (their last part is subnormal and counts as zero).
+ * the tensor cores sum in fp32; sums that are not finite are formed again from the operands, so that
+ * infinities and NaN come out as in fp32, and values below 2^-109 keep fewer than 24 bits (their
+ * last part is subnormal and counts as zero).
  * KDA_FLAG_CUDA_CORES multiplies in fp32 on CUDA cores instead.  The forward of up to 2 tokens, or
  * of up to 8 where w would have to be copied, runs on CUDA cores and reads both operands in place.
  */

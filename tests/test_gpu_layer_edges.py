@@ -247,3 +247,59 @@ def test_activation_gradient_tails_keep_their_relative_size(act):
     ref = (0.5 * erfc64(-z64 / math.sqrt(2)) + z64 * np.exp(-z64 * z64 / 2) / math.sqrt(2 * math.pi)
            if act == "gelu" else ol.act_grad(act, z64))
     check("db", db, ref, 3e-4 * np.abs(ref))
+
+
+# ------------------------------------------------------------------- infinities in fp32 operands
+
+def same(got, ref):
+    """Equal in every infinity's sign and place, and in the places of NaN."""
+    g, r = got.cpu(), ref.cpu()
+    assert torch.equal(torch.isnan(g), torch.isnan(r))
+    assert torch.equal(torch.isposinf(g), torch.isposinf(r)) and torch.equal(torch.isneginf(g), torch.isneginf(r))
+
+
+@pytest.mark.parametrize("T", [1, 8, 9, 64, 150, 700])
+@pytest.mark.parametrize("K,N", [(64, 72), (1100, 200)])
+def test_fp32_infinities_stay_infinities(T, K, N):
+    """An infinite or NaN term gives what fp32 sums give, for every row count: its infinity, or NaN
+    next to a zero, to another sign's infinity or to NaN."""
+    r = rng(36, T, K)
+    x = torch.from_numpy(r.standard_normal((T, K)).astype(np.float32))
+    w = torch.from_numpy(r.standard_normal((N, K)).astype(np.float32))
+    x[0, 5] = float("inf")
+    w[3, 5] = 0
+    w[7, K - 1] = float("-inf")
+    if T > 5:
+        x[2, 9] = float("nan")
+        x[4, 1], x[4, K - 2] = float("inf"), float("-inf")
+        x[5, K - 1] = float("-inf")
+    d = torch.from_numpy(r.standard_normal((T, N)).astype(np.float32))
+    if T > 5:
+        d[1, 11] = float("inf")
+    xg, wg, dg = x.to(DEV), w.to(DEV), d.to(DEV)
+    y = kda.linear(xg, wg)
+    dx, dw, db = kda.linear_bwd(xg, wg, dg, need_bias=True)
+    no_error()
+    same(y, x.double() @ w.double().t())
+    same(dx, d.double() @ w.double())
+    same(dw, d.double().t() @ x.double())
+    same(db, d.double().sum(0))
+    clean = [t for t in range(T) if t not in (0, 2, 4, 5)]
+    other = [n for n in range(N) if n != 7]
+    if clean:
+        x64, w64 = x.double().numpy()[clean], w.double().numpy()[other]
+        check("y", y[clean][:, other], x64 @ w64.T, product_tol(x64, w64.T, K, "f32"))
+
+
+def test_fp32_products_next_to_the_largest_value():
+    """Terms just below fp32's largest value stay finite: their leading parts round up past it."""
+    T, K, N = 40, 64, 48
+    x = torch.zeros((T, K), device=DEV)
+    w = torch.zeros((N, K), device=DEV)
+    a = 2.0 ** 64 * (1 - 2.0 ** -24)                         # its square lies a step below the largest value
+    x[:, 3], w[:, 3] = a, a
+    x[:, 7], w[:, 7] = 1.0, -(2.0 ** 100)
+    y = kda.linear(x, w)
+    no_error()
+    ref = np.full((T, N), a * a - 2.0 ** 100)
+    check("y", y, ref, 4 * U * ref)
