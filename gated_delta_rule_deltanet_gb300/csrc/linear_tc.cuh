@@ -223,7 +223,7 @@ __device__ __forceinline__ void join8(const uint16_t* p, int64_t ld, int64_t pla
 // The sum of element (i, j) as fp32 makes it, from the operands themselves.  The parts of an infinity are
 // itself, 0 and 0, and its products with another operand's parts have either sign, so that the sum of
 // the six products is NaN where fp32's is infinite.  Only sums that are not finite come here, one thread a
-// sum (1024 x 2048 -> 2048 with one infinity in every row: REPLACE ms where finite rows take 57 us).
+// sum (1024 x 2048 -> 2048 with one infinity in every row: 8.6 ms where finite rows take 57 us).
 template <bool AMN, bool BMN>
 __device__ __noinline__ float sum_again(const PartPlanes& P, int64_t i, int64_t j) {
   float s = 0.f;
