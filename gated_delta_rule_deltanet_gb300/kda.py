@@ -154,10 +154,7 @@ def prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch.Tenso
     elif out.dtype != torch.float32 or tuple(out.shape) != (T, HV, D) or not out.is_contiguous():
         raise ValueError("out must be contiguous float32 [T, HV, D]")
     need = workspace_size(p)
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    elif workspace.numel() * workspace.element_size() < need:
-        raise ValueError(f"workspace needs {need} bytes")
+    workspace = _workspace(need, workspace, dev)
     st = _on(dev, _lib.load().kda_prefill_fwd, 
         ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(log_decay),
         _ptr(input_row_offsets), _ptr(slot_idx), _ptr(state_pool), _ptr(out), _ptr(workspace),
@@ -529,6 +526,8 @@ def _gdp_params(q, k, v, beta, log_decay, num_seqs, slot_idx, state_pool, chunk,
 def _workspace(need, workspace, dev):
     if workspace is None:
         return torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the tensors' device")
     if workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace needs {need} bytes")
     return workspace
