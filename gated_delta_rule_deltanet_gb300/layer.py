@@ -134,6 +134,12 @@ def _rows(t, shape, dtypes, name):
     return 0
 
 
+def _apart(out, name, *others):
+    """An output's rows are written while other blocks still read the operands."""
+    if out is not None and out.numel() and any(o is not None and o.data_ptr() == out.data_ptr() for o in others):
+        raise ValueError(f"{name} must have memory of its own")
+
+
 def _dense(t, shape, dtype, name):
     if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}")
@@ -210,7 +216,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
     residual [T, N] float32 or bfloat16.  `activation`: none, relu, silu, gelu (erf form) or
     sigmoid.  Returns y [T, N] in `out_dtype` (default x's), or (y, z) with
     `save_pre_activation`, z [T, N] in x's dtype being what `linear_bwd` needs as
-    `pre_activation`.  `out` may be `residual` itself.
+    `pre_activation`.  `out` may be `residual` itself; it shares no memory with x or weight.
     """
     if stream is not None:
         with _on(stream, x):
@@ -218,6 +224,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
                           out_dtype=out_dtype, save_pre_activation=save_pre_activation,
                           cuda_cores=cuda_cores, out=out, workspace=workspace)
     scale = float(scale)
+    _apart(out, "out", x, weight)
     key = ("linear", x.shape, x.stride(), x.dtype, x.get_device(), x.data_ptr() & 15, _sig16(weight),
            _sig(bias), activation, _sig(residual), scale, out_dtype, _sig(out), cuda_cores)
     plan = _PLANS.get(key)
@@ -350,6 +357,7 @@ def residual_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
             return residual_norm(x, weight, residual=residual, post_weight=post_weight, gate=gate,
                                  scale=scale, eps=eps, out=out, h_out=h_out)
     scale, eps = float(scale), float(eps)
+    _apart(out, "out", h_out)
     key = ("residual_norm", _sig(x), _sig(weight), _sig(residual), _sig(post_weight), _sig(gate),
            scale, eps, _sig(out), _sig(h_out))
     plan = _PLANS.get(key)
