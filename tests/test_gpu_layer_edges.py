@@ -7,6 +7,7 @@ import math
 import os
 import re
 import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -303,3 +304,28 @@ def test_fp32_products_next_to_the_largest_value():
     no_error()
     ref = np.full((T, N), a * a - 2.0 ** 100)
     check("y", y, ref, 4 * U * ref)
+
+
+FIRST_CALLS = """
+import torch, gated_delta_rule_deltanet_gb300 as kda
+r = torch.Generator(device="cuda").manual_seed(1)
+x, w, d = (torch.randn(s, generator=r, device="cuda").bfloat16() for s in ((64, 256), (512, 256), (64, 512)))
+v, o = torch.randn(256, generator=r, device="cuda"), torch.randn((64, 2, 128), generator=r, device="cuda")
+def calls():
+    out = [kda.linear(x, w)] + list(kda.linear_bwd(x, w, d, need_bias=True))
+    out += [*kda.residual_norm(x, v, residual=x), *kda.residual_norm_bwd(x, x, v, x)[:3]]
+    return out + [kda.gated_norm(o, o, v[:128]), *kda.gated_norm_bwd(o, o, v[:128], o)]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    captured = calls()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(captured, calls())) and kda.get_device_error() == 0
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    """What the library sets up on its first calls (limits, the error word, maps) is allowed in a
+    capture."""
+    subprocess.run([sys.executable, "-c", FIRST_CALLS], check=True, cwd=kbuild.ROOT, timeout=300)
