@@ -2,8 +2,9 @@
 // of o, times weight, times act(gate), forward and backward (rms' as in norms.cu).
 //
 // Bound by HBM: 8 bytes an element forward with an fp32 o and bf16 gate and y, 14 backward.  32768
-// tokens x 32 heads x 128: 172 us, 92% of the measured copy rate; backward of 16384 x 16 x 128: 86 us,
-// 80% (60% of the issue slots go to the gate's exponential and the conversions).
+// tokens x 32 heads x 128: 172 us, 92% of the measured copy rate; backward of 16384 x 16 x 128: 87 us,
+// 80% (59% of the issue slots, most of them for the gate's exponential and the conversions; three blocks an
+// SM leave 80 registers a thread, with 36 bytes spilled there and up to 112 in fp32).
 #include <algorithm>
 
 #include "layer_common.cuh"

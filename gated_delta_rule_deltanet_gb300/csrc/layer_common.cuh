@@ -154,7 +154,8 @@ __device__ __forceinline__ void store_pairs(void* row, int c, int n, const float
 
 // ---------------------------------------------------------------- activations
 
-// sigmoid(z).  FAST (bf16 results): __expf's error, 2 + 1.2 |z| ulp, stays far below the bf16
+// sigmoid(z).  FAST (bf16 results, and the fp32 gradients that are formed from bf16 inputs with them: dbias,
+// gated_norm's d_o and d_weight): __expf's error, 2 + 1.2 |z| ulp, stays far below the bf16
 // rounding; otherwise expf.  The quotient is 0 where exp(-z) overflows.
 template <bool FAST>
 __device__ __forceinline__ float sigmoid_f(float z) {
@@ -175,7 +176,8 @@ __device__ __forceinline__ void normal_cdf(float z, float& phi, float& e) {
     e = __expf(-x * x);
     const float t = __fdividef(1.f, 1.f + 0.41f * x);
     const float poly =
-        t * (0.23381889f + t * (0.20009884f + t * (0.36317647f + t * (-0.19286337f + t * (0.57457983f - t * 0.17881072f)))));
+        t * (0.23381889f +
+             t * (0.20009884f + t * (0.36317647f + t * (-0.19286337f + t * (0.57457983f - t * 0.17881072f)))));
     const float tail = 0.5f * poly * e;             // of the side away from zero
     phi = z < 0.f ? tail : 1.f - tail;
   } else {

@@ -115,8 +115,13 @@ cudaError_t launch_gemm_simt(const Gemm& g, cudaStream_t st) {
 
 // dz = act'(z) d_y (the scale is applied to the sums), rounded to the operand type where a
 // product reads it, or as the three parts of fp32, and the column sums of the unrounded dz for the
-// bias.  Bound by HBM: d_y and z read once, dz written once (the sums alone over 16384 x 6144: 40 us,
-// 5 TB/s).  A block walks 256 columns (8 a lane) with eight row lanes whose sums meet in shared
+// bias.  The rounding is a choice: the tensor cores take bf16 operands, and keeping dz's rest in a
+// second plane would double both products.  It costs a rounding beside the results' own: dx and dw of
+// 4096 x 2048 -> 4096 with SiLU are 2.35e-3 of their norm off instead of 1.66e-3.  A caller who wants the
+// rest passes fp32 operands.
+// Bound by HBM without an activation: d_y read once (the sums alone over 16384 x 6144: 43 us, 4.7
+// TB/s); with one, by issue slots too (71 % of them; SiLU with dz written 106 us, 5.4 TB/s, gelu's sums alone
+// 139 us).  A block walks 256 columns (8 a lane) with eight row lanes whose sums meet in shared
 // memory; it writes one partial row, added in a fixed order afterwards.
 struct DzArgs {
   const void* dy;
@@ -249,7 +254,7 @@ static LinearLayout linear_layout(const kda_linear_params_t& p, bool bwd) {
   const bool copy_x = !bf || (p.flags & KDA_FLAG_UNALIGNED_X) || or_dense(p.x_row_stride, K) % 8;
   const bool copy_w = !bf || (p.flags & KDA_FLAG_UNALIGNED_W) || or_dense(p.w_row_stride, K) % 8;
   // Few tokens: from three on the tensor cores' ring streams an aligned bf16 weight faster (4 x 4096 ->
-  // 16384 from HBM: 33 against 27 us), but a copy of the weight would cost more than reading it.
+  // 16384 from HBM: 33 against 28 us), but a copy of the weight would cost more than reading it.
   L.rows = !bwd && !(p.flags & KDA_FLAG_CUDA_CORES) && (T <= 2 || (T <= kRowsMax && copy_w));
   L.tc = !L.rows && !(p.flags & KDA_FLAG_CUDA_CORES);
   size_t at = 0;

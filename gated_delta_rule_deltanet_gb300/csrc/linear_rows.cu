@@ -7,9 +7,8 @@
 // which come from L1; where there are too few rows for the SMs, 2 to 8 warps of a block share a
 // group of rows and split k, adding their sums in warp order.  Compared with the tensor-core
 // kernel, whose set-up (tensor maps, tensor memory, barriers, a cluster's sum) costs more than
-// the arithmetic at these sizes: 2048 -> 6144 for one token 8.5 -> 4.7 us (7.5 us with the weight
-// in HBM rather than L2).  The sums are fp32 in a
-// fixed order; fp32 weights are read as they are.
+// the arithmetic at these sizes: 2048 -> 6144 for one token 8.5 -> 4.8 us (6.3 us with the weight
+// in HBM rather than L2).  The sums are fp32 in a fixed order; fp32 weights are read as they are.
 #include <algorithm>
 
 #include "gemm.cuh"
@@ -89,7 +88,7 @@ __global__ void __launch_bounds__(256) gemm_rows_kernel(const Gemm g, const int 
 template <bool BF, bool VEC>
 cudaError_t launch_rows_t(const Gemm& g, cudaStream_t st) {
   const int64_t groups = (g.I + kR - 1) / kR;
-  // 16 warps an SM and at least two steps of k a warp
+  // 12 warps an SM and at least two steps of k a warp
   int split = 1;
   while (split < 8 && groups * split < static_cast<int64_t>(sm_count()) * 12 && g.C >= 512 * split * 2) split *= 2;
   const int64_t blocks = (groups + 8 / split - 1) / (8 / split);

@@ -17,14 +17,15 @@
 //                      move.  Persistent: the two accumulators alternate, one being multiplied
 //                      into while eight warps store the other through shared memory and TMA.
 //                      Bound by the tensor pipe and, over seconds, by power: 32768 x 4096 x 4096
-//                      535 us, 2.06 PFLOP/s (the vendor library's product: 532 us).
+//                      539 us, 2.04 PFLOP/s (the vendor library's product: 538 us), in a
+//                      long loop 608 us (600 us).
 //   gemm_split_kernel  small products, mostly few rows (decode: the weight is the work).  One CTA
 //                      holds a 128 x BN tile; a cluster of S CTAs splits the sum over c: each
 //                      pushes its part of every other CTA's columns into that CTA's shared
 //                      memory and adds what it receives in rank order, so the result does not
 //                      depend on timing and needs no workspace.  Bound by HBM and by set-up: 16
 //                      rows through 4096 -> 16384 from HBM 25.7 us (5.2 TB/s), 64 through 4096
-//                      -> 4096 11.4 us.
+//                      -> 4096 11.6 us.
 //
 // fp32 operands are split into three bf16 parts, x = hi + mid + lo with every part rounded to
 // nearest, which hold all 24 bits; the six products of parts above 2^-27 relative are summed,
@@ -32,10 +33,10 @@
 // rounding them, always towards zero, so a long sum would lose several times fp32's rounding.
 // The split kernel therefore moves the accumulator into registers every 64 steps of c, where it is
 // added with rounding (c = 4096: 1.7e-7 of the norm, an fp32 product on CUDA cores 1.1e-6, at 2.6
-// times its speed).  Where bf16 operands have an fp32 result over more than 1024 steps both kernels
-// do the same every 512, the pair kernel into a third stretch of tensor memory of 160 columns
-// (c = 4096: 4.8e-7 against 4.4e-6 without; 4096 x 8192 x 4096 245 us against 154).  A bf16 result
-// rounds by far more than the truncation.
+// times its speed; short sums are no closer than an fp32 product's, 1.2e-7 at c = 517).  Where bf16
+// operands have an fp32 result over more than 1024 steps both kernels do the same every 512, the pair
+// kernel into a third stretch of tensor memory of 160 columns (c = 4096: 4.8e-7 against 4.4e-6
+// without; 4096 x 8192 x 4096 246 us against 150).  A bf16 result rounds by far more than the truncation.
 //
 // Every wait is bounded; one that gives up raises KDA_DEVERR_TIMEOUT, and the CTAs leave through
 // the same barriers as otherwise.

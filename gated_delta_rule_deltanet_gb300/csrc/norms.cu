@@ -30,7 +30,7 @@ struct LiveOuts {
 };
 
 // A block adds 8 columns (one sector of each partial row) with 32 row lanes: some 20 loads a thread
-// for the 608 partial rows of the longest sums, 8 of them in flight (15 us with 32 columns and
+// for the 608 partial rows of 2048 columns (up to 2432 rows of 256), 8 of them in flight (15 us with 32 columns and
 // 8 row lanes, 4 us so).
 __global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict__ part, int parts,
                                                         int64_t cols, int segments, float alpha,
@@ -717,8 +717,11 @@ static bool residual_vec(const ResidualNormArgs& A, bool xbf) {
 }
 
 // The ring of a call, or stages = 0 where rows are better read directly: with fewer than three
-// rows a CTA there is nothing to run ahead of (256 rows of 4096: 4.6 us directly, 5.6 us through the
-// ring), and a stage has to fit twice.
+// rows a CTA there is nothing to run ahead of (256 bf16 rows of 4096 with a norm, a gate and an fp32 stream:
+// 4.6 us directly, 5.6 us through the ring), and a stage has to fit twice.  Backward rows above 4096
+// columns take the ring whenever a stage fits at all, though nothing runs ahead with one: beside the column
+// sums, four chunks a thread do not fit the registers, and a row that waits in shared memory spills
+// least (8192 bf16 rows of 8192 with a norm and a gate a token 329 us, 471 directly; of 16384 685 and 971).
 static RowRing row_ring(const ResidualNormArgs& A, bool xbf, bool hbf, bool bwd, int grid) {
   RowRing R{};
   R.xrow = static_cast<uint32_t>(A.N) * (xbf ? 2 : 4);
@@ -738,7 +741,6 @@ static RowRing row_ring(const ResidualNormArgs& A, bool xbf, bool hbf, bool bwd,
   R.stage = (at + 127) / 128 * 128;
   const size_t share = kRingBytes / rows_per_sm(A.N, bwd);
   R.stages = static_cast<int>(std::min<size_t>(kMaxStages, share / R.stage));
-  // (backward rows above 4096: four chunks a thread do not fit the registers beside the sums)
   if (bwd && row_shape(A.N).V == 4) return R;
   if (R.stages < 2 || A.T < 3 * static_cast<int64_t>(grid)) R.stages = 0;
   return R;
