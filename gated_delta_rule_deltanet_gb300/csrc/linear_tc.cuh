@@ -266,6 +266,15 @@ __device__ __forceinline__ void drain_phase(uint64_t* bar, uint32_t parity) {
   wait_phase(bar, parity, 100000000ull, &never);
 }
 
+// Before the loading warp leaves: the releases of the last stages, after `it` loads into a ring of N.  The
+// products' completion arrives on these barriers by itself (in the pair from the other CTA's thread), so
+// a CTA that did not wait for it could be gone, and its shared memory another's, when it does.
+template <int N>
+__device__ __forceinline__ void wait_released(uint64_t* empty, int it, unsigned long long limit, volatile int* abort) {
+  for (int j = it > N ? it - N : 0; j < it; ++j)
+    if (!wait_phase(&empty[j % N], (j / N) & 1, limit, abort)) return;
+}
+
 // A position in a ring of N stages and the parity of the pass over it.
 template <int N>
 struct Ring {
@@ -568,6 +577,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
           drain_phase(&full[j % kPairStages], (j / kPairStages) & 1);
       }
     }
+    if (ok) wait_released<kPairStages>(empty, it, A.wait_ns, &s_abort);
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0) {                               // the leader multiplies for the pair
@@ -900,6 +910,7 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       for (int j = max(0, it - S::stages); j < it; ++j)
         drain_phase(&full[j % S::stages], (j / S::stages) & 1);
     }
+    if (ok) wait_released<S::stages>(empty, it, A.wait_ns, &s_abort);
     __syncwarp();
   } else if (warp == 1) {
     const uint32_t idesc = tc::idesc_f16(128, BN, tc::kBF16, false, AMN, BMN);

@@ -213,6 +213,27 @@ def test_gradients_at_each_tile_width(width, dw_dtype):
     check("dw", dw, ref, product_tol(d64.T, x64, C, "bf16") + 2 * U * np.abs(ref))
 
 
+@pytest.mark.parametrize("K", [64, 200, 700])
+def test_pair_products_back_to_back(K):
+    """The pair's last releases arrive in both CTAs' shared memory: launched back to back with kernels
+    that take it over at once, among them short sums that end right behind their last products, every
+    call gives the same bits."""
+    r = rng(37, K)
+    x, x64 = dev(r.standard_normal((1664, K)), "bf16")
+    w, w64 = dev(r.standard_normal((1600, K)), "bf16")
+    few = x[:40].contiguous()
+    v = torch.ones(1600, device=DEV)
+    outs = []
+    for _ in range(40):
+        outs.append(kda.linear(x, w))
+        kda.linear(few, w)
+        kda.residual_norm(outs[-1], v, residual=outs[-1])
+    no_error()
+    check("y", outs[0], x64 @ w64.T, product_tol(x64, w64.T, K, "bf16"))
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
+
+
 # ------------------------------------------------------------------- the far side of the activations
 
 @pytest.mark.parametrize("act", ["gelu", "silu", "sigmoid"])
