@@ -266,15 +266,6 @@ __device__ __forceinline__ void drain_phase(uint64_t* bar, uint32_t parity) {
   wait_phase(bar, parity, 100000000ull, &never);
 }
 
-// Before the loading warp leaves: the releases of the last stages, after `it` loads into a ring of N.  The
-// products' completion arrives on these barriers by itself (in the pair from the other CTA's thread), so
-// a CTA that did not wait for it could be gone, and its shared memory another's, when it does.
-template <int N>
-__device__ __forceinline__ void wait_released(uint64_t* empty, int it, unsigned long long limit, volatile int* abort) {
-  for (int j = it > N ? it - N : 0; j < it; ++j)
-    if (!wait_phase(&empty[j % N], (j / N) & 1, limit, abort)) return;
-}
-
 // A position in a ring of N stages and the parity of the pass over it.
 template <int N>
 struct Ring {
@@ -577,7 +568,6 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
           drain_phase(&full[j % kPairStages], (j / kPairStages) & 1);
       }
     }
-    if (ok) wait_released<kPairStages>(empty, it, A.wait_ns, &s_abort);
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0) {                               // the leader multiplies for the pair
@@ -585,6 +575,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
       const uint64_t da0 = operand_desc<AMN>(smem), db0 = operand_desc<BMN>(smem + kOpBytes);
       Ring<kPairStages> at;
       int n = 0;
+      int64_t left = static_cast<int64_t>((tiles - first + step - 1) / step) * A.kblocks;   // stages to come
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step) {
         for (int base = 0; base < A.kblocks && ok; base += stretch, ++n) {
@@ -610,8 +601,10 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
               for (int q = 0; q < kBK / 16; ++q)
                 mma_pair(d, tc::desc_add(da, q * k_advance<AMN>()), tc::desc_add(db, q * k_advance<BMN>()), idesc,
                          k > base || q > 0);
-              commit_pair(&empty[s]);
+              // (A release that no load waits for could arrive when the CTA, or its peer, is gone.)
+              if (left > kPairStages) commit_pair(&empty[s]);
             }
+            --left;
             __syncwarp();
           }
           if (ok && elect_one()) commit_pair(&acc_full[b]);
@@ -910,7 +903,6 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       for (int j = max(0, it - S::stages); j < it; ++j)
         drain_phase(&full[j % S::stages], (j / S::stages) & 1);
     }
-    if (ok) wait_released<S::stages>(empty, it, A.wait_ns, &s_abort);
     __syncwarp();
   } else if (warp == 1) {
     const uint32_t idesc = tc::idesc_f16(128, BN, tc::kBF16, false, AMN, BMN);
@@ -946,7 +938,7 @@ gemm_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
               tc::mma_ss(d, tc::desc_add(da, pa + q * k_advance<AMN>()), tc::desc_add(db, pb + q * k_advance<BMN>()),
                          idesc, k > base || p > 0 || q > 0);
           }
-          tc::mma_commit(&empty[s]);
+          if (k + S::stages < k1) tc::mma_commit(&empty[s]);   // (only releases that a load waits for)
         }
         __syncwarp();
       }
