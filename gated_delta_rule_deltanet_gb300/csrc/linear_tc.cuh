@@ -215,7 +215,8 @@ __device__ __forceinline__ void join8(const uint16_t* p, int64_t ld, int64_t pla
       x[e] = c + e < C ? bf16_bits_to_f32(at[0]) + bf16_bits_to_f32(at[plane]) + bf16_bits_to_f32(at[2 * plane]) : 0.f;
     }
   } else {                                         // (rows are whole 128-byte lines)
-    const Raw8<true> hi = load_chunk<true, true>(p + r * ld + c, 0, 0, 8), mid = load_chunk<true, true>(p + plane + r * ld + c, 0, 0, 8),
+    const Raw8<true> hi = load_chunk<true, true>(p + r * ld + c, 0, 0, 8),
+                     mid = load_chunk<true, true>(p + plane + r * ld + c, 0, 0, 8),
                      lo = load_chunk<true, true>(p + 2 * plane + r * ld + c, 0, 0, 8);
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = c + e < C ? hi.f32(e) + mid.f32(e) + lo.f32(e) : 0.f;
@@ -1304,10 +1305,10 @@ cudaError_t launch_shape(const Gemm& g, int planes, cudaStream_t st) {
   if (planes == 1 && big >= sms / 4 && g.J > 128)
     return promote ? launch_pair<AMN, BMN, true>(g, A, planes, sms / 2, st)
                    : launch_pair<AMN, BMN, false>(g, A, planes, sms / 2, st);
-  // Few tiles, or few rows.  128 columns, 64 where there are no more rows or too few tiles to fill the
-  // SMs with a split.  An SM takes in some 90 GB/s, so a weight streams at HBM's rate only into most of them: splits as many as
-  // run at once (launch_split), with four steps a CTA at least; beyond four ways the exchange costs
-  // more than it saves unless c is long (16 x 4096 -> 4096: 4 ways 8.4 us, 8 ways 9.5 us).
+  // Few tiles, or few rows.  128 columns, 64 where there are no more rows or too few tiles to fill the SMs
+  // with a split.  An SM takes in some 90 GB/s, so a weight streams at HBM's rate only into most of them:
+  // splits as many as run at once (launch_split), with four steps a CTA at least; beyond four ways the
+  // exchange costs more than it saves unless c is long (16 x 4096 -> 4096: 4 ways 8.4 us, 8 ways 9.5 us).
   auto tiles_for = [&](int n) { return ((g.I + 127) / 128) * ((g.J + n - 1) / n); };
   const int bn = g.J <= 64 || tiles_for(128) * 8 <= sms ? 64 : 128;
   const int steps = A.kblocks * (planes == 3 ? 6 : 1);

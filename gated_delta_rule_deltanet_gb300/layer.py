@@ -268,8 +268,9 @@ def linear_bwd(x: torch.Tensor, weight: torch.Tensor, d_y: torch.Tensor, *,
                stream: Optional[torch.cuda.Stream] = None):
     """Backward of `linear` (kda_linear_bwd).  d_y [T, N] float32 or bfloat16; `pre_activation`
     as `linear` returned it (needed with an activation).  With an activation or a float32 d_y,
-    bfloat16 operands round act'(z) d_y to bfloat16 before the two products.  Returns (dx [T, K] in x's dtype,
-    dw [N, K] in `dw_dtype` (default x's), dbias [N] float32), None for those not needed.
+    bfloat16 operands round act'(z) d_y to bfloat16 before the two products.  Returns (dx [T, K]
+    in x's dtype, dw [N, K] in `dw_dtype` (default x's), dbias [N] float32), None for those not
+    needed.
     The residual's gradient is d_y itself."""
     if stream is not None:
         with _on(stream, x):
