@@ -1308,8 +1308,8 @@ cudaError_t launch_shape(const Gemm& g, int planes, cudaStream_t st) {
   // Few tiles, or few rows.  128 columns, 64 where there are no more rows or too few tiles to fill the SMs
   // with a split.  An SM takes in some 90 GB/s, so a weight streams at HBM's rate only into most of them:
   // splits as many as run at once (launch_split), with four steps a CTA at least; more than four ways only
-  // of long sums (16 x 8192 -> 2048: 4 ways 14.1 us, 8 ways 12.3 us; of 2048 steps they are alike, 16 x
-  // 2048 -> 1024 7.5 us; in between eight would gain, 16 x 4096 -> 2048 9.6 and 9.1 us).
+  // of long sums (16 x 8192 -> 2048: 4 ways 14.1 us, 8 ways 12.3 us; of half that eight would gain less, 16 x
+  // 4096 -> 2048 9.6 and 9.1 us).
   auto tiles_for = [&](int n) { return ((g.I + 127) / 128) * ((g.J + n - 1) / n); };
   const int bn = g.J <= 64 || tiles_for(128) * 8 <= sms ? 64 : 128;
   const int steps = A.kblocks * (planes == 3 ? 6 : 1);
