@@ -33,6 +33,7 @@ KDA_DEVERR_SLOT_DUP = 3
 KDA_DEVERR_TIMEOUT = 4
 KDA_DEVERR_DECAY_RANGE = 5
 KDA_DEVERR_ACCEPTED = 6
+KDA_DEVERR_PAGE = 7
 
 # every function include/kda.h declares
 EXPORTS = ("kda_abi_version", "kda_status_string", "kda_prefill_workspace_size",
@@ -44,7 +45,9 @@ EXPORTS = ("kda_abi_version", "kda_status_string", "kda_prefill_workspace_size",
            "kda_conv_gates_fwd", "kda_prefill_no_alloc_form", "kda_linear_fwd",
            "kda_linear_bwd", "kda_linear_workspace_size", "kda_residual_norm_fwd",
            "kda_residual_norm_bwd", "kda_gated_norm_fwd", "kda_gated_norm_bwd",
-           "kda_norm_workspace_size")
+           "kda_norm_workspace_size", "kda_rotary_fwd", "kda_rotary_bwd", "kda_cache_append",
+           "kda_cache_attention", "kda_cache_attention_workspace_size", "kda_cache_update",
+           "kda_cache_compact", "kda_cache_rows_workspace_size", "kda_cache_copy")
 
 KDA_ACT_NONE = 0
 KDA_ACT_RELU = 1
@@ -119,6 +122,36 @@ class KdaNormParams(ctypes.Structure):
     ]
 
 
+class KdaRotaryParams(ctypes.Structure):
+    """Mirror of kda_rotary_params_t."""
+
+    _fields_ = [("tokens", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in ("num_q_heads", "num_k_heads", "head_dim", "rot_dim", "dtype",
+                                      "interleaved", "wide_positions")] + [
+        ("magnitude", ctypes.c_float)] + [
+        (n, ctypes.c_int64) for n in ("q_row_stride", "k_row_stride", "q_out_row_stride",
+                                      "k_out_row_stride")]
+
+
+class KdaCacheParams(ctypes.Structure):
+    """Mirror of kda_cache_params_t."""
+
+    _fields_ = [("tokens", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in ("num_seqs", "num_q_heads", "num_kv_heads", "head_dim", "rot_dim",
+                                      "dtype", "o_dtype", "interleaved", "page_size", "max_pages",
+                                      "num_pages", "window", "span")] + [
+        (n, ctypes.c_float) for n in ("magnitude", "scale", "softcap")] + [
+        (n, ctypes.c_int64) for n in ("q_row_stride", "k_row_stride", "v_row_stride",
+                                      "q_out_row_stride", "page_stride", "page_row_stride",
+                                      "page_head_stride")]
+
+
+class KdaCacheRowsParams(ctypes.Structure):
+    """Mirror of kda_cache_rows_params_t."""
+
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "rows_out", "max_pages", "page_size", "num_pages")]
+
+
 class KdaError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
         self.status = status
@@ -187,6 +220,7 @@ def load():
         L.kda_prefill_bwd_workspace_size.restype = ctypes.c_int
         L.kda_conv_gates_fwd.argtypes = [pp, ctypes.c_int32] + [P] * 14
         L.kda_conv_gates_fwd.restype = ctypes.c_int
+        rp, cp, tp = (ctypes.POINTER(s) for s in (KdaRotaryParams, KdaCacheParams, KdaCacheRowsParams))
         Z, lp, np_ = ctypes.c_size_t, ctypes.POINTER(KdaLinearParams), ctypes.POINTER(KdaNormParams)
         for name, args in (("kda_linear_fwd", [lp] + [P] * 7 + [Z, P]),
                            ("kda_linear_bwd", [lp] + [P] * 8 + [Z, P]),
@@ -195,7 +229,17 @@ def load():
                            ("kda_residual_norm_bwd", [np_] + [P] * 13 + [Z, P]),
                            ("kda_gated_norm_fwd", [np_] + [P] * 5),
                            ("kda_gated_norm_bwd", [np_] + [P] * 8 + [Z, P]),
-                           ("kda_norm_workspace_size", [np_, ctypes.c_int32, ctypes.POINTER(Z)])):
+                           ("kda_norm_workspace_size", [np_, ctypes.c_int32, ctypes.POINTER(Z)]),
+                           ("kda_rotary_fwd", [rp] + [P] * 7),
+                           ("kda_rotary_bwd", [rp] + [P] * 7),
+                           ("kda_cache_append", [cp] + [P] * 11),
+                           ("kda_cache_attention", [cp] + [P] * 9 + [Z, P]),
+                           ("kda_cache_attention_workspace_size", [cp, ctypes.POINTER(Z)]),
+                           ("kda_cache_update", [tp] + [P] * 12 + [Z, P]),
+                           ("kda_cache_compact", [tp] + [P] * 9 + [Z, P]),
+                           ("kda_cache_rows_workspace_size", [tp, ctypes.POINTER(Z)]),
+                           ("kda_cache_copy", [P, P, P, ctypes.c_int32, P, P, ctypes.c_int64,
+                                               ctypes.c_int32, P])):
             getattr(L, name).argtypes = args
             getattr(L, name).restype = ctypes.c_int
         L.kda_set_stage_events.argtypes = [P, ctypes.c_int32]

@@ -1,0 +1,470 @@
+// cache_rows.cu -- the page tables of a key-value cache from one step to the next, the compaction of its pools
+// and the copying of pages (or of any pool's slots).
+//
+// Row r of a table holds len_r tokens in ceil(len_r / P) pages; refs[q] counts the references to page q, those of
+// the table and of anyone else; q is free where refs[q] is zero.
+//
+// An update makes new rows.  New row i goes on from old row parent[i] (or from nothing) with its first
+// kept_i = min(len of the parent, new_len_i) tokens and has pages for new_len_i.  Pages that the kept tokens fill are
+// shared.  A page that they end inside is open: tokens will be written behind them, so only one row may
+// hold it and no one else read it.  The lowest row that goes on in an open page keeps it if no full row and
+// no one outside the table refers to it; every other row gets a fresh page and the open one's contents.  Rows that no new
+// row goes on from are thereby freed, rows with several continuations forked, longer rows grown.
+// Fresh pages are the free ones from the lowest on, given out row by row.  Nothing is written to the old tables, and
+// fresh pages were free in them, so what still reads them (a step in flight) is not disturbed.
+//
+// A compaction of n used pages moves the k-th used page from n on into the k-th free page before n: as few pages as
+// can be, each into a page that is free, so that the old tables stay valid here too.
+//
+// Both are chains of short passes (count, rank, assign) over at most some million integers, bound by the latency of the
+// passes: one thread-block cluster runs them in one launch, with the cluster's hardware barrier between them.
+#include <algorithm>
+#include <limits.h>
+
+#include "cache_common.cuh"
+
+namespace kda {
+
+namespace {
+
+constexpr int kCluster = 8, kThreads = 1024, kWarps = kThreads / 32;
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// inclusive sum over the block; `total` gets the sum.  Two barriers.
+template <typename T>
+__device__ __forceinline__ T block_scan(T x, T* warp_sums, T& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T incl = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) warp_sums[warp] = incl;
+  __syncthreads();
+  T s = warp_sums[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  total = __shfl_sync(0xffffffffu, s, 31);
+  const T before = __shfl_sync(0xffffffffu, s, (warp + 31) & 31);
+  __syncthreads();
+  return incl + (warp ? before : 0);
+}
+
+struct Segment {                             // the pages of one CTA: multiples of 4 but the last
+  int begin, end;
+};
+__device__ __forceinline__ Segment segment(int n, int rank) {
+  const int per = ((n + kCluster - 1) / kCluster + 3) & ~3;
+  Segment s;
+  s.begin = min(static_cast<int64_t>(rank) * per, static_cast<int64_t>(n));
+  s.end = min(s.begin + per, n);
+  return s;
+}
+
+// pages of the row, or -1 for a length that its row cannot hold
+__device__ __forceinline__ int pages_of(int len, int P, int width) {
+  if (len < 0) return -1;
+  const int n = len / P + (len % P != 0);
+  return n <= width ? n : -1;
+}
+
+// Scratch of an update (int32): [N] counts, [N] first open row, [N] free pages in order, [S_out] pages that a row
+// keeps (its open one included), [S_out] its place among the fresh pages, words of the launch: 0 the error,
+// 1 copies in all, 8.. the CTAs' free pages.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) update_kernel(const RowsArgs a) {
+  __shared__ int warp_sums[32];
+  __shared__ int64_t warp_sums64[32];
+  __shared__ int stop;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x;
+  const int all = kCluster * kThreads, me = rank * kThreads + tid;
+  int32_t* counts = a.scratch;
+  int32_t* first = counts + a.N;
+  int32_t* free_list = first + a.N;
+  int32_t* have = free_list + a.N;
+  int32_t* place = have + a.S_out;
+  int32_t* words = place + a.S_out;
+  const Segment seg = segment(a.N, rank);
+
+  // 1. references as they are; free pages of the CTA
+  if (rank == 0 && tid == 0) words[0] = 0;
+  int mine = 0, total;
+  for (int q = seg.begin + tid; q < seg.end; q += kThreads) {
+    const int r = a.refs[q];
+    counts[q] = r;
+    first[q] = INT_MAX;
+    if (r == 0) {
+      ++mine;
+      a.out_refs[q] = 0;
+    }
+  }
+  block_scan(mine, warp_sums, total);
+  if (tid == 0) words[8 + rank] = total;
+  cluster_sync();
+
+  // 2. references of the old rows taken back, of the new rows' full pages added; a warp takes a row.  A row that goes
+  // on from itself keeps its full pages: nothing to count.
+  const auto fault = [&]() { atomicExch(words, 1); };
+  const auto kept_of = [&](int i, int& p) {
+    p = a.parent ? a.parent[i] : i;
+    return p < 0 || p >= a.S ? 0 : max(0, min(a.lens[p], a.new_lens[i]));
+  };
+  for (int r = rank * kWarps + warp; r < a.S; r += kCluster * kWarps) {
+    const int n = pages_of(a.lens[r], a.P, a.width);
+    if (n < 0) {
+      if (lane == 0) fault();
+      continue;
+    }
+    int skip = 0, p;
+    if (r < a.S_out) {
+      const int kept = kept_of(r, p);
+      if (p == r) skip = kept / a.P;
+    }
+    for (int j = lane; j < n; j += 32) {
+      const int q = a.table[static_cast<int64_t>(r) * a.width + j];
+      if (q == -1) continue;                 // a page that the row has given back
+      if (static_cast<uint32_t>(q) >= static_cast<uint32_t>(a.N)) fault();
+      else if (j >= skip) atomicSub(counts + q, 1);
+      else if (a.refs[q] <= 0) fault();
+    }
+  }
+  for (int i = rank * kWarps + warp; i < a.S_out; i += kCluster * kWarps) {
+    int p;
+    const int kept = kept_of(i, p), full = kept / a.P;
+    if (p >= a.S || pages_of(a.new_lens[i], a.P, a.width) < 0 || (p >= 0 && pages_of(a.lens[p], a.P, a.width) < 0)) {
+      if (lane == 0) fault();
+      continue;
+    }
+    if (p < 0) continue;
+    const int32_t* row = a.table + static_cast<int64_t>(p) * a.width;
+    for (int j = (p == i ? full : 0) + lane; j < full; j += 32) {
+      const int q = row[j];
+      if (q == -1) continue;
+      if (static_cast<uint32_t>(q) < static_cast<uint32_t>(a.N)) atomicAdd(counts + q, 1);
+      else fault();
+    }
+    if (lane == 0 && kept % a.P != 0) {
+      const int q = row[full];
+      if (static_cast<uint32_t>(q) < static_cast<uint32_t>(a.N)) atomicMin(first + q, i);
+      else fault();
+    }
+  }
+  cluster_sync();
+
+  // 3. the free pages in order; a page in use whose count went below zero was held more often than refs say
+  int before = 0, free_pages = 0;
+  for (int c = 0; c < kCluster; ++c) {
+    const int n = __ldcg(words + 8 + c);
+    if (c < rank) before += n;
+    free_pages += n;
+  }
+  for (int q0 = seg.begin; q0 < seg.end; q0 += kThreads) {
+    const int q = q0 + tid;
+    const int r = q < seg.end ? a.refs[q] : 1;
+    if (r < 0 || (q < seg.end && __ldcg(counts + q) < 0)) fault();
+    const int at = block_scan(static_cast<int>(r == 0), warp_sums, total) - 1;
+    if (r == 0) free_list[before + at] = q;
+    before += total;
+  }
+  // and the rows' needs, by the first CTA.  The lists of copies begin empty.
+  if (rank == 0) {
+    int64_t fresh = 0, sum;                  // in 64 bits: rows may ask for more than there is
+    int copies = 0;
+    bool bad = false;
+    for (int i0 = 0; i0 < a.S_out; i0 += kThreads) {
+      const int i = i0 + tid;
+      int need = 0, copy = 0, hold = 0, open = -1;
+      if (i < a.S_out && __ldcg(words) == 0) {
+        int p;
+        const int kept = kept_of(i, p);
+        hold = kept / a.P;
+        if (kept % a.P != 0) {
+          open = a.table[static_cast<int64_t>(p) * a.width + hold];
+          if (__ldcg(first + open) == i && __ldcg(counts + open) == 0) {
+            counts[open] = 1;                // no other row looks at it: each has another first row or finds this one's
+            ++hold;
+          } else {
+            copy = 1;
+          }
+        }
+        need = pages_of(a.new_lens[i], a.P, a.width) - hold;
+      }
+      const int64_t at = block_scan(static_cast<int64_t>(need), warp_sums64, sum) - need + fresh;
+      fresh += sum;
+      bad |= fresh > free_pages;
+      const int c = block_scan(copy, warp_sums, total) - 1 + copies;
+      copies += total;
+      if (i < a.S_out) {
+        have[i] = hold;
+        place[i] = static_cast<int32_t>(at);
+        if (copy) {
+          a.copy_src[c] = open;
+          a.copy_dst[c] = static_cast<int32_t>(at);          // becomes the page itself below
+        }
+      }
+    }
+    if (bad && tid == 0) fault();
+    if (tid == 0) words[1] = copies;
+  }
+  cluster_sync();
+
+  // 4. the new rows
+  if (tid == 0) stop = __ldcg(words);
+  __syncthreads();
+  if (stop) {
+    if (me == 0) raise_device_error(a.err, KDA_DEVERR_PAGE);
+    for (int q = seg.begin + tid; q < seg.end; q += kThreads) a.out_refs[q] = a.refs[q];
+    for (int64_t i = me; i < static_cast<int64_t>(a.S_out) * a.width; i += all) a.out_table[i] = -1;
+    for (int i = me; i < a.S_out; i += all) {
+      a.out_lens[i] = 0;
+      a.kept[i] = 0;
+      a.copy_src[i] = -1;
+      a.copy_dst[i] = -1;
+    }
+    return;
+  }
+  for (int q = seg.begin + tid; q < seg.end; q += kThreads)
+    if (a.refs[q] != 0) a.out_refs[q] = __ldcg(counts + q);
+  const int copies = __ldcg(words + 1);
+  for (int i = me; i < a.S_out; i += all) {
+    if (i < copies) {
+      a.copy_dst[i] = __ldcg(free_list + __ldcg(a.copy_dst + i));
+    } else {
+      a.copy_src[i] = -1;
+      a.copy_dst[i] = -1;
+    }
+  }
+  for (int i = rank * kWarps + warp; i < a.S_out; i += kCluster * kWarps) {
+    int p;
+    const int kept = kept_of(i, p), hold = __ldcg(have + i), at = __ldcg(place + i);
+    const int want = pages_of(a.new_lens[i], a.P, a.width);
+    const int32_t* row = a.table + static_cast<int64_t>(max(p, 0)) * a.width;
+    int32_t* out = a.out_table + static_cast<int64_t>(i) * a.width;
+    for (int j = lane; j < a.width; j += 32) {
+      int q = -1;
+      if (j < hold) {
+        q = row[j];
+      } else if (j < want) {
+        q = __ldcg(free_list + at + j - hold);
+        a.out_refs[q] = 1;
+      }
+      out[j] = q;
+    }
+    if (lane == 0) {
+      a.out_lens[i] = a.new_lens[i];
+      a.kept[i] = kept;
+    }
+  }
+}
+
+// Scratch of a compaction (int32): [N] the used pages by rank, [N] the free pages by rank, words of the launch:
+// 1 used pages among the first n, 8.. the CTAs' used pages, 16.. their errors.  page_map holds the ranks meanwhile.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) compact_kernel(const RowsArgs a) {
+  __shared__ int warp_sums[32];
+  __shared__ int stop;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x;
+  const int all = kCluster * kThreads, me = rank * kThreads + tid;
+  int32_t* used_list = a.scratch;
+  int32_t* free_list = used_list + a.N;
+  int32_t* words = free_list + a.N;
+  const Segment seg = segment(a.N, rank);
+
+  int mine = 0, total;
+  bool bad = false;
+  for (int q = seg.begin + tid; q < seg.end; q += kThreads) {
+    const int r = a.refs[q];
+    mine += r != 0;
+    bad |= r < 0;
+  }
+  block_scan(mine, warp_sums, total);
+  bad = __syncthreads_or(bad);
+  if (tid == 0) words[8 + rank] = bad ? -1 : total;
+  cluster_sync();
+
+  int before = 0, n = 0;
+  bad = false;
+  for (int c = 0; c < kCluster; ++c) {
+    const int x = __ldcg(words + 8 + c);
+    bad |= x < 0;
+    if (c < rank) before += x;
+    n += x;
+  }
+  // A row that names a free page, or a page that is not there, cannot be rewritten; nothing is.
+  bool wrong = false;
+  for (int r = rank * kWarps + warp; r < a.S; r += kCluster * kWarps) {
+    const int pages = pages_of(a.lens[r], a.P, a.width);
+    wrong |= pages < 0;
+    for (int j = lane; j < pages; j += 32) {
+      const int q = a.table[static_cast<int64_t>(r) * a.width + j];
+      wrong |= q != -1 && (static_cast<uint32_t>(q) >= static_cast<uint32_t>(a.N) || a.refs[q] == 0);
+    }
+  }
+  wrong = __syncthreads_or(wrong);
+  if (rank == 0 && tid == 0 && n == a.N) words[1] = n;
+  if (!bad) {
+    for (int q0 = seg.begin; q0 < seg.end; q0 += kThreads) {
+      const int q = q0 + tid;
+      const int used = q < seg.end && a.refs[q] != 0 ? 1 : 0;
+      const int at = block_scan(used, warp_sums, total) - used + before;     // used pages before q
+      if (q < seg.end) {
+        a.page_map[q] = used ? at : -1;
+        if (used) used_list[at] = q;
+        else free_list[q - at] = q;
+        if (q == n) words[1] = at;
+      }
+      before += total;
+    }
+  }
+  __syncthreads();
+  if (tid == 0) words[16 + rank] = bad || wrong;
+  cluster_sync();
+
+  if (tid == 0) {
+    int s = 0;
+    for (int c = 0; c < kCluster; ++c) s |= __ldcg(words + 16 + c);
+    stop = s;
+  }
+  __syncthreads();
+  const int half = a.N / 2;
+  if (stop) {                                // everything stays where it is
+    if (me == 0) raise_device_error(a.err, KDA_DEVERR_PAGE);
+    for (int q = me; q < a.N; q += all) {
+      a.page_map[q] = a.refs[q] != 0 ? q : -1;
+      a.out_refs[q] = a.refs[q];
+    }
+    for (int64_t i = me; i < static_cast<int64_t>(a.S) * a.width; i += all) a.out_table[i] = a.table[i];
+    for (int i = me; i < half; i += all) {
+      a.copy_src[i] = -1;
+      a.copy_dst[i] = -1;
+    }
+    return;
+  }
+  // where page q goes: to its rank's place in front, which a used page before n keeps
+  const int front = __ldcg(words + 1);       // used pages among the first n: those that stay
+  for (int q = me; q < a.N; q += all) {
+    const int at = __ldcg(a.page_map + q);
+    if (q >= n) a.out_refs[q] = 0;
+    if (at < 0) continue;
+    const int to = q < n ? q : __ldcg(free_list + at - front);
+    a.page_map[q] = to;
+    a.out_refs[to] = a.refs[q];
+  }
+  for (int i = me; i < half; i += all) {
+    const bool moves = i < n - front;
+    a.copy_src[i] = moves ? __ldcg(used_list + front + i) : -1;
+    a.copy_dst[i] = moves ? __ldcg(free_list + i) : -1;
+  }
+  cluster_sync();
+  for (int r = rank * kWarps + warp; r < a.S; r += kCluster * kWarps) {
+    const int pages = pages_of(a.lens[r], a.P, a.width);
+    const int64_t at = static_cast<int64_t>(r) * a.width;
+    for (int j = lane; j < a.width; j += 32) {
+      const int q = j < pages ? a.table[at + j] : -1;
+      a.out_table[at + j] = q < 0 ? -1 : __ldcg(a.page_map + q);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ copies
+
+constexpr int kMaxPools = 64, kCopyThreads = 256, kCopyUnroll = 4;
+
+struct Pools {
+  char* base[kMaxPools];
+  int64_t stride[kMaxPools];                 // bytes from page to page
+};
+
+// pool[dst[i]] = pool[src[i]] for i up to the list's end, every pool.  VB bytes a thread and move; a
+// block takes pieces of kCopyThreads * kCopyUnroll of them, all loaded before the first is stored.  Bound by HBM.
+template <typename V>
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const Pools pools, int num_pools, int64_t bytes, int64_t pieces,
+                                                            const int32_t* src, const int32_t* dst, int64_t n, int num_pages,
+                                                            int32_t* err) {
+  constexpr int64_t kPiece = static_cast<int64_t>(sizeof(V)) * kCopyThreads * kCopyUnroll;
+  const int64_t per_entry = pieces * num_pools;
+  for (int64_t at = blockIdx.x; at < n * per_entry; at += gridDim.x) {
+    const int64_t i = at / per_entry, rest = at - i * per_entry, pool = rest / pieces, piece = rest - pool * pieces;
+    const int32_t s = src[i], d = dst[i];
+    if (s < 0) return;                       // the list's end
+    if (s >= num_pages || d < 0 || d >= num_pages) {
+      if (threadIdx.x == 0) raise_device_error(err, KDA_DEVERR_PAGE);
+      continue;
+    }
+    const char* from = pools.base[pool] + s * pools.stride[pool];
+    char* to = pools.base[pool] + d * pools.stride[pool];
+    const int64_t b0 = piece * kPiece + threadIdx.x * static_cast<int64_t>(sizeof(V));
+    V x[kCopyUnroll];
+#pragma unroll
+    for (int u = 0; u < kCopyUnroll; ++u) {
+      const int64_t b = b0 + u * kCopyThreads * static_cast<int64_t>(sizeof(V));
+      if (b < bytes) x[u] = *reinterpret_cast<const V*>(from + b);
+    }
+#pragma unroll
+    for (int u = 0; u < kCopyUnroll; ++u) {
+      const int64_t b = b0 + u * kCopyThreads * static_cast<int64_t>(sizeof(V));
+      if (b < bytes) *reinterpret_cast<V*>(to + b) = x[u];
+    }
+  }
+}
+
+template <typename V>
+cudaError_t copy(const Pools& pools, int num_pools, int64_t bytes, const int32_t* src, const int32_t* dst, int64_t n,
+                 int num_pages, int32_t* err, cudaStream_t st) {
+  const int64_t pieces = (bytes + static_cast<int64_t>(sizeof(V)) * kCopyThreads * kCopyUnroll - 1) /
+                         (static_cast<int64_t>(sizeof(V)) * kCopyThreads * kCopyUnroll);
+  const int64_t blocks = std::min<int64_t>(n * pieces * num_pools, static_cast<int64_t>(sm_count()) * 8);
+  copy_kernel<V><<<static_cast<unsigned>(blocks), kCopyThreads, 0, st>>>(pools, num_pools, bytes, pieces, src, dst, n,
+                                                                         num_pages, err);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t cache_rows_workspace(const kda_cache_rows_params_t& p) {
+  return (static_cast<size_t>(3) * p.num_pages + 2 * static_cast<size_t>(p.rows_out) + 32) * sizeof(int32_t);
+}
+
+cudaError_t launch_cache_update(const RowsArgs& a, cudaStream_t st) {
+  update_kernel<<<kCluster, kThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_compact(const RowsArgs& a, cudaStream_t st) {
+  compact_kernel<<<kCluster, kThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_copy(void* const* pools, const int64_t* bytes, const int64_t* strides, int num_pools,
+                              const int32_t* src, const int32_t* dst, int64_t n, int num_pages, int32_t* err,
+                              cudaStream_t st) {
+  // pools of one page size and alignment go into one launch
+  for (int first = 0; first < num_pools;) {
+    Pools p;
+    int count = 0;
+    const int64_t size = bytes[first];
+    uint64_t bits = size;
+    while (first + count < num_pools && count < kMaxPools && bytes[first + count] == size) {
+      p.base[count] = static_cast<char*>(pools[first + count]);
+      p.stride[count] = strides[first + count];
+      bits |= reinterpret_cast<uintptr_t>(pools[first + count]) | strides[first + count];
+      ++count;
+    }
+    cudaError_t e = cudaSuccess;
+    if (size > 0) {
+      if (bits % 16 == 0) e = copy<uint4>(p, count, size, src, dst, n, num_pages, err, st);
+      else if (bits % 4 == 0) e = copy<uint32_t>(p, count, size, src, dst, n, num_pages, err, st);
+      else e = copy<uint8_t>(p, count, size, src, dst, n, num_pages, err, st);
+    }
+    if (e != cudaSuccess) return e;
+    first += count;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace kda

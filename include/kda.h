@@ -123,6 +123,8 @@ typedef enum kda_decay_kind {
  * fp32 CUDA-core path (KDA_FLAG_CUDA_CORES) takes any finite log-decay. */
 #define KDA_DEVERR_DECAY_RANGE 5
 #define KDA_DEVERR_ACCEPTED 6    /* kda_fold_accepted: accepted[b] > window */
+#define KDA_DEVERR_PAGE 7        /* kda_cache_*: a page, length, parent or reference count out of range, or
+                                    fewer free pages than are asked for */
 
 typedef struct kda_params {
   int32_t num_seqs;    /* B: sequences in the ragged batch (prefill) or decode batch */
@@ -619,6 +621,179 @@ kda_status_t kda_gated_norm_bwd(const kda_norm_params_t *p, const void *o, const
 
 /* Workspace bytes of kda_residual_norm_bwd (gated = 0) or kda_gated_norm_bwd (gated = 1). */
 kda_status_t kda_norm_workspace_size(const kda_norm_params_t *p, int32_t gated, size_t *bytes);
+
+/*
+ * The key-value cache of a hybrid model's softmax attention layers, which stand between the
+ * recurrent ones.  The cache of a layer is two pools of pages (keys and values): page q, row r and
+ * key head h at element q page_stride + r page_row_stride + h page_head_stride, head_dim
+ * elements each, so that [num_pages, page_size, HK, d] and [num_pages, HK, page_size, d] are both read
+ * in place.  A sequence's token j lies in row j % page_size of page block_table[b][j / page_size];
+ * one table serves all layers.  Entries that a call does not need are not read and may hold -1.
+ *
+ * Problems only the device can see (a page, length or position out of range) set KDA_DEVERR_PAGE;
+ * what they touch is then skipped (an append writes no row, an attention leaves the key out, an update or
+ * a compaction changes nothing).
+ */
+
+/* Rotary positions.  head_dim 1..1024, rot_dim even, 0 < rot_dim <= head_dim. */
+typedef struct kda_rotary_params {
+  int64_t tokens;         /* T */
+  int32_t num_q_heads;    /* H >= 0 */
+  int32_t num_k_heads;    /* HK >= 0 */
+  int32_t head_dim;       /* d */
+  int32_t rot_dim;        /* R: channels turned; those from R on pass */
+  int32_t dtype;          /* kda_dtype_t of q, k and the outputs */
+  int32_t interleaved;    /* pairs (2i, 2i + 1); otherwise (i, i + R / 2) */
+  int32_t wide_positions; /* positions are int64 (nonzero) or int32 */
+  float magnitude;        /* m */
+  /* elements between tokens; 0 means dense */
+  int64_t q_row_stride, k_row_stride, q_out_row_stride, k_out_row_stride;
+} kda_rotary_params_t;
+
+/*
+ * Turns each pair (a, b) of a head's channels at position p by the angle p frequencies[i]:
+ *
+ *     (a, b) -> m (a cos - b sin, b cos + a sin)
+ *
+ *   q [T, H, d], k [T, HK, d] (NULL with no heads)   positions [T], negative ones too; the angle is
+ *   good to 2^-24 of a turn for |p| < 2^31           frequencies [R / 2] fp64, radians per position
+ *   q_out, k_out: may be q, k (same pointer and stride)
+ * kda_rotary_bwd is the transposed map, for gradients.
+ */
+kda_status_t kda_rotary_fwd(const kda_rotary_params_t *p, const void *q, const void *k,
+                            const void *positions, const double *frequencies, void *q_out,
+                            void *k_out, void *stream);
+kda_status_t kda_rotary_bwd(const kda_rotary_params_t *p, const void *d_q, const void *d_k,
+                            const void *positions, const double *frequencies, void *dq_out,
+                            void *dk_out, void *stream);
+
+typedef struct kda_cache_params {
+  int64_t tokens;         /* append: T, rows of q, k and v; attention: ignored */
+  int32_t num_seqs;       /* B */
+  int32_t num_q_heads;    /* H: a multiple of HK */
+  int32_t num_kv_heads;   /* HK */
+  int32_t head_dim;       /* d: append 1..1024; attention a multiple of 16 bytes up to 256 elements */
+  int32_t rot_dim;        /* append: R, as in kda_rotary_params_t; 0 turns nothing */
+  int32_t dtype;          /* kda_dtype_t of q, k, v and the pages (append: of q_out) */
+  int32_t o_dtype;        /* attention: kda_dtype_t of o */
+  int32_t interleaved;    /* append: as in kda_rotary_params_t */
+  int32_t page_size;      /* rows of a page, >= 1 */
+  int32_t max_pages;      /* entries of a block_table row */
+  int32_t num_pages;      /* pages of the pools */
+  int32_t window;         /* attention: queries per sequence, 1..64 */
+  int32_t span;           /* attention: keys a query sees, its own included; 0 means all */
+  float magnitude;        /* append: m */
+  float scale;            /* attention: 0 means 1 / sqrt(d) */
+  float softcap;          /* attention: cap of the scores, 0 means none */
+  int64_t q_row_stride, k_row_stride, v_row_stride, q_out_row_stride; /* elements; 0 means dense */
+  int64_t page_stride, page_row_stride, page_head_stride;             /* elements; of both pools */
+} kda_cache_params_t;
+
+/*
+ * New tokens into the cache: q and k turned (as kda_rotary_fwd), k and v written into the pages.
+ * Token t of sequence b, the i-th of its new ones, stands at position start[b] + i.
+ *
+ *   q [T, H, d] or NULL (H = 0)     k, v [T, HK, d]
+ *   input_row_offsets [B + 1], or NULL: one token per sequence (T = B).  Tokens from its last entry on
+ *   belong to no sequence; nothing of them is read or written
+ *   frequencies [R / 2] or NULL (R = 0)      q_out [T, H, d], may be q
+ *   start [B] tokens already in the cache
+ * The pages of the new positions must be in the table.  A page row that two tokens are given races.
+ */
+kda_status_t kda_cache_append(const kda_cache_params_t *p, const void *q, const void *k, const void *v,
+                              const double *frequencies, void *key_pages, void *value_pages,
+                              const int32_t *block_table, const int32_t *start,
+                              const uint32_t *input_row_offsets, void *q_out, void *stream);
+
+/*
+ * Attention of a window of W queries per sequence (W = 1: a decode step) over its cache.  Query w of
+ * sequence b is row b W + w, at position p = lens[b] - W + w; its own key is in the cache.  For head
+ * h, key head h / (H / HK):
+ *
+ *     s_j = c(scale q . k_j) + slopes[h] (j - p)      max(0, p - span + 1) <= j <= p
+ *     o = softmax(s) v,   lse = log sum_j e^(s_j)     c(x) = softcap tanh(x / softcap)
+ *
+ *   q [B W, H, d]      lens [B]: tokens in the cache, the window's included
+ *   slopes [H] fp32 or NULL      o [B W, H, d] dense, o_dtype      lse [B W, H] fp32 or NULL
+ *   workspace >= kda_cache_attention_workspace_size(p) bytes, 256-byte aligned; calls that may run at
+ *   the same time need one each
+ * A query that sees no key (p < 0, an empty sequence) gets o = 0 and lse = -infinity.  What a query
+ * does not see does not reach it, NaN and infinities included.  Scores, sums and o are formed in
+ * fp32; with bf16 pages the products are exact and, where o is bf16, the softmax's weights are rounded to bf16 before
+ * they multiply v.  Pages, their strides and q are 16-byte aligned.  Repeated calls give the same bits.
+ */
+kda_status_t kda_cache_attention(const kda_cache_params_t *p, const void *q, const void *key_pages,
+                                 const void *value_pages, const int32_t *block_table,
+                                 const int32_t *lens, const float *slopes, void *o, float *lse,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+kda_status_t kda_cache_attention_workspace_size(const kda_cache_params_t *p, size_t *bytes);
+
+typedef struct kda_cache_rows_params {
+  int32_t rows;      /* S: rows of the table as it is */
+  int32_t rows_out;  /* update: rows of the new table; compact: ignored */
+  int32_t max_pages; /* entries of a row */
+  int32_t page_size;
+  int32_t num_pages;
+} kda_cache_rows_params_t;
+
+/*
+ * A cache's tables from one step to the next.  Row r holds lens[r] tokens; refs[q] counts the
+ * references to page q, the table's and any others; a page is free where it is 0.  New row i goes
+ * on from row parent[i] (-1: from nothing) with its first kept[i] = min(lens[parent[i]], new_lens[i])
+ * tokens, and has pages for new_lens[i].  So a row goes on (parent i), forks (several rows of one
+ * parent), is cut back (a shorter new_lens), grows, begins, or ends (no row goes on from it).
+ *
+ *   - Pages that the kept tokens fill are shared.  A page that they end inside is kept by the lowest
+ *     row that ends in it, if no full row and no one outside the table refers to it; the other rows get a fresh
+ *     page there and a line in the list of copies, for kda_cache_copy.
+ *   - Fresh pages are the free ones from the lowest on, row by row.  Pages that this call frees are
+ *     not handed out by it.
+ *   - The old tables are left as they are, and valid: only pages that they hold free are handed out.
+ *
+ *   block_table [S, max_pages]   lens [S]   refs [num_pages]   parent [rows_out] or NULL (row i from
+ *   row i; rows_out = rows)      new_lens [rows_out]
+ *   out_table [rows_out, max_pages], -1 behind a row's pages   out_lens, kept [rows_out]   out_refs
+ *   [num_pages]   copy_src, copy_dst [rows_out]: the copies, then -1
+ *   workspace >= kda_cache_rows_workspace_size bytes, 256-byte aligned
+ * The outputs share no memory with the inputs.  With KDA_DEVERR_PAGE (not enough free pages among its
+ * reasons) the new rows are empty, out_refs is refs and nothing is to be copied.
+ */
+kda_status_t kda_cache_update(const kda_cache_rows_params_t *p, const int32_t *block_table,
+                              const int32_t *lens, const int32_t *refs, const int32_t *parent,
+                              const int32_t *new_lens, int32_t *out_table, int32_t *out_lens,
+                              int32_t *out_refs, int32_t *kept, int32_t *copy_src,
+                              int32_t *copy_dst, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/*
+ * Used pages to the front of the pools: of n pages in use, the k-th from page n on goes to the k-th
+ * free page before n.
+ *   out_table [S, max_pages], out_refs [num_pages]: with the pages' new places
+ *   page_map [num_pages]: where each page goes, -1 for a free one
+ *   copy_src, copy_dst [num_pages / 2]: the moves, then -1
+ * Workspace, outputs and the old tables' validity as in kda_cache_update; with KDA_DEVERR_PAGE
+ * (a row naming a free page) every page stays.
+ */
+kda_status_t kda_cache_compact(const kda_cache_rows_params_t *p, const int32_t *block_table,
+                               const int32_t *lens, const int32_t *refs, int32_t *out_table,
+                               int32_t *out_refs, int32_t *page_map, int32_t *copy_src,
+                               int32_t *copy_dst, void *workspace, size_t workspace_bytes,
+                               void *stream);
+kda_status_t kda_cache_rows_workspace_size(const kda_cache_rows_params_t *p, size_t *bytes);
+
+/*
+ * pool[dst[i]] = pool[src[i]] for each i before the list's first negative src (behind which all are
+ * negative), for each of num_pools pools of num_pages pages: pages of a cache, or slots of a state or
+ * convolution pool (a forked sequence's recurrent state).  Page q of pool j is page_bytes[j] bytes at
+ * pools[j] + q page_strides[j].
+ *   pools, page_bytes, page_strides   HOST arrays of num_pools entries
+ *   src, dst [n] int32
+ * No page may be written twice or both read and written; an index >= num_pages (or a negative dst)
+ * sets KDA_DEVERR_PAGE and is skipped.
+ */
+kda_status_t kda_cache_copy(void *const *pools, const int64_t *page_bytes,
+                            const int64_t *page_strides, int32_t num_pools, const int32_t *src,
+                            const int32_t *dst, int64_t n, int32_t num_pages, void *stream);
 
 /*
  * Measurement aid (no counterpart on the pages).  Registers up to 8 CUDA events
