@@ -55,6 +55,11 @@ kda_status_t check_attention(const kda_cache_params_t* p) {
     return KDA_ERR_INVALID_ARG;
   const int64_t piece = 16 / static_cast<int64_t>(kda::dtype_bytes(p->dtype));
   if (p->window > kMaxWindow || p->head_dim > kMaxAttentionHead || p->head_dim % piece) return KDA_ERR_UNSUPPORTED;
+  // the units of work are counted in 32 bits: tiles of 32 keys and more, and 3 for each (sequence, key head, 8 rows)
+  const double rows = static_cast<double>(p->window) * (p->num_q_heads / p->num_kv_heads) / 2 + 1;
+  if (p->num_seqs * static_cast<double>(p->num_kv_heads) * rows * (static_cast<double>(p->max_pages) * p->page_size / 32 + 4) >=
+      2147483648.0)
+    return KDA_ERR_UNSUPPORTED;
   if (p->page_stride % piece || p->page_row_stride % piece || p->page_head_stride % piece || p->q_row_stride % piece)
     return KDA_ERR_INVALID_ARG;
   return KDA_OK;

@@ -39,14 +39,14 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // A stretch is counted in tiles and what an item costs beside them: the ring runs empty at its end, and the
 // warps' sums are joined.
-constexpr int kItemCost = 2, kMinUnits = 4;
+constexpr int kItemCost = 2, kMinUnits = 2;
 
 // A running maximum follows the scores only when one is this far above it (in powers of two): sums grow by up
 // to 2^10 more than they need to, which fp32 holds without loss, and most blocks need no exchange between lanes.
 constexpr float kSlack = 10.f;
 
-struct Join {                                // where stretch c begins inside an item that began in an earlier one
-  int32_t seq, item, parts, pad;             // parts == 0: nothing to join here
+struct Join {                                // an item that several stretches share
+  int32_t seq, item, parts, stretch;         // stretch: the first that begins inside it; parts == 0: nothing to join
 };
 
 struct Range {                               // a sequence's keys
@@ -71,8 +71,10 @@ __device__ __forceinline__ Range range_of(const AttentionArgs& a, int b) {
 
 struct Walk {                                // a stretch, item by item
   int b, item, tile;                         // where it stands
-  int64_t left;                              // units still to do
+  int left;                                  // units still to do
+  int n, k, rest, begin;                     // n stretches; stretch i begins at unit i k + i rest / n
   Range r;
+  __device__ __forceinline__ int begin_of(int i) const { return i * k + static_cast<uint32_t>(i * rest) / static_cast<uint32_t>(n); }
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
@@ -84,82 +86,87 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Finds this CTA's stretch.  Every CTA adds the units of all sequences up (B numbers); stretch c of n begins at
-// unit floor(c total / n).  Also notes where the CTA begins inside an item.
+// Finds this CTA's stretch.  Every CTA adds the units of all sequences up (B numbers, fewer than 2^31 units in all);
+// stretch c of n begins at unit floor(c total / n).
 template <int TILE>
-__device__ Walk find_stretch(const AttentionArgs& a, int items, Join* joins) {
-  __shared__ int64_t warp_sum[kWarps];
-  __shared__ int32_t found;                  // the sequence in which the stretch begins
-  __shared__ int64_t before;                 // and the units of those before it
+__device__ Walk find_stretch(const AttentionArgs& a, int items) {
+  __shared__ int warp_sum[kWarps];
+  __shared__ Walk found;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.B + kThreads - 1) / kThreads, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += static_cast<int64_t>(range_of<TILE>(a, b).tiles + kItemCost) * items;
-  int64_t incl = mine;
+  int mine = 0;
+  Range r{};
+  for (int b = b0; b < b1; ++b) {
+    r = range_of<TILE>(a, b);
+    mine += (r.tiles + kItemCost) * items;
+  }
+  int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+    const int x = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += x;
   }
   if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
-  int64_t total = 0, excl = incl - mine;
+  int total = 0, excl = incl - mine;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) excl += warp_sum[w];
     total += warp_sum[w];
   }
   const int c = blockIdx.x;
-  const int n = static_cast<int>(min(static_cast<int64_t>(gridDim.x), (total + kMinUnits - 1) / kMinUnits));
   Walk w;
+  w.n = min(static_cast<int>(gridDim.x), (total + kMinUnits - 1) / kMinUnits);
   w.left = 0;
-  if (c >= n) {
-    if (tid == 0) joins[c].parts = 0;
-    return w;
-  }
-  // floor(c total / n) in parts that fit: total = k n + rest
-  const int64_t k = total / n;
-  const int rest = static_cast<int>(total - k * n);
-  const auto begin_of = [&](int i) { return i * k + i * rest / n; };
-  const int64_t t0 = begin_of(c), t1 = begin_of(c + 1);
-  if (excl <= t0 && t0 < excl + mine) {
+  if (c >= w.n) return w;
+  w.k = static_cast<uint32_t>(total) / static_cast<uint32_t>(w.n);           // total = k n + rest
+  w.rest = total - w.k * w.n;
+  w.begin = w.begin_of(c);
+  w.left = w.begin_of(c + 1) - w.begin;
+  if (excl <= w.begin && w.begin < excl + mine) {
     for (int b = b0; b < b1; ++b) {
-      const int64_t x = static_cast<int64_t>(range_of<TILE>(a, b).tiles + kItemCost) * items;
-      if (t0 < excl + x) {
-        found = b;
-        before = excl;
+      if (per > 1) r = range_of<TILE>(a, b);
+      const int units = r.tiles + kItemCost;
+      if (w.begin < excl + units * items) {
+        w.b = b;
+        w.r = r;
+        w.item = static_cast<uint32_t>(w.begin - excl) / static_cast<uint32_t>(units);
+        w.tile = w.begin - excl - w.item * units;
+        found = w;
         break;
       }
-      excl += x;
+      excl += units * items;
     }
   }
   __syncthreads();
-  w.b = found;
-  w.r = range_of<TILE>(a, w.b);
-  const int64_t at = t0 - before;
-  const int units = w.r.tiles + kItemCost;
-  w.item = at <= 0x7fffffff ? static_cast<int>(at) / units : static_cast<int>(at / units);
-  w.tile = static_cast<int>(at - static_cast<int64_t>(w.item) * units);
-  w.left = t1 - t0;
-  if (tid == 0) {
-    const int64_t begin = t0 - w.tile, end = begin + w.r.tiles;      // the item's tiles
-    Join j{w.b, w.item, 0, 0};
-    if (w.tile > 0 && w.tile < w.r.tiles && begin_of(c - 1) <= begin) {
-      // the first stretch that begins inside the item: it, those after it that do, and the one before it
-      int e = static_cast<int>(min(static_cast<int64_t>(n - 1), c + (end - 1 - t0) / k));
-      while (e > c && begin_of(e) >= end) --e;
+  return found;
+}
+
+// Leaves word of the items that have to be joined, for the join kernel's block `at`: with as many blocks as items
+// (few items) that of the item, otherwise that of the stretch which is the first to begin inside it.
+__device__ __forceinline__ void note_joins(const AttentionArgs& a, const Walk& w, int items, int join_blocks, Join* joins) {
+  const int c = blockIdx.x;
+  Join j{w.b, w.item, 0, c};                 // of a stretch without work: parts 0
+  if (w.left > 0 && w.tile > 0 && w.tile < w.r.tiles) {
+    const int first = w.begin - w.tile, end = first + w.r.tiles;             // the item's tiles
+    if (w.begin_of(c - 1) <= first) {        // the first stretch to begin here: those after it that do, too
+      int e = c + min(w.n - 1 - c, static_cast<int>(static_cast<uint32_t>(end - 1 - w.begin) / static_cast<uint32_t>(w.k)));
+      while (e > c && w.begin_of(e) >= end) --e;
       j.parts = e - c + 2;
     }
-    joins[c] = j;
   }
-  return w;
+  if (static_cast<int64_t>(a.B) * items > join_blocks) joins[c] = j;
+  else if (j.parts) joins[w.b * items + w.item] = j;
+}
+__device__ __forceinline__ void note_whole(const AttentionArgs& a, const Walk& w, int items, int join_blocks, Join* joins) {
+  if (static_cast<int64_t>(a.B) * items <= join_blocks) joins[w.b * items + w.item].parts = 0;
 }
 
 // The next piece of the stretch: tiles [walk.tile, + n) of walk.item; false at the stretch's end.
 template <int TILE>
 __device__ __forceinline__ bool next_piece(const AttentionArgs& a, int items, Walk& w, int& n) {
   while (w.left > 0 && w.b < a.B) {
-    n = static_cast<int>(min(w.left, static_cast<int64_t>(w.r.tiles - w.tile)));
+    n = min(w.left, w.r.tiles - w.tile);
     if (n > 0) return true;
     w.left -= w.r.tiles + kItemCost - w.tile;            // begins behind the item's tiles
     w.tile = 0;
@@ -189,10 +196,18 @@ __device__ __forceinline__ RowPlace row_place(const AttentionArgs& a, int b, int
   return RowPlace{(static_cast<int64_t>(b) * a.W + w) * a.H + h, w, h};
 }
 
+// two channels; o need only be aligned to its elements
 template <bool BF_OUT>
-__device__ __forceinline__ void store_out(const AttentionArgs& a, int64_t at, float x) {
-  if constexpr (BF_OUT) static_cast<uint16_t*>(a.o)[at] = f32_to_bf16_bits(x);
-  else static_cast<float*>(a.o)[at] = x;
+__device__ __forceinline__ void store_out2(const AttentionArgs& a, int64_t at, float2 x) {
+  if constexpr (BF_OUT) {
+    uint16_t* o = static_cast<uint16_t*>(a.o) + at;
+    o[0] = f32_to_bf16_bits(x.x);
+    o[1] = f32_to_bf16_bits(x.y);
+  } else {
+    float* o = static_cast<float*>(a.o) + at;
+    o[0] = x.x;
+    o[1] = x.y;
+  }
 }
 
 // Parts in the workspace: ROWS rows of D sums, then ROWS pairs (m, l).  Stretch c leaves a part that began in an
@@ -200,41 +215,42 @@ __device__ __forceinline__ void store_out(const AttentionArgs& a, int64_t at, fl
 __device__ __forceinline__ int64_t part_floats(int rows, int D) { return static_cast<int64_t>(rows) * (D + 2); }
 
 // Adds the groups' sums (in shared memory, rows of DP + 2 floats: o, m, l) up and writes the rows of a piece: final
-// where the piece is the whole item, otherwise to the workspace.  A warp takes a row.
+// where the piece is the whole item, otherwise to the workspace.  Sixteen threads take a row.
 template <int DP, int ROWS, int GROUPS, bool BF_OUT>
 __device__ void finish_piece(const AttentionArgs& a, const float* sums, int b, int hk, int row0, int rows, float* part) {
-  const int lane = threadIdx.x & 31;
-  for (int r = threadIdx.x >> 5; r < min(ROWS, rows - row0); r += kWarps) {
+  const int x0 = threadIdx.x & 15;
+#pragma unroll
+  for (int pass = 0; pass < (ROWS + kThreads / 16 - 1) / (kThreads / 16); ++pass) {
+    const int r = pass * (kThreads / 16) + (threadIdx.x >> 4);
+    if (r >= min(ROWS, rows - row0)) break;
     float m = -INFINITY, f[GROUPS], l = 0.f;
 #pragma unroll
     for (int w = 0; w < GROUPS; ++w) m = fmaxf(m, sums[(w * ROWS + r) * (DP + 2) + DP]);
     const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
     for (int w = 0; w < GROUPS; ++w) {
-      const float* s = sums + (w * ROWS + r) * (DP + 2);
-      f[w] = ex2(s[DP] - base);
-      l += f[w] * s[DP + 1];
+      const float2 ml = *reinterpret_cast<const float2*>(sums + (w * ROWS + r) * (DP + 2) + DP);
+      f[w] = ex2(ml.x - base);
+      l += f[w] * ml.y;
     }
     const float inv = part ? 1.f : (l == 0.f ? 0.f : 1.f / l);       // a NaN stays one
     const RowPlace at = row_place(a, b, hk, row0 + r);
 #pragma unroll
-    for (int d = lane; d < DP; d += 32) {
+    for (int d = 2 * x0; d < DP; d += 32) {
       if (d >= a.D) break;
-      float x = 0.f;
+      float2 x = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < GROUPS; ++w) x += f[w] * sums[(w * ROWS + r) * (DP + 2) + d];
-      x = l == 0.f ? 0.f : x * inv;
-      if (part) part[static_cast<int64_t>(r) * a.D + d] = x;
-      else store_out<BF_OUT>(a, at.o * a.D + d, x);
-    }
-    if (lane == 0) {
-      if (part) {
-        float* ml = part + static_cast<int64_t>(ROWS) * a.D + 2 * r;
-        ml[0] = m;
-        ml[1] = l;
-      } else if (a.lse) {
-        a.lse[at.o] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      for (int w = 0; w < GROUPS; ++w) {
+        const float2 y = *reinterpret_cast<const float2*>(sums + (w * ROWS + r) * (DP + 2) + d);
+        x = fma2(make_float2(f[w], f[w]), y, x);
       }
+      x = l == 0.f ? make_float2(0.f, 0.f) : make_float2(x.x * inv, x.y * inv);
+      if (part) *reinterpret_cast<float2*>(part + static_cast<int64_t>(r) * a.D + d) = x;
+      else store_out2<BF_OUT>(a, at.o * a.D + d, x);
+    }
+    if (x0 == 0) {
+      if (part) *reinterpret_cast<float2*>(part + static_cast<int64_t>(ROWS) * a.D + 2 * r) = make_float2(m, l);
+      else if (a.lse) a.lse[at.o] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
   }
 }
@@ -296,7 +312,8 @@ struct Mma {
 // fp32: one part's rounding (2^-9) would be as large as that of a bf16 o.
 template <int DP, int RW, bool BF_OUT>
 __global__ void __launch_bounds__(kThreads, Mma<DP, RW>::kCtas)
-    attend_bf16_kernel(const AttentionArgs a, FastDiv page_div, int row_tiles, Join* joins, float* parts) {
+    attend_bf16_kernel(const AttentionArgs a, FastDiv page_div, int row_tiles, int join_blocks, Join* joins,
+                       float* parts) {
   using C = Mma<DP, RW>;
   constexpr int BK = C::kBK, H = C::kHalves, CR = C::kCopyRows, MB = BK / 16, PARTS = BF_OUT ? 2 : 3;
   constexpr int CH = DP / 8, KS = DP / 16;                     // 16-byte pieces of a row, steps along D
@@ -321,8 +338,9 @@ __global__ void __launch_bounds__(kThreads, Mma<DP, RW>::kCtas)
   const uint32_t k_frag = (lane & 15) * C::kRowBytes + ((((lane >> 4) & 1) ^ (lane & 7)) << 4);
   const uint32_t v_frag = ((lane & 7) + ((lane >> 4) << 3)) * C::kRowBytes + ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
 
-  Walk walk = find_stretch<C::kGroups * BK>(a, items, joins);
+  Walk walk = find_stretch<C::kGroups * BK>(a, items);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  bool noted = false;
   int n;
   while (next_piece<C::kGroups * BK>(a, items, walk, n)) {
     const int hk = walk.item / row_tiles, row0 = (walk.item - hk * row_tiles) * C::kRows;
@@ -345,13 +363,13 @@ __global__ void __launch_bounds__(kThreads, Mma<DP, RW>::kCtas)
 
     // Block i of this group begins at key base(i); half 2 i is its keys, 2 i + 1 its values.
     const auto base = [&](int i) { return r.begin + ((walk.tile + i) * C::kGroups + group) * BK; };
-    int page[CR];
+    int page[CR], page_after[CR];            // of the next block to be copied and the one after it
     int64_t off[CR];                         // the rows of the newest block in the ring, or -1
-    const auto pages_of = [&](int i) {
+    const auto pages_of = [&](int i, int (&to)[CR]) {
 #pragma unroll
       for (int x = 0; x < CR; ++x) {
         const int key = base(i) + row_first + 8 * x;
-        page[x] = i < n && key >= r.first && key < r.len ? table[page_div.div(key)] : -2;
+        to[x] = i < n && key >= r.first && key < r.len ? table[page_div.div(key)] : -2;
       }
     };
     const auto copy_half = [&](const void* from, int h) {
@@ -384,26 +402,38 @@ __global__ void __launch_bounds__(kThreads, Mma<DP, RW>::kCtas)
             }
           }
           copy_half(a.k, h);
-          pages_of(i + 1);
+#pragma unroll
+          for (int x = 0; x < CR; ++x) page[x] = page_after[x];
+          pages_of(i + 2, page_after);
         }
       }
       cp_async_commit();
     };
 
-    pages_of(0);
+    pages_of(0, page);
+    pages_of(1, page_after);
+    constexpr int QN = (C::kRows * CH + kThreads - 1) / kThreads;
+    uint4 q[QN];
 #pragma unroll
+    for (int x = 0; x < QN; ++x) {
+      const int i = tid + x * kThreads, row = i / CH, ch = i - row * CH;
+      q[x] = make_uint4(0, 0, 0, 0);
+      if (row < C::kRows && row0 + row < rows && ch < pieces) {
+        const RowPlace at = row_place(a, b, hk, row0 + row);
+        q[x] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                               (static_cast<int64_t>(b) * a.W + at.w) * a.q_stride +
+                                               static_cast<int64_t>(at.h) * a.D + ch * 8);
+      }
+    }
+#pragma unroll 1
     for (int h = 0; h < H - 1; ++h) issue(h);
 
-    for (int i = tid; i < C::kRows * CH; i += kThreads) {
-      const int row = i / CH, ch = i - row * CH;
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (row0 + row < rows && ch < pieces) {
-        const RowPlace at = row_place(a, b, hk, row0 + row);
-        x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                            (static_cast<int64_t>(b) * a.W + at.w) * a.q_stride +
-                                            static_cast<int64_t>(at.h) * a.D + ch * 8);
-      }
-      *reinterpret_cast<uint4*>(q_smem + row * C::kRowBytes + ((ch ^ (row & 7)) << 4)) = x;
+    if (!noted && tid == 0) note_joins(a, walk, items, join_blocks, joins);  // while the copies are under way
+    noted = true;
+#pragma unroll
+    for (int x = 0; x < QN; ++x) {
+      const int i = tid + x * kThreads, row = i / CH, ch = i - row * CH;
+      if (row < C::kRows) *reinterpret_cast<uint4*>(q_smem + row * C::kRowBytes + ((ch ^ (row & 7)) << 4)) = q[x];
     }
     float m[2], l[2], o[KS][4], slope[2];
     int pos[2];                              // positions of this lane's rows
@@ -600,104 +630,146 @@ __global__ void __launch_bounds__(kThreads, Mma<DP, RW>::kCtas)
     float* part = nullptr;
     if (n < r.tiles) part = parts + (2 * static_cast<int64_t>(blockIdx.x) + (walk.tile > 0 ? 0 : 1)) * part_floats(C::kRows, a.D);
     finish_piece<DP, C::kRows, C::kGroups, BF_OUT>(a, sums, b, hk, row0, rows, part);
+    if (!part && tid == 0) note_whole(a, walk, items, join_blocks, joins);
     piece_done<C::kGroups * BK>(a, items, walk);
   }
+  if (!noted && tid == 0) note_joins(a, walk, items, join_blocks, joins);      // nothing to do here
 }
 
 // ------------------------------------------------------------------ fp32
 
-template <int DP, int STAGES>
+// R rows (two, four or eight).  A lane forms the scores of KL keys (lane mod 8, + 8, ..) and two rows, where R < 8 of a
+// share of the channels; for the weighted sum it owns DP / 32 channels of all rows.
+template <int DP, int R>
 struct Simt {
-  static constexpr int kBK = 8, kRows = 8, kRowBytes = DP * 4;
-  static constexpr int kStage = 2 * kBK * kRowBytes;
-  static constexpr int kRing = kWarps * STAGES * kStage;
+  static constexpr int kKeys = DP == 256 ? 1 : 2;              // keys of a lane
+  static constexpr int kBK = 8 * kKeys, kRows = R, kRowBytes = DP * 4;
+  static constexpr int kHalves = DP == 64 ? 4 : 3, kHalf = kBK * kRowBytes;
+  static constexpr int kRing = kWarps * kHalves * kHalf;
   static constexpr int kPart = kWarps * kRows * (DP + 2) * 4;
+  static constexpr int kTop = kRing > kPart ? kRing : kPart;
   static constexpr int kQStride = DP + 4;                      // two rows apart is eight banks apart
   static constexpr int kQ = kRows * kQStride * 4;
-  static constexpr size_t kSmem = (kRing > kPart ? kRing : kPart) + kQ + kWarps * kBK * kRows * 4 + kWarps * kRows * 4;
+  static constexpr size_t kSmem = kTop + kQ + kWarps * (kBK + 1) * kRows * 4;
+  static constexpr int kCtas = DP == 64 ? 3 : 2;
 };
 
-// A lane forms the scores of one key (lane mod 8) and two rows (2 (lane / 8), + 1); for the weighted sum
-// it owns DP / 32 channels of all eight rows.
-template <int DP, int STAGES, bool BF_OUT>
-__global__ void __launch_bounds__(kThreads) attend_f32_kernel(const AttentionArgs a, FastDiv page_div, int row_tiles,
-                                                              Join* joins, float* parts) {
-  using C = Simt<DP, STAGES>;
-  constexpr int BK = C::kBK, CH = DP / 4, OC = DP / 32;
+template <int DP, int R, bool BF_OUT>
+__global__ void __launch_bounds__(kThreads, Simt<DP, R>::kCtas)
+    attend_f32_kernel(const AttentionArgs a, FastDiv page_div, int row_tiles, int join_blocks, Join* joins, float* parts) {
+  using C = Simt<DP, R>;
+  constexpr int BK = C::kBK, KL = C::kKeys, H = C::kHalves, CH = DP / 4, OC = DP / 32, DS = 8 / R;
   extern __shared__ __align__(1024) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = a.H / a.HK, rows = a.W * g, pieces = a.D / 4, items = a.HK * row_tiles;
-  unsigned char* ring = smem + warp * STAGES * C::kStage;
+  const int rows = a.W * (a.H / a.HK), pieces = a.D / 4, items = a.HK * row_tiles;
+  unsigned char* ring = smem + warp * H * C::kHalf;
   const uint32_t ring_u = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-  constexpr int kTop = C::kRing > C::kPart ? C::kRing : C::kPart;
-  float* q_smem = reinterpret_cast<float*>(smem + kTop);
-  float* weights = reinterpret_cast<float*>(smem + kTop + C::kQ) + warp * BK * C::kRows;   // [key][row]
-  float* factors = reinterpret_cast<float*>(smem + kTop + C::kQ) + kWarps * BK * C::kRows + warp * C::kRows;
+  float* q_smem = reinterpret_cast<float*>(smem + C::kTop);
+  float* weights = q_smem + C::kRows * C::kQStride + warp * (BK + 1) * R;    // [key][row], then the rows' factors
+  float* factors = weights + BK * R;
   const float scale2 = a.scale * kLog2e, cap2 = a.softcap * kLog2e, inv_cap = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
-  const int key_lane = lane & 7, pair = lane >> 3;
+  const int key_lane = lane & 7, pair = (lane >> 3) / DS, share = (lane >> 3) % DS;
 
-  // copies: this lane takes row lane / 4 of a block, pieces lane % 4, + 4, ..; piece x of row r lies at x ^ r
+  // copies: this lane takes rows lane / 4 (+ 8) of a block, pieces lane % 4, + 4, ..; piece x of row r lies at
+  // x ^ (r mod 8)
   const int row_c = lane >> 2, piece_c = lane & 3;
   const uint32_t to_even = row_c * C::kRowBytes + ((piece_c ^ row_c) << 4), to_odd = to_even ^ 64;
 
-  Walk walk = find_stretch<kWarps * BK>(a, items, joins);
+  Walk walk = find_stretch<kWarps * BK>(a, items);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  bool noted = false;
   int n;
   while (next_piece<kWarps * BK>(a, items, walk, n)) {
     const int hk = walk.item / row_tiles, row0 = (walk.item - hk * row_tiles) * C::kRows;
     const Range r = walk.r;
     const int b = walk.b;
-
-    __syncthreads();                         // the previous part's sums are read
-    for (int i = tid; pieces < CH && i < kWarps * STAGES * 2 * BK * CH; i += kThreads) {
-      const int row = i / CH, ch = i - row * CH;
-      if (ch >= pieces)
-        *reinterpret_cast<uint4*>(smem + row * C::kRowBytes + ((ch ^ (row & 7)) << 4)) = make_uint4(0, 0, 0, 0);
-    }
-    for (int i = tid; i < C::kRows * CH; i += kThreads) {
-      const int row = i / CH, ch = i - row * CH;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (row0 + row < rows && ch < pieces) {
-        const RowPlace at = row_place(a, b, hk, row0 + row);
-        x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) +
-                                             (static_cast<int64_t>(b) * a.W + at.w) * a.q_stride +
-                                             static_cast<int64_t>(at.h) * a.D + ch * 4);
-      }
-      *reinterpret_cast<float4*>(q_smem + row * C::kQStride + ch * 4) = x;
-    }
-    __syncthreads();
-
-    // block i of this warp begins at key base(i); this lane copies key base(i) + row_c
     const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
+    const int64_t head = static_cast<int64_t>(hk) * a.page_head_stride + piece_c * 4;
+
+    __syncthreads();                         // the previous piece's sums are read
+    if (pieces < CH) {
+      for (int i = tid; i < kWarps * H * BK * CH; i += kThreads) {
+        const int row = i / CH, ch = i - row * CH;
+        if (ch >= pieces)
+          *reinterpret_cast<uint4*>(smem + row * C::kRowBytes + ((ch ^ (row & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+      }
+      __syncthreads();
+    }
+
+    // block i of this warp begins at key base(i); half 2 i is its keys, 2 i + 1 its values
     const auto base = [&](int i) { return r.begin + ((walk.tile + i) * kWarps + warp) * BK; };
-    const auto inside = [&](int i, int key) { return i < n && key >= r.first && key < r.len; };
-    const auto page_of = [&](int i) {
-      const int key = base(i) + row_c;
-      return inside(i, key) ? table[page_div.div(key)] : -1;
-    };
-    uint32_t flags = 0;                      // a bit a stage, the newest lowest: is this lane's key there?
-    const auto issue = [&](int i, int page) {
-      const int key = base(i) + row_c;
-      const bool ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.num_pages);
-      if (!ok && inside(i, key)) raise_device_error(a.err, KDA_DEVERR_PAGE);
-      flags = (flags << 1) | (ok ? 1u : 0u);
-      if (i < n) {
-        const int in_page = key - static_cast<int>(page_div.div(key)) * a.P;
-        const int64_t off = ok ? page * a.page_stride + in_page * a.page_row_stride +
-                                     static_cast<int64_t>(hk) * a.page_head_stride + piece_c * 4 : 0;
-        const float *k = static_cast<const float*>(a.k) + off, *v = static_cast<const float*>(a.v) + off;
-        const uint32_t dst = ring_u + (i % STAGES) * C::kStage;
+    int page[KL], page_after[KL];            // of the next block to be copied and the one after it
+    int64_t off[KL];
+    const auto pages_of = [&](int i, int (&to)[KL]) {
 #pragma unroll
-        for (int c = 0; c < CH / 4; ++c) {
-          if (c * 4 + piece_c >= pieces) break;
-          const uint32_t at = dst + ((c & 1) ? to_odd : to_even) + (c >> 1) * 128;
-          cp_async16(at, ok ? k + c * 16 : k, ok);
-          cp_async16(at + BK * C::kRowBytes, ok ? v + c * 16 : v, ok);
+      for (int x = 0; x < KL; ++x) {
+        const int key = base(i) + row_c + 8 * x;
+        to[x] = i < n && key >= r.first && key < r.len ? table[page_div.div(key)] : -2;
+      }
+    };
+    const auto copy_half = [&](const void* from, int h) {
+      const uint32_t dst = ring_u + (h % H) * C::kHalf;
+#pragma unroll
+      for (int x = 0; x < KL; ++x) {
+        const bool ok = off[x] >= 0;
+        const float* src = static_cast<const float*>(from) + (ok ? off[x] : 0);
+#pragma unroll
+        for (int c = 0; c < CH / 4; ++c)
+          if (c * 4 + piece_c < pieces)
+            cp_async16(dst + ((c & 1) ? to_odd : to_even) + (c >> 1) * 128 + x * 8 * C::kRowBytes, src + (ok ? c * 16 : 0), ok);
+      }
+    };
+    const auto issue = [&](int h) {
+      const int i = h >> 1;
+      if (i < n) {
+        if (h & 1) {
+          copy_half(a.v, h);
+        } else {
+#pragma unroll
+          for (int x = 0; x < KL; ++x) {
+            const int key = base(i) + row_c + 8 * x;
+            off[x] = -1;
+            if (static_cast<uint32_t>(page[x]) < static_cast<uint32_t>(a.num_pages)) {
+              const int in_page = key - static_cast<int>(page_div.div(key)) * a.P;
+              off[x] = page[x] * a.page_stride + in_page * a.page_row_stride + head;
+            } else if (page[x] != -2) {
+              raise_device_error(a.err, KDA_DEVERR_PAGE);
+            }
+          }
+          copy_half(a.k, h);
+#pragma unroll
+          for (int x = 0; x < KL; ++x) page[x] = page_after[x];
+          pages_of(i + 2, page_after);
         }
       }
       cp_async_commit();
     };
 
+    pages_of(0, page);
+    pages_of(1, page_after);
+    constexpr int QN = (C::kRows * CH + kThreads - 1) / kThreads;
+    float4 q[QN];
+#pragma unroll
+    for (int x = 0; x < QN; ++x) {
+      const int i = tid + x * kThreads, row = i / CH, ch = i - row * CH;
+      q[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row < C::kRows && row0 + row < rows && ch < pieces) {
+        const RowPlace at = row_place(a, b, hk, row0 + row);
+        q[x] = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) +
+                                                (static_cast<int64_t>(b) * a.W + at.w) * a.q_stride +
+                                                static_cast<int64_t>(at.h) * a.D + ch * 4);
+      }
+    }
+#pragma unroll 1
+    for (int h = 0; h < H - 1; ++h) issue(h);
+
+    if (!noted && tid == 0) note_joins(a, walk, items, join_blocks, joins);  // while the copies are under way
+    noted = true;
+#pragma unroll
+    for (int x = 0; x < QN; ++x) {
+      const int i = tid + x * kThreads, row = i / CH, ch = i - row * CH;
+      if (row < C::kRows) *reinterpret_cast<float4*>(q_smem + row * C::kQStride + ch * 4) = q[x];
+    }
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, slope[2];
     int pos[2];
 #pragma unroll
@@ -706,105 +778,129 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const AttentionArg
       pos[i] = r.len - a.W + at.w;
       slope[i] = a.slopes ? a.slopes[at.h] * kLog2e : 0.f;
     }
-    float o[C::kRows][OC];
+    float2 o[R][OC / 2];
 #pragma unroll
-    for (int t = 0; t < C::kRows; ++t)
+    for (int t = 0; t < R; ++t)
 #pragma unroll
-      for (int e = 0; e < OC; ++e) o[t][e] = 0.f;
+      for (int e = 0; e < OC / 2; ++e) o[t][e] = make_float2(0.f, 0.f);
+    __syncthreads();
 
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) issue(i, page_of(i));
-    int next_page = page_of(STAGES - 1);
     for (int i = 0; i < n; ++i) {
-      issue(i + STAGES - 1, next_page);
-      next_page = page_of(i + STAGES);
-      cp_async_wait<STAGES - 1>();
+      const int key0 = base(i);
+      cp_async_wait<H - 2>();
       __syncwarp();
-      const int slot = i % STAGES, key0 = base(i);
-      const unsigned char* ks = ring + slot * C::kStage;
-      const unsigned char* vs = ks + BK * C::kRowBytes;
-      const uint32_t there = __ballot_sync(0xffffffffu, (flags >> (STAGES - 1)) & 1u);   // key j's at bit 4 j
+      issue(2 * i + H - 1);
+      const unsigned char* ks = ring + ((2 * i) % H) * C::kHalf + key_lane * C::kRowBytes;
 
-      float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll 8
-      for (int ch = 0; ch < pieces; ++ch) {
-        const float4 k = *reinterpret_cast<const float4*>(ks + key_lane * C::kRowBytes + ((ch ^ key_lane) << 4));
+      float2 acc[KL][2][2];                  // [key][row][half of a piece]: independent chains
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const float4 q = *reinterpret_cast<const float4*>(q_smem + (pair * 2 + t) * C::kQStride + ch * 4);
-          acc[t] = fma2(make_float2(k.x, k.y), make_float2(q.x, q.y), acc[t]);
-          acc[t] = fma2(make_float2(k.z, k.w), make_float2(q.z, q.w), acc[t]);
+      for (int x = 0; x < KL; ++x)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) acc[x][t][0] = acc[x][t][1] = make_float2(0.f, 0.f);
+#pragma unroll 8
+      for (int ch = share; ch < pieces; ch += DS) {
+        float4 q[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) q[t] = *reinterpret_cast<const float4*>(q_smem + (pair * 2 + t) * C::kQStride + ch * 4);
+#pragma unroll
+        for (int x = 0; x < KL; ++x) {
+          const float4 k = *reinterpret_cast<const float4*>(ks + x * 8 * C::kRowBytes + ((ch ^ key_lane) << 4));
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            acc[x][t][0] = fma2(make_float2(k.x, k.y), make_float2(q[t].x, q[t].y), acc[x][t][0]);
+            acc[x][t][1] = fma2(make_float2(k.z, k.w), make_float2(q[t].z, q[t].w), acc[x][t][1]);
+          }
         }
       }
-      const bool whole = there == 0xffffffffu && key0 + BK - 1 <= r.len - a.W && (a.span == 0 || key0 > r.len - 1 - a.span);
-      const int key = key0 + key_lane;
-      bool grew = false;
+      const bool whole = key0 >= r.first && key0 + BK - 1 <= r.len - a.W && (a.span == 0 || key0 > r.len - 1 - a.span);
+      float y[KL][2];
+      bool grows = false, sees[KL][2];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        float y = acc[t].x + acc[t].y;
-        y = a.softcap > 0.f ? cap2 * tanhf(y * inv_cap) : y * scale2;
-        if (a.slopes) y += slope[t] * static_cast<float>(key - pos[t]);
-        const bool seen = whole || (((there >> (4 * key_lane)) & 1) && key <= pos[t] && (a.span == 0 || key > pos[t] - a.span));
-        y = seen ? y : -INFINITY;
-        float top = y;
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-        const float now = fmaxf(m[t], top), from = now == -INFINITY ? 0.f : now;
-        const float f = ex2(m[t] - from);
-        grew |= now > m[t];
-        const float w = ex2(y - from);
-        l[t] = l[t] * f + w;
-        m[t] = now;
-        // a weight of a key that the row does not see is negative zero: its product is left out below
-        weights[key_lane * C::kRows + pair * 2 + t] = seen ? w : -0.f;
-        if (key_lane == 0) factors[pair * 2 + t] = f;
+      for (int x = 0; x < KL; ++x)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int key = key0 + key_lane + 8 * x, p = pos[t];
+          float z = (acc[x][t][0].x + acc[x][t][0].y) + (acc[x][t][1].x + acc[x][t][1].y);
+#pragma unroll
+          for (int d = 1; d < DS; d <<= 1) z += __shfl_xor_sync(0xffffffffu, z, 8 * d);
+          z = a.softcap > 0.f ? cap2 * tanhf(z * inv_cap) : z * scale2;
+          if (a.slopes) z += slope[t] * static_cast<float>(key - p);
+          sees[x][t] = whole || (key >= r.first && key <= p && (a.span == 0 || key > p - a.span));
+          y[x][t] = sees[x][t] ? z : -INFINITY;
+          grows |= y[x][t] > m[t] + kSlack;
+        }
+      const bool rescale = __any_sync(0xffffffffu, grows);
+      if (rescale) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          float top = y[0][t];
+#pragma unroll
+          for (int x = 1; x < KL; ++x) top = fmaxf(top, y[x][t]);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          const float now = fmaxf(m[t], top), f = ex2(m[t] - (now == -INFINITY ? 0.f : now));
+          l[t] *= f;
+          m[t] = now;
+          if (key_lane == 0 && share == 0) factors[pair * 2 + t] = f;
+        }
       }
-      __syncwarp();
-      if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-        for (int t = 0; t < C::kRows; ++t) {
+      for (int x = 0; x < KL; ++x) {
+        float w[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          w[t] = ex2(y[x][t] - (m[t] == -INFINITY ? 0.f : m[t]));
+          l[t] += w[t];
+          // a weight of a key that the row does not see is negative zero: its product is left out below
+          if (!sees[x][t]) w[t] = -0.f;
+        }
+        if (share == 0) *reinterpret_cast<float2*>(weights + (key_lane + 8 * x) * R + pair * 2) = make_float2(w[0], w[1]);
+      }
+
+      cp_async_wait<H - 2>();
+      __syncwarp();
+      issue(2 * i + H);
+      const unsigned char* vs = ring + ((2 * i + 1) % H) * C::kHalf;
+      if (rescale) {
+#pragma unroll
+        for (int t = 0; t < R; ++t) {
           const float f = factors[t];
 #pragma unroll
-          for (int e = 0; e < OC; ++e) o[t][e] *= f;
+          for (int e = 0; e < OC / 2; ++e) o[t][e] = mul2(make_float2(f, f), o[t][e]);
         }
       }
 #pragma unroll
       for (int j = 0; j < BK; ++j) {
-        float v[OC];
+        float2 v[OC / 2];
         const unsigned char* vrow = vs + j * C::kRowBytes;
         if constexpr (OC == 2) {
-          const int ch = lane >> 1;
-          const float2 x = *reinterpret_cast<const float2*>(vrow + ((ch ^ j) << 4) + (lane & 1) * 8);
-          v[0] = x.x; v[1] = x.y;
+          v[0] = *reinterpret_cast<const float2*>(vrow + (((lane >> 1) ^ (j & 7)) << 4) + (lane & 1) * 8);
         } else {
 #pragma unroll
           for (int c = 0; c < OC / 4; ++c) {
-            const float4 x = *reinterpret_cast<const float4*>(vrow + (((lane + 32 * c) ^ j) << 4));
-            v[4 * c] = x.x; v[4 * c + 1] = x.y; v[4 * c + 2] = x.z; v[4 * c + 3] = x.w;
+            const float4 x = *reinterpret_cast<const float4*>(vrow + (((lane + 32 * c) ^ (j & 7)) << 4));
+            v[2 * c] = make_float2(x.x, x.y);
+            v[2 * c + 1] = make_float2(x.z, x.w);
           }
         }
-        const float4 w0 = *reinterpret_cast<const float4*>(weights + j * C::kRows);
-        const float4 w1 = *reinterpret_cast<const float4*>(weights + j * C::kRows + 4);
-        const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-        if (whole) {
-#pragma unroll
-          for (int t = 0; t < C::kRows; ++t)
-#pragma unroll
-            for (int e = 0; e < OC; e += 2) {
-              const float2 x = fma2(make_float2(w[t], w[t]), make_float2(v[e], v[e + 1]), make_float2(o[t][e], o[t][e + 1]));
-              o[t][e] = x.x;
-              o[t][e + 1] = x.y;
-            }
+        float w[R];
+        if constexpr (R == 2) {
+          const float2 x = *reinterpret_cast<const float2*>(weights + j * R);
+          w[0] = x.x; w[1] = x.y;
         } else {
 #pragma unroll
-          for (int t = 0; t < C::kRows; ++t)
-            if (__float_as_uint(w[t]) != 0x80000000u)
-#pragma unroll
-              for (int e = 0; e < OC; ++e) o[t][e] += w[t] * v[e];
+          for (int c = 0; c < R / 4; ++c) {
+            const float4 x = *reinterpret_cast<const float4*>(weights + j * R + 4 * c);
+            w[4 * c] = x.x; w[4 * c + 1] = x.y; w[4 * c + 2] = x.z; w[4 * c + 3] = x.w;
+          }
         }
+#pragma unroll
+        for (int t = 0; t < R; ++t)
+          if (whole || __float_as_uint(w[t]) != 0x80000000u)
+#pragma unroll
+            for (int e = 0; e < OC / 2; ++e) o[t][e] = fma2(make_float2(w[t], w[t]), v[e], o[t][e]);
       }
-      __syncwarp();
     }
 
     cp_async_wait<0>();
@@ -816,96 +912,127 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const AttentionArg
       x += __shfl_xor_sync(0xffffffffu, x, 1);
       x += __shfl_xor_sync(0xffffffffu, x, 2);
       x += __shfl_xor_sync(0xffffffffu, x, 4);
-      if (key_lane == 0) {
-        float* to = sums + (warp * C::kRows + pair * 2 + t) * (DP + 2) + DP;
-        to[0] = m[t];
-        to[1] = x;
-      }
+      if (key_lane == 0 && share == 0)
+        *reinterpret_cast<float2*>(sums + (warp * R + pair * 2 + t) * (DP + 2) + DP) = make_float2(m[t], x);
     }
 #pragma unroll
-    for (int t = 0; t < C::kRows; ++t) {
-      float* to = sums + (warp * C::kRows + t) * (DP + 2);
+    for (int t = 0; t < R; ++t) {
+      float2* to = reinterpret_cast<float2*>(sums + (warp * R + t) * (DP + 2));
       if constexpr (OC == 2) {
-        to[2 * lane] = o[t][0];
-        to[2 * lane + 1] = o[t][1];
+        to[lane] = o[t][0];
       } else {
 #pragma unroll
-        for (int c = 0; c < OC / 4; ++c)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) to[(lane + 32 * c) * 4 + e] = o[t][4 * c + e];
+        for (int c = 0; c < OC / 4; ++c) {
+          to[(lane + 32 * c) * 2] = o[t][2 * c];
+          to[(lane + 32 * c) * 2 + 1] = o[t][2 * c + 1];
+        }
       }
     }
     __syncthreads();
     float* part = nullptr;
     if (n < r.tiles) part = parts + (2 * static_cast<int64_t>(blockIdx.x) + (walk.tile > 0 ? 0 : 1)) * part_floats(C::kRows, a.D);
-    finish_piece<DP, C::kRows, kWarps, BF_OUT>(a, sums, b, hk, row0, rows, part);
+    finish_piece<DP, R, kWarps, BF_OUT>(a, sums, b, hk, row0, rows, part);
+    if (!part && tid == 0) note_whole(a, walk, items, join_blocks, joins);
     piece_done<kWarps * BK>(a, items, walk);
   }
+  if (!noted && tid == 0) note_joins(a, walk, items, join_blocks, joins);      // nothing to do here
 }
 
 // ------------------------------------------------------------------ joining
 
-// Block (c, r): row r of the item that stretch c begins inside, where c is the first to.  Parts c - 1 (its second
-// place) and c, c + 1, .. (their first places) are added in a fixed order: a warp takes every eighth part, then the
-// warps' sums are added.  A chain of loads: the maxima, then the rows, four in flight for each warp.
-constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps;
+// Block (x, r): row r of the item that note_joins left at place x, which stretch c is the first to begin inside.  Parts
+// c - 1 (its second place) and c, c + 1, .. (their first places) are added in a fixed order: a warp takes every eighth part, then the
+// warps' sums are added.
+constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps, kJoinDepth = 4;
 
 template <bool BF_OUT>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttentionArgs a, int row_tiles, int tile_rows,
                                                             const Join* joins, const float* parts) {
-  __shared__ float warp_l[kJoinWarps];
+  __shared__ float2 warp_ml[kJoinWarps];
   __shared__ float4 warp_o[kJoinWarps][64];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 raw = __ldcg(reinterpret_cast<const int4*>(joins) + blockIdx.x);
-  const Join j{raw.x, raw.y, raw.z, 0};
+  const Join j{raw.x, raw.y, raw.z, raw.w};
   if (j.parts == 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int hk = j.item / row_tiles, row0 = (j.item - hk * row_tiles) * tile_rows, r = blockIdx.y;
   if (row0 + r >= a.W * (a.H / a.HK)) return;
   const int64_t stride = part_floats(tile_rows, a.D);
   const auto part_of = [&](int i) {
-    return parts + stride * (i == 0 ? 2 * (static_cast<int64_t>(blockIdx.x) - 1) + 1 : 2 * (static_cast<int64_t>(blockIdx.x) + i - 1));
+    return parts + stride * (i == 0 ? 2 * (static_cast<int64_t>(j.stretch) - 1) + 1 : 2 * (static_cast<int64_t>(j.stretch) + i - 1));
   };
   const auto ml_of = [&](int i) {
     return __ldcg(reinterpret_cast<const float2*>(part_of(i) + static_cast<int64_t>(tile_rows) * a.D) + r);
   };
+  // a lane holds pieces of four channels lane, + 32
   const int pieces = a.D / 4;
   float m = -INFINITY, l = 0.f;
   float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-  for (int i = lane; i < j.parts; i += 32) m = fmaxf(m, ml_of(i).x);
+  for (int i0 = warp; i0 < j.parts; i0 += kJoinWarps * kJoinDepth) {
+    float2 ml[kJoinDepth];
+    float4 x[kJoinDepth][2];
 #pragma unroll
-  for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-  const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
-  for (int i = warp; i < j.parts; i += kJoinWarps) {
-    const float2 ml = ml_of(i);
-    const float4* p = reinterpret_cast<const float4*>(part_of(i) + static_cast<int64_t>(r) * a.D);
-    const float f = ex2(ml.x - base);
-    l += f * ml.y;
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if (lane + 32 * e < pieces) {
-        const float4 x = __ldcg(p + lane + 32 * e);
-        o[e].x += f * x.x;
-        o[e].y += f * x.y;
-        o[e].z += f * x.z;
-        o[e].w += f * x.w;
+    for (int y = 0; y < kJoinDepth; ++y) {
+      const int i = i0 + y * kJoinWarps;
+      ml[y] = make_float2(-INFINITY, 0.f);
+      x[y][0] = x[y][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < j.parts) {
+        ml[y] = ml_of(i);
+        const float4* p = reinterpret_cast<const float4*>(part_of(i) + static_cast<int64_t>(r) * a.D);
+        if (lane < pieces) x[y][0] = __ldcg(p + lane);
+        if (lane + 32 < pieces) x[y][1] = __ldcg(p + lane + 32);
       }
+    }
+    float now = m;
+#pragma unroll
+    for (int y = 0; y < kJoinDepth; ++y) now = fmaxf(now, ml[y].x);
+    const float base = now == -INFINITY ? 0.f : now, f = ex2(m - base);
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      o[e].x *= f;
+      o[e].y *= f;
+      o[e].z *= f;
+      o[e].w *= f;
+    }
+#pragma unroll
+    for (int y = 0; y < kJoinDepth; ++y) {
+      const float g = ex2(ml[y].x - base);
+      l += g * ml[y].y;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        o[e].x += g * x[y][e].x;
+        o[e].y += g * x[y][e].y;
+        o[e].z += g * x[y][e].z;
+        o[e].w += g * x[y][e].w;
+      }
+    }
+    m = now;
   }
-  if (lane == 0) warp_l[warp] = l;
+  if (lane == 0) warp_ml[warp] = make_float2(m, l);
 #pragma unroll
   for (int e = 0; e < 2; ++e)
     if (lane + 32 * e < pieces) warp_o[warp][lane + 32 * e] = o[e];
   __syncthreads();
+  m = -INFINITY;
   l = 0.f;
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) l += warp_l[w];
-  const RowPlace at = row_place(a, j.seq, hk, row0 + r);
-  if (threadIdx.x < a.D) {
-    float x = 0.f;
+  for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, warp_ml[w].x);
+  const float base = m == -INFINITY ? 0.f : m;
+  float f[kJoinWarps];
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) x += reinterpret_cast<const float*>(warp_o[w])[threadIdx.x];
-    store_out<BF_OUT>(a, at.o * a.D + threadIdx.x, l == 0.f ? 0.f : x / l);
+  for (int w = 0; w < kJoinWarps; ++w) {
+    f[w] = ex2(warp_ml[w].x - base);
+    l += f[w] * warp_ml[w].y;
+  }
+  const RowPlace at = row_place(a, j.seq, hk, row0 + r);
+  const int d = 2 * threadIdx.x;
+  if (d < a.D) {
+    float2 x = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w)
+      x = fma2(make_float2(f[w], f[w]), reinterpret_cast<const float2*>(warp_o[w])[threadIdx.x], x);
+    store_out2<BF_OUT>(a, at.o * a.D + d, l == 0.f ? make_float2(0.f, 0.f) : make_float2(x.x / l, x.y / l));
   }
   if (threadIdx.x == 0 && a.lse) a.lse[at.o] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
@@ -918,18 +1045,18 @@ struct Variant {
   int rows, ctas;                            // rows of a tile, CTAs an SM
 };
 Variant variant_of(bool bf16, int D, int rows) {
-  if (!bf16) return Variant{8, D <= 64 ? 4 : D <= 128 ? 3 : 1};
+  if (!bf16) return Variant{rows > 4 ? 8 : rows > 2 ? 4 : 2, D > 64 ? 2 : 3};
   return Variant{rows > 16 ? 32 : rows > 8 ? 16 : 8, D > 128 ? 2 : 3};
 }
 
 int stretches_of(const Variant& v) { return std::min(kMaxStretches, sm_count() * v.ctas); }
 
 template <auto K, typename Config>
-cudaError_t run(const AttentionArgs& a, int row_tiles, int stretches, Join* joins, float* parts, cudaStream_t st) {
+cudaError_t run(const AttentionArgs& a, int row_tiles, int stretches, int join_blocks, Join* joins, float* parts, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = raise_smem(K, Config::kSmem, done);
   if (e != cudaSuccess) return e;
-  K<<<stretches, kThreads, Config::kSmem, st>>>(a, FastDiv(a.P), row_tiles, joins, parts);
+  K<<<stretches, kThreads, Config::kSmem, st>>>(a, FastDiv(a.P), row_tiles, join_blocks, joins, parts);
   return cudaGetLastError();
 }
 
@@ -941,25 +1068,25 @@ cudaError_t launch(const AttentionArgs& a, bool bf16, cudaStream_t st) {
   Join* joins = static_cast<Join*>(a.workspace);
   float* parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kMaxStretches * sizeof(Join));
   cudaError_t e;
-  const auto bf16_of = [&](auto dp) {
+  const int join_blocks = static_cast<int>(std::min<int64_t>(n, static_cast<int64_t>(a.B) * a.HK * tiles));
+  const auto of_width = [&](auto dp) {
     constexpr int DP = decltype(dp)::value;
-    if (v.rows == 8) return run<attend_bf16_kernel<DP, 1, BF_OUT>, Mma<DP, 1>>(a, tiles, n, joins, parts, st);
-    if (v.rows == 16) return run<attend_bf16_kernel<DP, 2, BF_OUT>, Mma<DP, 2>>(a, tiles, n, joins, parts, st);
-    return run<attend_bf16_kernel<DP, 4, BF_OUT>, Mma<DP, 4>>(a, tiles, n, joins, parts, st);
+    if (bf16) {
+      if (v.rows == 8) return run<attend_bf16_kernel<DP, 1, BF_OUT>, Mma<DP, 1>>(a, tiles, n, join_blocks, joins, parts, st);
+      if (v.rows == 16) return run<attend_bf16_kernel<DP, 2, BF_OUT>, Mma<DP, 2>>(a, tiles, n, join_blocks, joins, parts, st);
+      return run<attend_bf16_kernel<DP, 4, BF_OUT>, Mma<DP, 4>>(a, tiles, n, join_blocks, joins, parts, st);
+    }
+    if (v.rows == 2) return run<attend_f32_kernel<DP, 2, BF_OUT>, Simt<DP, 2>>(a, tiles, n, join_blocks, joins, parts, st);
+    if (v.rows == 4) return run<attend_f32_kernel<DP, 4, BF_OUT>, Simt<DP, 4>>(a, tiles, n, join_blocks, joins, parts, st);
+    return run<attend_f32_kernel<DP, 8, BF_OUT>, Simt<DP, 8>>(a, tiles, n, join_blocks, joins, parts, st);
   };
-  if (bf16) {
-    e = a.D <= 64    ? bf16_of(std::integral_constant<int, 64>{})
-        : a.D <= 128 ? bf16_of(std::integral_constant<int, 128>{})
-                     : bf16_of(std::integral_constant<int, 256>{});
-  } else {
-    if (a.D <= 64) e = run<attend_f32_kernel<64, 3, BF_OUT>, Simt<64, 3>>(a, tiles, n, joins, parts, st);
-    else if (a.D <= 128) e = run<attend_f32_kernel<128, 2, BF_OUT>, Simt<128, 2>>(a, tiles, n, joins, parts, st);
-    else e = run<attend_f32_kernel<256, 3, BF_OUT>, Simt<256, 3>>(a, tiles, n, joins, parts, st);
-  }
+  e = a.D <= 64    ? of_width(std::integral_constant<int, 64>{})
+      : a.D <= 128 ? of_width(std::integral_constant<int, 128>{})
+                   : of_width(std::integral_constant<int, 256>{});
   if (e != cudaSuccess) return e;
   // launched while the stretches still run: its blocks wait for them on the device
   cudaLaunchConfig_t config = {};
-  config.gridDim = dim3(n, std::min(v.rows, rows));
+  config.gridDim = dim3(join_blocks, std::min(v.rows, rows));
   config.blockDim = dim3(kJoinThreads);
   config.stream = st;
   cudaLaunchAttribute attribute;
