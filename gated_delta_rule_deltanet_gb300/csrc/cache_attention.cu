@@ -870,9 +870,8 @@ __global__ void __launch_bounds__(kThreads, Simt<DP, R>::kCtas)
           for (int e = 0; e < OC / 2; ++e) o[t][e] = mul2(make_float2(f, f), o[t][e]);
         }
       }
-#pragma unroll
-      for (int j = 0; j < BK; ++j) {
-        float2 v[OC / 2];
+      // key j's values and weights
+      const auto fetch = [&](int j, float2 (&v)[OC / 2], float (&w)[R]) {
         const unsigned char* vrow = vs + j * C::kRowBytes;
         if constexpr (OC == 2) {
           v[0] = *reinterpret_cast<const float2*>(vrow + (((lane >> 1) ^ (j & 7)) << 4) + (lane & 1) * 8);
@@ -884,7 +883,6 @@ __global__ void __launch_bounds__(kThreads, Simt<DP, R>::kCtas)
             v[2 * c + 1] = make_float2(x.z, x.w);
           }
         }
-        float w[R];
         if constexpr (R == 2) {
           const float2 x = *reinterpret_cast<const float2*>(weights + j * R);
           w[0] = x.x; w[1] = x.y;
@@ -895,11 +893,34 @@ __global__ void __launch_bounds__(kThreads, Simt<DP, R>::kCtas)
             w[4 * c] = x.x; w[4 * c + 1] = x.y; w[4 * c + 2] = x.z; w[4 * c + 3] = x.w;
           }
         }
+      };
+      if (whole) {
 #pragma unroll
-        for (int t = 0; t < R; ++t)
-          if (whole || __float_as_uint(w[t]) != 0x80000000u)
+        for (int j = 0; j < BK; ++j) {
+          float2 v[OC / 2];
+          float w[R];
+          fetch(j, v, w);
+#pragma unroll
+          for (int t = 0; t < R; ++t)
 #pragma unroll
             for (int e = 0; e < OC / 2; ++e) o[t][e] = fma2(make_float2(w[t], w[t]), v[e], o[t][e]);
+        }
+      } else {
+#pragma unroll 1
+        for (int j = 0; j < BK; ++j) {
+          float2 v[OC / 2];
+          float w[R];
+          fetch(j, v, w);
+#pragma unroll
+          for (int t = 0; t < R; ++t) {
+            const bool left_out = __float_as_uint(w[t]) == 0x80000000u;
+#pragma unroll
+            for (int e = 0; e < OC / 2; ++e) {
+              const float2 x = fma2(make_float2(w[t], w[t]), v[e], o[t][e]);
+              o[t][e] = left_out ? o[t][e] : x;
+            }
+          }
+        }
       }
     }
 
