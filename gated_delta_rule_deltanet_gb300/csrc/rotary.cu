@@ -23,15 +23,19 @@ namespace kda {
 
 namespace {
 
-constexpr int kThreads = 256, kUnroll = 4;
+constexpr int kThreads = 256, kUnroll = 4, kRounds = 2;
 constexpr int kMaxTokens = 16;               // of one block
 constexpr int kTableBytes = 16384;           // its sines and cosines
 
 struct Shape {                               // of the launch
   FastDiv slots, rows;                       // slots of a row, rows of a token
-  int32_t pair_slots;                        // slots that turn; the rest copy
+  int32_t pair_slots;                        // of pairs (i, i + R/2); the rest pass
   int32_t tokens;                            // of a block
 };
+
+// Place of pair i's sine: sixteen bytes more every eight pairs, so that lanes with neighbouring slots read other banks.
+__host__ __device__ constexpr int sine_at(int i) { return i + (i >> 3) * 2; }
+__host__ __device__ constexpr int sine_pitch(int half_r) { return (sine_at(half_r) + 1) & ~1; }
 
 // VE consecutive elements as loaded
 template <bool BF, int VE>
@@ -97,46 +101,92 @@ __device__ __forceinline__ float2 turned(int64_t p, uint64_t turn, float m) {
   return make_float2(m * c, m * s);
 }
 
-// the sequence that holds token t: the last one whose first token is at most t
+// The sequence that holds token t: the last one whose first token is at most t.  A warp looks at 32 at a time.
 __device__ __forceinline__ int sequence_of(const uint32_t* offsets, int B, int64_t t) {
-  int lo = 0, hi = B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (static_cast<int64_t>(offsets[mid]) <= t) lo = mid;
-    else hi = mid - 1;
+  int lo = 0, n = B;                         // it is among n from lo on
+  while (n > 1) {
+    const int stride = (n + 31) / 32, at = static_cast<int>(threadIdx.x & 31) * stride;
+    const bool before = at < n && static_cast<int64_t>(offsets[lo + at]) <= t;
+    const int k = max(0, __popc(__ballot_sync(0xffffffffu, before)) - 1) * stride;
+    lo += k;
+    n = min(stride, n - k);
   }
   return lo;
 }
 
 enum { kSkipQ = 1, kSkipKV = 2 };
 
-// HALF: pairs (i, i + R/2), a slot being VE of the first halves with their partners; otherwise pairs
-// (2i, 2i + 1), a slot being max(VE, 2) consecutive elements.  A slot is read whole before it is written, and no other
-// thread touches it, so the outputs may be the inputs.
+// A slot is two vectors of VE elements of a row: of pairs (i, i + R/2) (HALF) VE first halves and their partners, otherwise,
+// and of the channels that pass, two behind one another.  A thread has one slot of the row and goes through the rows
+// (of all heads, of all tokens of the block); a slot is read whole before it is written, and no other thread touches it, so
+// the outputs may be the inputs.  Its first slots are loaded before the sines are formed, its next ones before it comes to them.
 template <bool BF, int VE, bool HALF>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, const Shape sh) {
-  constexpr int kSpan = HALF ? VE : (VE < 2 ? 2 : VE);   // elements of a turning slot (of each half)
-  constexpr int kVecs = HALF ? 2 : kSpan / VE;           // vectors of a turning slot
-  extern __shared__ float2 sines[];                      // [tokens][R / 2]
+__global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryArgs a, const Shape sh) {
+  extern __shared__ __align__(16) float2 sines[];        // [tokens][sine_pitch]
   __shared__ int64_t position[kMaxTokens], page_at[kMaxTokens];
   __shared__ int32_t skip[kMaxTokens];
-  const int half_r = a.R / 2;
+  const int half_r = a.R / 2, pitch = sine_pitch(half_r), slots = sh.slots.d, rows = sh.rows.d;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * sh.tokens;
   const int tokens = static_cast<int>(min(static_cast<int64_t>(sh.tokens), a.T - t0));
-  const uint32_t per_token = sh.slots.d * sh.rows.d, units = per_token * tokens;
+  // rows that the block's threads take at a time, and this thread's slot and first row
+  const int at_once = max(1, kThreads / slots), all_rows = tokens * rows, step = at_once * gridDim.y;
+  const int lane_row = sh.slots.div(threadIdx.x);
+  int slot = threadIdx.x - lane_row * slots;
+  const int row0 = slots > kThreads || lane_row < at_once ? static_cast<int>(blockIdx.y) * at_once + lane_row : all_rows;
 
-  if (threadIdx.x < tokens) {
-    const int64_t t = t0 + threadIdx.x;
+  Vec<BF, VE> x[kUnroll][2];
+  int token[kUnroll], row[kUnroll];                      // row counts through the heads of q, k and v
+  int first, second;                                     // where the slot's vectors begin
+  const auto place = [&]() {
+    if (HALF && slot < sh.pair_slots) {
+      first = slot * VE;
+      second = first + half_r;
+    } else {
+      first = (HALF ? a.R : 0) + (slot - (HALF ? sh.pair_slots : 0)) * 2 * VE;
+      second = first + VE;
+    }
+  };
+  const auto load = [&](int r0) {
+#pragma unroll
+    for (int n = 0; n < kUnroll; ++n) {
+      const int r = r0 + n * step;
+      token[n] = -1;
+      if (r >= all_rows) continue;
+      token[n] = static_cast<int>(sh.rows.div(r));
+      row[n] = r - token[n] * rows;
+      const int64_t t = t0 + token[n];
+      const void* from = a.q;
+      int64_t at = t * a.q_stride + row[n] * a.D;
+      if (row[n] >= a.H) {
+        from = a.k;
+        at = t * a.k_stride + (row[n] - a.H) * a.D;
+        if (row[n] >= a.H + a.HK) {
+          from = a.v;
+          at = t * a.v_stride + (row[n] - a.H - a.HK) * a.D;
+        }
+      }
+      x[n][0].load(from, at + first);
+      if (second < a.D) x[n][1].load(from, at + second);
+    }
+  };
+  place();
+  int r0 = row0;
+  load(r0);
+
+  // a warp takes a token
+  for (int j = threadIdx.x >> 5; j < tokens; j += kThreads / 32) {
+    const int64_t t = t0 + j;
     int64_t p = 0, at = 0;
     int sk = 0;
     if (a.table) {
       int s = static_cast<int>(t);
       int64_t bos = t, eos = t + 1;
       if (a.offsets) {
+        const int64_t zero = a.offsets[0], end = a.offsets[a.B];
         s = sequence_of(a.offsets, a.B, t);
         bos = a.offsets[s];
         eos = a.offsets[s + 1];
-        if (bos > t || static_cast<int64_t>(a.offsets[a.B]) > a.T || a.offsets[0] != 0) {
+        if (bos > t || end > a.T || zero != 0) {
           raise_device_error(a.err, KDA_DEVERR_OFFSETS);
           eos = 0;
         }
@@ -158,77 +208,49 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, co
     } else {
       p = a.wide ? static_cast<const int64_t*>(a.positions)[t] : static_cast<const int32_t*>(a.positions)[t];
     }
-    position[threadIdx.x] = p;
-    page_at[threadIdx.x] = at;
-    skip[threadIdx.x] = sk;
+    if ((threadIdx.x & 31) == 0) {
+      position[j] = p;
+      page_at[j] = at;
+      skip[j] = sk;
+    }
   }
   __syncthreads();
   if (a.freq) {
-    for (int i = threadIdx.x; i < half_r; i += kThreads) {
-      const double x = a.freq[i] * 0.15915494309189533577;     // turns per position: 1 / 2 pi
-      const double fraction = x - floor(x);
+    // a thread keeps its pair and goes through the tokens
+    const int per = kThreads / max(1, min(half_r, kThreads)), share = threadIdx.x / max(1, half_r);
+    for (int i = half_r < kThreads ? threadIdx.x - share * half_r : threadIdx.x; i < half_r && share < per; i += kThreads) {
+      const double turns = a.freq[i] * 0.15915494309189533577;     // per position: 1 / 2 pi
+      const double fraction = turns - floor(turns);
       // fraction < 1, but its product with 2^64 may round up to 2^64, a whole turn
       const uint64_t turn = fraction * 0x1p64 >= 0x1p64 ? 0 : static_cast<uint64_t>(fraction * 0x1p64);
-      for (int j = 0; j < tokens; ++j) {
+      for (int j = share; j < tokens; j += per) {
         float2 cs = turned(position[j], turn, a.magnitude);
         if (a.transpose) cs.y = -cs.y;
-        sines[j * half_r + i] = cs;
+        sines[j * pitch + sine_at(i)] = cs;
       }
     }
     __syncthreads();
   }
 
-  const uint32_t step = kThreads * gridDim.y;
-  for (uint32_t u0 = blockIdx.y * kThreads + threadIdx.x; u0 < units; u0 += step * kUnroll) {
-    Vec<BF, VE> x[kUnroll][kVecs];
-    void* out[kUnroll];
-    int64_t to[kUnroll];
-    int token[kUnroll], slot[kUnroll];
-#pragma unroll
-    for (int n = 0; n < kUnroll; ++n) {
-      const uint32_t u = u0 + n * step;
-      out[n] = nullptr;
-      if (u >= units) continue;
-      const uint32_t row_of_all = sh.slots.div(u);
-      slot[n] = static_cast<int>(u - row_of_all * sh.slots.d);
-      token[n] = static_cast<int>(sh.rows.div(row_of_all));
-      int row = static_cast<int>(row_of_all - token[n] * sh.rows.d);
-      const int64_t t = t0 + token[n];
-      const void* from;
-      int64_t at;
-      if (row < a.H) {
-        if (skip[token[n]] & kSkipQ) continue;
-        from = a.q;
-        at = t * a.q_stride + row * a.D;
-        out[n] = a.q_out;
-        to[n] = t * a.q_out_stride + row * a.D;
-      } else {
-        if (skip[token[n]] & kSkipKV) continue;
-        row -= a.H;
-        const bool value = row >= a.HK;
-        if (value) row -= a.HK;
-        from = value ? a.v : a.k;
-        at = t * (value ? a.v_stride : a.k_stride) + row * a.D;
-        out[n] = value ? a.v_out : a.k_out;
-        to[n] = a.table ? page_at[token[n]] + row * a.page_head_stride : t * a.k_out_stride + row * a.D;
-        if (value) slot[n] |= 1 << 30;       // passes whole
-      }
-      const int s = slot[n] & ~(1 << 30);
-      const int first = s < sh.pair_slots ? s * kSpan : a.R + (s - sh.pair_slots) * VE;
-      at += first;
-      to[n] += first;
-      x[n][0].load(from, at);
-      if (s < sh.pair_slots && kVecs == 2) x[n][kVecs - 1].load(from, at + (HALF ? half_r : VE));
+  while (true) {
+    if (r0 >= all_rows) {                    // rows of more slots than threads: the next slot
+      slot += kThreads;
+      if (slots <= kThreads || slot >= slots) break;
+      place();
+      r0 = row0;
+      load(r0);
+      continue;
     }
+    // turn what is loaded
+    const bool turns = a.freq && (HALF ? slot < sh.pair_slots : first < a.R);
+    if (turns) {
+      const float2* at = sines + sine_at(HALF ? first : first / 2);
 #pragma unroll
-    for (int n = 0; n < kUnroll; ++n) {
-      if (!out[n]) continue;
-      const bool turns = slot[n] < sh.pair_slots && a.freq;
-      const int s = slot[n] & ~(1 << 30);
-      if (turns) {
-        const float2* cs = sines + token[n] * half_r + (HALF ? s * VE : s * kSpan / 2);
+      for (int n = 0; n < kUnroll; ++n) {
+        if (token[n] < 0 || row[n] >= a.H + a.HK) continue;
+        const float2* cs = at + token[n] * pitch;
+        float y0[VE], y1[VE];
         if constexpr (HALF) {
-          float y0[VE], y1[VE];
 #pragma unroll
           for (int e = 0; e < VE; ++e) {
             const float c = cs[e].x, d = cs[e].y, f = x[n][0].f32(e), g = x[n][1].f32(e);
@@ -239,47 +261,73 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, co
           x[n][1].set(y1);
         } else if constexpr (VE == 1) {
           const float c = cs[0].x, d = cs[0].y, f = x[n][0].f32(0), g = x[n][1].f32(0);
-          const float y0[1] = {f * c - g * d}, y1[1] = {g * c + f * d};
+          y0[0] = f * c - g * d;
+          y1[0] = g * c + f * d;
           x[n][0].set(y0);
           x[n][1].set(y1);
         } else {
-          float y[VE];
+          // pairs from R / 2 on pass, and may share a vector with ones that do not
 #pragma unroll
           for (int e = 0; e < VE; e += 2) {
-            const float c = cs[e / 2].x, d = cs[e / 2].y, f = x[n][0].f32(e), g = x[n][0].f32(e + 1);
-            y[e] = f * c - g * d;
-            y[e + 1] = g * c + f * d;
+            const float f = x[n][0].f32(e), g = x[n][0].f32(e + 1);
+            const bool on = first + e < a.R;
+            const float c = on ? cs[e / 2].x : 1.f, d = on ? cs[e / 2].y : 0.f;
+            y0[e] = on ? f * c - g * d : f;
+            y0[e + 1] = on ? g * c + f * d : g;
           }
-          x[n][0].set(y);
+          x[n][0].set(y0);
+#pragma unroll
+          for (int e = 0; e < VE; e += 2) {
+            const float f = x[n][1].f32(e), g = x[n][1].f32(e + 1);
+            const bool on = second + e < a.R;
+            const float c = on ? cs[(VE + e) / 2].x : 1.f, d = on ? cs[(VE + e) / 2].y : 0.f;
+            y1[e] = on ? f * c - g * d : f;
+            y1[e + 1] = on ? g * c + f * d : g;
+          }
+          x[n][1].set(y1);
         }
       }
-      x[n][0].store(out[n], to[n]);
-      if (s < sh.pair_slots && kVecs == 2) x[n][kVecs - 1].store(out[n], to[n] + (HALF ? half_r : VE));
     }
+#pragma unroll
+    for (int n = 0; n < kUnroll; ++n) {
+      if (token[n] < 0) continue;
+      const int64_t t = t0 + token[n];
+      const bool query = row[n] < a.H, value = row[n] >= a.H + a.HK;
+      if (skip[token[n]] & (query ? kSkipQ : kSkipKV)) continue;
+      const int head = row[n] - (query ? 0 : a.H) - (value ? a.HK : 0);
+      void* out = query ? a.q_out : value ? a.v_out : a.k_out;
+      const int64_t to = query     ? t * a.q_out_stride + head * a.D
+                         : a.table ? page_at[token[n]] + head * a.page_head_stride
+                                   : t * a.k_out_stride + head * a.D;
+      x[n][0].store(out, to + first);
+      if (second < a.D) x[n][1].store(out, to + second);
+    }
+    r0 += step * kUnroll;
+    if (r0 < all_rows) load(r0);
   }
 }
 
 template <bool BF, int VE, bool HALF>
 cudaError_t launch(const RotaryArgs& a, cudaStream_t st) {
-  constexpr int kSpan = HALF ? VE : (VE < 2 ? 2 : VE);
   Shape sh;
-  sh.pair_slots = (HALF ? a.R / 2 : a.R) / kSpan;
-  const int rows = a.H + a.HK + a.HV;
-  const int slots = sh.pair_slots + (a.D - a.R) / VE;
+  const auto slots_of = [](int elements) { return (elements + 2 * VE - 1) / (2 * VE); };
+  sh.pair_slots = HALF ? a.R / 2 / VE : 0;
+  const int rows = a.H + a.HK + a.HV, slots = HALF ? sh.pair_slots + slots_of(a.D - a.R) : slots_of(a.D);
   sh.slots = FastDiv(slots);
   sh.rows = FastDiv(rows);
   const int64_t per_token = static_cast<int64_t>(rows) * slots;
-  // About two rounds of kUnroll slots for each thread (rows loaded while others are stored), fewer tokens where
-  // that would leave SMs without a block, and no more sines than fit.
-  int64_t n = std::min<int64_t>(kMaxTokens, std::max<int64_t>(1, 2 * kUnroll * kThreads / per_token));
-  n = std::min<int64_t>(n, std::max<int64_t>(1, a.T / (2 * sm_count())));
-  if (a.R) n = std::min<int64_t>(n, std::max<int64_t>(1, kTableBytes / (a.R / 2 * static_cast<int64_t>(sizeof(float2)))));
+  // About kRounds rounds of kUnroll slots for each thread, fewer tokens where that would leave SMs without a block,
+  // and no more sines than fit.
+  int64_t n = std::min<int64_t>(kMaxTokens, std::max<int64_t>(1, kRounds * kUnroll * kThreads / per_token));
+  n = std::min<int64_t>(n, std::max<int64_t>(1, a.T / (8 * sm_count())));
+  if (a.R)
+    n = std::min<int64_t>(n, std::max<int64_t>(1, kTableBytes / (sine_pitch(a.R / 2) * static_cast<int64_t>(sizeof(float2)))));
   sh.tokens = static_cast<int32_t>(n);
   const int64_t blocks = (a.T + n - 1) / n;
   // few tokens: their heads are shared out to several blocks, each forming the sines for itself
   const int64_t split = std::max<int64_t>(
       1, std::min<int64_t>((n * per_token + kThreads - 1) / kThreads, 2 * sm_count() / blocks));
-  const size_t smem = a.freq ? n * (a.R / 2) * sizeof(float2) : 0;
+  const size_t smem = a.freq ? n * sine_pitch(a.R / 2) * sizeof(float2) : 0;
   rotary_kernel<BF, VE, HALF><<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(split)), kThreads, smem, st>>>(a, sh);
   return cudaGetLastError();
 }
@@ -292,9 +340,9 @@ cudaError_t launch_layout(const RotaryArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_rotary(const RotaryArgs& a, bool bf16, cudaStream_t st) {
-  // the widest vectors that every row, half row and tail starts on
+  // the widest vectors that every row and, of pairs (i, i + R/2), each half starts on
   const uint64_t esz = bf16 ? 2 : 4;
-  uint64_t bits = static_cast<uint64_t>(a.D) | (a.interleaved ? a.R : a.R / 2) | a.q_stride | a.k_stride | a.v_stride |
+  uint64_t bits = static_cast<uint64_t>(a.D) | (a.interleaved ? 0 : a.R / 2) | a.q_stride | a.k_stride | a.v_stride |
                   a.q_out_stride | a.k_out_stride;
   if (a.table) bits |= a.page_stride | a.page_row_stride | a.page_head_stride;
   for (const void* p : {a.q, a.k, a.v, static_cast<const void*>(a.q_out), static_cast<const void*>(a.k_out),

@@ -695,7 +695,7 @@ typedef struct kda_cache_params {
  *
  *   q [T, H, d] or NULL (H = 0)     k, v [T, HK, d]
  *   input_row_offsets [B + 1], or NULL: one token per sequence (T = B).  Tokens from its last entry on
- *   belong to no sequence; nothing of them is read or written
+ *   belong to no sequence; nothing of them is written
  *   frequencies [R / 2] or NULL (R = 0)      q_out [T, H, d], may be q
  *   start [B] tokens already in the cache
  * The pages of the new positions must be in the table.  A page row that two tokens are given races.
