@@ -75,15 +75,37 @@ __device__ __forceinline__ int pages_of(int len, int P, int width) {
   return n <= width ? n : -1;
 }
 
+// One new row: where it goes on from and what it keeps.
+struct Row {
+  int parent, kept, full, want, end;         // full pages kept; pages of the new row and of its parent (-1: too many)
+};
+__device__ __forceinline__ Row row_of(const RowsArgs& a, int i) {
+  Row r;
+  r.parent = a.parent ? a.parent[i] : i;
+  const int len = a.new_lens[i];
+  const bool from = r.parent >= 0 && r.parent < a.S;
+  const int old = from ? a.lens[r.parent] : 0;
+  r.kept = max(0, min(old, len));
+  r.full = r.kept / a.P;
+  r.want = r.parent < a.S ? pages_of(len, a.P, a.width) : -1;
+  r.end = pages_of(old, a.P, a.width);
+  return r;
+}
+
+constexpr int kAhead = 8;                    // entries of a row that a lane loads before it uses the first
+
 // Scratch of an update (int32): [N] counts, [N] first open row, [N] free pages in order, [S_out] pages that a row
 // keeps (its open one included), [S_out] its place among the fresh pages, words of the launch: 0 the error,
 // 1 copies in all, 8.. the CTAs' free pages.
+//
+// Each pass is a few dependent loads deep; what a pass needs of the rows and tables is loaded ahead of the barrier
+// before it where that barrier does not order it.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) update_kernel(const RowsArgs a) {
   __shared__ int warp_sums[32];
   __shared__ int64_t warp_sums64[32];
   __shared__ int stop;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x;
-  const int all = kCluster * kThreads, me = rank * kThreads + tid;
+  const int all = kCluster * kThreads, me = rank * kThreads + tid, my_row = warp * kCluster + rank, rows_at_once = kCluster * kWarps;
   int32_t* counts = a.scratch;
   int32_t* first = counts + a.N;
   int32_t* free_list = first + a.N;
@@ -91,10 +113,12 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
   int32_t* place = have + a.S_out;
   int32_t* words = place + a.S_out;
   const Segment seg = segment(a.N, rank);
+  const auto in_pool = [&](int q) { return static_cast<uint32_t>(q) < static_cast<uint32_t>(a.N); };
 
   // 1. references as they are; free pages of the CTA
   if (rank == 0 && tid == 0) words[0] = 0;
   int mine = 0, total;
+#pragma unroll 4
   for (int q = seg.begin + tid; q < seg.end; q += kThreads) {
     const int r = a.refs[q];
     counts[q] = r;
@@ -104,6 +128,15 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
       a.out_refs[q] = 0;
     }
   }
+  // the rows that this warp, and in the first CTA this thread, comes to first
+  Row mine_row = my_row < a.S_out ? row_of(a, my_row) : Row{};
+  Row thread_row = rank == 0 && tid < a.S_out ? row_of(a, tid) : Row{};
+  int thread_open = -1;                      // the page that the thread's row ends inside
+  const auto open_of = [&](const Row& r) {
+    const bool ok = r.parent >= 0 && r.parent < a.S && r.kept % a.P != 0 && r.full < a.width;
+    return ok ? a.table[static_cast<int64_t>(r.parent) * a.width + r.full] : -1;
+  };
+  if (rank == 0 && tid < a.S_out) thread_open = open_of(thread_row);
   block_scan(mine, warp_sums, total);
   if (tid == 0) words[8 + rank] = total;
   cluster_sync();
@@ -111,47 +144,52 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
   // 2. references of the old rows taken back, of the new rows' full pages added; a warp takes a row.  A row that goes
   // on from itself keeps its full pages: nothing to count.
   const auto fault = [&]() { atomicExch(words, 1); };
-  const auto kept_of = [&](int i, int& p) {
-    p = a.parent ? a.parent[i] : i;
-    return p < 0 || p >= a.S ? 0 : max(0, min(a.lens[p], a.new_lens[i]));
-  };
-  for (int r = rank * kWarps + warp; r < a.S; r += kCluster * kWarps) {
+  for (int r = my_row; r < a.S; r += rows_at_once) {
     const int n = pages_of(a.lens[r], a.P, a.width);
     if (n < 0) {
       if (lane == 0) fault();
       continue;
     }
-    int skip = 0, p;
+    int skip = 0;
     if (r < a.S_out) {
-      const int kept = kept_of(r, p);
-      if (p == r) skip = kept / a.P;
+      const Row own = r == my_row ? mine_row : row_of(a, r);
+      if (own.parent == r) skip = own.full;
     }
-    for (int j = lane; j < n; j += 32) {
-      const int q = a.table[static_cast<int64_t>(r) * a.width + j];
-      if (q == -1) continue;                 // a page that the row has given back
-      if (static_cast<uint32_t>(q) >= static_cast<uint32_t>(a.N)) fault();
-      else if (j >= skip) atomicSub(counts + q, 1);
-      else if (a.refs[q] <= 0) fault();
+    const int32_t* row = a.table + static_cast<int64_t>(r) * a.width;
+    for (int j0 = lane; j0 < n; j0 += 32 * kAhead) {
+      int q[kAhead];
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) q[x] = j0 + 32 * x < n ? row[j0 + 32 * x] : -1;
+      int bad = 0;
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        if (q[x] == -1) continue;            // a page that the row has given back
+        if (!in_pool(q[x])) bad = 1;
+        else if (j0 + 32 * x >= skip) atomicSub(counts + q[x], 1);
+        else bad |= a.refs[q[x]] <= 0;
+      }
+      if (bad) fault();
     }
   }
-  for (int i = rank * kWarps + warp; i < a.S_out; i += kCluster * kWarps) {
-    int p;
-    const int kept = kept_of(i, p), full = kept / a.P;
-    if (p >= a.S || pages_of(a.new_lens[i], a.P, a.width) < 0 || (p >= 0 && pages_of(a.lens[p], a.P, a.width) < 0)) {
+  for (int i = my_row; i < a.S_out; i += rows_at_once) {
+    const Row r = i == my_row ? mine_row : row_of(a, i);
+    if (r.want < 0 || r.end < 0) {
       if (lane == 0) fault();
       continue;
     }
-    if (p < 0) continue;
-    const int32_t* row = a.table + static_cast<int64_t>(p) * a.width;
-    for (int j = (p == i ? full : 0) + lane; j < full; j += 32) {
-      const int q = row[j];
-      if (q == -1) continue;
-      if (static_cast<uint32_t>(q) < static_cast<uint32_t>(a.N)) atomicAdd(counts + q, 1);
-      else fault();
+    if (r.parent < 0) continue;
+    const int32_t* row = a.table + static_cast<int64_t>(r.parent) * a.width;
+    for (int j0 = (r.parent == i ? r.full : 0) + lane; j0 < r.full; j0 += 32 * kAhead) {
+      int q[kAhead];
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) q[x] = j0 + 32 * x < r.full ? row[j0 + 32 * x] : -1;
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x)
+        if (in_pool(q[x])) atomicAdd(counts + q[x], 1);          // one that is not is found with its old row
     }
-    if (lane == 0 && kept % a.P != 0) {
-      const int q = row[full];
-      if (static_cast<uint32_t>(q) < static_cast<uint32_t>(a.N)) atomicMin(first + q, i);
+    if (lane == 0 && r.kept % a.P != 0) {
+      const int q = row[r.full];
+      if (in_pool(q)) atomicMin(first + q, i);
       else fault();
     }
   }
@@ -159,6 +197,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
 
   // 3. the free pages in order; a page in use whose count went below zero was held more often than refs say
   int before = 0, free_pages = 0;
+#pragma unroll
   for (int c = 0; c < kCluster; ++c) {
     const int n = __ldcg(words + 8 + c);
     if (c < rank) before += n;
@@ -172,7 +211,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
     if (r == 0) free_list[before + at] = q;
     before += total;
   }
-  // and the rows' needs, by the first CTA.  The lists of copies begin empty.
+  // and the rows' needs, by the first CTA
   if (rank == 0) {
     int64_t fresh = 0, sum;                  // in 64 bits: rows may ask for more than there is
     int copies = 0;
@@ -180,12 +219,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
     for (int i0 = 0; i0 < a.S_out; i0 += kThreads) {
       const int i = i0 + tid;
       int need = 0, copy = 0, hold = 0, open = -1;
-      if (i < a.S_out && __ldcg(words) == 0) {
-        int p;
-        const int kept = kept_of(i, p);
-        hold = kept / a.P;
-        if (kept % a.P != 0) {
-          open = a.table[static_cast<int64_t>(p) * a.width + hold];
+      if (i < a.S_out) {
+        const Row r = i0 == 0 ? thread_row : row_of(a, i);
+        open = i0 == 0 ? thread_open : open_of(r);
+        hold = r.full;
+        if (in_pool(open)) {
           if (__ldcg(first + open) == i && __ldcg(counts + open) == 0) {
             counts[open] = 1;                // no other row looks at it: each has another first row or finds this one's
             ++hold;
@@ -193,7 +231,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
             copy = 1;
           }
         }
-        need = pages_of(a.new_lens[i], a.P, a.width) - hold;
+        need = max(0, r.want - hold);
       }
       const int64_t at = block_scan(static_cast<int64_t>(need), warp_sums64, sum) - need + fresh;
       fresh += sum;
@@ -229,6 +267,31 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
     }
     return;
   }
+  for (int i = my_row; i < a.S_out; i += rows_at_once) {
+    const Row r = i == my_row ? mine_row : row_of(a, i);
+    const int hold = __ldcg(have + i), at = __ldcg(place + i);
+    const int32_t* row = a.table + static_cast<int64_t>(max(r.parent, 0)) * a.width;
+    int32_t* out = a.out_table + static_cast<int64_t>(i) * a.width;
+    for (int j0 = lane; j0 < a.width; j0 += 32 * kAhead) {
+      int q[kAhead];
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        const int j = j0 + 32 * x;
+        q[x] = j < hold ? row[j] : j < r.want ? __ldcg(free_list + at + j - hold) : -1;
+      }
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        const int j = j0 + 32 * x;
+        if (j >= hold && j < r.want) a.out_refs[q[x]] = 1;
+        if (j < a.width) out[j] = q[x];
+      }
+    }
+    if (lane == 0) {
+      a.out_lens[i] = a.new_lens[i];
+      a.kept[i] = r.kept;
+    }
+  }
+#pragma unroll 4
   for (int q = seg.begin + tid; q < seg.end; q += kThreads)
     if (a.refs[q] != 0) a.out_refs[q] = __ldcg(counts + q);
   const int copies = __ldcg(words + 1);
@@ -238,27 +301,6 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
     } else {
       a.copy_src[i] = -1;
       a.copy_dst[i] = -1;
-    }
-  }
-  for (int i = rank * kWarps + warp; i < a.S_out; i += kCluster * kWarps) {
-    int p;
-    const int kept = kept_of(i, p), hold = __ldcg(have + i), at = __ldcg(place + i);
-    const int want = pages_of(a.new_lens[i], a.P, a.width);
-    const int32_t* row = a.table + static_cast<int64_t>(max(p, 0)) * a.width;
-    int32_t* out = a.out_table + static_cast<int64_t>(i) * a.width;
-    for (int j = lane; j < a.width; j += 32) {
-      int q = -1;
-      if (j < hold) {
-        q = row[j];
-      } else if (j < want) {
-        q = __ldcg(free_list + at + j - hold);
-        a.out_refs[q] = 1;
-      }
-      out[j] = q;
-    }
-    if (lane == 0) {
-      a.out_lens[i] = a.new_lens[i];
-      a.kept[i] = kept;
     }
   }
 }
@@ -300,9 +342,14 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) com
   for (int r = rank * kWarps + warp; r < a.S; r += kCluster * kWarps) {
     const int pages = pages_of(a.lens[r], a.P, a.width);
     wrong |= pages < 0;
-    for (int j = lane; j < pages; j += 32) {
-      const int q = a.table[static_cast<int64_t>(r) * a.width + j];
-      wrong |= q != -1 && (static_cast<uint32_t>(q) >= static_cast<uint32_t>(a.N) || a.refs[q] == 0);
+    for (int j0 = lane; j0 < pages; j0 += 32 * kAhead) {
+      int q[kAhead];
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x)
+        q[x] = j0 + 32 * x < pages ? a.table[static_cast<int64_t>(r) * a.width + j0 + 32 * x] : -1;
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x)
+        wrong |= q[x] != -1 && (static_cast<uint32_t>(q[x]) >= static_cast<uint32_t>(a.N) || a.refs[q[x]] == 0);
     }
   }
   wrong = __syncthreads_or(wrong);
@@ -364,9 +411,15 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) com
   for (int r = rank * kWarps + warp; r < a.S; r += kCluster * kWarps) {
     const int pages = pages_of(a.lens[r], a.P, a.width);
     const int64_t at = static_cast<int64_t>(r) * a.width;
-    for (int j = lane; j < a.width; j += 32) {
-      const int q = j < pages ? a.table[at + j] : -1;
-      a.out_table[at + j] = q < 0 ? -1 : __ldcg(a.page_map + q);
+    for (int j0 = lane; j0 < a.width; j0 += 32 * kAhead) {
+      int q[kAhead];
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) q[x] = j0 + 32 * x < pages ? a.table[at + j0 + 32 * x] : -1;
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) q[x] = q[x] < 0 ? -1 : __ldcg(a.page_map + q[x]);
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x)
+        if (j0 + 32 * x < a.width) a.out_table[at + j0 + 32 * x] = q[x];
     }
   }
 }
