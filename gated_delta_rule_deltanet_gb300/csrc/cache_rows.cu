@@ -57,15 +57,38 @@ __device__ __forceinline__ T block_scan(T x, T* warp_sums, T& total) {
   return incl + (warp ? before : 0);
 }
 
-struct Segment {                             // the pages of one CTA: multiples of 4 but the last
+struct Segment {                             // the pages of one CTA; the first has the rows to see to and none
   int begin, end;
 };
 __device__ __forceinline__ Segment segment(int n, int rank) {
-  const int per = ((n + kCluster - 1) / kCluster + 3) & ~3;
+  const int per = (n + kCluster - 2) / (kCluster - 1);
   Segment s;
-  s.begin = min(static_cast<int64_t>(rank) * per, static_cast<int64_t>(n));
-  s.end = min(s.begin + per, n);
+  s.begin = rank == 0 ? 0 : min(static_cast<int64_t>(rank - 1) * per, static_cast<int64_t>(n));
+  s.end = rank == 0 ? 0 : min(s.begin + per, n);
   return s;
+}
+
+// Calls f(page, is it one, ones before it) for the pages of the segment, in order, with `before` ones ahead of the
+// segment: each thread takes kPages pages behind one another, loaded at once.
+constexpr int kPages = 8;
+template <typename Is, typename F>
+__device__ __forceinline__ void rank_pages(const Segment& seg, int before, int* warp_sums, const Is& is, const F& f) {
+  for (int q0 = seg.begin; q0 < seg.end; q0 += kThreads * kPages) {
+    const int at = q0 + threadIdx.x * kPages;
+    bool one[kPages];
+    int mine = 0, total;
+#pragma unroll
+    for (int x = 0; x < kPages; ++x) one[x] = at + x < seg.end && is(at + x);
+#pragma unroll
+    for (int x = 0; x < kPages; ++x) mine += one[x];
+    int rank = block_scan(mine, warp_sums, total) - mine + before;
+#pragma unroll
+    for (int x = 0; x < kPages; ++x) {
+      if (at + x < seg.end) f(at + x, one[x], rank);
+      rank += one[x];
+    }
+    before += total;
+  }
 }
 
 // pages of the row, or -1 for a length that its row cannot hold
@@ -92,6 +115,7 @@ __device__ __forceinline__ Row row_of(const RowsArgs& a, int i) {
   return r;
 }
 
+constexpr int kCounted = 4096;               // old rows whose children are counted; more are not, which costs time only
 constexpr int kAhead = 8;                    // entries of a row that a lane loads before it uses the first
 
 // Scratch of an update (int32): [N] counts, [N] first open row, [N] free pages in order, [S_out] pages that a row
@@ -103,7 +127,7 @@ constexpr int kAhead = 8;                    // entries of a row that a lane loa
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) update_kernel(const RowsArgs a) {
   __shared__ int warp_sums[32];
   __shared__ int64_t warp_sums64[32];
-  __shared__ int stop;
+  __shared__ int children[kCounted], shared_pages[kCounted];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x;
   const int all = kCluster * kThreads, me = rank * kThreads + tid, my_row = warp * kCluster + rank, rows_at_once = kCluster * kWarps;
   int32_t* counts = a.scratch;
@@ -112,11 +136,21 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
   int32_t* have = free_list + a.N;
   int32_t* place = have + a.S_out;
   int32_t* words = place + a.S_out;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Segment seg = segment(a.N, rank);
   const auto in_pool = [&](int q) { return static_cast<uint32_t>(q) < static_cast<uint32_t>(a.N); };
 
   // 1. references as they are; free pages of the CTA
   if (rank == 0 && tid == 0) words[0] = 0;
+  // The rows that this warp, and in the first CTA this thread, comes to first, and how an old row goes on: its
+  // children and the full pages that all of them keep, counted by each CTA for itself.
+  const Row mine_row = my_row < a.S_out ? row_of(a, my_row) : Row{};
+  const Row thread_row = tid < a.S_out ? row_of(a, tid) : Row{};
+  const bool counted = a.S <= kCounted;
+  for (int r = tid; counted && r < a.S; r += kThreads) {
+    children[r] = 0;
+    shared_pages[r] = INT_MAX;
+  }
   int mine = 0, total;
 #pragma unroll 4
   for (int q = seg.begin + tid; q < seg.end; q += kThreads) {
@@ -128,9 +162,6 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
       a.out_refs[q] = 0;
     }
   }
-  // the rows that this warp, and in the first CTA this thread, comes to first
-  Row mine_row = my_row < a.S_out ? row_of(a, my_row) : Row{};
-  Row thread_row = rank == 0 && tid < a.S_out ? row_of(a, tid) : Row{};
   int thread_open = -1;                      // the page that the thread's row ends inside
   const auto open_of = [&](const Row& r) {
     const bool ok = r.parent >= 0 && r.parent < a.S && r.kept % a.P != 0 && r.full < a.width;
@@ -139,22 +170,27 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
   if (rank == 0 && tid < a.S_out) thread_open = open_of(thread_row);
   block_scan(mine, warp_sums, total);
   if (tid == 0) words[8 + rank] = total;
+  for (int i = tid; counted && i < a.S_out; i += kThreads) {
+    const Row r = i == tid ? thread_row : row_of(a, i);
+    if (r.parent >= 0 && r.parent < a.S) {
+      atomicAdd(children + r.parent, 1);
+      atomicMin(shared_pages + r.parent, r.full);
+    }
+  }
   cluster_sync();
 
-  // 2. references of the old rows taken back, of the new rows' full pages added; a warp takes a row.  A row that goes
-  // on from itself keeps its full pages: nothing to count.
+  // 2. References of the old rows taken back, of the new rows' full pages added; a warp takes a row.  The pages that all
+  // children of a row keep change by their number less one, which is nothing for a row that only goes on; beyond
+  // them each child counts its own.
   const auto fault = [&]() { atomicExch(words, 1); };
+  const auto pages_shared = [&](int r) { return counted && children[r] > 0 ? shared_pages[r] : 0; };
   for (int r = my_row; r < a.S; r += rows_at_once) {
     const int n = pages_of(a.lens[r], a.P, a.width);
     if (n < 0) {
       if (lane == 0) fault();
       continue;
     }
-    int skip = 0;
-    if (r < a.S_out) {
-      const Row own = r == my_row ? mine_row : row_of(a, r);
-      if (own.parent == r) skip = own.full;
-    }
+    const int shared = pages_shared(r), change = counted ? children[r] - 1 : -1;
     const int32_t* row = a.table + static_cast<int64_t>(r) * a.width;
     for (int j0 = lane; j0 < n; j0 += 32 * kAhead) {
       int q[kAhead];
@@ -164,8 +200,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
 #pragma unroll
       for (int x = 0; x < kAhead; ++x) {
         if (q[x] == -1) continue;            // a page that the row has given back
+        const int add = j0 + 32 * x < shared ? change : -1;
         if (!in_pool(q[x])) bad = 1;
-        else if (j0 + 32 * x >= skip) atomicSub(counts + q[x], 1);
+        else if (add) atomicAdd(counts + q[x], add);
         else bad |= a.refs[q[x]] <= 0;
       }
       if (bad) fault();
@@ -179,7 +216,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
     }
     if (r.parent < 0) continue;
     const int32_t* row = a.table + static_cast<int64_t>(r.parent) * a.width;
-    for (int j0 = (r.parent == i ? r.full : 0) + lane; j0 < r.full; j0 += 32 * kAhead) {
+    for (int j0 = pages_shared(r.parent) + lane; j0 < r.full; j0 += 32 * kAhead) {
       int q[kAhead];
 #pragma unroll
       for (int x = 0; x < kAhead; ++x) q[x] = j0 + 32 * x < r.full ? row[j0 + 32 * x] : -1;
@@ -203,14 +240,17 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
     if (c < rank) before += n;
     free_pages += n;
   }
-  for (int q0 = seg.begin; q0 < seg.end; q0 += kThreads) {
-    const int q = q0 + tid;
-    const int r = q < seg.end ? a.refs[q] : 1;
-    if (r < 0 || (q < seg.end && __ldcg(counts + q) < 0)) fault();
-    const int at = block_scan(static_cast<int>(r == 0), warp_sums, total) - 1;
-    if (r == 0) free_list[before + at] = q;
-    before += total;
-  }
+  bool wrong = false;
+  rank_pages(seg, before, warp_sums,
+             [&](int q) {
+               const int r = a.refs[q];
+               wrong |= r < 0 || __ldcg(counts + q) < 0;
+               return r == 0;
+             },
+             [&](int q, bool free, int at) {
+               if (free) free_list[at] = q;
+             });
+  if (wrong) fault();
   // and the rows' needs, by the first CTA
   if (rank == 0) {
     int64_t fresh = 0, sum;                  // in 64 bits: rows may ask for more than there is
@@ -253,8 +293,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
   cluster_sync();
 
   // 4. the new rows
-  if (tid == 0) stop = __ldcg(words);
-  __syncthreads();
+  const int copies = __ldcg(words + 1), mine_have = my_row < a.S_out ? __ldcg(have + my_row) : 0,
+            mine_place = my_row < a.S_out ? __ldcg(place + my_row) : 0;
+  const bool stop = __ldcg(words) != 0;
   if (stop) {
     if (me == 0) raise_device_error(a.err, KDA_DEVERR_PAGE);
     for (int q = seg.begin + tid; q < seg.end; q += kThreads) a.out_refs[q] = a.refs[q];
@@ -269,7 +310,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
   }
   for (int i = my_row; i < a.S_out; i += rows_at_once) {
     const Row r = i == my_row ? mine_row : row_of(a, i);
-    const int hold = __ldcg(have + i), at = __ldcg(place + i);
+    const int hold = i == my_row ? mine_have : __ldcg(have + i), at = i == my_row ? mine_place : __ldcg(place + i);
     const int32_t* row = a.table + static_cast<int64_t>(max(r.parent, 0)) * a.width;
     int32_t* out = a.out_table + static_cast<int64_t>(i) * a.width;
     for (int j0 = lane; j0 < a.width; j0 += 32 * kAhead) {
@@ -294,7 +335,6 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
 #pragma unroll 4
   for (int q = seg.begin + tid; q < seg.end; q += kThreads)
     if (a.refs[q] != 0) a.out_refs[q] = __ldcg(counts + q);
-  const int copies = __ldcg(words + 1);
   for (int i = me; i < a.S_out; i += all) {
     if (i < copies) {
       a.copy_dst[i] = __ldcg(free_list + __ldcg(a.copy_dst + i));
@@ -315,6 +355,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) com
   int32_t* used_list = a.scratch;
   int32_t* free_list = used_list + a.N;
   int32_t* words = free_list + a.N;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Segment seg = segment(a.N, rank);
 
   int mine = 0, total;
@@ -355,18 +396,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) com
   wrong = __syncthreads_or(wrong);
   if (rank == 0 && tid == 0 && n == a.N) words[1] = n;
   if (!bad) {
-    for (int q0 = seg.begin; q0 < seg.end; q0 += kThreads) {
-      const int q = q0 + tid;
-      const int used = q < seg.end && a.refs[q] != 0 ? 1 : 0;
-      const int at = block_scan(used, warp_sums, total) - used + before;     // used pages before q
-      if (q < seg.end) {
-        a.page_map[q] = used ? at : -1;
-        if (used) used_list[at] = q;
-        else free_list[q - at] = q;
-        if (q == n) words[1] = at;
-      }
-      before += total;
-    }
+    rank_pages(seg, before, warp_sums, [&](int q) { return a.refs[q] != 0; },
+               [&](int q, bool used, int at) {           // `at` used pages before q
+                 a.page_map[q] = used ? at : -1;
+                 if (used) used_list[at] = q;
+                 else free_list[q - at] = q;
+                 if (q == n) words[1] = at;
+               });
   }
   __syncthreads();
   if (tid == 0) words[16 + rank] = bad || wrong;
@@ -440,6 +476,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const Pools pools, i
                                                             const int32_t* src, const int32_t* dst, int64_t n, int num_pages,
                                                             int32_t* err) {
   constexpr int64_t kPiece = static_cast<int64_t>(sizeof(V)) * kCopyThreads * kCopyUnroll;
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // launched while what makes the list may still run
   const int64_t per_entry = pieces * num_pools;
   for (int64_t at = blockIdx.x; at < n * per_entry; at += gridDim.x) {
     const int64_t i = at / per_entry, rest = at - i * per_entry, pool = rest / pieces, piece = rest - pool * pieces;
@@ -472,9 +509,16 @@ cudaError_t copy(const Pools& pools, int num_pools, int64_t bytes, const int32_t
   const int64_t pieces = (bytes + static_cast<int64_t>(sizeof(V)) * kCopyThreads * kCopyUnroll - 1) /
                          (static_cast<int64_t>(sizeof(V)) * kCopyThreads * kCopyUnroll);
   const int64_t blocks = std::min<int64_t>(n * pieces * num_pools, static_cast<int64_t>(sm_count()) * 8);
-  copy_kernel<V><<<static_cast<unsigned>(blocks), kCopyThreads, 0, st>>>(pools, num_pools, bytes, pieces, src, dst, n,
-                                                                         num_pages, err);
-  return cudaGetLastError();
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3(static_cast<unsigned>(blocks));
+  config.blockDim = dim3(kCopyThreads);
+  config.stream = st;
+  cudaLaunchAttribute attribute;
+  attribute.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attribute.val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = &attribute;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, copy_kernel<V>, pools, num_pools, bytes, pieces, src, dst, n, num_pages, err);
 }
 
 }  // namespace
