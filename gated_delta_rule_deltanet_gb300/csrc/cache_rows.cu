@@ -69,7 +69,7 @@ __device__ __forceinline__ Segment segment(int n, int rank) {
 }
 
 // Calls f(page, is it one, ones before it) for the pages of the segment, in order, with `before` ones ahead of the
-// segment: each thread takes kPages pages behind one another, loaded at once.
+// segment: each thread takes kPages pages behind one another, and `is` says of them at once which are ones.
 constexpr int kPages = 8;
 template <typename Is, typename F>
 __device__ __forceinline__ void rank_pages(const Segment& seg, int before, int* warp_sums, const Is& is, const F& f) {
@@ -77,8 +77,7 @@ __device__ __forceinline__ void rank_pages(const Segment& seg, int before, int* 
     const int at = q0 + threadIdx.x * kPages;
     bool one[kPages];
     int mine = 0, total;
-#pragma unroll
-    for (int x = 0; x < kPages; ++x) one[x] = at + x < seg.end && is(at + x);
+    is(at, seg.end, one);
 #pragma unroll
     for (int x = 0; x < kPages; ++x) mine += one[x];
     int rank = block_scan(mine, warp_sums, total) - mine + before;
@@ -242,10 +241,18 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
   }
   bool wrong = false;
   rank_pages(seg, before, warp_sums,
-             [&](int q) {
-               const int r = a.refs[q];
-               wrong |= r < 0 || __ldcg(counts + q) < 0;
-               return r == 0;
+             [&](int at, int end, bool (&free)[kPages]) {
+               int r[kPages], c[kPages];
+#pragma unroll
+               for (int x = 0; x < kPages; ++x) {
+                 r[x] = at + x < end ? a.refs[at + x] : 1;
+                 c[x] = at + x < end ? __ldcg(counts + at + x) : 0;
+               }
+#pragma unroll
+               for (int x = 0; x < kPages; ++x) {
+                 wrong |= (r[x] < 0) | (c[x] < 0);
+                 free[x] = r[x] == 0;
+               }
              },
              [&](int q, bool free, int at) {
                if (free) free_list[at] = q;
@@ -264,7 +271,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
         open = i0 == 0 ? thread_open : open_of(r);
         hold = r.full;
         if (in_pool(open)) {
-          if (__ldcg(first + open) == i && __ldcg(counts + open) == 0) {
+          const int lowest = __ldcg(first + open), others = __ldcg(counts + open);
+          if (lowest == i && others == 0) {
             counts[open] = 1;                // no other row looks at it: each has another first row or finds this one's
             ++hold;
           } else {
@@ -396,7 +404,14 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) com
   wrong = __syncthreads_or(wrong);
   if (rank == 0 && tid == 0 && n == a.N) words[1] = n;
   if (!bad) {
-    rank_pages(seg, before, warp_sums, [&](int q) { return a.refs[q] != 0; },
+    rank_pages(seg, before, warp_sums,
+               [&](int at, int end, bool (&used)[kPages]) {
+                 int r[kPages];
+#pragma unroll
+                 for (int x = 0; x < kPages; ++x) r[x] = at + x < end ? a.refs[at + x] : 0;
+#pragma unroll
+                 for (int x = 0; x < kPages; ++x) used[x] = r[x] != 0;
+               },
                [&](int q, bool used, int at) {           // `at` used pages before q
                  a.page_map[q] = used ? at : -1;
                  if (used) used_list[at] = q;
