@@ -399,10 +399,10 @@ def cache_update(block_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tens
         plan = _plan_rows(key, "kda_cache_update", block_table, lens, refs, parent, new_lens, page_size)
     (S, width), N, dev = plan.shape, plan.params.num_pages, plan.device
     if out is None:
-        # one piece of memory for the short rows and the counts
-        row = torch.empty(4 * S + N, dtype=torch.int32, device=dev)
-        out = CacheRows(torch.empty((S, width), dtype=torch.int32, device=dev),
-                        *row.split_with_sizes([S, N, S, S, S]))
+        # one piece of memory for the tables: an allocation takes longer than the kernel's launch
+        table, *rows = torch.empty(S * width + 4 * S + N, dtype=torch.int32, device=dev).split_with_sizes(
+            [S * width, S, N, S, S, S])
+        out = CacheRows(table.view(S, width), *rows)
     else:
         _device(refs, *out)
         _out(out, (("table", (S, width)), ("lens", (S,)), ("refs", (N,)), ("kept", (S,)), ("src", (S,)), ("dst", (S,))),
@@ -432,9 +432,9 @@ def cache_compact(block_table: torch.Tensor, lens: torch.Tensor, refs: torch.Ten
         plan = _plan_rows(key, "kda_cache_compact", block_table, lens, refs, None, None, page_size)
     shape, N, dev = plan.shape, plan.params.num_pages, plan.device
     if out is None:
-        out = CacheMoves(torch.empty(shape, dtype=torch.int32, device=dev),
-                         *torch.empty(2 * N + N // 2 * 2, dtype=torch.int32, device=dev)
-                         .split_with_sizes([N, N, N // 2, N // 2]))
+        table, *rows = torch.empty(shape[0] * shape[1] + 2 * N + 2 * (N // 2), dtype=torch.int32, device=dev) \
+            .split_with_sizes([shape[0] * shape[1], N, N, N // 2, N // 2])
+        out = CacheMoves(table.view(shape), *rows)
     else:
         _device(refs, *out)
         _out(out, (("table", shape), ("refs", (N,)), ("page_map", (N,)), ("src", (N // 2,)), ("dst", (N // 2,))),

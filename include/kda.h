@@ -631,7 +631,7 @@ kda_status_t kda_norm_workspace_size(const kda_norm_params_t *p, int32_t gated, 
  * one table serves all layers.  Entries that a call does not need are not read and may hold -1.
  *
  * Problems only the device can see (a page, length or position out of range) set KDA_DEVERR_PAGE;
- * what they touch is then skipped (an append writes no row, an attention leaves the key out, an update or
+ * what they touch is then skipped (an append writes no row, an attention reads zeros, an update or
  * a compaction changes nothing).
  */
 
@@ -755,6 +755,7 @@ typedef struct kda_cache_rows_params {
  *   out_table [rows_out, max_pages], -1 behind a row's pages   out_lens, kept [rows_out]   out_refs
  *   [num_pages]   copy_src, copy_dst [rows_out]: the copies, then -1
  *   workspace >= kda_cache_rows_workspace_size bytes, 256-byte aligned
+ * An entry of -1 among a row's pages is one that it has given back (behind a span): it stays -1.
  * The outputs share no memory with the inputs.  With KDA_DEVERR_PAGE (not enough free pages among its
  * reasons) the new rows are empty, out_refs is refs and nothing is to be copied.
  */

@@ -1,0 +1,227 @@
+"""The key-value cache's entry points without a GPU: every refusal comes back before anything touches
+CUDA."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_deltanet_gb300 as kda
+from gated_delta_rule_deltanet_gb300 import _lib, build as kbuild, cache
+from oracle import cache as oc
+
+A = 1 << 20                       # an aligned address that is never read: validation fails first
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    kbuild.build()
+    return _lib.load()
+
+
+def rotary_params(**kw):
+    base = dict(tokens=10, num_q_heads=4, num_k_heads=2, head_dim=16, rot_dim=8, dtype=1, magnitude=1.0)
+    base.update(kw)
+    return _lib.KdaRotaryParams(**base)
+
+
+def cache_params(**kw):
+    base = dict(tokens=3, num_seqs=3, num_q_heads=4, num_kv_heads=2, head_dim=16, rot_dim=0, dtype=1,
+                o_dtype=1, page_size=8, max_pages=5, num_pages=20, window=1, magnitude=1.0,
+                page_stride=8 * 2 * 16, page_row_stride=2 * 16, page_head_stride=16)
+    base.update(kw)
+    return _lib.KdaCacheParams(**base)
+
+
+def rows_params(**kw):
+    base = dict(rows=3, rows_out=4, max_pages=5, page_size=8, num_pages=20)
+    base.update(kw)
+    return _lib.KdaCacheRowsParams(**base)
+
+
+def test_struct_layouts():
+    assert ctypes.sizeof(_lib.KdaRotaryParams) == 72
+    assert _lib.KdaRotaryParams.magnitude.offset == 36 and _lib.KdaRotaryParams.q_row_stride.offset == 40
+    assert ctypes.sizeof(_lib.KdaCacheParams) == 128
+    assert _lib.KdaCacheParams.magnitude.offset == 60 and _lib.KdaCacheParams.page_stride.offset == 104
+    assert ctypes.sizeof(_lib.KdaCacheRowsParams) == 20
+
+
+@pytest.mark.parametrize("name", ["kda_rotary_fwd", "kda_rotary_bwd"])
+def test_rotary_refusals(lib, name):
+    def call(p=None, q=A, k=A, pos=A, f=A, qo=A, ko=A):
+        return getattr(lib, name)(ctypes.byref(p or rotary_params()), q, k, pos, f, qo, ko, None)
+    assert getattr(lib, name)(None, A, A, A, A, A, A, None) == INVALID
+    assert call(p=rotary_params(tokens=0), q=None, k=None, pos=None, f=None, qo=None, ko=None) == OK
+    assert call(p=rotary_params(num_q_heads=0, num_k_heads=0)) == OK
+    for kw in (dict(tokens=-1), dict(num_q_heads=-1), dict(head_dim=0), dict(dtype=2), dict(rot_dim=0),
+               dict(rot_dim=7), dict(rot_dim=18), dict(magnitude=float("nan")), dict(q_row_stride=63),
+               dict(k_out_row_stride=-32)):
+        assert call(p=rotary_params(**kw)) == INVALID, kw
+    for kw in (dict(head_dim=1026), dict(num_q_heads=1 << 22), dict(tokens=1 << 31)):
+        assert call(p=rotary_params(**kw)) == UNSUPPORTED, kw
+    assert call(q=None) == INVALID and call(k=None) == INVALID and call(pos=None) == INVALID
+    assert call(f=None) == INVALID and call(qo=None) == INVALID and call(ko=None) == INVALID
+    assert call(q=A + 1) == INVALID and call(pos=A + 2) == INVALID and call(f=A + 4) == INVALID
+    assert call(p=rotary_params(wide_positions=1), pos=A + 4) == INVALID
+
+
+def test_append_refusals(lib):
+    def call(p=None, q=A, k=A, v=A, f=None, kp=A, vp=A, table=A, start=A, off=None, qo=A):
+        return lib.kda_cache_append(ctypes.byref(p or cache_params()), q, k, v, f, kp, vp, table, start, off, qo, None)
+    assert call(p=cache_params(tokens=0, num_seqs=0), q=None, k=None, v=None) == OK
+    for kw in (dict(num_seqs=-1), dict(num_kv_heads=0), dict(dtype=3), dict(page_size=0), dict(max_pages=-1),
+               dict(rot_dim=3), dict(rot_dim=18), dict(magnitude=float("inf")), dict(page_head_stride=15),
+               dict(page_row_stride=31), dict(page_stride=255), dict(page_stride=0), dict(v_row_stride=31),
+               dict(tokens=4)):                                  # without offsets one token a sequence
+        assert call(p=cache_params(**kw)) == INVALID, kw
+    assert call(p=cache_params(head_dim=1026, page_head_stride=1026, page_row_stride=2052, page_stride=1 << 20)) == UNSUPPORTED
+    assert call(p=cache_params(rot_dim=8)) == INVALID            # turned channels without frequencies
+    assert call(f=A) == INVALID                                  # and the other way round
+    for kw in (dict(k=None), dict(v=None), dict(kp=None), dict(vp=None), dict(table=None), dict(start=None),
+               dict(q=None), dict(qo=None), dict(k=A + 1), dict(kp=A + 1), dict(table=A + 2), dict(off=A + 2)):
+        assert call(**kw) == INVALID, kw
+
+
+def test_attention_refusals(lib):
+    n = ctypes.c_size_t(0)
+
+    def size(**kw):
+        return lib.kda_cache_attention_workspace_size(ctypes.byref(cache_params(**kw)), ctypes.byref(n))
+    assert size() == OK and n.value > 0
+    # pages by heads: [num_pages, HK, page_size, d]
+    assert size(page_row_stride=16, page_head_stride=128) == OK
+    for kw in (dict(num_q_heads=0), dict(num_q_heads=3), dict(o_dtype=2), dict(window=0), dict(span=-1),
+               dict(scale=float("nan")), dict(softcap=-1.0), dict(softcap=float("inf")), dict(q_row_stride=60),
+               dict(page_row_stride=36), dict(page_stride=260), dict(page_row_stride=16, page_head_stride=120)):
+        assert size(**kw) == INVALID, kw
+    for kw in (dict(window=65), dict(head_dim=264, page_head_stride=264, page_row_stride=528, page_stride=8 * 528),
+               dict(head_dim=12), dict(max_pages=1 << 30, num_seqs=1 << 12)):
+        assert size(**kw) == UNSUPPORTED, kw
+    assert lib.kda_cache_attention_workspace_size(None, ctypes.byref(n)) == INVALID
+    assert lib.kda_cache_attention_workspace_size(ctypes.byref(cache_params()), None) == INVALID
+    size()
+    need = n.value
+
+    def call(p=None, q=A, k=A, v=A, t=A, lens=A, sl=None, o=A, lse=None, ws=A, nb=need):
+        return lib.kda_cache_attention(ctypes.byref(p or cache_params()), q, k, v, t, lens, sl, o, lse, ws, nb, None)
+    assert call(p=cache_params(num_seqs=0), q=None, k=None) == OK
+    for kw in (dict(q=None), dict(k=None), dict(v=None), dict(t=None), dict(lens=None), dict(o=None), dict(q=A + 8),
+               dict(k=A + 4), dict(v=A + 2), dict(t=A + 2), dict(lens=A + 1), dict(sl=A + 2), dict(o=A + 1), dict(lse=A + 2)):
+        assert call(**kw) == INVALID, kw
+    assert call(ws=None) == WORKSPACE and call(nb=need - 1) == WORKSPACE and call(ws=A + 128) == WORKSPACE
+
+
+def test_tables_refusals(lib):
+    n = ctypes.c_size_t(0)
+
+    def size(**kw):
+        return lib.kda_cache_rows_workspace_size(ctypes.byref(rows_params(**kw)), ctypes.byref(n))
+    assert size() == OK
+    for kw in (dict(rows=-1), dict(rows_out=-1), dict(max_pages=-1), dict(page_size=0), dict(num_pages=-1)):
+        assert size(**kw) == INVALID, kw
+    assert size(num_pages=(1 << 28) + 1) == UNSUPPORTED and size(rows=(1 << 24) + 1) == UNSUPPORTED
+    size()
+    need = n.value
+
+    def update(p=None, ws=A, nb=need, **kw):
+        a = dict(table=A, lens=A, refs=A, parent=A, new=A, ot=A, ol=A, orf=A, kept=A, src=A, dst=A)
+        a.update(kw)
+        return lib.kda_cache_update(ctypes.byref(p or rows_params()), *a.values(), ws, nb, None)
+    for name in ("table", "lens", "refs", "new", "ot", "ol", "orf", "kept", "src", "dst", "parent"):
+        assert update(**{name: None}) == INVALID, name           # no parent: rows_out has to be rows
+        assert update(**{name: A + 2}) == INVALID, name
+    assert update(ws=None) == WORKSPACE and update(nb=need - 4) == WORKSPACE and update(ws=A + 4) == WORKSPACE
+
+    def compact(ws=A, nb=need, **kw):
+        a = dict(table=A, lens=A, refs=A, ot=A, orf=A, pm=A, src=A, dst=A)
+        a.update(kw)
+        return lib.kda_cache_compact(ctypes.byref(rows_params()), *a.values(), ws, nb, None)
+    for name in ("table", "lens", "refs", "ot", "orf", "pm", "src", "dst"):
+        assert compact(**{name: None}) == INVALID and compact(**{name: A + 1}) == INVALID, name
+    assert compact(ws=None) == WORKSPACE and compact(nb=0) == WORKSPACE
+
+
+def test_copy_refusals(lib):
+    def call(pools=(A, A), size=(64, 64), stride=(64, 64), src=A, dst=A, n=4, pages=10, count=2):
+        P, I = ctypes.c_void_p, ctypes.c_int64
+        return lib.kda_cache_copy((P * 2)(*pools), (I * 2)(*size), (I * 2)(*stride), count, src, dst, n, pages, None)
+    assert call(count=0) == OK and call(n=0) == OK and call(pages=0) == OK
+    for kw in (dict(count=-1), dict(n=-1), dict(pages=-1), dict(src=None), dict(dst=None), dict(src=A + 1),
+               dict(pools=(A, None)), dict(size=(64, -1)), dict(stride=(64, 63))):
+        assert call(**kw) == INVALID, kw
+    assert call(n=1 << 31) == UNSUPPORTED
+
+
+def test_binding_refuses_host_tensors():
+    x, f = torch.zeros(3, 2, 8), torch.zeros(4, dtype=torch.float64)
+    pages, i = torch.zeros(5, 4, 2, 8), torch.zeros(3, dtype=torch.int32)
+    table = torch.zeros(3, 2, dtype=torch.int32)
+    for call in (lambda: kda.rotary(x, x, i, f), lambda: kda.rotary_bwd(x, None, i, f),
+                 lambda: kda.cache_append(x, x, x, f, pages, pages, table, i),
+                 lambda: kda.cache_attention(x, pages, pages, table, i),
+                 lambda: kda.cache_update(table, i, i, None, i, page_size=4),
+                 lambda: kda.cache_compact(table, i, i, page_size=4), lambda: kda.cache_copy([pages], i, i)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    kda.cache_copy([], i, i)                                     # nothing to copy
+
+
+@pytest.mark.parametrize("call", [
+    lambda x, t: cache._heads(x[0], "x"),                                  # not [T, H, d]
+    lambda x, t: cache._heads(x.half(), "x"),
+    lambda x, t: cache._heads(x[:, :, ::2], "x"),
+    lambda x, t: cache._heads(x.transpose(0, 1), "x"),
+    lambda x, t: cache._heads(x[:1].expand(6, 4, 8), "x"),                 # rows over one another
+    lambda x, t: cache._heads(x, "x", x[:3]),
+    lambda x, t: cache._heads(x, "x", x.bfloat16()),
+    lambda x, t: cache._layout("pairs"),
+    lambda x, t: cache._frequencies(torch.zeros(4), 8),                    # not fp64
+    lambda x, t: cache._frequencies(torch.zeros(5, dtype=torch.float64), 8),
+    lambda x, t: cache._frequencies(torch.zeros(0, dtype=torch.float64), 8),
+    lambda x, t: cache._place(x.transpose(0, 1), x, "out"),
+    lambda x, t: cache._place(x.bfloat16(), x, "out"),
+    lambda x, t: cache._pages(_lib.KdaCacheParams(), x[None], x[None].bfloat16(), t, 3),
+    lambda x, t: cache._pages(_lib.KdaCacheParams(), x, x, t, 3),
+    lambda x, t: cache._pages(_lib.KdaCacheParams(), x[None].expand(4, 6, 4, 8), x[None].expand(4, 6, 4, 8), t, 3),
+    lambda x, t: cache._pages(_lib.KdaCacheParams(), x[None], x[None], t.long(), 3),
+    lambda x, t: cache._pages(_lib.KdaCacheParams(), x[None], x[None], t, 4),
+    lambda x, t: cache._pages(_lib.KdaCacheParams(), x[None], x[None], t[:, ::2], 3),
+    lambda x, t: cache._index(t[0].long(), 2, "lens"),
+    lambda x, t: cache._index(t[:, 0], 3, "lens"),
+    lambda x, t: kda.rotary_frequencies(7, device="cpu"),
+    lambda x, t: kda.rotary_frequencies(8, scaling="cubic", device="cpu"),
+    lambda x, t: kda.rotary_frequencies(8, scaling="by_parts", factor=2.0, device="cpu"),
+    lambda x, t: kda.rotary_frequencies(8, base=0.0, device="cpu"),
+    lambda x, t: kda.rotary(x, x, t[:, 0], None),
+])
+def test_binding_checks(call):
+    with pytest.raises(ValueError):
+        call(torch.zeros(6, 4, 8), torch.zeros(3, 2, dtype=torch.int32))
+
+
+def test_outputs_have_memory_of_their_own():
+    x, f = torch.zeros(3, 2, 8), torch.zeros(4, dtype=torch.float64)
+    pages, i = torch.zeros(5, 4, 2, 8), torch.zeros(3, dtype=torch.int32)
+    table = torch.zeros(3, 2, dtype=torch.int32)
+    for call in (lambda: kda.rotary(x, x.clone(), i, f, q_out=pages[0, :3], k_out=pages[0, :3]),
+                 lambda: kda.cache_append(x, x.clone(), x.clone(), f, pages, pages, table, i, q_out=pages[0, :3]),
+                 lambda: kda.cache_attention(x, pages, pages, table, i, out=x)):
+        with pytest.raises(ValueError, match="memory of its own"):
+            call()
+    row = kda.CacheRows(table, i, i, i, i, i)
+    with pytest.raises(ValueError, match="memory of its own"):
+        cache._out(row, [(n, t.shape) for n, t in zip(row._fields, row)], (table,))
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(scaling="linear", factor=4.0), dict(scaling="ntk", factor=8.0),
+                                dict(scaling="by_parts", factor=8.0, trained_length=4096),
+                                dict(base=500000.0, scaling="by_parts", factor=16.0, trained_length=8192, slow=2.0, fast=20.0)])
+@pytest.mark.parametrize("R", [2, 50, 128])
+def test_frequencies(kw, R):
+    f, m = kda.rotary_frequencies(R, device="cpu", **kw)
+    ref, mr = oc.frequencies(R, **kw)
+    assert f.dtype == torch.float64
+    # a power and a few products in fp64
+    assert np.allclose(f.numpy(), ref, rtol=1e-14, atol=0) and abs(m - mr) < 1e-15
