@@ -283,10 +283,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ bool bf16x2_not_finite(uint32_t x) {
-  return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
-}
-
 // DP: the head's channels rounded up (zeros behind D).  RW warps, each with eight rows, share a ring and with
 // it every block of BK keys; the 4 / RW groups take the blocks of a tile in turn.  H halves (the keys or the values of a
 // block) make a ring.
@@ -310,6 +306,10 @@ struct Mma {
 //
 // The weights e^(s - m) enter the second product in two bf16 parts (16 bits), three (24) where o is stored in
 // fp32: one part's rounding (2^-9) would be as large as that of a bf16 o.
+//
+// Weights and parts of zero turn an infinite value into a NaN, also where a row's mask leaves its key out.  So a piece
+// whose sums do not come out finite is done again with `exact` set: the weighted sums key by key on CUDA cores, of what a
+// row sees alone.
 template <int DP, int RW, bool BF_OUT>
 __global__ void __launch_bounds__(kThreads, Mma<DP, RW>::kCtas)
     attend_bf16_kernel(const AttentionArgs a, FastDiv page_div, int row_tiles, int join_blocks, Join* joins,
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, Mma<DP, RW>::kCtas)
 
   Walk walk = find_stretch<C::kGroups * BK>(a, items);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  bool noted = false;
+  bool noted = false, exact = false;
   int n;
   while (next_piece<C::kGroups * BK>(a, items, walk, n)) {
     const int hk = walk.item / row_tiles, row0 = (walk.item - hk * row_tiles) * C::kRows;
@@ -544,18 +544,7 @@ __global__ void __launch_bounds__(kThreads, Mma<DP, RW>::kCtas)
       group_sync();
       issue(2 * i + H);
       const uint32_t vs = ring_u + ((2 * i + 1) % H) * C::kHalf;
-      bool poison = false;
-      if (!whole) {
-        // A value that is not finite would reach the rows whose mask leaves it out as 0 x infinity.
-        bool bad = false;
-        for (int x = lane; x < BK * CH; x += 32) {
-          const uint4 y = *reinterpret_cast<const uint4*>(ring + (vs - ring_u) + x * 16);
-          bad |= bf16x2_not_finite(y.x) | bf16x2_not_finite(y.y) | bf16x2_not_finite(y.z) | bf16x2_not_finite(y.w);
-        }
-        poison = __any_sync(0xffffffffu, bad);
-      }
-      if (poison) {
-        // key by key, leaving out what a row does not see
+      if (exact) {
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
 #pragma unroll 1
@@ -607,7 +596,17 @@ __global__ void __launch_bounds__(kThreads, Mma<DP, RW>::kCtas)
 
     // the groups' sums, over the rings
     cp_async_wait<0>();
-    __syncthreads();
+    float zero = 0.f * (l[0] + l[1]);
+#pragma unroll
+    for (int d = 0; d < KS; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) zero = fmaf(o[d][e], 0.f, zero);
+    const bool finite = !__syncthreads_or(!(zero == 0.f));
+    if (!finite && !exact) {
+      exact = true;
+      continue;
+    }
+    exact = false;
     float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {

@@ -421,6 +421,37 @@ def test_attention_a_draft_that_is_not_finite_spoils_its_own_row():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_infinite_values_and_keys_that_are_seen(dtype):
+    """An infinite value makes its channel infinite, of either sign; a key with infinite scores of the lower sign has
+    no weight, of the higher one makes a NaN of the row."""
+    r = rng(20)
+    table, ((kp, k64), (vp, _)) = paged(r, [40], 16, dtype, 1, 64)
+    q = torch.ones((1, 2, 64), dtype=DT[dtype], device=DEV)
+    at = (int(table[0, 1]), 3)
+    good = kda.cache_attention(q, kp, vp, ints(table), ints([40]))
+    v = vp.clone()
+    v[at][0, 5], v[at][0, 6] = float("inf"), float("-inf")
+    o = kda.cache_attention(q, kp, v, ints(table), ints([40]))
+    assert torch.all(o[..., 5] == float("inf")) and torch.all(o[..., 6] == -float("inf"))
+    rest = [c for c in range(64) if c not in (5, 6)]
+    # another order of the sums
+    assert torch.allclose(o[..., rest].float(), good[..., rest].float(), rtol=2 * R(o.dtype), atol=2.0 ** -14)
+    k = kp.clone()
+    k[at][0, 9] = float("-inf")
+    o, l = kda.cache_attention(q, k, vp, ints(table), ints([40]), return_lse=True)
+    keep = [j for j in range(40) if j != 19]
+    kk = np.stack([k64[table[0, j // 16], j % 16] for j in keep])
+    vv = np.stack([host(vp)[table[0, j // 16], j % 16] for j in keep])
+    ref, rl, mass, big, prod = oc.attention(host(q), kk, vv, 1, 0.125)
+    E = 2 * 64 * U * prod + 8 * U * (1 + big) + 2.0 ** -21
+    check("o", o, ref, (2 * E + 140 * U + 2.0 ** -16)[..., None] * mass)
+    check("lse", l, rl, E + 140 * U + 4 * U * np.abs(rl))
+    k[at][0, 9] = float("inf")
+    assert torch.isnan(kda.cache_attention(q, k, vp, ints(table), ints([40]))).all()
+    no_error()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attention_bad_pages_and_lengths(dtype):
     r = rng(16)
     lens, P = [30, 30, 30], 16
