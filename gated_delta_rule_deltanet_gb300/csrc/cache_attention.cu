@@ -283,12 +283,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-// DP: the head's channels rounded up (zeros behind D).  RW warps, each with eight rows, share a ring and with
-// it every block of BK keys; the 4 / RW groups take the blocks of a tile in turn.  H halves (the keys or the values of a
-// block) make a ring.
-template <int DP, int RW>
+// DP: the head's channels rounded up (zeros behind D).  RW warps, each with NT tiles of eight rows, share a ring and
+// with it every block of BK keys; the 4 / RW groups take the blocks of a tile in turn.  H halves (the keys or the values of
+// a block) make a ring.
+template <int DP, int RW, int NT>
 struct Mma {
-  static constexpr int kGroups = kWarps / RW, kRows = 8 * RW, kRowBytes = DP * 2;
+  static constexpr int kGroups = kWarps / RW, kRows = 8 * NT * RW, kRowBytes = DP * 2;
   static constexpr int kCopyRows = DP == 64 ? 4 : 2;           // rows that a lane copies a part of
   static constexpr int kBK = 8 * kCopyRows * RW;
   static constexpr int kHalves = DP == 256 ? 3 : 4, kHalf = kBK * kRowBytes;
@@ -297,7 +297,7 @@ struct Mma {
   static constexpr int kTop = kRing > kPart ? kRing : kPart;
   static constexpr int kQ = kRows * kRowBytes;
   static constexpr size_t kSmem = kTop + kQ;
-  static constexpr int kCtas = DP == 256 ? 2 : 3;              // an SM, by shared memory and registers
+  static constexpr int kCtas = DP == 256 || NT == 2 ? 2 : 3;   // an SM, by shared memory and registers
 };
 
 // Scores and sums transposed: S^T = K Q^T and O^T += V^T P^T, keys and channels as the M of m16n8k16, rows
@@ -310,11 +310,11 @@ struct Mma {
 // Weights and parts of zero turn an infinite value into a NaN, also where a row's mask leaves its key out.  So a piece
 // whose sums do not come out finite is done again with `exact` set: the weighted sums key by key on CUDA cores, of what a
 // row sees alone.
-template <int DP, int RW, bool BF_OUT>
-__global__ void __launch_bounds__(kThreads, Mma<DP, RW>::kCtas)
+template <int DP, int RW, int NT, bool BF_OUT>
+__global__ void __launch_bounds__(kThreads, Mma<DP, RW, NT>::kCtas)
     attend_bf16_kernel(const AttentionArgs a, FastDiv page_div, int row_tiles, int join_blocks, Join* joins,
                        float* parts) {
-  using C = Mma<DP, RW>;
+  using C = Mma<DP, RW, NT>;
   constexpr int BK = C::kBK, H = C::kHalves, CR = C::kCopyRows, MB = BK / 16, PARTS = BF_OUT ? 2 : 3;
   constexpr int CH = DP / 8, KS = DP / 16;                     // 16-byte pieces of a row, steps along D
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -435,26 +435,32 @@ __global__ void __launch_bounds__(kThreads, Mma<DP, RW>::kCtas)
       const int i = tid + x * kThreads, row = i / CH, ch = i - row * CH;
       if (row < C::kRows) *reinterpret_cast<uint4*>(q_smem + row * C::kRowBytes + ((ch ^ (row & 7)) << 4)) = q[x];
     }
-    float m[2], l[2], o[KS][4], slope[2];
-    int pos[2];                              // positions of this lane's rows
+    float m[NT][2], l[NT][2], o[NT][KS][4], slope[NT][2];
+    int pos[NT][2];                          // positions of this lane's rows
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      m[e] = -INFINITY;
-      l[e] = 0.f;
-      const RowPlace at = row_place(a, b, hk, min(row0 + row_warp * 8 + piece_c * 2 + e, rows - 1));
-      pos[e] = r.len - a.W + at.w;
-      slope[e] = a.slopes ? a.slopes[at.h] * kLog2e : 0.f;
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[t][e] = -INFINITY;
+        l[t][e] = 0.f;
+        const RowPlace at = row_place(a, b, hk, min(row0 + (row_warp * NT + t) * 8 + piece_c * 2 + e, rows - 1));
+        pos[t][e] = r.len - a.W + at.w;
+        slope[t][e] = a.slopes ? a.slopes[at.h] * kLog2e : 0.f;
+      }
+#pragma unroll
+      for (int d = 0; d < KS; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][d][e] = 0.f;
     }
-#pragma unroll
-    for (int d = 0; d < KS; ++d)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
     __syncthreads();
     // q as the second operand: one ldmatrix holds two steps
-    uint32_t qf[KS / 2][4];
+    uint32_t qf[NT][KS / 2][4];
 #pragma unroll
-    for (int kk = 0; kk < KS / 2; ++kk)
-      ldmatrix4(qf[kk], (q_u + (row_warp * 8 + (lane & 7)) * C::kRowBytes + (((lane >> 3) ^ (lane & 7)) << 4)) ^ (kk << 6));
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int kk = 0; kk < KS / 2; ++kk)
+        ldmatrix4(qf[t][kk], (q_u + ((row_warp * NT + t) * 8 + (lane & 7)) * C::kRowBytes +
+                              (((lane >> 3) ^ (lane & 7)) << 4)) ^ (kk << 6));
 
     for (int i = 0; i < n; ++i) {
       const int key0 = base(i);
@@ -463,11 +469,13 @@ __global__ void __launch_bounds__(kThreads, Mma<DP, RW>::kCtas)
       issue(2 * i + H - 1);
       const uint32_t ks = ring_u + ((2 * i) % H) * C::kHalf;
 
-      float s[MB][4];
+      float s[NT][MB][4];
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[mb][e] = 0.f;
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[t][mb][e] = 0.f;
 #pragma unroll
       for (int kk = 0; kk < KS / 2; ++kk) {
         if (kk * 32 >= a.D) break;
@@ -477,8 +485,11 @@ __global__ void __launch_bounds__(kThreads, Mma<DP, RW>::kCtas)
           const uint32_t at = ((ks + k_frag) ^ (kk << 6)) + mb * 16 * C::kRowBytes;
           ldmatrix4(k0, at);
           ldmatrix4(k1, at ^ 32);
-          mma16816(s[mb], k0, qf[kk][0], qf[kk][1]);
-          mma16816(s[mb], k1, qf[kk][2], qf[kk][3]);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            mma16816(s[t][mb], k0, qf[t][kk][0], qf[t][kk][1]);
+            mma16816(s[t][mb], k1, qf[t][kk][2], qf[t][kk][3]);
+          }
         }
       }
 
@@ -487,55 +498,62 @@ __global__ void __launch_bounds__(kThreads, Mma<DP, RW>::kCtas)
       const auto seen = [&](int key, int p) { return key >= r.first && key <= p && (a.span == 0 || key > p - a.span); };
       bool grows = false;
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float y = s[mb][e];
-          const int key = key0 + mb * 16 + row_c + (e >> 1) * 8, p = pos[e & 1];
-          y = a.softcap > 0.f ? cap2 * tanhf(y * inv_cap) : y * scale2;
-          if (a.slopes) y += slope[e & 1] * static_cast<float>(key - p);
-          if (!whole) y = seen(key, p) ? y : -INFINITY;
-          s[mb][e] = y;
-          grows |= y > m[e & 1] + kSlack;
-        }
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float y = s[t][mb][e];
+            const int key = key0 + mb * 16 + row_c + (e >> 1) * 8, p = pos[t][e & 1];
+            y = a.softcap > 0.f ? cap2 * tanhf(y * inv_cap) : y * scale2;
+            if (a.slopes) y += slope[t][e & 1] * static_cast<float>(key - p);
+            if (!whole) y = seen(key, p) ? y : -INFINITY;
+            s[t][mb][e] = y;
+            grows |= y > m[t][e & 1] + kSlack;
+          }
       if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float top = -INFINITY;
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int mb = 0; mb < MB; ++mb) top = fmaxf(top, fmaxf(s[mb][e], s[mb][e + 2]));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          const float now = fmaxf(m[e], top);
-          const float f = ex2(m[e] - (now == -INFINITY ? 0.f : now));
-          m[e] = now;
-          l[e] *= f;
+          for (int e = 0; e < 2; ++e) {
+            float top = -INFINITY;
 #pragma unroll
-          for (int d = 0; d < KS; ++d) {
-            o[d][e] *= f;
-            o[d][e + 2] *= f;
+            for (int mb = 0; mb < MB; ++mb) top = fmaxf(top, fmaxf(s[t][mb][e], s[t][mb][e + 2]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            const float now = fmaxf(m[t][e], top);
+            const float f = ex2(m[t][e] - (now == -INFINITY ? 0.f : now));
+            m[t][e] = now;
+            l[t][e] *= f;
+#pragma unroll
+            for (int d = 0; d < KS; ++d) {
+              o[t][d][e] *= f;
+              o[t][d][e + 2] *= f;
+            }
           }
-        }
       }
-      uint32_t pf[MB][PARTS][2];
-      const float from[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+      uint32_t pf[NT][MB][PARTS][2];
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb) {
+      for (int t = 0; t < NT; ++t) {
+        const float from[2] = {m[t][0] == -INFINITY ? 0.f : m[t][0], m[t][1] == -INFINITY ? 0.f : m[t][1]};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[mb][e] = ex2(s[mb][e] - from[e & 1]);
-          l[e & 1] += s[mb][e];
-        }
+        for (int mb = 0; mb < MB; ++mb) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float y0 = s[mb][2 * j], y1 = s[mb][2 * j + 1];
+          for (int e = 0; e < 4; ++e) {
+            s[t][mb][e] = ex2(s[t][mb][e] - from[e & 1]);
+            l[t][e & 1] += s[t][mb][e];
+          }
 #pragma unroll
-          for (int x = 0; x < PARTS; ++x) {
-            const uint32_t w = pack_bf16(y0, y1);
-            pf[mb][x][j] = transpose8(w);
-            y0 -= __uint_as_float(w << 16);
-            y1 -= __uint_as_float(w & 0xffff0000u);
+          for (int j = 0; j < 2; ++j) {
+            float y0 = s[t][mb][2 * j], y1 = s[t][mb][2 * j + 1];
+#pragma unroll
+            for (int x = 0; x < PARTS; ++x) {
+              const uint32_t w = pack_bf16(y0, y1);
+              pf[t][mb][x][j] = transpose8(w);
+              y0 -= __uint_as_float(w << 16);
+              y1 -= __uint_as_float(w & 0xffff0000u);
+            }
           }
         }
       }
@@ -546,49 +564,50 @@ __global__ void __launch_bounds__(kThreads, Mma<DP, RW>::kCtas)
       const uint32_t vs = ring_u + ((2 * i + 1) % H) * C::kHalf;
       if (exact) {
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb) {
 #pragma unroll 1
-          for (int j = 0; j < 16; ++j) {
-            const int src = ((j & 7) << 2) | (lane & 3), key = key0 + mb * 16 + j;
-            const float u0 = __shfl_sync(0xffffffffu, s[mb][0], src), u1 = __shfl_sync(0xffffffffu, s[mb][1], src);
-            const float u2 = __shfl_sync(0xffffffffu, s[mb][2], src), u3 = __shfl_sync(0xffffffffu, s[mb][3], src);
-            const float w[2] = {j < 8 ? u0 : u2, j < 8 ? u1 : u3};
-            const unsigned char* v = ring + (vs - ring_u) + (mb * 16 + j) * C::kRowBytes;
+            for (int j = 0; j < 16; ++j) {
+              const int src = ((j & 7) << 2) | (lane & 3), key = key0 + mb * 16 + j;
+              const float u0 = __shfl_sync(0xffffffffu, s[t][mb][0], src), u1 = __shfl_sync(0xffffffffu, s[t][mb][1], src);
+              const float u2 = __shfl_sync(0xffffffffu, s[t][mb][2], src), u3 = __shfl_sync(0xffffffffu, s[t][mb][3], src);
+              const float w[2] = {j < 8 ? u0 : u2, j < 8 ? u1 : u3};
+              const unsigned char* v = ring + (vs - ring_u) + (mb * 16 + j) * C::kRowBytes;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              if (!seen(key, pos[e])) continue;
+              for (int e = 0; e < 2; ++e) {
+                if (!seen(key, pos[t][e])) continue;
 #pragma unroll
-              for (int d = 0; d < KS; ++d)
+                for (int d = 0; d < KS; ++d)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {          // channel 16 d + 8 h + lane / 4
-                  const uint16_t x = *reinterpret_cast<const uint16_t*>(v + (((d * 2 + h) ^ (j & 7)) << 4) + row_c * 2);
-                  o[d][2 * h + e] += w[e] * bf16_bits_to_f32(x);
-                }
+                  for (int h = 0; h < 2; ++h) {        // channel 16 d + 8 h + lane / 4
+                    const uint16_t x = *reinterpret_cast<const uint16_t*>(v + (((d * 2 + h) ^ (j & 7)) << 4) + row_c * 2);
+                    o[t][d][2 * h + e] += w[e] * bf16_bits_to_f32(x);
+                  }
+              }
             }
           }
-        }
       } else {
 #pragma unroll
         for (int d = 0; d < KS; ++d) {
           if (d * 16 >= a.D) break;
-          float x[4] = {0.f, 0.f, 0.f, 0.f};
+          // For an fp32 o the sums of a block are formed by themselves and added in fp32: the tensor cores cut their sums off,
+          // which over a long cache would lean one way.
+          float x[NT][4] = {};
 #pragma unroll
           for (int mb = 0; mb < MB; ++mb) {
             uint32_t vf[4];
             ldmatrix4_trans(vf, ((vs + v_frag) ^ (d << 5)) + mb * 16 * C::kRowBytes);
-            if constexpr (BF_OUT) {
-              mma16816(o[d], vf, pf[mb][0][0], pf[mb][0][1]);
-              mma16816(o[d], vf, pf[mb][1][0], pf[mb][1][1]);
-            } else {
-              // the tensor cores cut their sums off, which over a long cache would lean one way: those of a block
-              // are formed by themselves and added in fp32
 #pragma unroll
-              for (int y = PARTS - 1; y >= 0; --y) mma16816(x, vf, pf[mb][y][0], pf[mb][y][1]);
-            }
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int y = PARTS - 1; y >= 0; --y) mma16816(BF_OUT ? o[t][d] : x[t], vf, pf[t][mb][y][0], pf[t][mb][y][1]);
           }
           if constexpr (!BF_OUT) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[d][e] += x[e];
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[t][d][e] += x[t][e];
           }
         }
       }
@@ -596,11 +615,15 @@ __global__ void __launch_bounds__(kThreads, Mma<DP, RW>::kCtas)
 
     // the groups' sums, over the rings
     cp_async_wait<0>();
-    float zero = 0.f * (l[0] + l[1]);
+    float zero = 0.f;
 #pragma unroll
-    for (int d = 0; d < KS; ++d)
+    for (int t = 0; t < NT; ++t) {
+      zero = fmaf(l[t][0] + l[t][1], 0.f, zero);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) zero = fmaf(o[d][e], 0.f, zero);
+      for (int d = 0; d < KS; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) zero = fmaf(o[t][d][e], 0.f, zero);
+    }
     const bool finite = !__syncthreads_or(!(zero == 0.f));
     if (!finite && !exact) {
       exact = true;
@@ -609,22 +632,24 @@ __global__ void __launch_bounds__(kThreads, Mma<DP, RW>::kCtas)
     exact = false;
     float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float x = l[e];
-      x += __shfl_xor_sync(0xffffffffu, x, 4);
-      x += __shfl_xor_sync(0xffffffffu, x, 8);
-      x += __shfl_xor_sync(0xffffffffu, x, 16);
-      float* to = sums + (group * C::kRows + row_warp * 8 + piece_c * 2 + e) * (DP + 2);
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int d = 0; d < KS; ++d) {
-        to[d * 16 + row_c] = o[d][e];
-        to[d * 16 + 8 + row_c] = o[d][e + 2];
+      for (int e = 0; e < 2; ++e) {
+        float x = l[t][e];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        float* to = sums + (group * C::kRows + (row_warp * NT + t) * 8 + piece_c * 2 + e) * (DP + 2);
+#pragma unroll
+        for (int d = 0; d < KS; ++d) {
+          to[d * 16 + row_c] = o[t][d][e];
+          to[d * 16 + 8 + row_c] = o[t][d][e + 2];
+        }
+        if (row_c == 0) {
+          to[DP] = m[t][e];
+          to[DP + 1] = x;
+        }
       }
-      if (row_c == 0) {
-        to[DP] = m[e];
-        to[DP + 1] = x;
-      }
-    }
     __syncthreads();
     float* part = nullptr;
     if (n < r.tiles) part = parts + (2 * static_cast<int64_t>(blockIdx.x) + (walk.tile > 0 ? 0 : 1)) * part_floats(C::kRows, a.D);
@@ -960,45 +985,49 @@ __global__ void __launch_bounds__(kThreads, Simt<DP, R>::kCtas)
 
 // ------------------------------------------------------------------ joining
 
-// Block (x, r): row r of the item that note_joins left at place x, which stretch c is the first to begin inside.  Parts
-// c - 1 (its second place) and c, c + 1, .. (their first places) are added in a fixed order: a warp takes every eighth part, then the
-// warps' sums are added.
-constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps, kJoinDepth = 4;
+// Row r of the item that note_joins left at place x, which stretch c is the first to begin inside: parts c - 1 (its second
+// place) and c, c + 1, .. (their first places) are added in a fixed order.  WPR warps take a row, every WPR-th part each,
+// kJoinDepth of them in flight, then their sums are added.  Eight warps where an item has many parts (41 of each of 16 rows:
+// the call takes 9.8 us, 14.9 with one warp), one where items are many and have few (two or three of each of 64 rows
+// of 256 items: 149 us with eight, whose blocks' launches set the pace, 110 with one).
+constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps, kJoinDepth = 4, kFewParts = 8;
 
-template <bool BF_OUT>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttentionArgs a, int row_tiles, int tile_rows,
-                                                            const Join* joins, const float* parts) {
+template <int WPR, bool BF_OUT>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttentionArgs a, int row_tiles, int tile_rows, int rows_of_item,
+                                                            int all_rows, const Join* joins, const float* parts) {
   __shared__ float2 warp_ml[kJoinWarps];
   __shared__ float4 warp_o[kJoinWarps][64];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 raw = __ldcg(reinterpret_cast<const int4*>(joins) + blockIdx.x);
-  const Join j{raw.x, raw.y, raw.z, raw.w};
-  if (j.parts == 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int hk = j.item / row_tiles, row0 = (j.item - hk * row_tiles) * tile_rows, r = blockIdx.y;
-  if (row0 + r >= a.W * (a.H / a.HK)) return;
+  const int index = blockIdx.x * (kJoinWarps / WPR) + warp / WPR, place = index / rows_of_item, r = index - place * rows_of_item;
+  Join j{0, 0, 0, 0};
+  if (index < all_rows) {
+    const int4 raw = __ldcg(reinterpret_cast<const int4*>(joins) + place);
+    j = Join{raw.x, raw.y, raw.z, raw.w};
+  }
+  const int hk = j.item / row_tiles, row0 = (j.item - hk * row_tiles) * tile_rows;
+  if (row0 + r >= a.W * (a.H / a.HK)) j.parts = 0;
+  if (WPR == kJoinWarps && j.parts == 0) return;          // otherwise warps of a block may have rows while others have none
   const int64_t stride = part_floats(tile_rows, a.D);
   const auto part_of = [&](int i) {
     return parts + stride * (i == 0 ? 2 * (static_cast<int64_t>(j.stretch) - 1) + 1 : 2 * (static_cast<int64_t>(j.stretch) + i - 1));
-  };
-  const auto ml_of = [&](int i) {
-    return __ldcg(reinterpret_cast<const float2*>(part_of(i) + static_cast<int64_t>(tile_rows) * a.D) + r);
   };
   // a lane holds pieces of four channels lane, + 32
   const int pieces = a.D / 4;
   float m = -INFINITY, l = 0.f;
   float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-  for (int i0 = warp; i0 < j.parts; i0 += kJoinWarps * kJoinDepth) {
+  for (int i0 = warp % WPR; i0 < j.parts; i0 += WPR * kJoinDepth) {
     float2 ml[kJoinDepth];
     float4 x[kJoinDepth][2];
 #pragma unroll
     for (int y = 0; y < kJoinDepth; ++y) {
-      const int i = i0 + y * kJoinWarps;
+      const int i = i0 + y * WPR;
       ml[y] = make_float2(-INFINITY, 0.f);
       x[y][0] = x[y][1] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < j.parts) {
-        ml[y] = ml_of(i);
-        const float4* p = reinterpret_cast<const float4*>(part_of(i) + static_cast<int64_t>(r) * a.D);
+        const float* part = part_of(i);
+        ml[y] = __ldcg(reinterpret_cast<const float2*>(part + static_cast<int64_t>(tile_rows) * a.D) + r);
+        const float4* p = reinterpret_cast<const float4*>(part + static_cast<int64_t>(r) * a.D);
         if (lane < pieces) x[y][0] = __ldcg(p + lane);
         if (lane + 32 < pieces) x[y][1] = __ldcg(p + lane + 32);
       }
@@ -1029,32 +1058,45 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttentionArgs 
     }
     m = now;
   }
-  if (lane == 0) warp_ml[warp] = make_float2(m, l);
-#pragma unroll
-  for (int e = 0; e < 2; ++e)
-    if (lane + 32 * e < pieces) warp_o[warp][lane + 32 * e] = o[e];
-  __syncthreads();
-  m = -INFINITY;
-  l = 0.f;
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, warp_ml[w].x);
-  const float base = m == -INFINITY ? 0.f : m;
-  float f[kJoinWarps];
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
-    f[w] = ex2(warp_ml[w].x - base);
-    l += f[w] * warp_ml[w].y;
-  }
   const RowPlace at = row_place(a, j.seq, hk, row0 + r);
-  const int d = 2 * threadIdx.x;
-  if (d < a.D) {
-    float2 x = make_float2(0.f, 0.f);
+  if constexpr (WPR == 1) {
+    if (j.parts == 0) return;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w)
-      x = fma2(make_float2(f[w], f[w]), reinterpret_cast<const float2*>(warp_o[w])[threadIdx.x], x);
-    store_out2<BF_OUT>(a, at.o * a.D + d, l == 0.f ? make_float2(0.f, 0.f) : make_float2(x.x / l, x.y / l));
+    for (int e = 0; e < 2; ++e)
+      if (lane + 32 * e < pieces) {
+        const int64_t to = at.o * a.D + 4 * (lane + 32 * e);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        store_out2<BF_OUT>(a, to, l == 0.f ? make_float2(0.f, 0.f) : make_float2(o[e].x * inv, o[e].y * inv));
+        store_out2<BF_OUT>(a, to + 2, l == 0.f ? make_float2(0.f, 0.f) : make_float2(o[e].z * inv, o[e].w * inv));
+      }
+  } else {
+    if (lane == 0) warp_ml[warp] = make_float2(m, l);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (lane + 32 * e < pieces) warp_o[warp][lane + 32 * e] = o[e];
+    __syncthreads();
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, warp_ml[w].x);
+    const float base = m == -INFINITY ? 0.f : m;
+    float f[kJoinWarps];
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      f[w] = ex2(warp_ml[w].x - base);
+      l += f[w] * warp_ml[w].y;
+    }
+    const int d = 2 * threadIdx.x;
+    if (d < a.D) {
+      float2 x = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w)
+        x = fma2(make_float2(f[w], f[w]), reinterpret_cast<const float2*>(warp_o[w])[threadIdx.x], x);
+      store_out2<BF_OUT>(a, at.o * a.D + d, l == 0.f ? make_float2(0.f, 0.f) : make_float2(x.x / l, x.y / l));
+    }
   }
-  if (threadIdx.x == 0 && a.lse) a.lse[at.o] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  if ((WPR == 1 ? lane : static_cast<int>(threadIdx.x)) == 0 && a.lse)
+    a.lse[at.o] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // ------------------------------------------------------------------ host
@@ -1066,7 +1108,8 @@ struct Variant {
 };
 Variant variant_of(bool bf16, int D, int rows) {
   if (!bf16) return Variant{rows > 4 ? 8 : rows > 2 ? 4 : 2, D > 64 ? 2 : 3};
-  return Variant{rows > 16 ? 32 : rows > 8 ? 16 : 8, D > 128 ? 2 : 3};
+  if (D > 128) return Variant{rows > 16 ? 32 : rows > 8 ? 16 : 8, 2};
+  return rows > 8 ? Variant{rows > 32 ? 64 : rows > 16 ? 32 : 16, 2} : Variant{8, 3};
 }
 
 int stretches_of(const Variant& v) { return std::min(kMaxStretches, sm_count() * v.ctas); }
@@ -1092,9 +1135,14 @@ cudaError_t launch(const AttentionArgs& a, bool bf16, cudaStream_t st) {
   const auto of_width = [&](auto dp) {
     constexpr int DP = decltype(dp)::value;
     if (bf16) {
-      if (v.rows == 8) return run<attend_bf16_kernel<DP, 1, BF_OUT>, Mma<DP, 1>>(a, tiles, n, join_blocks, joins, parts, st);
-      if (v.rows == 16) return run<attend_bf16_kernel<DP, 2, BF_OUT>, Mma<DP, 2>>(a, tiles, n, join_blocks, joins, parts, st);
-      return run<attend_bf16_kernel<DP, 4, BF_OUT>, Mma<DP, 4>>(a, tiles, n, join_blocks, joins, parts, st);
+      if (v.rows == 8) return run<attend_bf16_kernel<DP, 1, 1, BF_OUT>, Mma<DP, 1, 1>>(a, tiles, n, join_blocks, joins, parts, st);
+      // two tiles a warp where their sums fit the registers: each key and value is read from the ring for both
+      constexpr int NT = DP > 128 ? 1 : 2, RW = 2 / NT;
+      if (v.rows == 16) return run<attend_bf16_kernel<DP, RW, NT, BF_OUT>, Mma<DP, RW, NT>>(a, tiles, n, join_blocks, joins, parts, st);
+      if (v.rows == 32)
+        return run<attend_bf16_kernel<DP, 2 * RW, NT, BF_OUT>, Mma<DP, 2 * RW, NT>>(a, tiles, n, join_blocks, joins, parts, st);
+      if constexpr (NT == 2)
+        return run<attend_bf16_kernel<DP, 4, 2, BF_OUT>, Mma<DP, 4, 2>>(a, tiles, n, join_blocks, joins, parts, st);
     }
     if (v.rows == 2) return run<attend_f32_kernel<DP, 2, BF_OUT>, Simt<DP, 2>>(a, tiles, n, join_blocks, joins, parts, st);
     if (v.rows == 4) return run<attend_f32_kernel<DP, 4, BF_OUT>, Simt<DP, 4>>(a, tiles, n, join_blocks, joins, parts, st);
@@ -1105,8 +1153,10 @@ cudaError_t launch(const AttentionArgs& a, bool bf16, cudaStream_t st) {
                    : of_width(std::integral_constant<int, 256>{});
   if (e != cudaSuccess) return e;
   // launched while the stretches still run: its blocks wait for them on the device
+  const int rows_of_item = std::min(v.rows, rows), all_rows = join_blocks * rows_of_item;
+  const bool few = static_cast<int64_t>(a.B) * a.HK * tiles * kFewParts >= n;            // parts of an item, about
   cudaLaunchConfig_t config = {};
-  config.gridDim = dim3(join_blocks, std::min(v.rows, rows));
+  config.gridDim = dim3(few ? (all_rows + kJoinWarps - 1) / kJoinWarps : all_rows);
   config.blockDim = dim3(kJoinThreads);
   config.stream = st;
   cudaLaunchAttribute attribute;
@@ -1114,8 +1164,8 @@ cudaError_t launch(const AttentionArgs& a, bool bf16, cudaStream_t st) {
   attribute.val.programmaticStreamSerializationAllowed = 1;
   config.attrs = &attribute;
   config.numAttrs = 1;
-  return cudaLaunchKernelEx(&config, join_kernel<BF_OUT>, a, tiles, v.rows, static_cast<const Join*>(joins),
-                            static_cast<const float*>(parts));
+  return cudaLaunchKernelEx(&config, few ? join_kernel<1, BF_OUT> : join_kernel<kJoinWarps, BF_OUT>, a, tiles, v.rows,
+                            rows_of_item, all_rows, static_cast<const Join*>(joins), static_cast<const float*>(parts));
 }
 
 }  // namespace
