@@ -248,7 +248,7 @@ kda_status_t kda_cache_update(const kda_cache_rows_params_t* p, const int32_t* b
   if (s != KDA_OK) return s;
   const bool in = p->rows > 0, out = p->rows_out > 0, pages = p->num_pages > 0, wide = p->max_pages > 0;
   if ((in && !lens) || (in && wide && !block_table) || (pages && (!refs || !out_refs)) || (out && wide && !out_table) ||
-      (out && (!new_lens || !out_lens || !kept || !copy_src || !copy_dst)) || (!parent && p->rows != p->rows_out))
+      (out && (!new_lens || !out_lens || !kept || !copy_src || !copy_dst)) || (out && !parent && p->rows != p->rows_out))
     return KDA_ERR_INVALID_ARG;
   for (const void* x : {static_cast<const void*>(block_table), static_cast<const void*>(lens), static_cast<const void*>(refs),
                         static_cast<const void*>(parent), static_cast<const void*>(new_lens),

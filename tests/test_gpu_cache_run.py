@@ -1,11 +1,14 @@
 """The key-value cache's tables on the GPU against `oracle/cache.py`, and the operators together as a
 hybrid model's server runs them: streams, captured graphs, forks beside the recurrent states."""
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
 
 import gated_delta_rule_deltanet_gb300 as kda
-from gated_delta_rule_deltanet_gb300 import _lib
+from gated_delta_rule_deltanet_gb300 import _lib, build as kbuild
 from oracle import cache as oc
 
 pytestmark = pytest.mark.gpu
@@ -465,3 +468,63 @@ def test_an_attention_sublayer_is_trained_through_its_rotation():
     for a, b in zip(*grads):
         # both in fp32 through a softmax of sums of 16 products: a few hundred roundings of terms up to |q| |k| ~ 40
         assert torch.allclose(a, b, rtol=1e-4, atol=1e-4)
+
+
+def test_tables_of_nothing():
+    z = dict(dtype=torch.int32, device=DEV)
+    r = kda.cache_update(torch.empty((0, 4), **z), ints([]), ints([0, 0, 2]), ints([-1, -1]), ints([3, 0]), page_size=2)
+    assert r.table.cpu().tolist() == [[0, 1, -1, -1], [-1] * 4] and r.refs.cpu().tolist() == [1, 1, 2]
+    r = kda.cache_update(torch.empty((0, 4), **z), ints([]), ints([]), None, ints([]), page_size=2)
+    assert r.table.shape == (0, 4)
+    r = kda.cache_update(ints([[1]]), ints([2]), ints([0, 1]), ints([]), ints([]), page_size=2)       # every row ends
+    assert r.refs.cpu().tolist() == [0, 0]
+    c = kda.cache_compact(torch.empty((0, 4), **z), ints([]), ints([0, 3, 0]), page_size=2)
+    assert c.page_map.cpu().tolist() == [-1, 0, -1]
+    c = kda.cache_compact(torch.full((2, 1), -1, **z), ints([0, 0]), ints([]), page_size=2)
+    assert torch.all(c.table == -1)
+    no_error()
+
+
+def test_update_asks_for_more_pages_than_there_are_in_all():
+    """Needs whose sum passes 2^31."""
+    S, width = 40000, 60000
+    table = torch.empty((0, width), dtype=torch.int32, device=DEV)
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GB")
+    r = kda.cache_update(table, ints([]), ints([0] * 50), ints([-1] * S), ints([width] * S), page_size=1)
+    page_error()
+    assert not r.lens.any() and not r.refs.any()
+
+
+FIRST_CALLS = """
+import torch
+import gated_delta_rule_deltanet_gb300 as kda
+dev = "cuda:0"
+f = torch.tensor([1.0, 0.5, 0.25, 0.125], dtype=torch.float64, device=dev)
+x = torch.randn((3, 2, 64), device=dev).bfloat16()
+y = torch.randn((3, 2, 32), device=dev)
+pages = [torch.randn((9, 4, 2, 64), device=dev).bfloat16() for _ in range(2)]
+wide = [torch.randn((9, 4, 2, 32), device=dev) for _ in range(2)]
+i = lambda *a: torch.tensor(a, dtype=torch.int32, device=dev)
+table, lens, refs = torch.tensor([[0, 1], [2, -1], [3, -1]], dtype=torch.int32, device=dev), i(5, 1, 4), i(1, 1, 1, 1, 0, 0, 0, 0, 0)
+parent, new, start = i(0, 0, 2), i(6, 6, 5), i(4, 0, 3)
+
+def calls():
+    a = kda.cache_append(x, x, x, f, *pages, table, start)
+    return [a, *kda.rotary(x, x, start, f), kda.cache_attention(a, *pages, table, lens),
+            kda.cache_attention(y, *wide, table, lens),
+            *kda.cache_update(table, lens, refs, parent, new, page_size=4, pools=pages),
+            *kda.cache_compact(table, lens, refs, page_size=4, pools=wide)]
+
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    captured = calls()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(captured, calls())) and kda.get_device_error() == 0
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    subprocess.run([sys.executable, "-c", FIRST_CALLS], check=True, cwd=kbuild.ROOT, timeout=300)
