@@ -11,20 +11,26 @@
 // 2018) in base 2.  A row that sees no key has o = 0 and lse = -infinity.
 //
 // Bound by HBM: each key and value is read once for all rows of its group (queries x heads of one key head).
-// The work is cut into tiles of 4 x BK keys of a (sequence, key head) and the row of all tiles into equal stretches,
-// one for each CTA, whatever the sequences' lengths: a stretch that begins or ends inside a (sequence, key
-// head) leaves (m, l, unnormalised o) of its part in the workspace, and a second kernel joins the parts in the
-// order of the stretches, so that repeated calls give the same bits.  The lengths stay on the device: a captured
-// graph follows them.
+// The work is cut into tiles of keys of an item (a sequence, a key head and up to 64 of its rows), and the row of all
+// tiles into equal stretches, one for each CTA, whatever the sequences' lengths: a stretch that begins or ends inside an
+// item leaves (m, l, unnormalised o) of its part in the workspace, and a second kernel joins the parts in the order of
+// the stretches, so that repeated calls give the same bits.  The lengths stay on the device: a captured graph follows
+// them.
 //
-// Inside a CTA each of four warps takes every fourth block of BK keys, copies it into its own ring in shared
-// memory (cp.async, rows of 16-byte pieces stored at piece ^ (row mod 8)) and keeps its own m, l and o, so that the
-// warps wait for one another only where a part ends.
+// Inside a CTA four warps form groups of one, two or four, as the rows of an item ask for.  A group takes every
+// so many-th block of keys, copies it into a ring of its own in shared memory (cp.async, rows of 16-byte pieces stored at
+// piece ^ (row mod 8)) and keeps m, l and o for itself, so that groups wait for one another only where a piece ends.
 //
-//   bf16   BK = 16: scores and o by mma.m16n8k16 with fp32 accumulators, the rows as M.  A window's rows are
-//          few: at 16 rows the products take a fifth of the time that the copies take, so the tensor memory path,
-//          whose smallest M is 64 and whose accumulators come back through tcgen05.ld, would have nothing to give.
-//   fp32   BK = 8: fp32 on CUDA cores (tensor cores would round the operands to tf32).
+//   bf16   products by mma.sync with fp32 accumulators: at eight rows the tensor pipe is active for 14% of the time that
+//          the copies take, so the tensor memory path, whose smallest M is 64 and whose accumulators come back through
+//          tcgen05.ld, would have nothing to give.
+//   fp32   CUDA cores throughout.  Products of two tf32 parts on tensor cores took 282 us where these take 194 (64
+//          sequences, 1.2 GB) and left 1.2e-6 of the norm where these leave 1.2e-7.
+//
+// One GB300 (of measured HBM): 256 sequences of 256 to 8192 keys, 8 key heads of 128, 2.2 GB of bf16 pages 345-356 us
+// (92-95%); 3 sequences of up to 262144 keys 150-156 us (91-95%); heads of 64 75-81%, of 256 79%; 32 and 64 rows a key
+// head 76% and 31%; fp32 pages 87-93% with two rows, 75% with eight.  One sequence of 5000 keys 9.8 us: a chain of some
+// 12 k cycles through both kernels.
 #include <algorithm>
 #include <type_traits>
 
@@ -37,8 +43,9 @@ namespace {
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// A stretch is counted in tiles and what an item costs beside them: the ring runs empty at its end, and the
-// warps' sums are joined.
+// A stretch is counted in units: tiles, and what an item costs beside them (the ring runs empty at its end, and the
+// groups' sums are joined).  61 short sequences with costs of 1, 2 and 4: 31.5, 29.5, 33.2 us; one sequence of 5000 keys
+// in stretches of 2 units 9.9 us, of 4 12.1.
 constexpr int kItemCost = 2, kMinUnits = 2;
 
 // A running maximum follows the scores only when one is this far above it (in powers of two): sums grow by up
@@ -74,7 +81,9 @@ struct Walk {                                // a stretch, item by item
   int left;                                  // units still to do
   int n, k, rest, begin;                     // n stretches; stretch i begins at unit i k + i rest / n
   Range r;
-  __device__ __forceinline__ int begin_of(int i) const { return i * k + static_cast<uint32_t>(i * rest) / static_cast<uint32_t>(n); }
+  __device__ __forceinline__ int begin_of(int i) const {
+    return i * k + static_cast<uint32_t>(i * rest) / static_cast<uint32_t>(n);
+  }
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
@@ -297,7 +306,8 @@ struct Mma {
   static constexpr int kTop = kRing > kPart ? kRing : kPart;
   static constexpr int kQ = kRows * kRowBytes;
   static constexpr size_t kSmem = kTop + kQ;
-  static constexpr int kCtas = DP == 256 || NT == 2 ? 2 : 3;   // an SM, by shared memory and registers
+  // an SM, by shared memory and registers; four with rings of three halves: 352 us where three take 345 (2.2 GB)
+  static constexpr int kCtas = DP == 256 || NT == 2 ? 2 : 3;
 };
 
 // Scores and sums transposed: S^T = K Q^T and O^T += V^T P^T, keys and channels as the M of m16n8k16, rows
@@ -381,7 +391,8 @@ __global__ void __launch_bounds__(kThreads, Mma<DP, RW, NT>::kCtas)
 #pragma unroll
         for (int c = 0; c < CH / 4; ++c)
           if (c * 4 + piece_c < pieces)
-            cp_async16(dst + ((c & 1) ? to_odd : to_even) + (c >> 1) * 128 + x * 8 * C::kRowBytes, src + (ok ? c * 32 : 0), ok);
+            cp_async16(dst + ((c & 1) ? to_odd : to_even) + (c >> 1) * 128 + x * 8 * C::kRowBytes,
+                       src + (ok ? c * 32 : 0), ok);
       }
     };
     const auto issue = [&](int h) {
@@ -591,8 +602,8 @@ __global__ void __launch_bounds__(kThreads, Mma<DP, RW, NT>::kCtas)
 #pragma unroll
         for (int d = 0; d < KS; ++d) {
           if (d * 16 >= a.D) break;
-          // For an fp32 o the sums of a block are formed by themselves and added in fp32: the tensor cores cut their sums off,
-          // which over a long cache would lean one way.
+          // For an fp32 o the sums of a block are formed by themselves and added in fp32: the tensor cores cut their sums
+          // off, which over a long cache would lean one way.
           float x[NT][4] = {};
 #pragma unroll
           for (int mb = 0; mb < MB; ++mb) {
@@ -652,7 +663,8 @@ __global__ void __launch_bounds__(kThreads, Mma<DP, RW, NT>::kCtas)
       }
     __syncthreads();
     float* part = nullptr;
-    if (n < r.tiles) part = parts + (2 * static_cast<int64_t>(blockIdx.x) + (walk.tile > 0 ? 0 : 1)) * part_floats(C::kRows, a.D);
+    if (n < r.tiles)
+      part = parts + (2 * static_cast<int64_t>(blockIdx.x) + (walk.tile > 0 ? 0 : 1)) * part_floats(C::kRows, a.D);
     finish_piece<DP, C::kRows, C::kGroups, BF_OUT>(a, sums, b, hk, row0, rows, part);
     if (!part && tid == 0) note_whole(a, walk, items, join_blocks, joins);
     piece_done<C::kGroups * BK>(a, items, walk);
@@ -740,7 +752,8 @@ __global__ void __launch_bounds__(kThreads, Simt<DP, R>::kCtas)
 #pragma unroll
         for (int c = 0; c < CH / 4; ++c)
           if (c * 4 + piece_c < pieces)
-            cp_async16(dst + ((c & 1) ? to_odd : to_even) + (c >> 1) * 128 + x * 8 * C::kRowBytes, src + (ok ? c * 16 : 0), ok);
+            cp_async16(dst + ((c & 1) ? to_odd : to_even) + (c >> 1) * 128 + x * 8 * C::kRowBytes,
+                       src + (ok ? c * 16 : 0), ok);
       }
     };
     const auto issue = [&](int h) {
@@ -975,7 +988,8 @@ __global__ void __launch_bounds__(kThreads, Simt<DP, R>::kCtas)
     }
     __syncthreads();
     float* part = nullptr;
-    if (n < r.tiles) part = parts + (2 * static_cast<int64_t>(blockIdx.x) + (walk.tile > 0 ? 0 : 1)) * part_floats(C::kRows, a.D);
+    if (n < r.tiles)
+      part = parts + (2 * static_cast<int64_t>(blockIdx.x) + (walk.tile > 0 ? 0 : 1)) * part_floats(C::kRows, a.D);
     finish_piece<DP, R, kWarps, BF_OUT>(a, sums, b, hk, row0, rows, part);
     if (!part && tid == 0) note_whole(a, walk, items, join_blocks, joins);
     piece_done<kWarps * BK>(a, items, walk);
@@ -993,13 +1007,15 @@ __global__ void __launch_bounds__(kThreads, Simt<DP, R>::kCtas)
 constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps, kJoinDepth = 4, kFewParts = 8;
 
 template <int WPR, bool BF_OUT>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttentionArgs a, int row_tiles, int tile_rows, int rows_of_item,
-                                                            int all_rows, const Join* joins, const float* parts) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttentionArgs a, int row_tiles, int tile_rows,
+                                                            int rows_of_item, int all_rows, const Join* joins,
+                                                            const float* parts) {
   __shared__ float2 warp_ml[kJoinWarps];
   __shared__ float4 warp_o[kJoinWarps][64];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int index = blockIdx.x * (kJoinWarps / WPR) + warp / WPR, place = index / rows_of_item, r = index - place * rows_of_item;
+  const int index = blockIdx.x * (kJoinWarps / WPR) + warp / WPR;
+  const int place = index / rows_of_item, r = index - place * rows_of_item;
   Join j{0, 0, 0, 0};
   if (index < all_rows) {
     const int4 raw = __ldcg(reinterpret_cast<const int4*>(joins) + place);
@@ -1010,7 +1026,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttentionArgs 
   if (WPR == kJoinWarps && j.parts == 0) return;          // otherwise warps of a block may have rows while others have none
   const int64_t stride = part_floats(tile_rows, a.D);
   const auto part_of = [&](int i) {
-    return parts + stride * (i == 0 ? 2 * (static_cast<int64_t>(j.stretch) - 1) + 1 : 2 * (static_cast<int64_t>(j.stretch) + i - 1));
+    const int64_t c = j.stretch;
+    return parts + stride * (i == 0 ? 2 * (c - 1) + 1 : 2 * (c + i - 1));
   };
   // a lane holds pieces of four channels lane, + 32
   const int pieces = a.D / 4;
@@ -1115,7 +1132,8 @@ Variant variant_of(bool bf16, int D, int rows) {
 int stretches_of(const Variant& v) { return std::min(kMaxStretches, sm_count() * v.ctas); }
 
 template <auto K, typename Config>
-cudaError_t run(const AttentionArgs& a, int row_tiles, int stretches, int join_blocks, Join* joins, float* parts, cudaStream_t st) {
+cudaError_t run(const AttentionArgs& a, int row_tiles, int stretches, int join_blocks, Join* joins, float* parts,
+                cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = raise_smem(K, Config::kSmem, done);
   if (e != cudaSuccess) return e;
@@ -1132,21 +1150,29 @@ cudaError_t launch(const AttentionArgs& a, bool bf16, cudaStream_t st) {
   float* parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kMaxStretches * sizeof(Join));
   cudaError_t e;
   const int join_blocks = static_cast<int>(std::min<int64_t>(n, static_cast<int64_t>(a.B) * a.HK * tiles));
+  const auto bf16_of = [&](auto dp, auto rw, auto nt) {
+    constexpr int DP = decltype(dp)::value, RW = decltype(rw)::value, NT = decltype(nt)::value;
+    return run<attend_bf16_kernel<DP, RW, NT, BF_OUT>, Mma<DP, RW, NT>>(a, tiles, n, join_blocks, joins, parts, st);
+  };
+  const auto f32_of = [&](auto dp, auto rows_of_tile) {
+    constexpr int DP = decltype(dp)::value, R = decltype(rows_of_tile)::value;
+    return run<attend_f32_kernel<DP, R, BF_OUT>, Simt<DP, R>>(a, tiles, n, join_blocks, joins, parts, st);
+  };
+  using std::integral_constant;
   const auto of_width = [&](auto dp) {
-    constexpr int DP = decltype(dp)::value;
-    if (bf16) {
-      if (v.rows == 8) return run<attend_bf16_kernel<DP, 1, 1, BF_OUT>, Mma<DP, 1, 1>>(a, tiles, n, join_blocks, joins, parts, st);
-      // two tiles a warp where their sums fit the registers: each key and value is read from the ring for both
-      constexpr int NT = DP > 128 ? 1 : 2, RW = 2 / NT;
-      if (v.rows == 16) return run<attend_bf16_kernel<DP, RW, NT, BF_OUT>, Mma<DP, RW, NT>>(a, tiles, n, join_blocks, joins, parts, st);
-      if (v.rows == 32)
-        return run<attend_bf16_kernel<DP, 2 * RW, NT, BF_OUT>, Mma<DP, 2 * RW, NT>>(a, tiles, n, join_blocks, joins, parts, st);
-      if constexpr (NT == 2)
-        return run<attend_bf16_kernel<DP, 4, 2, BF_OUT>, Mma<DP, 4, 2>>(a, tiles, n, join_blocks, joins, parts, st);
+    if (!bf16) {
+      if (v.rows == 2) return f32_of(dp, integral_constant<int, 2>{});
+      if (v.rows == 4) return f32_of(dp, integral_constant<int, 4>{});
+      return f32_of(dp, integral_constant<int, 8>{});
     }
-    if (v.rows == 2) return run<attend_f32_kernel<DP, 2, BF_OUT>, Simt<DP, 2>>(a, tiles, n, join_blocks, joins, parts, st);
-    if (v.rows == 4) return run<attend_f32_kernel<DP, 4, BF_OUT>, Simt<DP, 4>>(a, tiles, n, join_blocks, joins, parts, st);
-    return run<attend_f32_kernel<DP, 8, BF_OUT>, Simt<DP, 8>>(a, tiles, n, join_blocks, joins, parts, st);
+    if (v.rows == 8) return bf16_of(dp, integral_constant<int, 1>{}, integral_constant<int, 1>{});
+    // Two tiles a warp where their sums fit the registers: each key and value is read from the ring for both (64
+    // rows: one pass over the keys instead of two).
+    constexpr int NT = decltype(dp)::value > 128 ? 1 : 2, RW = 2 / NT;
+    constexpr integral_constant<int, NT> nt{};
+    if (v.rows == 16) return bf16_of(dp, integral_constant<int, RW>{}, nt);
+    if (v.rows == 32) return bf16_of(dp, integral_constant<int, 2 * RW>{}, nt);
+    return bf16_of(dp, integral_constant<int, 4>{}, nt);
   };
   e = a.D <= 64    ? of_width(std::integral_constant<int, 64>{})
       : a.D <= 128 ? of_width(std::integral_constant<int, 128>{})

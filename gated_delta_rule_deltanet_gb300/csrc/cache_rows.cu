@@ -18,6 +18,8 @@
 //
 // Both are chains of short passes (count, rank, assign) over at most some million integers, bound by the latency of the
 // passes: one thread-block cluster runs them in one launch, with the cluster's hardware barrier between them.
+// One GB300: 256 rows of up to 250 pages one step on 15 us, with a list of copies that is empty; 64 rows to 512 of up to
+// 960 pages 37 us, 12 of them copies; a compaction that moves 1.15 GB 379 us, 358 of them copies (95% of measured HBM).
 #include <algorithm>
 #include <limits.h>
 
@@ -128,7 +130,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
   __shared__ int64_t warp_sums64[32];
   __shared__ int children[kCounted], shared_pages[kCounted];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x;
-  const int all = kCluster * kThreads, me = rank * kThreads + tid, my_row = warp * kCluster + rank, rows_at_once = kCluster * kWarps;
+  const int all = kCluster * kThreads, me = rank * kThreads + tid;
+  const int my_row = warp * kCluster + rank, rows_at_once = kCluster * kWarps;
   int32_t* counts = a.scratch;
   int32_t* first = counts + a.N;
   int32_t* free_list = first + a.N;

@@ -14,7 +14,9 @@
 // give the quadrant, the rest an argument of at most an eighth of a turn for sincospif.
 //
 // Bound by HBM: every value is read and written once, and the sines (R/2 for each token, whatever its heads) are
-// formed once into shared memory by the block that turns the token's heads.
+// formed once into shared memory by the block that turns the token's heads.  One GB300: 16384 tokens x 40 heads x 128
+// bf16 57 us (87% of measured HBM, 57% of the issue slots), 14 k tokens of 16 + 16 heads with v into pages 67 us (76%), one
+// token of each of 256 sequences 4.7 us.  With every slot's row and place found by division the first took 67 us.
 #include <algorithm>
 
 #include "cache_common.cuh"
@@ -23,6 +25,7 @@ namespace kda {
 
 namespace {
 
+// two rounds: 56.8 us for the first case above and 66.8 for the second, four 56.4 and 69.0
 constexpr int kThreads = 256, kUnroll = 4, kRounds = 2;
 constexpr int kMaxTokens = 16;               // of one block
 constexpr int kTableBytes = 16384;           // its sines and cosines
@@ -119,7 +122,8 @@ enum { kSkipQ = 1, kSkipKV = 2 };
 // A slot is two vectors of VE elements of a row: of pairs (i, i + R/2) (HALF) VE first halves and their partners, otherwise,
 // and of the channels that pass, two behind one another.  A thread has one slot of the row and goes through the rows
 // (of all heads, of all tokens of the block); a slot is read whole before it is written, and no other thread touches it, so
-// the outputs may be the inputs.  Its first slots are loaded before the sines are formed, its next ones before it comes to them.
+// the outputs may be the inputs.  Its first slots are loaded before the sines are formed, its next ones before it comes
+// to them.  Three blocks an SM at 80 registers: 56.4 us where four at 64 take 61.0.
 template <bool BF, int VE, bool HALF>
 __global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryArgs a, const Shape sh) {
   extern __shared__ __align__(16) float2 sines[];        // [tokens][sine_pitch]
@@ -321,14 +325,15 @@ cudaError_t launch(const RotaryArgs& a, cudaStream_t st) {
   int64_t n = std::min<int64_t>(kMaxTokens, std::max<int64_t>(1, kRounds * kUnroll * kThreads / per_token));
   n = std::min<int64_t>(n, std::max<int64_t>(1, a.T / (8 * sm_count())));
   if (a.R)
-    n = std::min<int64_t>(n, std::max<int64_t>(1, kTableBytes / (sine_pitch(a.R / 2) * static_cast<int64_t>(sizeof(float2)))));
+    n = std::min<int64_t>(n, std::max<int64_t>(1, kTableBytes / (sine_pitch(a.R / 2) * int64_t{sizeof(float2)})));
   sh.tokens = static_cast<int32_t>(n);
   const int64_t blocks = (a.T + n - 1) / n;
   // few tokens: their heads are shared out to several blocks, each forming the sines for itself
   const int64_t split = std::max<int64_t>(
       1, std::min<int64_t>((n * per_token + kThreads - 1) / kThreads, 2 * sm_count() / blocks));
   const size_t smem = a.freq ? n * sine_pitch(a.R / 2) * sizeof(float2) : 0;
-  rotary_kernel<BF, VE, HALF><<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(split)), kThreads, smem, st>>>(a, sh);
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(split));
+  rotary_kernel<BF, VE, HALF><<<grid, kThreads, smem, st>>>(a, sh);
   return cudaGetLastError();
 }
 

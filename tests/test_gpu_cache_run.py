@@ -89,6 +89,26 @@ def test_update_without_parents_and_with_another_number_of_rows():
     check_update(table, lens, refs, np.full(5, -1), np.array([0, 1, 4, 5, 32]), 4)
 
 
+@pytest.mark.parametrize("width", [64, 515, 516, 1100])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_update_wide_tables(width, shift):
+    """Rows of several rounds of a warp, by fours and one by one, of tables that begin anywhere."""
+    r = rng(11, width)
+    table, lens, refs = random_tables(r, 9, 2, width, 12000, full=0.9)
+    parent, new = np.array([0, 0, 1, 5, 5, 5, -1, 8]), np.array([0] * 8)
+    new = np.minimum(np.where(parent >= 0, lens[parent] + r.integers(-40, 40, 8), 777), 2 * width).clip(0)
+    ref = oc.update(table, lens, refs, parent, new, 2)
+    t = torch.full((9 * width + shift,), -7, dtype=torch.int32, device=DEV)[shift:].view(9, width)
+    t.copy_(ints(table))
+    o = [torch.empty(n + shift, dtype=torch.int32, device=DEV)[shift:] for n in (8 * width, 8, 12000, 8, 8, 8)]
+    out = kda.CacheRows(o[0].view(8, width), *o[1:])
+    kda.cache_update(t, ints(lens), ints(refs), ints(parent), ints(new), page_size=2, out=out)
+    no_error()
+    for x, y in zip(out, ref):
+        if not isinstance(y, list):
+            assert np.array_equal(x.cpu().numpy(), y)
+
+
 def test_update_references_from_elsewhere():
     """A page that someone outside the table holds is copied before it is written, and stays when its rows end."""
     table, lens, refs = np.array([[0, 1], [2, -1]], np.int32), np.array([6, 3]), np.array([1, 2, 1, 0, 0, 0], np.int32)
