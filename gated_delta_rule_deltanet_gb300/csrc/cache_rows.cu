@@ -19,7 +19,7 @@
 // Both are chains of short passes (count, rank, assign) over at most some million integers, bound by the latency of the
 // passes: one thread-block cluster runs them in one launch, with the cluster's hardware barrier between them.
 // One GB300: 256 rows of up to 250 pages one step on 15 us, with a list of copies that is empty; 64 rows to 512 of up to
-// 960 pages 37 us, 12 of them copies; a compaction that moves 1.15 GB 379 us, 358 of them copies (95% of measured HBM).
+// 960 pages 32 us, 12 of them copies; a compaction that moves 1.15 GB 379 us, 358 of them copies (95% of measured HBM).
 #include <algorithm>
 #include <limits.h>
 
@@ -29,7 +29,11 @@ namespace kda {
 
 namespace {
 
-constexpr int kCluster = 8, kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
+// Entries of the new table and references from which sixteen blocks run instead of eight: what an SM moves bounds large
+// tables, the barriers small ones.  2.0 M entries 139 us by eight, 80 by sixteen; 520 k (with copies) 36.8 and 32.0; 70 k
+// 13.0 and 15.0.
+constexpr int64_t kManyEntries = 1 << 17;
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -62,8 +66,9 @@ __device__ __forceinline__ T block_scan(T x, T* warp_sums, T& total) {
 struct Segment {                             // the pages of one CTA; the first has the rows to see to and none
   int begin, end;
 };
+template <int CL>
 __device__ __forceinline__ Segment segment(int n, int rank) {
-  const int per = (n + kCluster - 2) / (kCluster - 1);
+  const int per = (n + CL - 2) / (CL - 1);
   Segment s;
   s.begin = rank == 0 ? 0 : min(static_cast<int64_t>(rank - 1) * per, static_cast<int64_t>(n));
   s.end = rank == 0 ? 0 : min(s.begin + per, n);
@@ -101,12 +106,12 @@ __device__ __forceinline__ int pages_of(int len, int P, int width) {
 
 // One new row: where it goes on from and what it keeps.
 struct Row {
-  int parent, kept, full, want, end;         // full pages kept; pages of the new row and of its parent (-1: too many)
+  int parent, len, kept, full, want, end;    // full pages kept; pages of the new row and of its parent (-1: too many)
 };
 __device__ __forceinline__ Row row_of(const RowsArgs& a, int i) {
   Row r;
   r.parent = a.parent ? a.parent[i] : i;
-  const int len = a.new_lens[i];
+  const int len = r.len = a.new_lens[i];
   const bool from = r.parent >= 0 && r.parent < a.S;
   const int old = from ? a.lens[r.parent] : 0;
   r.kept = max(0, min(old, len));
@@ -125,13 +130,14 @@ constexpr int kAhead = 8;                    // entries of a row that a lane loa
 //
 // Each pass is a few dependent loads deep; what a pass needs of the rows and tables is loaded ahead of the barrier
 // before it where that barrier does not order it.
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) update_kernel(const RowsArgs a) {
+template <int CL>
+__global__ void __launch_bounds__(kThreads) update_kernel(const RowsArgs a) {
   __shared__ int warp_sums[32];
   __shared__ int64_t warp_sums64[32];
   __shared__ int children[kCounted], shared_pages[kCounted];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x;
-  const int all = kCluster * kThreads, me = rank * kThreads + tid;
-  const int my_row = warp * kCluster + rank, rows_at_once = kCluster * kWarps;
+  const int all = CL * kThreads, me = rank * kThreads + tid;
+  const int my_row = warp * CL + rank, rows_at_once = CL * kWarps;
   int32_t* counts = a.scratch;
   int32_t* first = counts + a.N;
   int32_t* free_list = first + a.N;
@@ -139,14 +145,18 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
   int32_t* place = have + a.S_out;
   int32_t* words = place + a.S_out;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const Segment seg = segment(a.N, rank);
+  const Segment seg = segment<CL>(a.N, rank);
   const auto in_pool = [&](int q) { return static_cast<uint32_t>(q) < static_cast<uint32_t>(a.N); };
 
   // 1. references as they are; free pages of the CTA
   if (rank == 0 && tid == 0) words[0] = 0;
-  // The rows that this warp, and in the first CTA this thread, comes to first, and how an old row goes on: its
+  // The two rows that this warp, and in the first CTA that this thread, comes to first, and how an old row goes on: its
   // children and the full pages that all of them keep, counted by each CTA for itself.
   const Row mine_row = my_row < a.S_out ? row_of(a, my_row) : Row{};
+  const Row next_row = my_row + rows_at_once < a.S_out ? row_of(a, my_row + rows_at_once) : Row{};
+  const auto row_at = [&](int i) {
+    return i == my_row ? mine_row : i == my_row + rows_at_once ? next_row : row_of(a, i);
+  };
   const Row thread_row = tid < a.S_out ? row_of(a, tid) : Row{};
   const bool counted = a.S <= kCounted;
   for (int r = tid; counted && r < a.S; r += kThreads) {
@@ -211,7 +221,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
     }
   }
   for (int i = my_row; i < a.S_out; i += rows_at_once) {
-    const Row r = i == my_row ? mine_row : row_of(a, i);
+    const Row r = row_at(i);
     if (r.want < 0 || r.end < 0) {
       if (lane == 0) fault();
       continue;
@@ -237,7 +247,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
   // 3. the free pages in order; a page in use whose count went below zero was held more often than refs say
   int before = 0, free_pages = 0;
 #pragma unroll
-  for (int c = 0; c < kCluster; ++c) {
+  for (int c = 0; c < CL; ++c) {
     const int n = __ldcg(words + 8 + c);
     if (c < rank) before += n;
     free_pages += n;
@@ -304,8 +314,14 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
   cluster_sync();
 
   // 4. the new rows
-  const int copies = __ldcg(words + 1), mine_have = my_row < a.S_out ? __ldcg(have + my_row) : 0,
-            mine_place = my_row < a.S_out ? __ldcg(place + my_row) : 0;
+  const int copies = __ldcg(words + 1);
+  int hold_of[2], place_of[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int i = my_row + x * rows_at_once;
+    hold_of[x] = i < a.S_out ? __ldcg(have + i) : 0;
+    place_of[x] = i < a.S_out ? __ldcg(place + i) : 0;
+  }
   const bool stop = __ldcg(words) != 0;
   if (stop) {
     if (me == 0) raise_device_error(a.err, KDA_DEVERR_PAGE);
@@ -320,8 +336,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
     return;
   }
   for (int i = my_row; i < a.S_out; i += rows_at_once) {
-    const Row r = i == my_row ? mine_row : row_of(a, i);
-    const int hold = i == my_row ? mine_have : __ldcg(have + i), at = i == my_row ? mine_place : __ldcg(place + i);
+    const Row r = row_at(i);
+    const int nth = i == my_row ? 0 : i == my_row + rows_at_once ? 1 : 2;
+    const int hold = nth == 0 ? hold_of[0] : nth == 1 ? hold_of[1] : __ldcg(have + i);
+    const int at = nth == 0 ? place_of[0] : nth == 1 ? place_of[1] : __ldcg(place + i);
     const int32_t* row = a.table + static_cast<int64_t>(max(r.parent, 0)) * a.width;
     int32_t* out = a.out_table + static_cast<int64_t>(i) * a.width;
     for (int j0 = lane; j0 < a.width; j0 += 32 * kAhead) {
@@ -339,13 +357,15 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
       }
     }
     if (lane == 0) {
-      a.out_lens[i] = a.new_lens[i];
+      a.out_lens[i] = r.len;
       a.kept[i] = r.kept;
     }
   }
 #pragma unroll 4
-  for (int q = seg.begin + tid; q < seg.end; q += kThreads)
-    if (a.refs[q] != 0) a.out_refs[q] = __ldcg(counts + q);
+  for (int q = seg.begin + tid; q < seg.end; q += kThreads) {
+    const int r = a.refs[q], count = __ldcg(counts + q);
+    if (r != 0) a.out_refs[q] = count;
+  }
   for (int i = me; i < a.S_out; i += all) {
     if (i < copies) {
       a.copy_dst[i] = __ldcg(free_list + __ldcg(a.copy_dst + i));
@@ -357,17 +377,18 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) upd
 }
 
 // Scratch of a compaction (int32): [N] the used pages by rank, [N] the free pages by rank, words of the launch:
-// 1 used pages among the first n, 8.. the CTAs' used pages, 16.. their errors.  page_map holds the ranks meanwhile.
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) compact_kernel(const RowsArgs a) {
+// 1 used pages among the first n, 8.. the CTAs' used pages, 32.. their errors.  page_map holds the ranks meanwhile.
+template <int CL>
+__global__ void __launch_bounds__(kThreads) compact_kernel(const RowsArgs a) {
   __shared__ int warp_sums[32];
   __shared__ int stop;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x;
-  const int all = kCluster * kThreads, me = rank * kThreads + tid;
+  const int all = CL * kThreads, me = rank * kThreads + tid;
   int32_t* used_list = a.scratch;
   int32_t* free_list = used_list + a.N;
   int32_t* words = free_list + a.N;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const Segment seg = segment(a.N, rank);
+  const Segment seg = segment<CL>(a.N, rank);
 
   int mine = 0, total;
   bool bad = false;
@@ -383,7 +404,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) com
 
   int before = 0, n = 0;
   bad = false;
-  for (int c = 0; c < kCluster; ++c) {
+  for (int c = 0; c < CL; ++c) {
     const int x = __ldcg(words + 8 + c);
     bad |= x < 0;
     if (c < rank) before += x;
@@ -391,7 +412,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) com
   }
   // A row that names a free page, or a page that is not there, cannot be rewritten; nothing is.
   bool wrong = false;
-  for (int r = rank * kWarps + warp; r < a.S; r += kCluster * kWarps) {
+  for (int r = rank * kWarps + warp; r < a.S; r += CL * kWarps) {
     const int pages = pages_of(a.lens[r], a.P, a.width);
     wrong |= pages < 0;
     for (int j0 = lane; j0 < pages; j0 += 32 * kAhead) {
@@ -423,12 +444,12 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) com
                });
   }
   __syncthreads();
-  if (tid == 0) words[16 + rank] = bad || wrong;
+  if (tid == 0) words[32 + rank] = bad || wrong;
   cluster_sync();
 
   if (tid == 0) {
     int s = 0;
-    for (int c = 0; c < kCluster; ++c) s |= __ldcg(words + 16 + c);
+    for (int c = 0; c < CL; ++c) s |= __ldcg(words + 32 + c);
     stop = s;
   }
   __syncthreads();
@@ -462,7 +483,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) com
     a.copy_dst[i] = moves ? __ldcg(free_list + i) : -1;
   }
   cluster_sync();
-  for (int r = rank * kWarps + warp; r < a.S; r += kCluster * kWarps) {
+  for (int r = rank * kWarps + warp; r < a.S; r += CL * kWarps) {
     const int pages = pages_of(a.lens[r], a.P, a.width);
     const int64_t at = static_cast<int64_t>(r) * a.width;
     for (int j0 = lane; j0 < a.width; j0 += 32 * kAhead) {
@@ -542,17 +563,60 @@ cudaError_t copy(const Pools& pools, int num_pools, int64_t bytes, const int32_t
 }  // namespace
 
 size_t cache_rows_workspace(const kda_cache_rows_params_t& p) {
-  return (static_cast<size_t>(3) * p.num_pages + 2 * static_cast<size_t>(p.rows_out) + 32) * sizeof(int32_t);
+  return (static_cast<size_t>(3) * p.num_pages + 2 * static_cast<size_t>(p.rows_out) + 64) * sizeof(int32_t);
 }
 
+namespace {
+
+// One cluster of CL blocks.  Sixteen are more than every device has to grant a cluster: `granted` says whether this one does.
+template <int CL, auto K>
+cudaError_t launch_cluster(const RowsArgs& a, cudaStream_t st, bool* granted = nullptr) {
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3(CL);
+  config.blockDim = dim3(kThreads);
+  config.stream = st;
+  cudaLaunchAttribute attribute;
+  attribute.id = cudaLaunchAttributeClusterDimension;
+  attribute.val.clusterDim = {CL, 1, 1};
+  config.attrs = &attribute;
+  config.numAttrs = 1;
+  if (granted) {
+    static std::atomic<uint64_t> yes{0}, no{0};          // by device, asked once
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+    if (!((yes.load(std::memory_order_relaxed) | no.load(std::memory_order_relaxed)) & bit)) {
+      int n = 0;
+      const bool ok = cudaFuncSetAttribute(K, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                      cudaOccupancyMaxActiveClusters(&n, K, &config) == cudaSuccess && n > 0;
+      if (!ok) cudaGetLastError();
+      (ok ? yes : no).fetch_or(bit, std::memory_order_relaxed);
+    }
+    *granted = (yes.load(std::memory_order_relaxed) & bit) != 0;
+    if (!*granted) return cudaSuccess;
+  }
+  return cudaLaunchKernelEx(&config, K, a);
+}
+
+template <auto K8, auto K16>
+cudaError_t launch_rows(const RowsArgs& a, int64_t entries, cudaStream_t st) {
+  if (entries >= kManyEntries) {
+    bool granted = false;
+    const cudaError_t e = launch_cluster<16, K16>(a, st, &granted);
+    if (e != cudaSuccess || granted) return e;
+  }
+  return launch_cluster<8, K8>(a, st);
+}
+
+}  // namespace
+
 cudaError_t launch_cache_update(const RowsArgs& a, cudaStream_t st) {
-  update_kernel<<<kCluster, kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_rows<update_kernel<8>, update_kernel<16>>(a, static_cast<int64_t>(a.S_out) * a.width + a.N, st);
 }
 
 cudaError_t launch_cache_compact(const RowsArgs& a, cudaStream_t st) {
-  compact_kernel<<<kCluster, kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_rows<compact_kernel<8>, compact_kernel<16>>(a, static_cast<int64_t>(a.S) * a.width + a.N, st);
 }
 
 cudaError_t launch_cache_copy(void* const* pools, const int64_t* bytes, const int64_t* strides, int num_pools,
