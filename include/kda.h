@@ -719,8 +719,9 @@ kda_status_t kda_cache_append(const kda_cache_params_t *p, const void *q, const 
  *   the same time need one each
  * A query that sees no key (p < 0, an empty sequence) gets o = 0 and lse = -infinity.  What a query
  * does not see does not reach it, NaN and infinities included.  Scores, sums and o are formed in
- * fp32; with bf16 pages the products are exact and, where o is bf16, the softmax's weights are rounded to bf16 before
- * they multiply v.  Pages, their strides and q are 16-byte aligned.  Repeated calls give the same bits.
+ * fp32; with bf16 pages the products are exact and the softmax's weights multiply v with 16 bits, with 24 where o is
+ * fp32.  Pages, their strides and q are 16-byte aligned.  Repeated calls give the same bits.  KDA_ERR_UNSUPPORTED:
+ * tables so wide that B HK max_pages page_size passes some 2^33 (2^36 / rows of a key head).
  */
 kda_status_t kda_cache_attention(const kda_cache_params_t *p, const void *q, const void *key_pages,
                                  const void *value_pages, const int32_t *block_table,
