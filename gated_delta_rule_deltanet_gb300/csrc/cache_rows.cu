@@ -121,7 +121,7 @@ __device__ __forceinline__ Row row_of(const RowsArgs& a, int i) {
   return r;
 }
 
-constexpr int kCounted = 4096;               // old rows whose children are counted; more are not, which costs time only
+constexpr int kCounted = 4096;               // old rows whose children are counted; of more, each page is counted singly
 constexpr int kAhead = 8;                    // entries of a row that a lane loads before it uses the first
 
 // Scratch of an update (int32): [N] counts, [N] first open row, [N] free pages in order, [S_out] pages that a row
@@ -193,7 +193,8 @@ __global__ void __launch_bounds__(kThreads) update_kernel(const RowsArgs a) {
 
   // 2. References of the old rows taken back, of the new rows' full pages added; a warp takes a row.  The pages that all
   // children of a row keep change by their number less one, which is nothing for a row that only goes on; beyond
-  // them each child counts its own.
+  // them each child counts its own.  A row that names a free page is found here, whatever is added: what children
+  // add can make up for what the row takes back, and the page would be handed out while they hold it.
   const auto fault = [&]() { atomicExch(words, 1); };
   const auto pages_shared = [&](int r) { return counted && children[r] > 0 ? shared_pages[r] : 0; };
   for (int r = my_row; r < a.S; r += rows_at_once) {
@@ -213,9 +214,12 @@ __global__ void __launch_bounds__(kThreads) update_kernel(const RowsArgs a) {
       for (int x = 0; x < kAhead; ++x) {
         if (q[x] == -1) continue;            // a page that the row has given back
         const int add = j0 + 32 * x < shared ? change : -1;
-        if (!in_pool(q[x])) bad = 1;
-        else if (add) atomicAdd(counts + q[x], add);
-        else bad |= a.refs[q[x]] <= 0;
+        if (!in_pool(q[x])) {
+          bad = 1;
+          continue;
+        }
+        bad |= a.refs[q[x]] <= 0;
+        if (add) atomicAdd(counts + q[x], add);
       }
       if (bad) fault();
     }

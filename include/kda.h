@@ -757,8 +757,10 @@ typedef struct kda_cache_rows_params {
  *   [num_pages]   copy_src, copy_dst [rows_out]: the copies, then -1
  *   workspace >= kda_cache_rows_workspace_size bytes, 256-byte aligned
  * An entry of -1 among a row's pages is one that it has given back (behind a span): it stays -1.
- * The outputs share no memory with the inputs.  With KDA_DEVERR_PAGE (not enough free pages among its
- * reasons) the new rows are empty, out_refs is refs and nothing is to be copied.
+ * The outputs share no memory with the inputs.  With KDA_DEVERR_PAGE (a row that names a free page or one that is
+ * not there, and not enough free pages, among its reasons) the new rows are empty, out_refs is refs and nothing is to be
+ * copied.  refs has to count every reference of the table.  A page that is held more often than it says is
+ * found where it says 0 or where its count would fall below 0; otherwise it is not, and becomes free too early.
  */
 kda_status_t kda_cache_update(const kda_cache_rows_params_t *p, const int32_t *block_table,
                               const int32_t *lens, const int32_t *refs, const int32_t *parent,

@@ -127,3 +127,13 @@ def test_compact_moves_as_few_pages_as_can_be():
     assert np.all(f[:n] > 0) and not f[n:].any() and len(moves) == (refs[n:] > 0).sum()
     assert all(refs[b] == 0 for _, b in moves)
     assert np.array_equal(np.where(table >= 0, where[table], -1), t)
+
+
+@pytest.mark.parametrize("parent", [[0, 1], [1, 1], [0, 0], [-1, -1]])
+@pytest.mark.parametrize("page", range(4))
+def test_update_takes_no_row_that_names_a_free_page(parent, page):
+    table, refs = np.array([[0, 1], [2, 3]], np.int32), np.array([1, 1, 1, 1, 0, 0, 0, 0], np.int32)
+    oc.update(table, [8, 5], refs, parent, [8, 8], 4)
+    refs[page] = 0
+    with pytest.raises(ValueError, match="free page"):
+        oc.update(table, [8, 5], refs, parent, [8, 8], 4)
