@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, Mma<DP, RW, NT>::kCtas)
 #pragma unroll
       for (int x = 0; x < CR; ++x) {
         const int key = base(i) + row_first + 8 * x;
-        to[x] = i < n && key >= r.first && key < r.len ? table[page_div.div(key)] : -2;
+        to[x] = i < n && key >= r.first && key < r.len ? table[page_div.div(key)] : -1;
       }
     };
     const auto copy_half = [&](const void* from, int h) {
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, Mma<DP, RW, NT>::kCtas)
             if (static_cast<uint32_t>(page[x]) < static_cast<uint32_t>(a.num_pages)) {
               const int in_page = key - static_cast<int>(page_div.div(key)) * a.P;
               off[x] = page[x] * a.page_stride + in_page * a.page_row_stride + head;
-            } else if (page[x] != -2) {
+            } else if (key >= r.first && key < r.len) {       // any other entry is a bad one; zeros are read
               raise_device_error(a.err, KDA_DEVERR_PAGE);
             }
           }
@@ -740,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, Simt<DP, R>::kCtas)
 #pragma unroll
       for (int x = 0; x < KL; ++x) {
         const int key = base(i) + row_c + 8 * x;
-        to[x] = i < n && key >= r.first && key < r.len ? table[page_div.div(key)] : -2;
+        to[x] = i < n && key >= r.first && key < r.len ? table[page_div.div(key)] : -1;
       }
     };
     const auto copy_half = [&](const void* from, int h) {
@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, Simt<DP, R>::kCtas)
             if (static_cast<uint32_t>(page[x]) < static_cast<uint32_t>(a.num_pages)) {
               const int in_page = key - static_cast<int>(page_div.div(key)) * a.P;
               off[x] = page[x] * a.page_stride + in_page * a.page_row_stride + head;
-            } else if (page[x] != -2) {
+            } else if (key >= r.first && key < r.len) {       // any other entry is a bad one; zeros are read
               raise_device_error(a.err, KDA_DEVERR_PAGE);
             }
           }

@@ -1,5 +1,7 @@
 """The key-value cache on the GPU where a caller's data are at the edge of what it may hold: tables whose pages
-the references call free.
+the references call free, entries that are out of range.
+
+Tolerances as in `test_gpu_cache.py`: E for the scores, (n / 16 + 64) 2 U for sums, 2 (E + 2^-21) for weights.
 """
 import numpy as np
 import pytest
@@ -11,10 +13,25 @@ from oracle import cache as oc
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
+U = 2.0 ** -24
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def rng(*seed):
+    return np.random.Generator(np.random.PCG64([*seed]))
+
+
+def dev(a, dtype):
+    t = torch.from_numpy(np.ascontiguousarray(a, np.float32)).to(DT[dtype])
+    return t.to(DEV), t.double().numpy()
 
 
 def ints(a):
     return torch.tensor(np.asarray(a), dtype=torch.int32, device=DEV)
+
+
+def host(t):
+    return t.double().cpu().numpy()
 
 
 def no_error():
@@ -25,6 +42,29 @@ def no_error():
 def error():
     torch.cuda.synchronize()
     return kda.get_device_error()
+
+
+def close(name, got, ref, tol):
+    """Element by element, beside half a step of the stored type."""
+    g = host(got)
+    half = torch.finfo(got.dtype).eps / 2
+    lim = np.broadcast_to(tol, ref.shape)
+    lim = lim + half * (np.abs(ref) + lim) + 1e-37
+    assert np.array_equal(np.isfinite(g), np.isfinite(ref)), f"{name}: finite elsewhere"
+    fine = np.isfinite(ref)
+    assert np.array_equal(g[~fine], ref[~fine], equal_nan=True), name
+    off = np.abs(g[fine] - ref[fine]) / lim[fine]
+    assert np.all(off <= 1), f"{name}: off by {off.max()} of what it may be"
+
+
+def reference(q64, k, v, W, out, D, **kw):
+    """o, lse and their tolerances for one sequence."""
+    ref, rl, mass, big, prod = oc.attention(q64, k, v, W, D ** -0.5, **kw)
+    E = 2 * D * U * prod + 8 * U * (1 + big) + 2.0 ** -21
+    sums = (len(k) / 16 + 64) * 2 * U
+    tol = (2 * E + sums + (2.0 ** -16 if out == torch.bfloat16 else 0))[..., None] * mass
+    seen = np.isfinite(rl)
+    return ref, rl, tol, np.where(seen, E + sums + 4 * U * np.abs(np.where(seen, rl, 0)), 0)
 
 
 # ------------------------------------------------------------------------------------------ tables
@@ -52,6 +92,11 @@ def test_update_refuses_a_free_page_of_any_row(parent, new, free):
     refused(np.array([[0, 1], [2, 3]], np.int32), [8, 5], refs, parent, new, 4)
 
 
+def test_update_refuses_a_free_page_whose_changes_cancel():
+    """One row that names it ends, another one forks."""
+    refused(np.array([[0, 1], [0, 3]], np.int32), [8, 5], [0, 1, 1, 1, 0, 0, 0, 0], [-1, 1, 1], [0, 5, 5], 4)
+
+
 @pytest.mark.parametrize("S", [4096, 4097, 6000])
 @pytest.mark.parametrize("fork", [False, True])
 @pytest.mark.parametrize("page", [0, 1])
@@ -69,3 +114,29 @@ def test_update_refuses_a_free_page_of_many_rows(S, fork, page):
     assert np.array_equal(got.table.cpu().numpy(), ref[0]) and np.array_equal(got.refs.cpu().numpy(), ref[2])
     refs[table[17, page]] = 0
     refused(table, [5] * S, refs, parent, new, 4)
+
+
+# --------------------------------------------------------------------------------------- attention
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("entry", [-1, -2, -3, -2 ** 31, 2 ** 31 - 1, 9])
+@pytest.mark.parametrize("at", [0, 1, 2])
+def test_attention_over_a_bad_page_reads_zeros(entry, at, dtype):
+    r = rng(1)
+    lens, P, D = [30, 41, 30], 16, 32
+    table = np.array([[0, 1, -1], [2, 3, 4], [5, 6, -1]], np.int32)
+    (kp, k64), (vp, v64) = (dev(r.standard_normal((9, P, 1, D)), dtype) for _ in range(2))
+    q, q64 = dev(r.standard_normal((3, 2, D)), dtype)
+    good, gl = kda.cache_attention(q, kp, vp, ints(table), ints(lens), return_lse=True)
+    no_error()
+    bad = table.copy()
+    bad[1, at] = entry
+    o, l = kda.cache_attention(q, kp, vp, ints(bad), ints(lens), return_lse=True)
+    assert error() == _lib.KDA_DEVERR_PAGE
+    k64, v64 = (x[[2, 3, 4]].copy() for x in (k64, v64))
+    k64[at], v64[at] = 0, 0
+    ref, rl, tol, ltol = reference(q64[1:2], k64.reshape(-1, 1, D)[:41], v64.reshape(-1, 1, D)[:41], 1, o.dtype, D)
+    close("o", o[1:2], ref, tol)
+    close("lse", l[1:2], rl, ltol)
+    assert torch.equal(o[[0, 2]], good[[0, 2]]) and torch.equal(l[[0, 2]], gl[[0, 2]])
+    no_error()
