@@ -67,7 +67,7 @@ __device__ __forceinline__ Range range_of(const AttentionArgs& a, int b) {
   r.len = a.lens[b];
   if (r.len < 0 || r.len > cap) {
     raise_device_error(a.err, KDA_DEVERR_PAGE);
-    r.len = r.len < 0 ? 0 : cap;
+    r.len = 0;
   }
   r.first = a.span ? static_cast<int>(max(static_cast<int64_t>(0), static_cast<int64_t>(r.len) - a.W - a.span + 1)) : 0;
   r.first = min(r.first, r.len);

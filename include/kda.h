@@ -631,8 +631,9 @@ kda_status_t kda_norm_workspace_size(const kda_norm_params_t *p, int32_t gated, 
  * one table serves all layers.  Entries that a call does not need are not read and may hold -1.
  *
  * Problems only the device can see (a page, length or position out of range) set KDA_DEVERR_PAGE;
- * what they touch is then skipped (an append writes no row, an attention reads zeros, an update or
- * a compaction changes nothing).
+ * what they touch is then skipped: an append writes no row, an attention reads zeros in place of a page and
+ * takes a sequence whose length does not fit its row of the table for an empty one, an update or a compaction changes
+ * nothing.
  */
 
 /* Rotary positions.  head_dim 1..1024, rot_dim even, 0 < rot_dim <= head_dim. */

@@ -1,5 +1,5 @@
 """The key-value cache on the GPU where a caller's data are at the edge of what it may hold: tables whose pages
-the references call free, entries that are out of range.
+the references call free, entries and lengths that are out of range.
 
 Tolerances as in `test_gpu_cache.py`: E for the scores, (n / 16 + 64) 2 U for sums, 2 (E + 2^-21) for weights.
 """
@@ -139,4 +139,23 @@ def test_attention_over_a_bad_page_reads_zeros(entry, at, dtype):
     close("o", o[1:2], ref, tol)
     close("lse", l[1:2], rl, ltol)
     assert torch.equal(o[[0, 2]], good[[0, 2]]) and torch.equal(l[[0, 2]], gl[[0, 2]])
+    no_error()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("W", [1, 4])
+@pytest.mark.parametrize("length", [49, 1000, 2 ** 31 - 1, -1, -2 ** 31])
+def test_a_length_out_of_range_is_an_empty_sequence(length, W, dtype):
+    r = rng(2)
+    lens, P, D = [30, 41, 30], 16, 32
+    table = np.array([[0, 1, -1], [2, 3, 4], [5, 6, -1]], np.int32)
+    kp, vp = (dev(r.standard_normal((9, P, 1, D)), dtype)[0] for _ in range(2))
+    q, _ = dev(r.standard_normal((3 * W, 2, D)), dtype)
+    good, gl = kda.cache_attention(q, kp, vp, ints(table), ints(lens), window=W, return_lse=True)
+    no_error()
+    o, l = kda.cache_attention(q, kp, vp, ints(table), ints([30, length, 30]), window=W, return_lse=True)
+    assert error() == _lib.KDA_DEVERR_PAGE
+    assert not o[W:2 * W].any() and torch.all(l[W:2 * W] == -float("inf"))
+    keep = [i for i in range(3 * W) if i // W != 1]
+    assert torch.equal(o[keep], good[keep]) and torch.equal(l[keep], gl[keep])
     no_error()
