@@ -49,8 +49,28 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kItemCost = 2, kMinUnits = 2;
 
 // A running maximum follows the scores only when one is this far above it (in powers of two): sums grow by up
-// to 2^10 more than they need to, which fp32 holds without loss, and most blocks need no exchange between lanes.
+// to 2^10 more than they need to, and most blocks need no exchange between lanes.
 constexpr float kSlack = 10.f;
+
+// Sums of weighted values from 2^115 (kLarge) on might overflow, if not now then where up to four groups and 608 parts
+// are added, although their quotient by l does not.  A piece with such sums is done again with weights times 2^-33
+// (`shrink`), so that values up to the end of fp32's range add up over 2^22 keys; l is scaled alike and m raised by 33.
+// What this costs every call: 0.3 us of 27 (fp32 drafts), 1 of 111 (64 rows); elsewhere nothing to be seen.
+constexpr float kLarge = 0x1p115f, kShrink = 33.f;
+__device__ __forceinline__ float shrink(float w) {           // what is above zero stays so: an infinite value remains one
+  return w > 0.f ? fmaxf(w * 0x1p-33f, 0x1p-149f) : w;
+}
+// raises m, from a whole number on, which is exact; returns the factor of l and o that goes with the rounding up
+__device__ __forceinline__ float raise(float& m) {
+  const float whole = ceilf(m), f = ex2(m == -INFINITY ? 0.f : m - whole);
+  m = whole + kShrink;
+  return f;
+}
+__device__ __forceinline__ float max_nan(float x, float y) { // NaN where one of the two is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
 
 struct Join {                                // an item that several stretches share
   int32_t seq, item, parts, stretch;         // stretch: the first that begins inside it; parts == 0: nothing to join
@@ -224,7 +244,7 @@ __device__ __forceinline__ void store_out2(const AttentionArgs& a, int64_t at, f
 __device__ __forceinline__ int64_t part_floats(int rows, int D) { return static_cast<int64_t>(rows) * (D + 2); }
 
 // Adds the groups' sums (in shared memory, rows of DP + 2 floats: o, m, l) up and writes the rows of a piece: final
-// where the piece is the whole item, otherwise to the workspace.  Sixteen threads take a row.
+// where the piece is the whole item, otherwise to the workspace.  Sixteen threads take a row. 
 template <int DP, int ROWS, int GROUPS, bool BF_OUT>
 __device__ void finish_piece(const AttentionArgs& a, const float* sums, int b, int hk, int row0, int rows, float* part) {
   const int x0 = threadIdx.x & 15;
@@ -318,8 +338,8 @@ struct Mma {
 // fp32: one part's rounding (2^-9) would be as large as that of a bf16 o.
 //
 // Weights and parts of zero turn an infinite value into a NaN, also where a row's mask leaves its key out.  So a piece
-// whose sums do not come out finite is done again with `exact` set: the weighted sums key by key on CUDA cores, of what a
-// row sees alone.
+// whose sums do not come out finite, or too large, is done again with `exact` set: the weighted sums key by key on CUDA
+// cores, of what a row sees alone, scaled as said at kShrink.
 template <int DP, int RW, int NT, bool BF_OUT>
 __global__ void __launch_bounds__(kThreads, Mma<DP, RW, NT>::kCtas)
     attend_bf16_kernel(const AttentionArgs a, FastDiv page_div, int row_tiles, int join_blocks, Join* joins,
@@ -583,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, Mma<DP, RW, NT>::kCtas)
               const int src = ((j & 7) << 2) | (lane & 3), key = key0 + mb * 16 + j;
               const float u0 = __shfl_sync(0xffffffffu, s[t][mb][0], src), u1 = __shfl_sync(0xffffffffu, s[t][mb][1], src);
               const float u2 = __shfl_sync(0xffffffffu, s[t][mb][2], src), u3 = __shfl_sync(0xffffffffu, s[t][mb][3], src);
-              const float w[2] = {j < 8 ? u0 : u2, j < 8 ? u1 : u3};
+              const float w[2] = {shrink(j < 8 ? u0 : u2), shrink(j < 8 ? u1 : u3)};
               const unsigned char* v = ring + (vs - ring_u) + (mb * 16 + j) * C::kRowBytes;
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
@@ -626,21 +646,20 @@ __global__ void __launch_bounds__(kThreads, Mma<DP, RW, NT>::kCtas)
 
     // the groups' sums, over the rings
     cp_async_wait<0>();
-    float zero = 0.f;
+    float largest = 0.f;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      zero = fmaf(l[t][0] + l[t][1], 0.f, zero);
+      largest = max_nan(largest, l[t][0] + l[t][1]);
 #pragma unroll
       for (int d = 0; d < KS; ++d)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) zero = fmaf(o[t][d][e], 0.f, zero);
+        for (int e = 0; e < 4; ++e) largest = max_nan(largest, fabsf(o[t][d][e]));
     }
-    const bool finite = !__syncthreads_or(!(zero == 0.f));
-    if (!finite && !exact) {
+    const bool fine = !__syncthreads_or(!(largest < kLarge));
+    if (!fine && !exact) {
       exact = true;
       continue;
     }
-    exact = false;
     float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -657,10 +676,13 @@ __global__ void __launch_bounds__(kThreads, Mma<DP, RW, NT>::kCtas)
           to[d * 16 + 8 + row_c] = o[t][d][e + 2];
         }
         if (row_c == 0) {
-          to[DP] = m[t][e];
-          to[DP + 1] = x;
+          // m + 33 is rounded to 2^-19: 1.3e-6 of the piece's weight beside others.  Raised from a whole number, as in fp32,
+          // 64 rows take 114 us instead of 112.
+          to[DP] = exact ? m[t][e] + kShrink : m[t][e];
+          to[DP + 1] = exact ? shrink(x) : x;
         }
       }
+    exact = false;
     __syncthreads();
     float* part = nullptr;
     if (n < r.tiles)
@@ -713,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, Simt<DP, R>::kCtas)
 
   Walk walk = find_stretch<kWarps * BK>(a, items);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  bool noted = false;
+  bool noted = false, again = false;         // again: the sums came out too large, see kShrink
   int n;
   while (next_piece<kWarps * BK>(a, items, walk, n)) {
     const int hk = walk.item / row_tiles, row0 = (walk.item - hk * row_tiles) * C::kRows;
@@ -888,6 +910,7 @@ __global__ void __launch_bounds__(kThreads, Simt<DP, R>::kCtas)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           w[t] = ex2(y[x][t] - (m[t] == -INFINITY ? 0.f : m[t]));
+          if (again) w[t] = shrink(w[t]);
           l[t] += w[t];
           // a weight of a key that the row does not see is negative zero: its product is left out below
           if (!sees[x][t]) w[t] = -0.f;
@@ -962,7 +985,32 @@ __global__ void __launch_bounds__(kThreads, Simt<DP, R>::kCtas)
     }
 
     cp_async_wait<0>();
-    __syncthreads();
+    float largest = 0.f;
+#pragma unroll
+    for (int t = 0; t < R; ++t)
+#pragma unroll
+      for (int e = 0; e < OC / 2; ++e) largest = max_nan(largest, max_nan(fabsf(o[t][e].x), fabsf(o[t][e].y)));
+    const bool fine = !__syncthreads_or(!(largest < kLarge));
+    if (!fine && !again) {
+      again = true;
+      continue;
+    }
+    if (again) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const float f = raise(m[t]);
+        l[t] *= f;
+        if (key_lane == 0 && share == 0) factors[pair * 2 + t] = f;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int t = 0; t < R; ++t) {
+        const float f = factors[t];
+#pragma unroll
+        for (int e = 0; e < OC / 2; ++e) o[t][e] = mul2(make_float2(f, f), o[t][e]);
+      }
+      again = false;
+    }
     float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {

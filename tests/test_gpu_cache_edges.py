@@ -1,5 +1,6 @@
 """The key-value cache on the GPU where a caller's data are at the edge of what it may hold: tables whose pages
-the references call free, entries and lengths that are out of range.
+the references call free, entries and lengths that are out of range, values near
+the end of fp32's range.
 
 Tolerances as in `test_gpu_cache.py`: E for the scores, (n / 16 + 64) 2 U for sums, 2 (E + 2^-21) for weights.
 """
@@ -158,4 +159,86 @@ def test_a_length_out_of_range_is_an_empty_sequence(length, W, dtype):
     assert not o[W:2 * W].any() and torch.all(l[W:2 * W] == -float("inf"))
     keep = [i for i in range(3 * W) if i // W != 1]
     assert torch.equal(o[keep], good[keep]) and torch.equal(l[keep], gl[keep])
+    no_error()
+
+
+def test_attention_weights_of_later_keys_do_not_overflow():
+    """A first block sets the running maximum, a key 9.9 powers of two above it follows: values of 1e36 stay finite."""
+    D = 64
+    for dtype in ("bf16", "f32"):
+        k, v = np.zeros((200, 1, D)), np.full((200, 1, D), 1e36)
+        k[150, 0, 0] = 9.9 * np.log(2) * D ** 0.5
+        q = np.zeros((1, 2, D))
+        q[..., 0] = 1
+        compare(dtype, q, k, v, 1)
+
+
+def compare(dtype, q, k, v, W, out=None, P=16, plant=None, **kw):
+    """One sequence whose page table is in order, against fp64."""
+    n, HK, D = k.shape
+    pages = max(1, -(-n // P))
+    room = [np.zeros((pages * P, HK, D)) for _ in range(2)]
+    for x, y in zip(room, (k, v)):
+        x[:n] = y
+    (kp, k64), (vp, v64) = (dev(x.reshape(pages, P, HK, D), dtype) for x in room)
+    k64, v64 = (x.reshape(-1, HK, D)[:n] for x in (k64, v64))
+    if plant:
+        plant(kp, vp)
+    q, q64 = dev(q, dtype)
+    o, l = kda.cache_attention(q, kp, vp, ints(np.arange(pages)[None]), ints([n]), window=W, out_dtype=DT[out or dtype],
+                               return_lse=True, **kw)
+    no_error()
+    ref, rl, tol, ltol = reference(q64, k64, v64, W, o.dtype, D, **kw)
+    # where weights are scaled by 2^-33, maxima are raised and log2 of the sums lowered by 33: both rounded to 2^-19
+    close("o", o, ref, tol + 2.0 ** -19 * np.abs(v64).max())
+    close("lse", l, rl, ltol + 2.0 ** -18)
+    return o, l
+
+
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("n,H,HK,W,D", [(1, 1, 1, 1, 64), (40, 2, 1, 1, 64), (700, 2, 2, 1, 128), (6000, 4, 1, 1, 64),
+                                        (900, 4, 2, 4, 128), (500, 12, 1, 1, 128), (500, 8, 1, 8, 64), (300, 4, 1, 2, 256),
+                                        (300, 8, 1, 3, 256), (20000, 1, 1, 1, 32)])
+@pytest.mark.parametrize("top", [1e35, 3e37, 2e38])
+def test_attention_of_values_near_the_end_of_the_range(top, n, H, HK, W, D, dtype, out):
+    """Sums of many such values pass the range, their weighted means do not: of one sign (the sums grow with every key)
+    and of both, with a span, a cap and scores that rise."""
+    r = rng(3, n, H, D)
+    q, k = r.standard_normal((W, H, D)), r.standard_normal((n, HK, D))
+    v = top * r.uniform(0.5, 1, (n, HK, D))
+    compare(dtype, q, k, v, W, out)
+    compare(dtype, q, k, v * r.choice([-1, 1], v.shape), W, out, span=max(1, n // 2), softcap=4.0)
+    k += np.linspace(0, 3, n)[:, None, None] * q[:1, :1]
+    compare(dtype, q, k, v, W, out)
+
+
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+def test_attention_of_large_values_beside_small_ones_and_hidden_infinities(dtype, out):
+    """A few large values where most are small, in channels of their own, and infinite ones behind the end and in a
+    draft's own row: the other channels and rows keep their accuracy."""
+    r = rng(4)
+    n, D, W = 3000, 64, 3
+    q, k, v = r.standard_normal((W, 2, D)), r.standard_normal((n, 1, D)), r.standard_normal((n, 1, D))
+    v[::7, 0, 5] = 1e38
+
+    def behind(kp, vp):
+        vp.view(-1, 1, D)[n:] = float("inf")
+        kp.view(-1, 1, D)[n:] = float("nan")
+    compare(dtype, q, k, v, W, out, plant=behind)
+    o, l = compare(dtype, q, k, v, W, out)
+
+    def last(kp, vp):
+        vp.view(-1, 1, D)[n - 1] = float("inf")
+    with pytest.raises(AssertionError, match="finite elsewhere"):
+        compare(dtype, q, k, v, W, out, plant=last)
+    pages = -(-n // 16)
+    kp, vp = (torch.zeros((pages * 16, 1, D), dtype=DT[dtype], device=DEV) for _ in range(2))
+    kp[:n], vp[:n] = dev(k, dtype)[0], dev(v, dtype)[0]
+    vp[n - 1] = float("inf")
+    a, b = kda.cache_attention(dev(q, dtype)[0], kp.view(pages, 16, 1, D), vp.view(pages, 16, 1, D), ints(np.arange(pages)[None]),
+                               ints([n]), window=W, out_dtype=DT[out], return_lse=True)
+    half = torch.finfo(a.dtype).eps / 2
+    mean = np.abs(v).max(axis=(0, 1))          # the same products in another order, of weights that are scaled
+    assert np.all(np.abs(host(a[:-1]) - host(o[:-1])) <= 2 * half * np.abs(host(o[:-1])) + 2.0 ** -14 * mean)
+    assert torch.all(a[-1] == float("inf")) and torch.allclose(b, l, rtol=0, atol=2.0 ** -16)
     no_error()
