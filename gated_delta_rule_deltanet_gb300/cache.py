@@ -367,10 +367,10 @@ def _plan_rows(key, name, block_table, lens, refs, parent, new_lens, page_size):
 
 def _out(given, like, inputs):
     """The outputs that are given: of the shapes needed and of memory that no input has."""
-    for t, (name, shape) in zip(given, like):
+    for i, (t, (name, shape)) in enumerate(zip(given, like)):
         if t.shape != shape or t.dtype != torch.int32 or not t.is_contiguous():
             raise ValueError(f"out.{name} must be contiguous int32 {list(shape)}")
-        _apart(t, f"out.{name}", *inputs, *(u for u in given if u is not t))
+        _apart(t, f"out.{name}", *inputs, *given[i + 1:])
     return given
 
 

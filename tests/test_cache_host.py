@@ -225,3 +225,13 @@ def test_frequencies(kw, R):
     assert f.dtype == torch.float64
     # a power and a few products in fp64
     assert np.allclose(f.numpy(), ref, rtol=1e-14, atol=0) and abs(m - mr) < 1e-15
+
+
+@pytest.mark.parametrize("a,b", [("lens", "kept"), ("src", "dst"), ("kept", "dst")])
+def test_one_tensor_for_two_outputs_is_refused(a, b):
+    row = kda.CacheRows(*(torch.zeros(s, dtype=torch.int32) for s in ((3, 2), 3, 5, 3, 3, 3)))
+    like = [(n, t.shape) for n, t in zip(row._fields, row)]
+    inputs = (torch.zeros((3, 2), dtype=torch.int32), torch.zeros(3, dtype=torch.int32), None)
+    assert cache._out(row, like, inputs) is row
+    with pytest.raises(ValueError, match="memory of its own"):
+        cache._out(row._replace(**{a: getattr(row, b)}), like, inputs)
