@@ -13,8 +13,8 @@ import torch
 from . import _lib
 from ._lib import KdaCacheParams, KdaCacheRowsParams, KdaError, KdaRotaryParams
 from .kda import _INDEX_DTYPES, _QKV_DTYPES
-from .layer import (_PLANS, _Plan, _apart, _call, _current_device, _dense, _device, _keep, _on, _p, _raw_stream,
-                    _sig, _sig16, _space)
+from .layer import (_PLANS, _Plan, _apart, _call, _current_device, _dense, _device, _keep, _on, _p, _pairs,
+                    _raw_stream, _sig, _sig16, _space)
 
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = ("none", "linear", "ntk", "by_parts")
@@ -86,11 +86,9 @@ def _frequencies(f, D):
 
 
 def _place(out, x, name):
-    """Checks an output that is given: x itself, or memory of its own."""
+    """Checks an output that is given."""
     if out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError(f"{name} must be shaped and typed like its input")
-    if out.data_ptr() == x.data_ptr() and out.numel() and out.stride() != x.stride():
-        raise ValueError(f"{name} must be its input itself or have memory of its own")
     return _heads(out, name)
 
 
@@ -117,17 +115,17 @@ def _plan_rotary(key, name, q, k, positions, frequencies, layout, magnitude, q_o
 
 def _rotary(name, q, k, positions, frequencies, layout, magnitude, q_out, k_out):
     magnitude = float(magnitude)
-    _apart(q_out, "q_out", k, k_out)
-    _apart(k_out, "k_out", q)
-    # a q_out that is q takes its place in the key: its strides are then q's
-    key = (name, _sig(q), _sig(k), _sig(positions), _sig(frequencies), layout, magnitude, _sig(q_out), _sig(k_out),
-           q_out is not None and q_out.data_ptr() == q.data_ptr(),
-           k_out is not None and k is not None and k_out.data_ptr() == k.data_ptr())
+    key = (name, _sig(q), _sig(k), _sig(positions), _sig(frequencies), layout, magnitude, _sig(q_out), _sig(k_out))
     plan = _PLANS.get(key)
     if plan is None:
+        pairs = _apart(_pairs((q, k, q_out, k_out), ("q_out", 2, 0, True), ("q_out", 2, 1), ("q_out", 2, 3),
+                              ("k_out", 3, 0), ("k_out", 3, 1, True)), q, k, q_out, k_out)
         if frequencies is None:
             raise ValueError("frequencies must be contiguous float64 [R / 2], R at most the head size")
         plan = _plan_rotary(key, name, q, k, positions, frequencies, layout, magnitude, q_out, k_out)
+        plan.pairs = pairs
+    elif plan.pairs:
+        _apart(plan.pairs, q, k, q_out, k_out)
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=plan.device)
     if k_out is None and k is not None:
@@ -239,14 +237,17 @@ def cache_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
             return cache_append(q, k, v, frequencies, k_pages, v_pages, block_table, start,
                                 input_row_offsets=input_row_offsets, layout=layout, magnitude=magnitude, q_out=q_out)
     magnitude = float(magnitude)
-    _apart(q_out, "q_out", k, v, k_pages, v_pages)
     key = ("cache_append", _sig(q), _sig(k), _sig(v), _sig(frequencies), _sig(k_pages), _sig(v_pages),
-           _sig(block_table), _sig(start), _sig(input_row_offsets), layout, magnitude, _sig(q_out),
-           q_out is not None and q is not None and q_out.data_ptr() == q.data_ptr())
+           _sig(block_table), _sig(start), _sig(input_row_offsets), layout, magnitude, _sig(q_out))
     plan = _PLANS.get(key)
     if plan is None:
+        pairs = _apart(_pairs((q_out, q, k, v, k_pages, v_pages), ("q_out", 0, 1, True), ("q_out", 0, 2), ("q_out", 0, 3),
+                              ("q_out", 0, 4), ("q_out", 0, 5)), q_out, q, k, v, k_pages, v_pages)
         plan = _plan_append(key, q, k, v, frequencies, k_pages, v_pages, block_table, start, input_row_offsets,
                             layout, magnitude, q_out)
+        plan.pairs = pairs
+    elif plan.pairs:
+        _apart(plan.pairs, q_out, q, k, v, k_pages, v_pages)
     if q is not None and q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=plan.device)
     _call(plan, _p(q), k.data_ptr(), v.data_ptr(), _p(frequencies), k_pages.data_ptr(), v_pages.data_ptr(),
@@ -303,13 +304,17 @@ def cache_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
                                    softcap=softcap, span=span, slopes=slopes, out_dtype=out_dtype,
                                    return_lse=return_lse, out=out, workspace=workspace)
     scale, softcap = float(scale), float(softcap)
-    _apart(out, "out", q, k_pages, v_pages)
     key = ("cache_attention", _sig16(q), _sig16(k_pages), _sig16(v_pages), _sig(block_table), _sig(lens), window, scale,
            softcap, span, _sig(slopes), out_dtype, _sig(out))
     plan = _PLANS.get(key)
     if plan is None:
+        pairs = _apart(_pairs((out, q, k_pages, v_pages), ("out", 0, 1), ("out", 0, 2), ("out", 0, 3)), out, q, k_pages,
+                       v_pages)
         plan = _plan_attention(key, q, k_pages, v_pages, block_table, lens, window, scale, softcap, span, slopes,
                                out_dtype, out)
+        plan.pairs = pairs
+    elif plan.pairs:
+        _apart(plan.pairs, out, q, k_pages, v_pages)
     if out is None:
         out = torch.empty(plan.shape, dtype=plan.dtype, device=plan.device)
     lse = torch.empty(plan.shape[:2], dtype=torch.float32, device=plan.device) if return_lse else None
@@ -366,11 +371,21 @@ def _plan_rows(key, name, block_table, lens, refs, parent, new_lens, page_size):
 
 
 def _out(given, like, inputs):
-    """The outputs that are given: of the shapes needed and of memory that no input has."""
-    for i, (t, (name, shape)) in enumerate(zip(given, like)):
+    """The outputs that are given: of the shapes needed and of memory that no input and no other output has."""
+    spans = [(t.data_ptr(), t.nbytes, None) for t in inputs if t is not None]
+    for t, (name, shape) in zip(given, like):
         if t.shape != shape or t.dtype != torch.int32 or not t.is_contiguous():
             raise ValueError(f"out.{name} must be contiguous int32 {list(shape)}")
-        _apart(t, f"out.{name}", *inputs, *given[i + 1:])
+        spans.append((t.data_ptr(), t.nbytes, name))
+    spans.sort(key=lambda x: x[0])
+    end, out_end, last = 0, 0, None            # of all and of the outputs so far; the output that ends there
+    for at, nbytes, name in spans:
+        if nbytes and at < (out_end if name is None else end):
+            raise ValueError(f"out.{name or last} must have memory of its own")
+        if nbytes:
+            end = max(end, at + nbytes)
+            if name is not None:
+                out_end, last = at + nbytes, name
     return given
 
 

@@ -28,7 +28,7 @@ _MAX_PLANS = 4096
 
 
 class _Plan:
-    __slots__ = ("fn", "params", "ref", "device", "index", "nbytes", "shape", "dtype", "dtype2")
+    __slots__ = ("fn", "params", "ref", "device", "index", "nbytes", "shape", "dtype", "dtype2", "pairs")
 
     def __init__(self, name, params, device, nbytes=0, shape=None, dtype=None, dtype2=None):
         self.fn = getattr(_lib.load(), name)
@@ -40,6 +40,7 @@ class _Plan:
         self.shape = shape
         self.dtype = dtype
         self.dtype2 = dtype2
+        self.pairs = ()
 
 
 def _sig(t):
@@ -134,10 +135,73 @@ def _rows(t, shape, dtypes, name):
     return 0
 
 
-def _apart(out, name, *others):
-    """An output's rows are written while other blocks still read the operands."""
-    if out is not None and out.numel() and any(o is not None and o.data_ptr() == out.data_ptr() for o in others):
-        raise ValueError(f"{name} must have memory of its own")
+def _runs(t):
+    """How the elements of t lie: (number, bytes apart) of its dimensions from the outermost on, joined where they can
+    be, and the bytes of a dense run."""
+    width, dims = t.element_size(), []
+    run = width
+    for apart, n in sorted((s * width, n) for s, n in zip(t.stride(), t.shape) if n > 1 and s > 0):
+        if not dims and apart == run:
+            run *= n
+        elif dims and apart == dims[-1][0] * dims[-1][1]:
+            dims[-1] = (n * dims[-1][0], dims[-1][1])
+        else:
+            dims.append((n, apart))
+    return dims[::-1], run
+
+
+def _reach(outer, run):
+    return run + sum((n - 1) * s for n, s in outer)
+
+
+def _runs_meet(a, outer_a, run_a, b, outer_b, run_b):
+    ends_a, ends_b = _reach(outer_a, run_a), _reach(outer_b, run_b)
+    if a + ends_a <= b or b + ends_b <= a:
+        return False
+    if not outer_a and not outer_b:
+        return True
+    if outer_a and outer_b and outer_a[0][1] == outer_b[0][1]:
+        (n, s), (m, _) = outer_a[0], outer_b[0]
+        inner_a, inner_b = ends_a - (n - 1) * s, ends_b - (m - 1) * s
+        if inner_a <= s and inner_b <= s:
+            # blocks in step, as of two columns of one packed array: b's block i lies `shift` behind a's block i + k
+            # or, the step before, i + k + 1
+            k, shift = divmod(b - a, s)
+            return any(-m < i < n and _runs_meet(0, outer_a[1:], run_a, d, outer_b[1:], run_b)
+                       for i, d in ((k, shift), (k + 1, shift - s)))
+    if not outer_a or outer_b and ends_a < ends_b:
+        a, outer_a, run_a, ends_a, b, outer_b, run_b, ends_b = b, outer_b, run_b, ends_b, a, outer_a, run_a, ends_a
+    n, s = outer_a[0]
+    inner = ends_a - (n - 1) * s
+    return any(_runs_meet(a + i * s, outer_a[1:], run_a, b, outer_b, run_b)
+               for i in range(max(0, (b - a - inner) // s + 1), min(n - 1, (b + ends_b - 1 - a) // s) + 1))
+
+
+def _pairs(tensors, *which):
+    """What a plan keeps to tell whether an output shares memory with another tensor, whose blocks would write what others
+    still read.  `which`: (name of the output, its place among `tensors`, the other's), and True where the output may
+    be the other one itself."""
+    pairs = []
+    for name, i, j, *itself in which:
+        x, y = tensors[i], tensors[j]
+        if x is not None and y is not None and x.numel() and y.numel():
+            a, b = _runs(x), _runs(y)
+            # bytes between the rows where both are rows that far apart, as two columns of one packed array
+            step = a[0][0][1] if len(a[0]) == len(b[0]) == 1 and a[0][0][1] == b[0][0][1] else 0
+            pairs.append((i, _reach(*a), j, _reach(*b), name, a, b, step, bool(itself) and a == b))
+    return tuple(pairs)
+
+
+def _apart(pairs, *tensors):
+    for i, ends_a, j, ends_b, name, runs_a, runs_b, step, itself in pairs:
+        a, b = tensors[i].data_ptr(), tensors[j].data_ptr()
+        if a >= b + ends_b or b >= a + ends_a or itself and a == b:
+            continue
+        if step and runs_a[1] <= (b - a) % step <= step - runs_b[1]:
+            continue
+        if _runs_meet(a, *runs_a, b, *runs_b):
+            raise ValueError(f"{name} must have memory of its own" + (" or be its input itself" if itself else ""))
+    return pairs
 
 
 def _dense(t, shape, dtype, name):
@@ -224,13 +288,16 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
                           out_dtype=out_dtype, save_pre_activation=save_pre_activation,
                           cuda_cores=cuda_cores, out=out, workspace=workspace)
     scale = float(scale)
-    _apart(out, "out", x, weight)
     key = ("linear", x.shape, x.stride(), x.dtype, x.get_device(), x.data_ptr() & 15, _sig16(weight),
            _sig(bias), activation, _sig(residual), scale, out_dtype, _sig(out), cuda_cores)
     plan = _PLANS.get(key)
     if plan is None:
+        pairs = _apart(_pairs((out, x, weight), ("out", 0, 1), ("out", 0, 2)), out, x, weight)
         plan = _plan_linear(key, x, weight, bias, activation, residual, scale, out_dtype, out,
                             cuda_cores)
+        plan.pairs = pairs
+    elif plan.pairs:
+        _apart(plan.pairs, out, x, weight)
     if out is None:
         out = torch.empty(plan.shape, dtype=plan.dtype, device=plan.device)
     z = torch.empty(plan.shape, dtype=x.dtype, device=plan.device) if save_pre_activation else None
@@ -359,13 +426,16 @@ def residual_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
             return residual_norm(x, weight, residual=residual, post_weight=post_weight, gate=gate,
                                  scale=scale, eps=eps, out=out, h_out=h_out)
     scale, eps = float(scale), float(eps)
-    _apart(out, "out", h_out)
     key = ("residual_norm", _sig(x), _sig(weight), _sig(residual), _sig(post_weight), _sig(gate),
            scale, eps, _sig(out), _sig(h_out))
     plan = _PLANS.get(key)
     if plan is None:
+        pairs = _apart(_pairs((out, h_out), ("out", 0, 1)), out, h_out)
         plan = _plan_residual_norm(key, x, weight, residual, post_weight, gate, scale, eps, out,
                                    h_out)
+        plan.pairs = pairs
+    elif plan.pairs:
+        _apart(plan.pairs, out, h_out)
     if h_out is None:
         h_out = torch.empty(plan.shape, dtype=plan.dtype, device=plan.device)
     if out is None and weight is not None:

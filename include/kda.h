@@ -658,7 +658,7 @@ typedef struct kda_rotary_params {
  *
  *   q [T, H, d], k [T, HK, d] (NULL with no heads)   positions [T], negative ones too; the angle is
  *   good to 2^-24 of a turn for |p| < 2^31           frequencies [R / 2] fp64, radians per position
- *   q_out, k_out: may be q, k (same pointer and stride)
+ *   q_out, k_out: may be q, k (same pointer and stride); otherwise they share no memory with q, k or one another
  * kda_rotary_bwd is the transposed map, for gradients.
  */
 kda_status_t kda_rotary_fwd(const kda_rotary_params_t *p, const void *q, const void *k,

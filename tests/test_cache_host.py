@@ -235,3 +235,35 @@ def test_one_tensor_for_two_outputs_is_refused(a, b):
     assert cache._out(row, like, inputs) is row
     with pytest.raises(ValueError, match="memory of its own"):
         cache._out(row._replace(**{a: getattr(row, b)}), like, inputs)
+
+
+def test_outputs_that_overlap_by_a_shift_are_refused():
+    """Blocks would write rows that others have not read yet; columns of one packed array that only alternate are apart."""
+    f, i, table = torch.zeros(4, dtype=torch.float64), torch.zeros(3, dtype=torch.int32), torch.zeros(3, 2, dtype=torch.int32)
+    big, pages = torch.zeros(8, 2, 8), torch.zeros(5, 4, 2, 8)
+    q, k, packed = big[:3], torch.zeros(3, 2, 8), torch.zeros(3, 9, 8)
+    a, b, c = packed[:, :2], packed[:, 2:4], packed[:, 1:3]
+    for call in (lambda: kda.rotary(q, None, i, f, q_out=big[1:4]), lambda: kda.rotary(k, q, i, f, k_out=big[2:5]),
+                 lambda: kda.rotary_bwd(q, None, i, f, dq_out=big[1:4]), lambda: kda.rotary(a, b, i, f, q_out=c),
+                 lambda: kda.rotary(a, b, i, f, q_out=b), lambda: kda.rotary(a, b, i, f, k_out=c),
+                 lambda: kda.rotary(a, None, i, f, q_out=packed.view(-1)[:48].view(3, 2, 8)),
+                 lambda: kda.rotary(k, k.clone(), i, f, q_out=q, k_out=big[1:4]),
+                 lambda: kda.cache_append(q, k, k.clone(), f, pages, pages.clone(), table, i, q_out=big[1:4]),
+                 lambda: kda.cache_append(k, k.clone(), k.clone(), f, pages, pages.clone(), table, i, q_out=pages[1, 1:]),
+                 lambda: kda.cache_attention(q, pages, pages, table, i, out=big[1:4]),
+                 lambda: kda.cache_attention(q, pages, pages, table, i, out=pages[4, 1:])):
+        with pytest.raises(ValueError, match="memory of its own"):
+            call()
+    for call in (lambda: kda.rotary(q, k, i, f, q_out=q, k_out=big[3:6]), lambda: kda.rotary(a, b, i, f, q_out=a, k_out=b),
+                 lambda: kda.rotary(a, b, i, f, q_out=packed[:, 4:6], k_out=packed[:, 7:9]),
+                 lambda: kda.cache_attention(q, pages, pages, table, i, out=big[3:6])):
+        with pytest.raises(ValueError, match="CUDA"):            # what comes next on the host
+            call()
+    room = torch.zeros(64, dtype=torch.int32)
+    row = kda.CacheRows(room[:6].view(3, 2), room[6:9], room[9:14], room[14:17], room[17:20], room[20:23])
+    like = [(n, t.shape) for n, t in zip(row._fields, row)]
+    cache._out(row, like, (room[23:29], room[29:32], None, room[23:27]))
+    for bad, inputs in ((row._replace(kept=room[8:11]), ()), (row, (room[22:25],)), (row, (room[13:14],)),
+                        (row._replace(dst=room[19:22]), ()), (row, (room[0:64],))):
+        with pytest.raises(ValueError, match="memory of its own"):
+            cache._out(bad, like, inputs)
