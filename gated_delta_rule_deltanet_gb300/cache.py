@@ -245,13 +245,17 @@ def cache_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
                               ("q_out", 0, 4), ("q_out", 0, 5)), q_out, q, k, v, k_pages, v_pages)
         plan = _plan_append(key, q, k, v, frequencies, k_pages, v_pages, block_table, start, input_row_offsets,
                             layout, magnitude, q_out)
-        plan.pairs = pairs
+        plan.pairs, plan.pools = pairs, _pairs((k_pages, v_pages), ("k_pages", 0, 1))
+        plan.reach = plan.pools[0][1] if plan.pools else 0
     elif plan.pairs:
         _apart(plan.pairs, q_out, q, k, v, k_pages, v_pages)
+    keys, values = k_pages.data_ptr(), v_pages.data_ptr()
+    if -plan.reach < keys - values < plan.reach:
+        _apart(plan.pools, k_pages, v_pages)
     if q is not None and q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=plan.device)
-    _call(plan, _p(q), k.data_ptr(), v.data_ptr(), _p(frequencies), k_pages.data_ptr(), v_pages.data_ptr(),
-          block_table.data_ptr(), start.data_ptr(), _p(input_row_offsets), _p(q_out))
+    _call(plan, _p(q), k.data_ptr(), v.data_ptr(), _p(frequencies), keys, values, block_table.data_ptr(),
+          start.data_ptr(), _p(input_row_offsets), _p(q_out))
     return q_out
 
 

@@ -28,7 +28,8 @@ _MAX_PLANS = 4096
 
 
 class _Plan:
-    __slots__ = ("fn", "params", "ref", "device", "index", "nbytes", "shape", "dtype", "dtype2", "pairs")
+    __slots__ = ("fn", "params", "ref", "device", "index", "nbytes", "shape", "dtype", "dtype2", "pairs",
+                 "pools", "reach")
 
     def __init__(self, name, params, device, nbytes=0, shape=None, dtype=None, dtype2=None):
         self.fn = getattr(_lib.load(), name)

@@ -699,7 +699,8 @@ typedef struct kda_cache_params {
  *   belong to no sequence; nothing of them is written
  *   frequencies [R / 2] or NULL (R = 0)      q_out [T, H, d], may be q
  *   start [B] tokens already in the cache
- * The pages of the new positions must be in the table.  A page row that two tokens are given races.
+ * The pages of the new positions must be in the table.  A page row that two tokens are given races.  The two pools
+ * share no memory, and none with q, k, v or q_out.
  */
 kda_status_t kda_cache_append(const kda_cache_params_t *p, const void *q, const void *k, const void *v,
                               const double *frequencies, void *key_pages, void *value_pages,

@@ -267,3 +267,26 @@ def test_outputs_that_overlap_by_a_shift_are_refused():
                         (row._replace(dst=room[19:22]), ()), (row, (room[0:64],))):
         with pytest.raises(ValueError, match="memory of its own"):
             cache._out(bad, like, inputs)
+
+
+def test_one_pool_for_keys_and_values_is_refused(monkeypatch):
+    """Two blocks would write one row.  The check of an append's pools comes behind those of its plan, made up here."""
+    class Called(Exception):
+        pass
+
+    def called(*a):
+        raise Called
+    monkeypatch.setattr(cache, "_plan_append", lambda *a: cache._Plan("kda_cache_append", cache_params(), torch.device("cuda:0")))
+    monkeypatch.setattr(cache, "_call", called)
+    x, i, table = torch.zeros(3, 2, 8), torch.zeros(3, dtype=torch.int32), torch.zeros(3, 2, dtype=torch.int32)
+    both, by_row = torch.zeros(6, 4, 2, 8), torch.zeros(5, 4, 2, 2, 8)
+
+    def append(kp, vp):
+        kda.cache_append(None, x, x, None, kp, vp, table, i)
+    for kp, vp in ((both, both), (both[1:], both[:-1]), (both[:, 1:], both[:, :-1]), (by_row[:, :, 0], by_row[:, :, 0])):
+        with pytest.raises(ValueError, match="memory of its own"):
+            append(kp, vp)
+    for kp, vp in ((both, both.clone()), (by_row[:, :, 0], by_row[:, :, 1]), (by_row[:, :, :, 0], by_row[:, :, :, 1]),
+                   (both[:3], both[3:]), (both[:, :2], both[:, 2:])):
+        with pytest.raises(Called):
+            append(kp, vp)
