@@ -176,9 +176,11 @@ def _pages(p, k_pages, v_pages, block_table, B):
     head = k_pages.stride(2) if HK > 1 else D
     row = k_pages.stride(1) if P > 1 else HK * D
     page = k_pages.stride(0) if N > 1 else P * HK * D
-    if not (((HK == 1 or head >= D) and (P == 1 or row >= HK * D) or (P == 1 or row >= D) and (HK == 1 or head >= P * D))
-            and (N <= 1 or page >= P * HK * D)):
-        raise ValueError("the pages' rows must not overlap")
+    span = D
+    for apart, n in sorted(((head, HK), (row, P), (page, N))):
+        if n > 1 and apart < span:
+            raise ValueError("the pages' heads must not overlap")
+        span += apart * max(0, n - 1)
     if block_table.dim() != 2 or block_table.shape[0] != B or block_table.dtype != torch.int32 \
             or not block_table.is_contiguous():
         raise ValueError("block_table must be contiguous int32 [num_seqs, max_pages]")
@@ -228,7 +230,7 @@ def cache_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
     into the pages, q [T, H, d] (or None) turned and returned.
 
     k_pages, v_pages [num_pages, page_size, HK, d], any strides that keep the heads' channels together
-    (a transposed view of [num_pages, HK, page_size, d] too); block_table [B, max_pages] int32; start
+    (permuted views of [num_pages, HK, page_size, d], [HK, num_pages, page_size, d] and the like too); block_table [B, max_pages] int32; start
     [B] int32: the tokens that each sequence already holds, the position of its first new one.
     Without `input_row_offsets` every row is a sequence's one new token (the decode form); with it, tokens from
     its last entry on are left alone.  `frequencies` None: nothing is turned."""

@@ -2,6 +2,8 @@
 // runs on the host before any launch.
 #include <math.h>
 
+#include <algorithm>
+
 #include "cache_common.cuh"
 
 static_assert(sizeof(kda_rotary_params_t) == 72, "kda_rotary_params_t layout is part of the ABI");
@@ -27,15 +29,22 @@ bool rotation_ok(int32_t R, int32_t d, float magnitude) {
   return R >= 0 && R % 2 == 0 && R <= d && isfinite(magnitude);
 }
 
-// rows of the pages do not overlap: the larger of the two strides inside a page spans the other dimension
+// The heads of the pages do not overlap: of pages, rows and heads, in whatever order, each is as far apart as what lies
+// between two of it spans (in fp64: strides of 2^40 times extents of 2^31).
 bool pages_ok(const kda_cache_params_t* p) {
-  const int64_t row = p->page_row_stride, head = p->page_head_stride, d = p->head_dim;
-  if (row < 1 || head < 1 || p->page_stride < 1 || row > kMaxStride || head > kMaxStride || p->page_stride > kMaxStride)
-    return false;
-  const int64_t P = p->page_size, HK = p->num_kv_heads;
-  const bool by_rows = (HK == 1 || head >= d) && (P == 1 || row >= HK * d);
-  const bool by_heads = (P == 1 || row >= d) && (HK == 1 || head >= P * d);
-  return (by_rows || by_heads) && (p->num_pages <= 1 || p->page_stride >= P * HK * d);
+  struct Extent {
+    int64_t stride, size;
+  } e[3] = {{p->page_head_stride, p->num_kv_heads}, {p->page_row_stride, p->page_size}, {p->page_stride, p->num_pages}};
+  for (const Extent& x : e)
+    if (x.stride < 1 || x.stride > kMaxStride) return false;
+  std::sort(e, e + 3, [](const Extent& x, const Extent& y) { return x.stride < y.stride; });
+  double span = p->head_dim;
+  for (const Extent& x : e) {
+    if (x.size <= 1) continue;
+    if (static_cast<double>(x.stride) < span) return false;
+    span += static_cast<double>(x.stride) * (x.size - 1);
+  }
+  return true;
 }
 
 kda_status_t check_cache(const kda_cache_params_t* p) {

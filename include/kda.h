@@ -626,7 +626,7 @@ kda_status_t kda_norm_workspace_size(const kda_norm_params_t *p, int32_t gated, 
  * The key-value cache of a hybrid model's softmax attention layers, which stand between the
  * recurrent ones.  The cache of a layer is two pools of pages (keys and values): page q, row r and
  * key head h at element q page_stride + r page_row_stride + h page_head_stride, head_dim
- * elements each, so that [num_pages, page_size, HK, d] and [num_pages, HK, page_size, d] are both read
+ * elements each, so that [num_pages, page_size, HK, d], [num_pages, HK, page_size, d] and any other order are read
  * in place.  A sequence's token j lies in row j % page_size of page block_table[b][j / page_size];
  * one table serves all layers.  Entries that a call does not need are not read and may hold -1.
  *

@@ -290,3 +290,30 @@ def test_one_pool_for_keys_and_values_is_refused(monkeypatch):
                    (both[:3], both[3:]), (both[:, :2], both[:, 2:])):
         with pytest.raises(Called):
             append(kp, vp)
+
+
+def test_pages_of_any_order(lib):
+    """Pages, rows and heads may lie in any order, with room between them; they may not lie over one another."""
+    n = ctypes.c_size_t(0)
+
+    def size(page, row, head, **kw):
+        p = cache_params(page_stride=page, page_row_stride=row, page_head_stride=head, **kw)
+        return lib.kda_cache_attention_workspace_size(ctypes.byref(p), ctypes.byref(n))
+    N, P, HK, D = 20, 8, 2, 16
+    for a, b, c in ((P * HK * D, HK * D, D), (P * HK * D, D, P * D), (HK * D, N * HK * D, D), (D, N * D, P * N * D),
+                    (P * D, D, N * P * D), (D, HK * N * D, N * D), (1024, 2 * HK * D, D)):
+        assert size(a, b, c) == OK, (a, b, c)
+    for a, b, c in ((P * HK * D, 2 * HK * D, D), (P * HK * D, HK * D, 8), (HK * D, HK * D, D), (D, N * D, P * D), (D, D, D),
+                    (P * HK * D - 8, HK * D, D)):
+        assert size(a, b, c) == INVALID, (a, b, c)
+    assert size(8, 8, 8, num_pages=1, page_size=1, num_kv_heads=1, num_q_heads=1) == OK       # extents of one
+    assert size(1 << 40, 1 << 40, 1 << 40) == INVALID and size(1 << 40, D, 1 << 39) == OK
+    for order in ("NPHD", "NHPD", "HNPD", "PNHD", "PHND", "HPND"):
+        lens = dict(N=N, P=P, H=HK, D=D)
+        x = torch.zeros([lens[c] for c in order]).permute([order.index(c) for c in "NPHD"])
+        p = _lib.KdaCacheParams()
+        cache._pages(p, x, x, torch.zeros(3, 2, dtype=torch.int32), 3)
+        assert (p.page_stride, p.page_row_stride, p.page_head_stride) == x.stride()[:3]
+    with pytest.raises(ValueError, match="overlap"):
+        x = torch.zeros(9999).as_strided((N, P, HK, D), (P * HK * D, 2 * HK * D, D, 1))
+        cache._pages(_lib.KdaCacheParams(), x, x, torch.zeros(3, 2, dtype=torch.int32), 3)

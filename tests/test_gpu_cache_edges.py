@@ -1,6 +1,6 @@
 """The key-value cache on the GPU where a caller's data are at the edge of what it may hold: tables whose pages
 the references call free, entries and lengths that are out of range, values near
-the end of fp32's range.
+the end of fp32's range, pools of any order of their dimensions.
 
 Tolerances as in `test_gpu_cache.py`: E for the scores, (n / 16 + 64) 2 U for sums, 2 (E + 2^-21) for weights.
 """
@@ -242,3 +242,26 @@ def test_attention_of_large_values_beside_small_ones_and_hidden_infinities(dtype
     assert np.all(np.abs(host(a[:-1]) - host(o[:-1])) <= 2 * half * np.abs(host(o[:-1])) + 2.0 ** -14 * mean)
     assert torch.all(a[-1] == float("inf")) and torch.allclose(b, l, rtol=0, atol=2.0 ** -16)
     no_error()
+
+
+# -------------------------------------------------------------------------------------------- pools
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("order", ["NPHD", "NHPD", "HNPD", "PNHD", "PHND", "HPND"])
+def test_pools_of_any_order_of_their_dimensions(order, dtype):
+    r = rng(5)
+    size = dict(N=7, P=8, H=2, D=32)
+    back = [order.index(c) for c in "NPHD"]
+    pools = [torch.from_numpy(r.standard_normal([size[c] for c in order]).astype(np.float32)).to(DEV, DT[dtype]).permute(back)
+             for _ in range(2)]
+    dense = [p.contiguous() for p in pools]
+    table, start = ints([[0, 3, 6], [5, 2, -1]]), ints([19, 8])
+    k, v = (dev(r.standard_normal((5, 2, 32)), dtype)[0] for _ in range(2))
+    q = dev(r.standard_normal((5, 4, 32)), dtype)[0]
+    f, _ = kda.rotary_frequencies(32, device=DEV)
+    out = []
+    for kp, vp in (pools, dense):
+        y = kda.cache_append(q, k, v, f, kp, vp, table, start, input_row_offsets=ints([0, 3, 5]))
+        out.append([y, kda.cache_attention(y[[2, 4]], kp, vp, table, ints([22, 10]))])
+    no_error()
+    assert all(torch.equal(a, b) for a, b in zip(*out)) and all(torch.equal(a, b) for a, b in zip(pools, dense))
