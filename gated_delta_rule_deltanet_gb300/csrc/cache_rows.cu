@@ -116,7 +116,7 @@ __device__ __forceinline__ Row row_of(const RowsArgs& a, int i) {
   const int old = from ? a.lens[r.parent] : 0;
   r.kept = max(0, min(old, len));
   r.full = r.kept / a.P;
-  r.want = r.parent < a.S ? pages_of(len, a.P, a.width) : -1;
+  r.want = r.parent >= -1 && r.parent < a.S ? pages_of(len, a.P, a.width) : -1;
   r.end = pages_of(old, a.P, a.width);
   return r;
 }

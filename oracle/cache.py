@@ -83,6 +83,8 @@ def update(table, lens, refs, parent, new_lens, P):
     pages = lambda n: -(-n // P)                                              # noqa: E731
     if any(pages(n) > width for n in list(lens) + list(new_lens)):
         raise ValueError("a row is too long")
+    if any(not -1 <= p < S for p in parent):
+        raise ValueError("no such parent")
     if any(q >= 0 and refs[q] <= 0 for r in range(S) for q in table[r, :pages(lens[r])]):
         raise ValueError("a row names a free page")
     free = [q for q, r in enumerate(refs) if r == 0]

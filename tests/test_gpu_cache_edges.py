@@ -98,6 +98,15 @@ def test_update_refuses_a_free_page_whose_changes_cancel():
     refused(np.array([[0, 1], [0, 3]], np.int32), [8, 5], [0, 1, 1, 1, 0, 0, 0, 0], [-1, 1, 1], [0, 5, 5], 4)
 
 
+@pytest.mark.parametrize("bad", [-2, -2 ** 31, 2, 2 ** 31 - 1])
+@pytest.mark.parametrize("at", [0, 2])
+def test_update_refuses_a_parent_out_of_range(bad, at):
+    """-1 is the one that stands for nothing."""
+    parent = [0, 1, -1]
+    parent[at] = bad
+    refused(np.array([[0, 1], [2, 3]], np.int32), [8, 5], [1, 1, 1, 1, 0, 0, 0, 0], parent, [8, 5, 3], 4)
+
+
 @pytest.mark.parametrize("S", [4096, 4097, 6000])
 @pytest.mark.parametrize("fork", [False, True])
 @pytest.mark.parametrize("page", [0, 1])
