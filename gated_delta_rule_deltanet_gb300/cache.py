@@ -428,11 +428,12 @@ def cache_update(block_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tens
         _device(refs, *out)
         _out(out, (("table", (S, width)), ("lens", (S,)), ("refs", (N,)), ("kept", (S,)), ("src", (S,)), ("dst", (S,))),
              (block_table, lens, refs, parent, new_lens))
+    copy = _find_copy(pools, out.src, out.dst, N) if pools else None
     space, address, nbytes = _space(plan, workspace)
     _call(plan, block_table.data_ptr(), lens.data_ptr(), refs.data_ptr(), _p(parent), new_lens.data_ptr(),
           *[t.data_ptr() for t in out], address, nbytes)
-    if pools:
-        _copy(pools, out.src, out.dst, N)
+    if copy is not None:
+        _copy(copy, pools, out.src, out.dst)
     return out
 
 
@@ -460,10 +461,11 @@ def cache_compact(block_table: torch.Tensor, lens: torch.Tensor, refs: torch.Ten
         _device(refs, *out)
         _out(out, (("table", shape), ("refs", (N,)), ("page_map", (N,)), ("src", (N // 2,)), ("dst", (N // 2,))),
              (block_table, lens, refs))
+    copy = _find_copy(pools, out.src, out.dst, N) if pools else None
     space, address, nbytes = _space(plan, workspace)
     _call(plan, block_table.data_ptr(), lens.data_ptr(), refs.data_ptr(), *[t.data_ptr() for t in out], address, nbytes)
-    if pools:
-        _copy(pools, out.src, out.dst, N)
+    if copy is not None:
+        _copy(copy, pools, out.src, out.dst)
     return out
 
 
@@ -493,11 +495,13 @@ def _plan_copy(key, pools, src, dst, num_pages):
     return _keep(key, p)
 
 
-def _copy(pools, src, dst, num_pages=None):
+def _find_copy(pools, src, dst, num_pages=None):
+    """The plan of a copy, its pools checked."""
     key = ("cache_copy", _sig(src), _sig(dst), num_pages, *[_sig(t) for t in pools])
-    p = _PLANS.get(key)
-    if p is None:
-        p = _plan_copy(key, pools, src, dst, num_pages)
+    return _PLANS.get(key) or _plan_copy(key, pools, src, dst, num_pages)
+
+
+def _copy(p, pools, src, dst):
     args = (p.addresses(*[t.data_ptr() for t in pools]), p.sizes, p.strides, p.n, src.data_ptr(), dst.data_ptr(),
             p.entries, p.num_pages)
     if _current_device() == p.index:
@@ -519,4 +523,4 @@ def cache_copy(pools: Sequence[torch.Tensor], src: torch.Tensor, dst: torch.Tens
     if stream is not None:
         with _on(stream, src):
             return cache_copy(pools, src, dst)
-    _copy(pools, src, dst)
+    _copy(_find_copy(pools, src, dst), pools, src, dst)

@@ -126,6 +126,22 @@ def test_update_refuses_a_free_page_of_many_rows(S, fork, page):
     refused(table, [5] * S, refs, parent, new, 4)
 
 
+@pytest.mark.parametrize("what", ["pages", "rows", "host"])
+def test_pools_are_looked_at_before_anything_is_written(what):
+    pool = {"pages": torch.zeros((7, 4), device=DEV), "rows": torch.zeros((8, 4), device=DEV)[:, ::2],
+            "host": torch.zeros((8, 4))}[what]
+    table, lens, refs = ints([[0, 1], [2, 3]]), ints([8, 5]), ints([1, 1, 1, 1, 0, 0, 0, 0])
+    rows = kda.CacheRows(*(torch.full(s, 99, dtype=torch.int32, device=DEV) for s in ((2, 2), (2,), (8,), (2,), (2,), (2,))))
+    with pytest.raises(ValueError):
+        kda.cache_update(table, lens, refs, None, lens, page_size=4, pools=[pool], out=rows)
+    moves = kda.CacheMoves(*(torch.full(s, 99, dtype=torch.int32, device=DEV) for s in ((2, 2), (8,), (8,), (4,), (4,))))
+    with pytest.raises(ValueError):
+        kda.cache_compact(table, lens, refs, page_size=4, pools=[pool], out=moves)
+    torch.cuda.synchronize()
+    assert all(torch.all(t == 99) for t in (*rows, *moves))
+    no_error()
+
+
 # --------------------------------------------------------------------------------------- attention
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
