@@ -141,8 +141,9 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
     """Rotary positions (kda_rotary_fwd): the channel pairs of q [T, H, d] and k [T, HK, d] (or None)
     turned by positions[t] * frequencies[i] and multiplied by `magnitude`; channels from
     2 * frequencies.numel() on pass.  `layout`: pairs (i, i + R/2) ("half") or (2i, 2i + 1)
-    ("interleaved").  positions [T] int32 or int64 of any size: angles are formed in 64-bit fixed
-    point; frequencies as `rotary_frequencies` returns them.  q and k may be column blocks of a packed projection.
+    ("interleaved").  positions [T] int32 or int64: angles are formed in 64-bit fixed point, off
+    by up to 2^-28 + |p f| 2^-55 of a turn (2^-24 at 2^31 and one radian a position); frequencies as `rotary_frequencies`
+    returns them.  q and k may be column blocks of a packed projection.
     Returns (q', k'), dense unless `q_out` / `k_out` are given, which may be q and k themselves."""
     if stream is not None:
         with _on(stream, q):
@@ -230,8 +231,9 @@ def cache_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
     into the pages, q [T, H, d] (or None) turned and returned.
 
     k_pages, v_pages [num_pages, page_size, HK, d], any strides that keep the heads' channels together
-    (permuted views of [num_pages, HK, page_size, d], [HK, num_pages, page_size, d] and the like too); block_table [B, max_pages] int32; start
-    [B] int32: the tokens that each sequence already holds, the position of its first new one.
+    (permuted views of [num_pages, HK, page_size, d], [HK, num_pages, page_size, d] and the like too), that
+    share no memory; block_table [B, max_pages] int32; start [B] int32: the tokens that each sequence
+    already holds, the position of its first new one.
     Without `input_row_offsets` every row is a sequence's one new token (the decode form); with it, tokens from
     its last entry on are left alone.  `frequencies` None: nothing is turned."""
     if stream is not None:
@@ -515,9 +517,10 @@ def _copy(p, pools, src, dst):
 
 def cache_copy(pools: Sequence[torch.Tensor], src: torch.Tensor, dst: torch.Tensor, *,
                stream: Optional[torch.cuda.Stream] = None) -> None:
-    """pool[dst[i]] = pool[src[i]] in every pool, in one launch for pools of one size (kda_cache_copy): pages of a cache, or
-    slots of a recurrent state or convolution pool (a forked sequence's state).  src, dst [n] int32;
-    the list ends at its first negative src.  No slot may be written twice or both read and written."""
+    """pool[dst[i]] = pool[src[i]] in every pool (kda_cache_copy): pages of a cache, or slots of a recurrent state or
+    convolution pool (a forked sequence's state); up to 64 neighbouring pools of one size go in one launch.
+    src, dst [n] int32; the list ends at its first negative src, and every src behind it has to be
+    negative.  No slot may be written twice or both read and written."""
     if not pools:
         return
     if stream is not None:

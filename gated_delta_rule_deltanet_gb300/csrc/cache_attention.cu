@@ -10,8 +10,9 @@
 // with m and l kept as running values (Milakov and Gimelshein, "Online normalizer calculation for softmax",
 // 2018) in base 2.  A row that sees no key has o = 0 and lse = -infinity.
 //
-// Bound by HBM: each key and value is read once for all rows of its group (queries x heads of one key head).
-// The work is cut into tiles of keys of an item (a sequence, a key head and up to 64 of its rows), and the row of all
+// Bound by HBM: each key and value is read once for up to 64 rows of its group (queries x heads of one key head), 32 where
+// heads are wider than 128 and 8 with fp32 pages; more rows read it once more for each such tile of rows.  The
+// work is cut into tiles of keys of an item (a sequence, a key head and one of its tiles of rows), and the row of all
 // tiles into equal stretches, one for each CTA, whatever the sequences' lengths: a stretch that begins or ends inside an
 // item leaves (m, l, unnormalised o) of its part in the workspace, and a second kernel joins the parts in the order of
 // the stretches, so that repeated calls give the same bits.  The lengths stay on the device: a captured graph follows
@@ -29,7 +30,7 @@
 //
 // One GB300 (of measured HBM): 256 sequences of 256 to 8192 keys, 8 key heads of 128, 2.2 GB of bf16 pages 345-356 us
 // (92-95%); 3 sequences of up to 262144 keys 150-156 us (91-95%); heads of 64 75-81%, of 256 79%; 32 and 64 rows a key
-// head 76% and 31%; fp32 pages 87-93% with two rows, 75% with eight.  One sequence of 5000 keys 9.8 us: a chain of some
+// head 76% and 31%; fp32 pages 87-93% with two rows, 75% with eight.  One sequence of 5000 keys 9.9 us: a chain of some
 // 12 k cycles through both kernels.
 #include <algorithm>
 #include <type_traits>
@@ -44,8 +45,8 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // A stretch is counted in units: tiles, and what an item costs beside them (the ring runs empty at its end, and the
-// groups' sums are joined).  61 short sequences with costs of 1, 2 and 4: 31.5, 29.5, 33.2 us; one sequence of 5000 keys
-// in stretches of 2 units 9.9 us, of 4 12.1.
+// groups' sums are joined).  61 short sequences with costs of 1, 2 and 4: 30.4, 27.5, 31.3 us; one sequence of 5000 keys
+// in stretches of 2 units 9.9 us, of 4 12.0.
 constexpr int kItemCost = 2, kMinUnits = 2;
 
 // A running maximum follows the scores only when one is this far above it (in powers of two): sums grow by up
@@ -1050,8 +1051,8 @@ __global__ void __launch_bounds__(kThreads, Simt<DP, R>::kCtas)
 // Row r of the item that note_joins left at place x, which stretch c is the first to begin inside: parts c - 1 (its second
 // place) and c, c + 1, .. (their first places) are added in a fixed order.  WPR warps take a row, every WPR-th part each,
 // kJoinDepth of them in flight, then their sums are added.  Eight warps where an item has many parts (41 of each of 16 rows:
-// the call takes 9.8 us, 14.9 with one warp), one where items are many and have few (two or three of each of 64 rows
-// of 256 items: 149 us with eight, whose blocks' launches set the pace, 110 with one).
+// the call takes 9.9 us, 14.9 with one warp), one where items are many and have few (two or three of each of 64 rows
+// of 256 items: 155 us with eight, whose blocks' launches set the pace, 111 with one).
 constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps, kJoinDepth = 4, kFewParts = 8;
 
 template <int WPR, bool BF_OUT>

@@ -18,8 +18,8 @@
 //
 // Both are chains of short passes (count, rank, assign) over at most some million integers, bound by the latency of the
 // passes: one thread-block cluster runs them in one launch, with the cluster's hardware barrier between them.
-// One GB300: 256 rows of up to 250 pages one step on 15 us, with a list of copies that is empty; 64 rows to 512 of up to
-// 960 pages 32 us, 12 of them copies; a compaction that moves 1.15 GB 379 us, 358 of them copies (95% of measured HBM).
+// One GB300: 256 rows of up to 250 pages one step on 14 us, with a list of copies that is empty; 64 rows to 512 of up to
+// 960 pages 33 us, 12 of them copies; a compaction that moves 1.15 GB 379 us, 358 of them copies (95% of measured HBM).
 #include <algorithm>
 #include <limits.h>
 
@@ -31,8 +31,8 @@ namespace {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 // Entries of the new table and references from which sixteen blocks run instead of eight: what an SM moves bounds large
-// tables, the barriers small ones.  2.0 M entries 139 us by eight, 80 by sixteen; 520 k (with copies) 36.8 and 32.0; 70 k
-// 13.0 and 15.0.
+// tables, the barriers small ones.  2.0 M entries 130 us by eight, 74 by sixteen; 520 k (with copies) 37.1 and 33.1; 70 k
+// 14.2 and 14.4; a compaction of 2 k 10.5 and 12.3.
 constexpr int64_t kManyEntries = 1 << 17;
 
 __device__ __forceinline__ void cluster_sync() {
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kThreads) update_kernel(const RowsArgs a) {
   // them each child counts its own.  A row that names a free page is found here where it adds
   // nothing (by refs) or takes back (by the count's start, which the addition returns); what rows only add to a free
   // page is found at its count in pass 3.  All by refs: eight continuations of 64 prompts 38 us instead of 33, 2048 rows
-  // one step on 84 instead of 75.
+  // one step on 84 instead of 74.
   const auto fault = [&]() { atomicExch(words, 1); };
   const auto pages_shared = [&](int r) { return counted && children[r] > 0 ? shared_pages[r] : 0; };
   for (int r = my_row; r < a.S; r += rows_at_once) {

@@ -10,8 +10,9 @@
 //
 // The angle.  p f_i in fp32 is off by up to p 2^-24: 0.06 rad at p = 10^6.  Whole turns do not matter and p
 // is an integer, so f_i / 2 pi is kept as a fraction of a turn in 64-bit fixed point and multiplied by p modulo
-// 2^64: two integer multiplications, off by no more than p 2^-64 turns beside f_i's own rounding.  The two top bits
-// give the quadrant, the rest an argument of at most an eighth of a turn for sincospif.
+// 2^64: two integer multiplications, off by no more than p 2^-64 turns.  Before them f_i / 2 pi is rounded in fp64, the
+// constant and the product, together by 2^-52.3 of itself: p f_i 2^-55 turns.  The two top bits give the quadrant, the rest
+// an argument of at most an eighth of a turn, rounded to 2^-28 of a turn, for sincospif.
 //
 // Bound by HBM: every value is read and written once, and the sines (R/2 for each token, whatever its heads) are
 // formed once into shared memory by the block that turns the token's heads.  One GB300: 16384 tokens x 40 heads x 128

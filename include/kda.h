@@ -657,7 +657,7 @@ typedef struct kda_rotary_params {
  *     (a, b) -> m (a cos - b sin, b cos + a sin)
  *
  *   q [T, H, d], k [T, HK, d] (NULL with no heads)   positions [T], negative ones too; the angle is
- *   good to 2^-24 of a turn for |p| < 2^31           frequencies [R / 2] fp64, radians per position
+ *   off by up to 2^-28 + |p f| 2^-55 of a turn       frequencies [R / 2] fp64, radians per position
  *   q_out, k_out: may be q, k (same pointer and stride); otherwise they share no memory with q, k or one another
  * kda_rotary_bwd is the transposed map, for gradients.
  */
